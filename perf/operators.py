@@ -413,11 +413,11 @@ def _encode_plain(x, bits):
     n, width = x.shape
     groups = _groups(width)
     x = torch.nn.functional.pad(x.double(), (0, groups * GROUP - width)).view(n, groups, GROUP)
-    r = x @ _hadamard(torch.float64)
-    norm = r.pow(2).sum(-1, keepdim=True).sqrt()
-    u = r / norm.clamp(min=1e-12)
+    r = x @ _hadamard(torch.float64).sign()  # sums without 1/sqrt(128): exact for narrow types, where ties happen
+    norm = x.pow(2).sum(-1, keepdim=True).sqrt()
     lv = torch.from_numpy(_codebook(bits)).to(DEV).double()
-    code = (u[..., None] > (lv[1:] + lv[:-1]) / 2).sum(-1)  # a tie falls to the lower level
+    border = (lv[1:] + lv[:-1]) / 2 * (norm.clamp(min=1e-12) * math.sqrt(GROUP))[..., None]
+    code = (r[..., None] > border).sum(-1)  # a tie falls to the lower level
     if bits == 5:
         code = (code - 1) & 3
     return _pack(code.view(n, groups * GROUP), _width(bits)), norm[..., 0].half()
