@@ -30,7 +30,9 @@ GROUP = 128
 __all__ = [
     "cq_levels", "cq_code_width", "cq_codebook_init", "cq_packed_bytes", "cq_encode",
     "cq_act_quant_int8", "cq_gemv", "cq_gemv_grouped", "cq_gemv_shared", "cq_gemm", "cq_gemm_grouped", "cq_gemm_noalloc",
-    "cq_gather_rows", "cq_kv_write", "cq_kv_attend", "cq_device_status", "cq_cact_write", "cq_cact_open", "cq_cact_open_memory", "CactReader",
+    "cq_gather_rows", "cq_kv_write", "cq_kv_attend",
+    "cq_rope_init", "cq_qk_norm_rope", "cq_kv_plan", "cq_kv_geometry", "cq_kv_write_slots", "cq_kv_tree_attend",
+    "cq_device_status", "cq_cact_write", "cq_cact_open", "cq_cact_open_memory", "CactReader",
     "CQError", "library_path", "GROUP",
 ]
 
@@ -508,3 +510,8 @@ def cq_cact_open_memory(data: bytes) -> CactReader:
     buf = ctypes.create_string_buffer(bytes(data), len(data))
     check(_lib().cq_cact_open_memory(ctypes.cast(buf, ctypes.c_void_p), len(data), ctypes.byref(h)))
     return CactReader(h)
+
+
+# the paged cache's serving steps; imported last, they use the helpers above
+from .paged import (cq_kv_geometry, cq_kv_plan, cq_kv_tree_attend, cq_kv_write_slots,  # noqa: E402
+                    cq_qk_norm_rope, cq_rope_init)

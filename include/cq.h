@@ -376,6 +376,168 @@ typedef struct cq_kv_seq {
 int cq_kv_attend(const cq_kv_geom *geom, const cq_kv_seq *seqs, int n_seqs,
                  void *stream);
 
+/* ------------------------------------- paged CQ KV cache: serving steps -- */
+/*
+ * The steps between the projections and the output projection of a model
+ * that serves many requests from one pool of cache blocks, with drafted
+ * tokens (a plain decode step is one drafted token per request). The pages
+ * have no counterpart beyond the CQ cache itself ([CF] "Five regions").
+ *
+ * A paged cache is the cache of cq_kv_write with its `cap` rows cut into
+ * blocks: block b is rows b*block_size .. (b+1)*block_size - 1, and a
+ * request's token t lives in row block_table[t / block_size] * block_size +
+ * t % block_size, its slot. One cache of one block per request is the
+ * unpaged layout, and cq_kv_write and cq_gather_rows work on the same blob.
+ * Lengths, tables and slots are device memory, so that a captured CUDA graph
+ * serves any lengths up to the sizes given by the host.
+ */
+
+/* Element types of the tensors below. */
+#define CQ_T_F32 0
+#define CQ_T_F16 1
+#define CQ_T_BF16 2
+
+/* Position rotation rates for cq_qk_norm_rope: rates[i] is the part of a
+ * turn by which one position rotates pair i, as a 64-bit binary fraction:
+ * inv_freq[i] / (2 pi) * 2^64, its integer part dropped. The kernel multiplies
+ * them by integer positions modulo 2^64, so an angle is as exact at a position
+ * of 10^9 as at 1.
+ * inv_freq: rot_dim/2 host values (radians per position, finite), or NULL for
+ * theta^(-2i/rot_dim). rates: host buffer of `cap` values, or NULL to query
+ * the count only; n_rates receives rot_dim/2 and may be NULL.
+ * Errors: CQ_ERR_ARG (theta not positive and finite where it is used, cap too
+ * small, an inv_freq that is not finite), CQ_ERR_SHAPE (rot_dim odd, negative
+ * or over 256). */
+int cq_rope_init(int rot_dim, double theta, const double *inv_freq,
+                 uint64_t *rates, size_t cap, size_t *n_rates);
+
+/* One call of cq_qk_norm_rope. Strides are in elements; the last dimension
+ * is contiguous. q and k may be slices of one projection's output. */
+typedef struct cq_qk_desc {
+    const void *q, *k;             /* [n_tokens][heads][head_dim], in_dtype */
+    void *q_out, *k_out;           /* same shapes, q_out_dtype and k_out_dtype */
+    const float *q_weight, *k_weight; /* [head_dim], device; NULL: all ones */
+    const int32_t *positions;      /* [n_tokens], device */
+    const uint64_t *rates;         /* rot_dim/2, HOST (cq_rope_init) */
+    int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h;
+    int64_t qo_stride_t, qo_stride_h, ko_stride_t, ko_stride_h;
+    int in_dtype, q_out_dtype, k_out_dtype; /* CQ_T_* */
+    int n_tokens, n_q_heads, n_kv_heads;    /* a head count may be 0 */
+    int head_dim;                  /* even, 2..256 */
+    int rot_dim;                   /* even, 0..head_dim: the leading part that rotates */
+    int interleaved;               /* pairs (2i, 2i+1); else (i, i + rot_dim/2) */
+    float eps, weight_offset;
+} cq_qk_desc;
+
+/* Norm of every query and key head and its position rotation, in one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * (weight_offset + weight)
+ *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t),
+ *   t = positions[token] * inv_freq[pair]
+ * in fp32, rounded once to the output type (weight_offset 1 is the
+ * zero-centred norm, whose stored weights lie around 0). An output may be its
+ * own input (same pointer, strides and type) and otherwise must not overlap
+ * one. Errors: CQ_ERR_ARG, CQ_ERR_SHAPE, CQ_ERR_CUDA. */
+int cq_qk_norm_rope(const cq_qk_desc *d, void *stream);
+
+/* One call of cq_kv_plan; all pointers are device memory. */
+typedef struct cq_kv_step {
+    const int32_t *seq_lens;  /* [n_seqs] tokens that a request has in the cache */
+    const int32_t *new_lens;  /* [n_seqs] tokens that this step adds (0 allowed) */
+    const int32_t *held;      /* [n_seqs] blocks its table row holds already */
+    int32_t *block_table;     /* [n_seqs][max_blocks], rows table_stride apart; updated */
+    const int32_t *free_list; /* [free_cap] stack of free blocks; its top is entry n_free-1 */
+    const int32_t *n_free;    /* [1] */
+    int32_t *held_out;        /* [n_seqs] */
+    int32_t *n_free_out;      /* [1] */
+    int32_t *slots;           /* [n_tokens] cache row of each new token, -1 past the last */
+    int32_t *positions;       /* [n_tokens] position in its request, -1 past the last */
+    int32_t *token_seq;       /* [n_tokens] its request, -1 past the last */
+    int32_t *cu_new;          /* [n_seqs + 1] first new token of each request, then their number */
+    int64_t table_stride;
+    int n_seqs, max_blocks, block_size, free_cap;
+    int n_tokens;             /* room of slots, positions and token_seq */
+} cq_kv_step;
+
+/* Block tables and slot maps of one step, from the requests' lengths: the new
+ * tokens of request s take positions seq_lens[s] .. seq_lens[s] + new_lens[s]
+ * - 1. A request with new tokens needs ceil((seq_lens + new_lens) /
+ * block_size) blocks; those past the `held` ones are taken from the top of
+ * the free stack, requests in order and each request's blocks in order, and
+ * written into its table row. Blocks kept from rejected drafts (held above
+ * the need) stay and are used first. Neither seq_lens nor free_list changes:
+ * the next step passes the lengths after acceptance, held_out and n_free_out.
+ * Where the stack runs out, or a table row would need more than max_blocks,
+ * the missing blocks and their tokens' slots are -1; where the tokens do not
+ * fit into n_tokens, the rest is dropped; each marks the device status word,
+ * which a following cq_device_status reports as CQ_ERR_INDEX. n_free_out =
+ * n_free minus the blocks asked for: negative by what is missing. Lengths
+ * below zero count as zero. held_out and n_free_out must not be held and
+ * n_free themselves. Errors: CQ_ERR_ARG, CQ_ERR_SHAPE, CQ_ERR_CUDA. */
+int cq_kv_plan(const cq_kv_step *s, void *stream);
+
+/* Encodes k[n][n_kv_heads*head_dim_k] and v[n][n_kv_heads*head_dim_v]
+ * (`dtype`, rows k_stride and v_stride elements apart) into rows slots[i] of
+ * the two caches (`cap` rows each), one launch for both. Rows with slot -1
+ * are skipped; a slot outside [-1, cap) is skipped too and marks the device
+ * status word (CQ_ERR_INDEX). The slots of a call must be distinct.
+ * The encoding is cq_kv_write's definition with every decision exact: a
+ * coordinate or a norm that fp32 places too near a border is decided in 64
+ * bits. Of the geometry this call reads the key/value heads, head widths,
+ * bits and codebooks. Errors: CQ_ERR_ARG, CQ_ERR_SHAPE, CQ_ERR_CUDA. */
+int cq_kv_write_slots(const cq_kv_geom *geom, uint8_t *k_cache,
+                      uint8_t *v_cache, int cap, const void *k,
+                      int64_t k_stride, const void *v, int64_t v_stride,
+                      int dtype, const int32_t *slots, int n, void *stream);
+
+/* Largest number of drafted tokens per request of cq_kv_tree_attend. */
+#define CQ_TREE_MAX_NODES 256
+
+/* One call of cq_kv_tree_attend; device memory unless marked. Strides in
+ * elements; the last dimension of q and o is contiguous. */
+typedef struct cq_kv_tree {
+    const uint8_t *k_cache, *v_cache; /* `cap` rows each */
+    const int32_t *block_table;  /* [n_seqs][max_blocks], rows table_stride apart */
+    const int32_t *context_lens; /* [n_seqs] tokens before the drafted ones */
+    const int32_t *cu_nodes;     /* [n_seqs + 1] first drafted token of each request */
+    const uint32_t *mask;        /* [n_nodes][mask_words] or NULL: causal */
+    const void *q;               /* [n_nodes][n_q_heads][head_dim_k] */
+    void *o;                     /* [n_nodes][n_q_heads][head_dim_v] */
+    void *workspace;             /* cq_kv_tree_workspace bytes, 16-byte aligned */
+    size_t workspace_bytes;
+    int64_t table_stride, q_stride_t, q_stride_h, o_stride_t, o_stride_h;
+    int cap, max_blocks, block_size, n_seqs;
+    int n_nodes;                 /* rows of q and o */
+    int max_nodes;               /* most drafted tokens of a request, 0..CQ_TREE_MAX_NODES */
+    int mask_words;              /* >= ceil(max_nodes / 32); ignored without mask */
+    int dtype;                   /* of q and o: CQ_T_F16 or CQ_T_BF16 */
+} cq_kv_tree;
+
+/* Bytes of workspace that cq_kv_tree_attend needs on the current device for
+ * this geometry and these sizes; 0 on invalid arguments. */
+size_t cq_kv_tree_workspace(const cq_kv_geom *geom, int n_seqs, int max_nodes);
+
+/* Attention of drafted tokens over a paged CQ cache:
+ *   o[i][b] = sum_t p[i][b][t] v_hat[t][h],
+ *   p[i][b] = softmax_t(scale * <q[i][b], k_hat[t][h]>),  h = b / (n_q_heads / n_kv_heads)
+ * for drafted token i of request s over its context (positions 0 ..
+ * context_lens[s] - 1) and those drafted tokens j of its request whose bit
+ * j % 32 of mask[i][j / 32] is set (its ancestors and itself, for a tree).
+ * Drafted token j stands in the cache at position context_lens[s] + j. With
+ * mask NULL token i attends drafted tokens 0 .. i: a linear draft or a chunk
+ * of a prompt. A token that attends nothing gets o = 0. What a token does not
+ * attend has no influence on it, whatever bytes the cache holds there; rows
+ * past the drafted tokens are never read.
+ * The caches are never expanded in memory; the arithmetic is that of
+ * cq_kv_attend (fp16 levels and rotated queries on the tensor cores, fp32
+ * logits, softmax and sums, probabilities times norms in fp16). Block numbers
+ * outside the cache, and lengths outside the given sizes, are skipped and
+ * mark the device status word (CQ_ERR_INDEX). Every head must lie within two
+ * groups of 128 of its cache row (all head widths up to 128, and 256).
+ * Errors: CQ_ERR_ARG, CQ_ERR_SHAPE, CQ_ERR_CUDA; CQ_ERR_TIMEOUT through
+ * cq_device_status if a pipeline wait gave up. */
+int cq_kv_tree_attend(const cq_kv_geom *geom, const cq_kv_tree *t,
+                      void *stream);
+
 /* Reads and clears the device-side status word (synchronises `stream`).
  * CQ_OK; CQ_ERR_TIMEOUT if a bounded wait gave up (results of that call are
  * invalid); CQ_ERR_INDEX if a gather met an index out of range (and no wait
