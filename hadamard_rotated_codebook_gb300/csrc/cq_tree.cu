@@ -26,8 +26,7 @@
 //
 // Roles of the 16 warps: 0-7 softmax (two warpgroups, half the columns each; they also rotate the queries
 // and write the partials), 8-11 expand keys into TMEM (a thread per cache row; the A operand), 12-15
-// expand values into shared memory; warp 8 also issues the MMAs, S of a tile when its keys are
-// there and then O of the tile before. The expanders fetch their own codes by cp.async into a
+// expand values into shared memory; warp 8 also issues the first product of each tile and warp 12 the second. The expanders fetch their own codes by cp.async into a
 // ring a few tiles ahead, so they wait for nobody's loads but their own. (A warp of its own for the MMAs would
 // cost every thread a fifth of its registers: they are handed out to four warps at a time.)
 // Every wait is bounded: when one gives up, the flag s_abort makes all later waits return at once and every role
@@ -63,6 +62,7 @@ struct TreeParams {
     uint32_t tk[8], tv[8];  // level tables: low bytes of 16 fp16 levels, then high bytes
     float k_mult, v_mult;   // scale * log2(e) / sqrt(128) * 2^(table exponent); 2^(table exponent) / sqrt(128)
     int n_units, hq, per, dk, dv, wk, wv, kgroups, vgroups;
+    uint32_t div_mul, div_shift;  // t / block_size = t * div_mul >> div_shift
     int rows;        // most query heads of a unit
     int ncol_max;    // column tiles of a request with max_nodes tokens
     int grid;
@@ -96,17 +96,26 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+// The issuing warp runs as a whole and one elected lane issues: operands then stay in uniform registers (a branch
+// to one lane made each MMA cost about 100 cycles of moves).
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xFFFFFFFF;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+        : "memory");
 }
 // D += A B with A in tensor memory (lane = row, a column holds two fp16) or in shared memory.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(acc));
+    asm volatile(
+        "{\n .reg .pred p, e;\n elect.sync _|e, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc));
+    asm volatile(
+        "{\n .reg .pred p, e;\n elect.sync _|e, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 // Shared-memory operand in 128-byte swizzled atoms of 8 rows of 128 bytes, atoms 1024 bytes apart
 // along the rows. K-major: a row is one M/N index, 64 of K. MN-major: a row is one K index, 64 of M/N,
@@ -263,7 +272,7 @@ __device__ __forceinline__ int run_of(long long total, int grid, long long tile)
 }
 
 struct Shared {
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2], sc_full[2], z_full, drain;
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2], sc_full[2], z_full, drain[2];
     uint32_t tmem;
     volatile int abort;
     int zmax;
@@ -421,81 +430,83 @@ struct Plan {
     static constexpr int oV = 0, oP = oV + kVBuf * NG * kVBytes, oZ = oP + 2 * kPBytes, oRing = oZ + NG * kZBytes;
     static constexpr int oNorm = oRing + 2 * kDepth * kRing, oShared = oNorm + 2 * kDepth * kNorm;
     static constexpr int kSmem = oShared + (int)sizeof(Shared) + 1024;
+    static constexpr int kSoft = NG == 2 ? 136 : 160, kExp = 256 - kSoft;  // registers of the roles
     // TMEM columns
     static constexpr int cK = 0, cS = 2 * NG * 64, cO = cS + 2 * N;
     static_assert(cO + NG * N <= 512, "tensor memory");
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-// The side of one expander thread: fetches its cache row's codes and norms of the tiles ahead.
+// One expander thread's cache row of the tiles ahead. The block number of the next tile is loaded a tile before it is used, in
+// straight-line code (a load under a branch would be waited for where the branch ends).
 struct Fetch {
     Cursor c;
-    bool more, ok;
+    const uint8_t *codes;  // the cache, at the unit's first group
+    const __half *norms;
+    uint32_t g0, ng;
     int blk, off;
+    bool ok, more;
 };
 
-template <int N, int NG, bool KEYS>
-__device__ __forceinline__ void fetch_block(const TreeParams &p, Fetch &f, int row) {
-    f.ok = false;
-    if (!f.more) return;
-    const int t = f.c.tile * kTile + row;
-    if (t < f.c.len) {
-        const int b = (unsigned)t / (unsigned)p.t.block_size;
-        f.off = t - b * p.t.block_size;
-        f.blk = p.t.block_table[f.c.s * p.t.table_stride + b];  // b < max_blocks: len is cut to the table
-        f.ok = true;
-    }
-}
-
-template <int N, int NG, bool KEYS>
-__device__ __forceinline__ bool fetch_codes(const TreeParams &p, const Fetch &f, uint32_t ring, uint32_t norm, int row) {
+template <bool KEYS>
+__device__ __forceinline__ void fetch_unit(const TreeParams &p, Fetch &f) {
+    const TreeUnit &u = p.unit[f.c.u];
     const int w = KEYS ? p.wk : p.wv, groups = KEYS ? p.kgroups : p.vgroups;
     const uint8_t *cache = KEYS ? p.t.k_cache : p.t.v_cache;
-    const size_t stride = (size_t)groups * 16 * w;
+    f.g0 = KEYS ? u.gk : u.gv;
+    f.ng = KEYS ? u.ngk : u.ngv;
+    f.codes = cache + f.g0 * 16 * w;
+    f.norms = reinterpret_cast<const __half *>(cache + (size_t)p.t.cap * ((size_t)groups * 16 * w));
+}
+
+__device__ __forceinline__ void fetch_block(const TreeParams &p, Fetch &f, int row) {
+    const int t = f.c.tile * kTile + row, tc = max(0, min(t, f.c.len - 1));
+    const int b = (int)((uint64_t)(uint32_t)tc * p.div_mul >> p.div_shift);  // tc / block_size
+    f.off = tc - b * p.t.block_size;
+    f.ok = t < f.c.len;
+    f.blk = p.t.block_table[f.c.s * p.t.table_stride + b];  // b < max_blocks: len is cut to the table
+}
+
+// Starts the copies of the row's codes and norms; the norm's half of its word in `odd`.
+template <int NG, bool KEYS, int W>
+__device__ __forceinline__ bool fetch_codes(const TreeParams &p, const Fetch &f, uint32_t ring, uint32_t norm, int row, uint32_t &odd) {
+    const int groups = KEYS ? p.kgroups : p.vgroups;
     const long long r = (long long)f.blk * p.t.block_size + f.off;
     bool ok = f.ok;
     if (ok && (f.blk < 0 || r >= p.t.cap)) {
         ok = false;
         atomicOr(p.status, kStatusIndex);
     }
-    const TreeUnit &u = p.unit[f.c.u];
-    const int g0 = KEYS ? u.gk : u.gv, ng = KEYS ? u.ngk : u.ngv;
+    const size_t at0 = (size_t)r * groups + f.g0;
+    odd = (uint32_t)at0 & 1;
+    if (!ok) return false;
+    const uint8_t *src = f.codes + (size_t)r * (groups * 16 * W);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
+        if (g == 1 && f.ng == 1) break;
         const uint32_t nd = norm + (g * kTile + row) * 4;
-        if (!ok || g >= ng) {
-            continue;
-        }
-        const uint8_t *src = cache + (size_t)r * stride + (size_t)(g0 + g) * 16 * w;
         const uint32_t dst = ring + (g * 4 * kTile + row) * 16;
-        for (int i = 0; i < w; ++i) cp_async16(dst + i * kTile * 16, src + 16 * i);
+#pragma unroll
+        for (int i = 0; i < W; ++i) cp_async16(dst + i * kTile * 16, src + g * 16 * W + 16 * i);
         // the norm as the 4-byte word that holds it, unless that word would end past the cache
-        const size_t at = (size_t)r * groups + g0 + g, all = (size_t)p.t.cap * groups;
-        const __half *nsrc = reinterpret_cast<const __half *>(cache + (size_t)p.t.cap * stride);
-        if ((at | 1) < all) cp_async4(nd, nsrc + (at & ~(size_t)1));
-        else sts32(nd, (uint32_t)__half_as_ushort(nsrc[at]) << (at & 1 ? 16 : 0));
+        const size_t at = at0 + g;
+        if ((at | 1) < (size_t)p.t.cap * groups) cp_async4(nd, f.norms + (at & ~(size_t)1));
+        else sts32(nd, (uint32_t)__half_as_ushort(f.norms[at]));
     }
-    return ok;
-}
-
-// A norm word's half is picked by the parity of its index, kept in a bit per ring stage.
-template <bool KEYS>
-__device__ __forceinline__ uint32_t norm_odd(const TreeParams &p, const Fetch &f) {
-    const int groups = KEYS ? p.kgroups : p.vgroups;
-    const TreeUnit &u = p.unit[f.c.u];
-    return (uint32_t)((((long long)f.blk * p.t.block_size + f.off) * groups + (KEYS ? u.gk : u.gv)) & 1);
+    return true;
 }
 __device__ __forceinline__ float norm_value(uint32_t word, uint32_t odd) {
     return __half2float(__ushort_as_half((unsigned short)(odd ? word >> 16 : word)));
 }
 
-// The two products of tile i, issued by one thread. `first`: the tile starts its item's part.
+// The two products of tile i, issued by one warp. `first`: the tile starts its item's part.
 template <int N, int NG>
 __device__ __forceinline__ void issue_scores(const TreeParams &p, Shared &sh, uint8_t *smem, long long i, bool two) {
     using L = Plan<N, NG>;
     const int b = (int)(i & 1);
     const uint32_t par = (uint32_t)(i >> 1) & 1, tmem = sh.tmem;
     const uint64_t dz = desc_sw128(smem_u32(smem + L::oZ), 16);
+    __syncwarp();
     wait(sh, &sh.k_full[b], par, p.status, 0x47490004u);
     wait(sh, &sh.s_empty[b], par ^ 1, p.status, 0x47490005u);
     fence_after();
@@ -544,29 +555,32 @@ __device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, int 
     Fetch f;
     f.c = sh.start;
     f.more = true;
-    f.blk = f.off = 0;
     const long long tiles = f.c.left;
-    fetch_block<N, NG, KEYS>(p, f, row);
-    // per ring stage: the cache row exists; parity of the first norm's index; the tile starts its item's part; second groups
-    uint32_t valid = 0, odd = 0, starts = 0, has2 = 0, val2 = 0;
+    fetch_unit<KEYS>(p, f);
+    fetch_block(p, f, row);
+    // per ring stage: the cache row exists; half of the first norm's word; the tile starts or ends its item's part; second group
+    uint32_t valid = 0, odd = 0, starts = 0, ends = 0, has2 = 0;
     bool item_starts = true;
     int fs = 0;
-    uint32_t zpar = 0;                              // the issuer's: queries of the next item
-    bool before = false, first_b = false, two_b = false;  // and the tile before
+    uint32_t zpar = 0;                    // warp 8: parity of the next item's queries
+    bool owed = false, first_b = false, two_b = false;  // warp 12: the tile before waits for its sums
     auto fetch = [&]() {
         if (f.more) {
-            const bool ok = fetch_codes<N, NG, KEYS>(p, f, ring0 + fs * L::kRing, norm0 + fs * L::kNorm, row);
-            valid = (valid & ~(1u << fs)) | (uint32_t)ok << fs;
-            odd = (odd & ~(1u << fs)) | norm_odd<KEYS>(p, f) << fs;
-            starts = (starts & ~(1u << fs)) | (uint32_t)item_starts << fs;
-            if (NG == 2) {
-                has2 = (has2 & ~(1u << fs)) | (uint32_t)((KEYS ? p.unit[f.c.u].ngk : p.unit[f.c.u].ngv) == 2) << fs;
-                val2 = (val2 & ~(1u << fs)) | (uint32_t)(p.unit[f.c.u].ngv == 2) << fs;
-            }
+            uint32_t o;
+            const bool ok = fetch_codes<NG, KEYS, W>(p, f, ring0 + fs * L::kRing, norm0 + fs * L::kNorm, row, o);
+            const uint32_t bit = 1u << fs;
+            const int u = f.c.u;
             f.more = f.c.advance(p, N);
-            item_starts = f.c.tile == 0;
-            fetch_block<N, NG, KEYS>(p, f, row);
+            const bool next_starts = f.c.tile == 0;
+            valid = ok ? valid | bit : valid & ~bit;
+            odd = o ? odd | bit : odd & ~bit;
+            starts = item_starts ? starts | bit : starts & ~bit;
+            ends = next_starts || !f.more ? ends | bit : ends & ~bit;
+            if (NG == 2) has2 = f.ng == 2 ? has2 | bit : has2 & ~bit;
+            item_starts = next_starts;
+            if (f.c.u != u) fetch_unit<KEYS>(p, f);
         }
+        if (f.more) fetch_block(p, f, row);
         cp_commit();
         fs = fs + 1 == L::kDepth ? 0 : fs + 1;
     };
@@ -672,32 +686,31 @@ __device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, int 
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(KEYS ? &sh.k_full[b] : &sh.v_full[vb]);
-        if (KEYS && q == 0) {
+        // The products. The second one of a tile is issued an expansion later, when its weights are there, but at
+        // once where the item's part ends, for its partials wait for it.
+        if (q == 0) {
             const bool first = starts >> rs & 1;
-            if (lane == 0) {
-                if (first) {  // the item before ends with its sums, which its partials wait for; then come this one's queries
-                    if (before) issue_sums<N, NG>(p, sh, smem, i - 1, first_b, two_b);
+            if (KEYS) {
+                if (first) {
                     wait(sh, &sh.z_full, zpar, p.status, 0x47490006u);
-                    issue_scores<N, NG>(p, sh, smem, i, two);
-                } else {
-                    issue_scores<N, NG>(p, sh, smem, i, two);
-                    issue_sums<N, NG>(p, sh, smem, i - 1, first_b, two_b);
+                    zpar ^= 1;
                 }
+                issue_scores<N, NG>(p, sh, smem, i, two);
+            } else {
+                if (owed) issue_sums<N, NG>(p, sh, smem, i - 1, first_b, two_b);
+                owed = !(ends >> rs & 1);
+                if (!owed) issue_sums<N, NG>(p, sh, smem, i, first, two);
+                first_b = first, two_b = two;
             }
-            if (first) zpar ^= 1;
-            before = true, first_b = first, two_b = val2 >> rs & 1;
             __syncwarp();
         }
         rs = rs + 1 == L::kDepth ? 0 : rs + 1;
         fetch();
     }
-    if (KEYS && q == 0) {
-        if (lane == 0) {
-            issue_sums<N, NG>(p, sh, smem, tiles - 1, first_b, two_b);
-            mma_commit(&sh.drain);  // MMAs in flight finish before tensor memory is freed
-            for (unsigned k = 0; k < kSpin; ++k)
-                if (mbar_try(&sh.drain, 0)) break;
-        }
+    if (q == 0) {  // MMAs in flight finish before tensor memory is freed
+        mma_commit(&sh.drain[KEYS]);
+        for (unsigned k = 0; k < kSpin; ++k)
+            if (mbar_try(&sh.drain[KEYS], 0)) break;
         __syncwarp();
     }
     cp_wait<0>();
@@ -871,100 +884,104 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
             const float nk = sh.scal[b][0][row] * mult, ln = sh.scal[b][1][row], inv = sh.scal[b][2][row];
             wait(sh, &sh.s_full[b], par, p.status, 0x4749000Au);
             fence_after();
-            float d[NC];
-            const uint32_t ts = tm + L::cS + b * N + c0;
-            auto logits = [&]() {  // d = log2 of the weights, before the reference
+            // Column by column in halves of X: the denominators of all columns and the logits of one half fit the registers.
 #pragma unroll
-                for (int k = 0; k < NC; k += X) tmem_ld<X>(ts + k, d + k);
-                wait_ld<NC>(d);
-                if (masked) {
+            for (int hf = 0; hf < NC; hf += X) {
+                float d[X];
+                const int cx = c0 + hf;
+                const uint32_t ts = tm + L::cS + b * N + cx;
+                auto logits = [&]() {  // d = log2 of the weights, before the reference
+                    tmem_ld<X>(ts, d);
+                    wait_ld<X>(d);
+                    if (masked) {
 #pragma unroll
-                    for (int k = 0; k < NC; ++k) {
-                        const float x = fmaf(d[k], nk, ln);
-                        d[k] = see[k >> 5] >> (k & 31) & 1 ? x : -INFINITY;
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < NC; ++k) d[k] = fmaf(d[k], nk, ln);
-                }
-            };
-            auto minus_reference = [&]() {
-#pragma unroll
-                for (int k = 0; k < NC; k += 4) {
-                    const float4 m = *reinterpret_cast<const float4 *>(&sh.m[c0 + k]);
-                    d[k] -= m.x, d[k + 1] -= m.y, d[k + 2] -= m.z, d[k + 3] -= m.w;
-                }
-            };
-            logits();
-            minus_reference();
-            float top = d[0];
-#pragma unroll
-            for (int k = 1; k < NC; ++k) top = fmaxf(top, d[k]);
-            if (bar_or(2 + wg, 128, top > kRaise)) {
-                // ---------------------------------- raise references --
-                logits();
-                float mine[(NC + 31) / 32];
-#pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    const float x = unordered(__reduce_max_sync(0xFFFFFFFFu, ordered(fmaxf(d[k], -INFINITY))));
-                    if (lane == (k & 31)) mine[k >> 5] = x;
-                }
-#pragma unroll
-                for (int k = 0; k < (NC + 31) / 32; ++k)
-                    if (lane + 32 * k < NC) sh.wmax[warp][lane + 32 * k] = mine[k];
-                bar_sync(2 + wg, 128);
-                bool raised = false;
-                if (row < NC) {
-                    const float old = sh.m[c0 + row];
-                    float x = sh.wmax[4 * wg][row];
-#pragma unroll
-                    for (int k = 1; k < 4; ++k) x = fmaxf(x, sh.wmax[4 * wg + k][row]);
-                    raised = x > old + kRaise;
-                    sh.f[c0 + row] = raised ? ex2(old - x) : 1.0f;
-                    if (raised) sh.m[c0 + row] = x;
-                }
-                raised = bar_or(2 + wg, 128, raised);
-                minus_reference();
-                if (raised) {
-#pragma unroll
-                    for (int k = 0; k < NC; ++k) l[k] *= sh.f[c0 + k];
-                    if (it) {  // the first tile's product does not accumulate
-                        wait(sh, &sh.p_empty[b ^ 1], (uint32_t)((i - 1) >> 1) & 1, p.status, 0x4749000Bu);
-                        fence_after();
-                        for (int g = 0; g < u.ngv; ++g) {
-#pragma unroll
-                            for (int k = 0; k < NC; k += 8) {
-                                float o[8];
-                                const uint32_t to = tm + L::cO + g * N + c0 + k;
-                                tmem_ld<8>(to, o);
-                                wait_ld<8>(o);
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) o[j] *= sh.f[c0 + k + j];
-                                tmem_st8(to, o);
-                            }
+                        for (int k = 0; k < X; ++k) {
+                            const float x = fmaf(d[k], nk, ln);
+                            d[k] = see[hf / 32] >> k & 1 ? x : -INFINITY;
                         }
-                        wait_st();
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < X; ++k) d[k] = fmaf(d[k], nk, ln);
+                    }
+                };
+                auto minus_reference = [&]() {
+#pragma unroll
+                    for (int k = 0; k < X; k += 4) {
+                        const float4 m = *reinterpret_cast<const float4 *>(&sh.m[cx + k]);
+                        d[k] -= m.x, d[k + 1] -= m.y, d[k + 2] -= m.z, d[k + 3] -= m.w;
+                    }
+                };
+                logits();
+                minus_reference();
+                float top = d[0];
+#pragma unroll
+                for (int k = 1; k < X; ++k) top = fmaxf(top, d[k]);
+                if (bar_or(2 + wg, 128, top > kRaise)) {
+                    // ---------------------------------- raise references --
+                    logits();
+                    float mine = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < X; ++k) {
+                        const float x = unordered(__reduce_max_sync(0xFFFFFFFFu, ordered(fmaxf(d[k], -INFINITY))));
+                        if (lane == k) mine = x;
+                    }
+                    if (lane < X) sh.wmax[warp][lane] = mine;
+                    bar_sync(2 + wg, 128);
+                    bool raised = false;
+                    if (row < X) {
+                        const float old = sh.m[cx + row];
+                        float x = sh.wmax[4 * wg][row];
+#pragma unroll
+                        for (int k = 1; k < 4; ++k) x = fmaxf(x, sh.wmax[4 * wg + k][row]);
+                        raised = x > old + kRaise;
+                        sh.f[cx + row] = raised ? ex2(old - x) : 1.0f;
+                        if (raised) sh.m[cx + row] = x;
+                    }
+                    raised = bar_or(2 + wg, 128, raised);
+                    minus_reference();
+                    if (raised) {
+#pragma unroll
+                        for (int k = 0; k < X; ++k) l[hf + k] *= sh.f[cx + k];
+                        if (it) {  // the first tile's product does not accumulate
+                            wait(sh, &sh.p_empty[b ^ 1], (uint32_t)((i - 1) >> 1) & 1, p.status, 0x4749000Bu);
+                            fence_after();
+                            for (int g = 0; g < u.ngv; ++g) {
+#pragma unroll 1
+                                for (int k = 0; k < X; k += 8) {
+                                    float o[8];
+                                    const uint32_t to = tm + L::cO + g * N + cx + k;
+                                    tmem_ld<8>(to, o);
+                                    wait_ld<8>(o);
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) o[j] *= sh.f[cx + k + j];
+                                    tmem_st8(to, o);
+                                }
+                            }
+                            wait_st();
+                        }
                     }
                 }
-            }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.s_empty[b]);
-            wait(sh, &sh.p_empty[b], par ^ 1, p.status, 0x4749000Cu);
-            // weights in fp16: cache row `row`, columns c0 .. c0 + NC - 1 (the MN-major B operand)
-            const uint32_t pb = smem_u32(smem + L::oP) + b * L::kPBytes + (c0 >> 6) * (kTile * 128) + (row >> 3) * 1024 + (row & 7) * 128;
-#pragma unroll
-            for (int k = 0; k < NC; k += 8) {
-                uint32_t h[4];
-#pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const float x = ex2(d[k + j]), y = ex2(d[k + j + 1]);
-                    l[k + j] = fmaf(x, inv, l[k + j]);
-                    l[k + j + 1] = fmaf(y, inv, l[k + j + 1]);
-                    const __half2 v = __floats2half2_rn(x, y);
-                    h[j >> 1] = *reinterpret_cast<const uint32_t *>(&v);
+                if (hf + X == NC) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.s_empty[b]);
                 }
-                sts128(pb + (((((c0 + k) & 63) >> 3) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+                if (hf == 0) wait(sh, &sh.p_empty[b], par ^ 1, p.status, 0x4749000Cu);
+                // weights in fp16: cache row `row`, columns cx .. cx + X - 1 (the MN-major B operand)
+                const uint32_t pb = smem_u32(smem + L::oP) + b * L::kPBytes + (cx >> 6) * (kTile * 128) + (row >> 3) * 1024 + (row & 7) * 128;
+#pragma unroll
+                for (int k = 0; k < X; k += 8) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        const float x = ex2(d[k + j]), y = ex2(d[k + j + 1]);
+                        l[hf + k + j] = fmaf(x, inv, l[hf + k + j]);
+                        l[hf + k + j + 1] = fmaf(y, inv, l[hf + k + j + 1]);
+                        const __half2 v = __floats2half2_rn(x, y);
+                        h[j >> 1] = *reinterpret_cast<const uint32_t *>(&v);
+                    }
+                    sts128(pb + (((((cx + k) & 63) >> 3) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+                }
             }
             fence_async();
             __syncwarp();
@@ -1028,7 +1045,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             mbar_init(&sh.sc_full[i], 8);
         }
         mbar_init(&sh.z_full, 8);
-        mbar_init(&sh.drain, 1);
+        mbar_init(&sh.drain[0], 1);
+        mbar_init(&sh.drain[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     __syncthreads();
@@ -1043,15 +1061,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     __syncthreads();
     fence_after();
     // A softmax thread of many columns keeps logits and denominators in registers: the expanders give theirs up.
-    // 256 x 168 + 256 x 88 = 512 x 128, what the block was launched with.
+    // 256 (kSoft + kExp) = 512 x 128, what the block was launched with.
     if (warp < 8) {
-        if (N >= 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n");
+        if (N >= 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(L::kSoft));
         softmax_role<N, NG>(p, sh, smem, warp, lane);
     } else if (warp < 12) {
-        if (N >= 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+        if (N >= 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kExp));
         expand_any<N, NG, true>(p, sh, smem, tid - 256, warp & 3, lane);
     } else {
-        if (N >= 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+        if (N >= 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kExp));
         expand_any<N, NG, false>(p, sh, smem, tid - 384, warp & 3, lane);
     }
     fence_before();
@@ -1215,6 +1233,12 @@ int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float 
     p.hq = g.n_q_heads, p.per = g.n_q_heads / g.n_kv_heads, p.dk = g.head_dim_k, p.dv = g.head_dim_v;
     p.wk = width_of(g.k_bits), p.wv = width_of(g.v_bits);
     p.kgroups = in_padded(g.n_kv_heads * p.dk) / kGroup, p.vgroups = in_padded(g.n_kv_heads * p.dv) / kGroup;
+    // t / block_size for t < 2^31: a product with 2^(31 + l) / block_size rounded up, 2^l >= block_size
+    int l = 0;
+    while (l < 31 && (1u << l) < (unsigned)t.block_size) ++l;
+    p.div_shift = 31 + l;
+    p.div_mul = (uint32_t)(((1ull << (31 + l)) + (unsigned)t.block_size - 1) / (unsigned)t.block_size);
+    if (!t.max_blocks) p.t.block_table = t.cu_nodes, p.t.table_stride = 0;  // no token is read, but entry 0 is
     p.rows = s.rows, p.ncol_max = s.ncol_max, p.grid = sm_count();
     p.status = device_status_ptr();
     if (!p.status) return set_error(CQ_ERR_CUDA, "no device status word");
