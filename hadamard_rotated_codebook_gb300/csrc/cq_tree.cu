@@ -24,11 +24,11 @@
 // lengths are read on the device, and the longest request cannot hold the launch up. Each run leaves
 // unrotated partial sums; a second kernel joins them, rotates and writes o.
 //
-// Roles of the 16 warps: 0-7 softmax (two warpgroups, half the columns each; they also rotate the queries
-// and write the partials), 8-11 expand keys into TMEM (a thread per cache row; the A operand), 12-15
-// expand values into shared memory; warp 8 also issues the first product of each tile and warp 12 the second. The expanders fetch their own codes by cp.async into a
-// ring a few tiles ahead, so they wait for nobody's loads but their own. (A warp of its own for the MMAs would
-// cost every thread a fifth of its registers: they are handed out to four warps at a time.)
+// Roles of the 16 warps. Softmax: one or two warpgroups (N of 64 and more), each with its share of the columns; they
+// also rotate the queries and write the partials. Expansion: a thread per cache row turns its codes into fp16 levels, keys
+// into TMEM (the A operand) and values into shared memory, in two warpgroups where the columns are few and
+// in one where softmax needs the registers. One warp issues the MMAs, two fetch codes, norms and block numbers
+// into a ring some tiles ahead.
 // Every wait is bounded: when one gives up, the flag s_abort makes all later waits return at once and every role
 // runs through its remaining tiles without waiting, so that the block's barriers stay matched.
 #include <cuda_bf16.h>
@@ -45,8 +45,8 @@ namespace cq {
 namespace {
 
 constexpr int kTile = 128;        // cache rows per tile
-constexpr int kSoftThreads = 256;
 constexpr int kThreads = 512;
+constexpr int kMaxDepth = 8;      // stages of the ring of codes
 constexpr unsigned kSpin = 1u << 20;   // polls of up to ~1 us
 constexpr float kNoMax = -1e30f;       // reference of a column that has attended nothing yet
 constexpr float kRaise = 8.0f;         // log2 of the largest weight before a reference is raised
@@ -62,6 +62,7 @@ struct TreeParams {
     uint32_t tk[8], tv[8];  // level tables: low bytes of 16 fp16 levels, then high bytes
     float k_mult, v_mult;   // scale * log2(e) / sqrt(128) * 2^(table exponent); 2^(table exponent) / sqrt(128)
     int n_units, hq, per, dk, dv, wk, wv, kgroups, vgroups;
+    int depth, stage, o_tab_v, o_ring;  // ring stages and their bytes; offsets behind the key table's
     uint32_t div_mul, div_shift;  // t / block_size = t * div_mul >> div_shift
     int rows;        // most query heads of a unit
     int ncol_max;    // column tiles of a request with max_nodes tokens
@@ -76,19 +77,11 @@ __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-                 : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool mbar_try(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
                  : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+                 : "r"(bar), "r"(parity), "r"(1000u)
                  : "memory");
     return ok != 0;
 }
@@ -187,8 +180,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ bool bar_or(int id, int n, bool v) {
     uint32_t r;
@@ -204,6 +195,38 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
+// Two fp32 operations in one instruction.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void f2_get(F2 a, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// A value that every lane holds alike, in a form the compiler knows to be so.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
 
 // ------------------------------------------------------------------ schedule --
@@ -235,7 +258,7 @@ __device__ __forceinline__ int cols_of(const TreeParams &p, int n, int N) { retu
 struct Cursor {
     int s, u, c, tile, ntiles, ncol, first, n, ctx, len;
     int item;        // items before this one
-    long long left;  // tiles of this block's run from here on
+    int left;        // tiles of this block's run from here on
     __device__ void take(const TreeParams &p, int N) {
         const Seq q = seq_at(p, s);
         first = q.first, n = q.n, ctx = q.ctx, len = q.len;
@@ -254,7 +277,7 @@ struct Cursor {
             take(p, N);
         } while (!n);
     }
-    __device__ bool advance(const TreeParams &p, int N) {  // to the next tile; false after the last
+    __device__ __forceinline__ bool advance(const TreeParams &p, int N) {  // to the next tile; false after the last
         if (--left <= 0) return false;
         if (++tile == ntiles) next_item(p, N);
         return true;
@@ -272,7 +295,8 @@ __device__ __forceinline__ int run_of(long long total, int grid, long long tile)
 }
 
 struct Shared {
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2], sc_full[2], z_full, drain[2];
+    uint64_t ring_full[kMaxDepth], ring_empty[kMaxDepth];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], sc_full[2], p_full, p_empty, z_full, drain;
     uint32_t tmem;
     volatile int abort;
     int zmax;
@@ -282,22 +306,22 @@ struct Shared {
     long long scan_i[kThreads / 32];
     Cursor start;
     float scal[2][3][kTile];      // per tile buffer: n_k, log2 n_v, 1 / n_v
-    alignas(16) float m[128];     // column references (read four at a time)
-    float f[128];                 // factors of the last raise
-    float wmax[8][64];            // column maxima of a softmax warp
+    alignas(16) float minus_m[128];  // column references, negated (read four at a time)
+    alignas(16) float f[128];        // factors of the last raise
+    float wmax[8][32];            // column maxima of a softmax warp
     float lsum[8][64];
     uint32_t mask[CQ_TREE_MAX_NODES][4];  // columns (bits) that attend drafted token j
 };
 
+// The roles' loops run side by side on an SM and have to fit its instruction cache together (where they did not, each role
+// waited for instructions most of the time): loops are kept rolled, and what runs once per item out of line.
 __device__ __forceinline__ void wait(Shared &sh, uint64_t *bar, uint32_t parity, unsigned int *status, unsigned code) {
-    if (mbar_test(bar, parity)) return;
-    for (unsigned i = 0; !sh.abort; ++i) {
-        if (mbar_try(bar, parity)) return;
+    const uint32_t b = smem_u32(bar);
+    for (unsigned i = 0; !mbar_try(b, parity) && !sh.abort; ++i)
         if (i >= kSpin) {
             atomicOr(status, code);
             sh.abort = 1;
         }
-    }
 }
 
 // Fills sh.start with this block's first tile and sh.total; false if it has none.
@@ -355,7 +379,7 @@ __device__ bool find_run(const TreeParams &p, Shared &sh) {
             c.u = it / c.ncol;
             c.c = it - c.u * c.ncol;
             c.item = (int)(bb + ib - b) + it;
-            c.left = w1 - w0;
+            c.left = (int)(w1 - w0);
             sh.start = c;
         }
         __syncthreads();
@@ -420,91 +444,150 @@ __device__ __forceinline__ void expand_quarter(const uint32_t *c, const uint32_t
 // ---------------------------------------------------------------- the kernel --
 template <int N, int NG>
 struct Plan {
+    static constexpr int kSoftWG = N >= 64 ? 2 : 1, kExpWG = 3 - kSoftWG;  // warpgroups
+    static constexpr int kSoft = 4 * kSoftWG, kExp = 4 * kExpWG;            // warps; then the issuer, two fetchers, one idle
     static constexpr int kVBuf = NG == 1 ? 2 : 1;
-    static constexpr int kDepth = NG == 2 ? 2 : N >= 128 ? 3 : N >= 64 ? 4 : 6;  // tiles of codes in flight
     static constexpr int kVBytes = 2 * kTile * 128;            // one group's values: 128 rows x 128 fp16
     static constexpr int kPBytes = kTile * (N <= 64 ? 128 : 256);
     static constexpr int kZBytes = N * 256;                    // one group
-    static constexpr int kRing = NG * 4 * kTile * 16;          // one stage of one side (four-bit codes)
-    static constexpr int kNorm = NG * kTile * 4;
-    static constexpr int oV = 0, oP = oV + kVBuf * NG * kVBytes, oZ = oP + 2 * kPBytes, oRing = oZ + NG * kZBytes;
-    static constexpr int oNorm = oRing + 2 * kDepth * kRing, oShared = oNorm + 2 * kDepth * kNorm;
-    static constexpr int kSmem = oShared + (int)sizeof(Shared) + 1024;
-    static constexpr int kSoft = NG == 2 ? 136 : 160, kExp = 256 - kSoft;  // registers of the roles
+    static constexpr int oV = 0, oP = oV + kVBuf * NG * kVBytes, oZ = oP + kPBytes, oShared = oZ + NG * kZBytes;
+    static constexpr int oTab = oShared + ((int)sizeof(Shared) + 127) / 128 * 128;
+    static constexpr int kLimit = 232448 - 1024;               // a block's shared memory, less the alignment of its start
+    // registers of the roles where softmax takes two warpgroups: 256 kSoftRegs + 128 (kExpRegs + kRestRegs) = 512 x 128
+    static constexpr int kSoftRegs = 168, kExpRegs = 104, kRestRegs = 72;
     // TMEM columns
     static constexpr int cK = 0, cS = 2 * NG * 64, cO = cS + 2 * N;
     static_assert(cO + NG * N <= 512, "tensor memory");
-    static_assert(kSmem <= 232448, "shared memory");
 };
 
-// One expander thread's cache row of the tiles ahead. The block number of the next tile is loaded a tile before it is used, in
-// straight-line code (a load under a branch would be waited for where the branch ends).
-struct Fetch {
-    Cursor c;
-    const uint8_t *codes;  // the cache, at the unit's first group
-    const __half *norms;
-    uint32_t g0, ng;
+// Level tables in shared memory (one group per row): entry e at e * 128 bytes, repeated for every lane so that no two lanes of a
+// warp meet in a bank. A code pair gives one fp16 pair (3 and 4 bits, and 2 bits where space is short), a byte of two-bit
+// codes four levels. Against permutes of register tables (1.3 to 3.1 instructions a value on the half-rate
+// integer pipe, which bounded the kernel) a pair costs two integer instructions and a load.
+__host__ __device__ constexpr bool wide_two(int N) { return N <= 32; }
+__host__ __device__ constexpr int table_bytes(int w, int N) { return w == 4 || (w == 2 && wide_two(N)) ? 256 * 128 : w == 3 ? 64 * 128 : 16 * 128; }
+
+// Two warps fetch: a lane has the cache rows `lane` and `lane + 64` of the tiles ahead. The block numbers of the next tile are loaded a
+// tile before they are used, in straight-line code (a load under a branch would be waited for where the branch ends).
+struct RowAt {
     int blk, off;
-    bool ok, more;
+    bool ok;
+};
+__device__ __forceinline__ RowAt row_at(const TreeParams &p, const Cursor &c, int row) {
+    RowAt r;
+    const int t = c.tile * kTile + row, tc = max(0, min(t, c.len - 1));
+    const int b = (int)((uint64_t)(uint32_t)tc * p.div_mul >> p.div_shift);  // tc / block_size
+    r.off = tc - b * p.t.block_size;
+    r.ok = t < c.len;
+    r.blk = p.t.block_table[c.s * p.t.table_stride + b];  // b < max_blocks: len is cut to the table
+    return r;
+}
+
+// A stage of the ring: codes of the keys as [group][16-byte chunk][row], then of the values; a word per row and side: bit 0 the
+// row exists, bit 1 the half of the norm words that holds the first group's norm, bit 2 the norm itself is in the upper
+// half (where the word would end past the cache); norm words as [side][group][row].
+template <int NG>
+struct Stage {
+    static constexpr int kInfo = 2 * kTile * 4, kNorms = 2 * NG * kTile * 4;
+    __host__ __device__ static constexpr int codes(int w) { return NG * w * kTile * 16; }
+    __host__ __device__ static constexpr int bytes(int wk, int wv) { return codes(wk) + codes(wv) + kInfo + kNorms; }
 };
 
+// A side of the cache as the fetchers take it.
+struct Side {
+    const uint8_t *codes;  // at the unit's first group
+    const __half *norms;   // likewise
+    uint32_t stride, groups, g0, ng, w;
+};
 template <bool KEYS>
-__device__ __forceinline__ void fetch_unit(const TreeParams &p, Fetch &f) {
-    const TreeUnit &u = p.unit[f.c.u];
-    const int w = KEYS ? p.wk : p.wv, groups = KEYS ? p.kgroups : p.vgroups;
+__device__ __forceinline__ Side side_of(const TreeParams &p, int unit) {
+    Side s;
+    const TreeUnit &u = p.unit[unit];
+    s.g0 = KEYS ? u.gk : u.gv, s.ng = KEYS ? u.ngk : u.ngv;
+    s.w = KEYS ? p.wk : p.wv, s.groups = KEYS ? p.kgroups : p.vgroups;
+    s.stride = s.groups * 16 * s.w;
     const uint8_t *cache = KEYS ? p.t.k_cache : p.t.v_cache;
-    f.g0 = KEYS ? u.gk : u.gv;
-    f.ng = KEYS ? u.ngk : u.ngv;
-    f.codes = cache + f.g0 * 16 * w;
-    f.norms = reinterpret_cast<const __half *>(cache + (size_t)p.t.cap * ((size_t)groups * 16 * w));
+    s.codes = cache + s.g0 * 16 * s.w;
+    s.norms = reinterpret_cast<const __half *>(cache + (size_t)p.t.cap * s.stride);
+    return s;
 }
 
-__device__ __forceinline__ void fetch_block(const TreeParams &p, Fetch &f, int row) {
-    const int t = f.c.tile * kTile + row, tc = max(0, min(t, f.c.len - 1));
-    const int b = (int)((uint64_t)(uint32_t)tc * p.div_mul >> p.div_shift);  // tc / block_size
-    f.off = tc - b * p.t.block_size;
-    f.ok = t < f.c.len;
-    f.blk = p.t.block_table[f.c.s * p.t.table_stride + b];  // b < max_blocks: len is cut to the table
-}
-
-// Starts the copies of the row's codes and norms; the norm's half of its word in `odd`.
-template <int NG, bool KEYS, int W>
-__device__ __forceinline__ bool fetch_codes(const TreeParams &p, const Fetch &f, uint32_t ring, uint32_t norm, int row, uint32_t &odd) {
-    const int groups = KEYS ? p.kgroups : p.vgroups;
-    const long long r = (long long)f.blk * p.t.block_size + f.off;
-    bool ok = f.ok;
-    if (ok && (f.blk < 0 || r >= p.t.cap)) {
-        ok = false;
-        atomicOr(p.status, kStatusIndex);
-    }
-    const size_t at0 = (size_t)r * groups + f.g0;
-    odd = (uint32_t)at0 & 1;
-    if (!ok) return false;
-    const uint8_t *src = f.codes + (size_t)r * (groups * 16 * W);
+template <int NG>
+__device__ __forceinline__ void fetch_side(const Side &s, uint32_t r, size_t all, uint32_t codes, uint32_t info, uint32_t norms) {
+    const uint8_t *src = s.codes + (size_t)r * s.stride;
+    const size_t at = (size_t)r * s.groups + s.g0;
+    uint32_t word = 1 | (uint32_t)(at & 1) << 1;
+    const uint32_t chunks = NG == 2 ? s.ng * s.w : s.w;
+#pragma unroll
+    for (int i = 0; i < 4 * NG; ++i)
+        if (i < chunks) cp_async16(codes + i * kTile * 16, src + i * 16);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        if (g == 1 && f.ng == 1) break;
-        const uint32_t nd = norm + (g * kTile + row) * 4;
-        const uint32_t dst = ring + (g * 4 * kTile + row) * 16;
-#pragma unroll
-        for (int i = 0; i < W; ++i) cp_async16(dst + i * kTile * 16, src + g * 16 * W + 16 * i);
-        // the norm as the 4-byte word that holds it, unless that word would end past the cache
-        const size_t at = at0 + g;
-        if ((at | 1) < (size_t)p.t.cap * groups) cp_async4(nd, f.norms + (at & ~(size_t)1));
-        else sts32(nd, (uint32_t)__half_as_ushort(f.norms[at]));
+        if (g >= s.ng) break;
+        if (((at + g) | 1) < all) cp_async4(norms + g * kTile * 4, s.norms + ((at + g) & ~(size_t)1));
+        else word |= 4 | (uint32_t)__half_as_ushort(s.norms[at + g]) << 16;  // the last norm of all: never the first of two
     }
-    return true;
+    sts32(info, word);
 }
-__device__ __forceinline__ float norm_value(uint32_t word, uint32_t odd) {
-    return __half2float(__ushort_as_half((unsigned short)(odd ? word >> 16 : word)));
+
+template <int N, int NG>
+__device__ void fetch_role(const TreeParams &p, Shared &sh, uint8_t *smem, int lane) {
+    Cursor c = sh.start;
+    const int tiles = uniform(c.left);
+    const uint32_t ring = smem_u32(smem) + p.o_ring;
+    RowAt r[2] = {row_at(p, c, lane), row_at(p, c, lane + 64)};
+    int st = 0, unit = c.u;
+    uint32_t par = 1;
+    Side sk = side_of<true>(p, unit), sv = side_of<false>(p, unit);
+    const size_t all_k = (size_t)p.t.cap * sk.groups, all_v = (size_t)p.t.cap * sv.groups;
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+        if (c.u != unit) {
+            unit = c.u;
+            sk = side_of<true>(p, unit), sv = side_of<false>(p, unit);
+        }
+        c.advance(p, N);
+        wait(sh, &sh.ring_empty[st], par, p.status, 0x4749000Eu);
+        const uint32_t kc = ring + st * p.stage + lane * 16, vc = kc + Stage<NG>::codes(p.wk);
+        const uint32_t info = vc + Stage<NG>::codes(p.wv) - lane * 12, nrm = info + Stage<NG>::kInfo;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const RowAt now = r[k];
+            r[k] = row_at(p, c, lane + 64 * k);
+            const long long at = (long long)now.blk * p.t.block_size + now.off;
+            bool ok = now.ok;
+            if (ok && (now.blk < 0 || at >= p.t.cap)) {
+                ok = false;
+                atomicOr(p.status, kStatusIndex);
+            }
+            if (ok) {
+                fetch_side<NG>(sk, (uint32_t)at, all_k, kc + 1024 * k, info + 256 * k, nrm + 256 * k);
+                fetch_side<NG>(sv, (uint32_t)at, all_v, vc + 1024 * k, info + 256 * k + kTile * 4, nrm + 256 * k + NG * kTile * 4);
+            } else {
+                sts32(info + 256 * k, 0);
+                sts32(info + 256 * k + kTile * 4, 0);
+            }
+        }
+        // two arrivals a lane: one when its copies have landed, one for what it stored itself
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(&sh.ring_full[st])) : "memory");
+        mbar_arrive(&sh.ring_full[st]);
+        if (++st == p.depth) st = 0, par ^= 1;
+    }
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+}
+
+// Norm of group g from a row's info and norm words (a norm given in the info word is that of the last group).
+__device__ __forceinline__ float norm_value(uint32_t info, uint32_t word, int g, int last) {
+    const uint32_t bits = info & 4 && g == last ? info >> 16 : ((info >> 1) + g) & 1 ? word >> 16 : word & 0xFFFFu;
+    return __half2float(__ushort_as_half((unsigned short)bits));
 }
 
 // The two products of tile i, issued by one warp. `first`: the tile starts its item's part.
 template <int N, int NG>
-__device__ __forceinline__ void issue_scores(const TreeParams &p, Shared &sh, uint8_t *smem, long long i, bool two) {
+__device__ __forceinline__ void issue_scores(const TreeParams &p, Shared &sh, uint8_t *smem, uint32_t tmem, int i, bool two) {
     using L = Plan<N, NG>;
-    const int b = (int)(i & 1);
-    const uint32_t par = (uint32_t)(i >> 1) & 1, tmem = sh.tmem;
+    const int b = i & 1;
+    const uint32_t par = (uint32_t)(i >> 1) & 1;
     const uint64_t dz = desc_sw128(smem_u32(smem + L::oZ), 16);
     __syncwarp();
     wait(sh, &sh.k_full[b], par, p.status, 0x47490004u);
@@ -513,7 +596,7 @@ __device__ __forceinline__ void issue_scores(const TreeParams &p, Shared &sh, ui
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if (g == 1 && !two) break;
-#pragma unroll
+#pragma unroll 2
         for (int k = 0; k < 8; ++k)
             mma_ts(tmem + L::cS + b * N, tmem + L::cK + (b * NG + g) * 64 + 8 * k,
                    dz + (uint64_t)((g * L::kZBytes + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), idesc_f16(128, N, 0, 0), (g | k) != 0);
@@ -522,206 +605,247 @@ __device__ __forceinline__ void issue_scores(const TreeParams &p, Shared &sh, ui
     mma_commit(&sh.s_full[b]);
 }
 template <int N, int NG>
-__device__ __forceinline__ void issue_sums(const TreeParams &p, Shared &sh, uint8_t *smem, long long i, bool first, bool two) {
+__device__ __forceinline__ void issue_sums(const TreeParams &p, Shared &sh, uint8_t *smem, uint32_t tmem, int i, bool first, bool two) {
     using L = Plan<N, NG>;
-    const int b = (int)(i & 1), vb = L::kVBuf == 2 ? b : 0;
-    const uint32_t par = (uint32_t)(i >> 1) & 1, tmem = sh.tmem;
-    wait(sh, &sh.v_full[vb], L::kVBuf == 2 ? par : (uint32_t)(i & 1), p.status, 0x47490007u);
-    wait(sh, &sh.p_full[b], par, p.status, 0x47490008u);
+    const int vb = L::kVBuf == 2 ? i & 1 : 0;
+    wait(sh, &sh.v_full[vb], L::kVBuf == 2 ? (uint32_t)(i >> 1) & 1 : (uint32_t)(i & 1), p.status, 0x47490007u);
+    wait(sh, &sh.p_full, (uint32_t)(i & 1), p.status, 0x47490008u);
+    __syncwarp();
     fence_after();
-    const uint64_t dp = desc_sw128(smem_u32(smem + L::oP) + b * L::kPBytes, kTile * 128);
+    const uint64_t dp = desc_sw128(smem_u32(smem + L::oP), kTile * 128);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if (g == 1 && !two) break;
         const uint64_t dv = desc_sw128(smem_u32(smem + L::oV) + (vb * NG + g) * L::kVBytes, kTile * 128);
-#pragma unroll
+#pragma unroll 2
         for (int k = 0; k < 8; ++k)  // 16 cache rows: two atoms
             mma_ss(tmem + L::cO + g * N, dv + (uint64_t)(k * 2048 >> 4), dp + (uint64_t)(k * 2048 >> 4), idesc_f16(128, N, 1, 1),
                    !first || k);
     }
     mma_commit(&sh.v_empty[vb]);
-    mma_commit(&sh.p_empty[b]);
+    mma_commit(&sh.p_empty);
 }
 
-// One side's expander warps: keys into tensor memory, values into shared memory.
-template <int N, int NG, bool KEYS, int W>
-__device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, int row, int q, int lane) {
-    using L = Plan<N, NG>;
-    const uint32_t ring0 = smem_u32(smem + L::oRing) + (KEYS ? 0 : L::kDepth * L::kRing);
-    const uint32_t norm0 = smem_u32(smem + L::oNorm) + (KEYS ? 0 : L::kDepth * L::kNorm);
-    uint32_t tab[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) tab[i] = KEYS ? p.tk[i] : p.tv[i];
-    Fetch f;
-    f.c = sh.start;
-    f.more = true;
-    const long long tiles = f.c.left;
-    fetch_unit<KEYS>(p, f);
-    fetch_block(p, f, row);
-    // per ring stage: the cache row exists; half of the first norm's word; the tile starts or ends its item's part; second group
-    uint32_t valid = 0, odd = 0, starts = 0, ends = 0, has2 = 0;
-    bool item_starts = true;
-    int fs = 0;
-    uint32_t zpar = 0;                    // warp 8: parity of the next item's queries
-    bool owed = false, first_b = false, two_b = false;  // warp 12: the tile before waits for its sums
-    auto fetch = [&]() {
-        if (f.more) {
-            uint32_t o;
-            const bool ok = fetch_codes<NG, KEYS, W>(p, f, ring0 + fs * L::kRing, norm0 + fs * L::kNorm, row, o);
-            const uint32_t bit = 1u << fs;
-            const int u = f.c.u;
-            f.more = f.c.advance(p, N);
-            const bool next_starts = f.c.tile == 0;
-            valid = ok ? valid | bit : valid & ~bit;
-            odd = o ? odd | bit : odd & ~bit;
-            starts = item_starts ? starts | bit : starts & ~bit;
-            ends = next_starts || !f.more ? ends | bit : ends & ~bit;
-            if (NG == 2) has2 = f.ng == 2 ? has2 | bit : has2 & ~bit;
-            item_starts = next_starts;
-            if (f.c.u != u) fetch_unit<KEYS>(p, f);
+template <int N, int NG>
+__device__ void issue_role(const TreeParams &p, Shared &sh, uint8_t *smem) {
+    Cursor c = sh.start;
+    const uint32_t tmem = uniform(sh.tmem);
+    const int tiles = uniform(c.left);
+    uint32_t zpar = 0;
+    bool first = true, next_first = true;  // tile i, tile i + 1 starts its item's part
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+        const bool two_k = NG == 2 && uniform(p.unit[c.u].ngk == 2), two_v = NG == 2 && uniform(p.unit[c.u].ngv == 2);
+        if (next_first) {
+            wait(sh, &sh.z_full, zpar, p.status, 0x47490006u);
+            zpar ^= 1;
+            issue_scores<N, NG>(p, sh, smem, tmem, i, two_k);
         }
-        if (f.more) fetch_block(p, f, row);
-        cp_commit();
-        fs = fs + 1 == L::kDepth ? 0 : fs + 1;
+        first = next_first;
+        const bool more = c.advance(p, N);
+        next_first = uniform(!more || c.tile == 0);
+        if (!next_first) issue_scores<N, NG>(p, sh, smem, tmem, i + 1, two_k);  // while softmax works on tile i
+        issue_sums<N, NG>(p, sh, smem, tmem, i, first, two_v);
+    }
+    mma_commit(&sh.drain);  // MMAs in flight finish before tensor memory is freed
+    for (unsigned k = 0; k < kSpin; ++k)
+        if (mbar_try(smem_u32(&sh.drain), 0)) break;
+    __syncwarp();
+}
+
+// ------------------------------------------------------------- expansion --
+// The W words of a row's quarter h (32 codes) from a ring stage.
+template <int W>
+__device__ __forceinline__ void load_quarter(uint32_t codes, int row, int h, uint32_t (&c)[W]) {
+    if (W == 4) {
+        const uint4 v = lds128(codes + (h * kTile + row) * 16);
+        c[0] = v.x, c[1] = v.y, c[W - 2] = v.z, c[W - 1] = v.w;
+    } else if (W == 2) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(c[0]), "=r"(c[1]) : "r"(codes + ((h >> 1) * kTile + row) * 16 + (h & 1) * 8));
+    } else {
+#pragma unroll
+        for (int k = 0; k < W; ++k) c[k] = lds32(codes + (((W * h + k) >> 2) * kTile + row) * 16 + ((W * h + k) & 3) * 4);
+    }
+}
+
+// 32 codes in words c as 16 fp16 pairs in their order, from the table at `tab` (plus this lane's place in a row).
+template <int N, int W>
+__device__ __forceinline__ void lookup_quarter(const uint32_t *c, uint32_t tab, uint32_t (&r)[16]) {
+    if (W == 2 && wide_two(N)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t x = c[j / 4];
+            const int s = 8 * (j & 3) - 7;
+            const uint32_t a = tab + ((s < 0 ? x << 7 : x >> (s < 0 ? 0 : s)) & 0x7F80u);
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(r[2 * j]), "=r"(r[2 * j + 1]) : "r"(a));
+        }
+    } else {
+        constexpr int kBits = 2 * W;
+        constexpr uint32_t kMask = ((1u << kBits) - 1) << 7;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int at = kBits * j, w = at / 32, s = at % 32;  // the pair's bits: from bit s of word w
+            uint32_t x;
+            if (s + kBits > 32) x = __funnelshift_r(c[w], c[w + 1], s) << 7;
+            else x = s < 7 ? c[w] << (7 - s) : c[w] >> (s - 7);
+            asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(r[j]) : "r"(tab + (x & kMask)));
+        }
+    }
+}
+
+// Fills a table (all threads); t: the levels' bytes as in TreeParams.
+__device__ void fill_table(uint8_t *dst, const uint32_t (&t)[8], int w, bool wide) {
+    auto level = [&](int q) -> uint32_t {
+        const uint32_t lo = t[q >> 2] >> (8 * (q & 3)) & 255u, hi = t[4 + (q >> 2)] >> (8 * (q & 3)) & 255u;
+        return lo | hi << 8;
     };
+    const int entries = w == 4 || wide ? 256 : w == 3 ? 64 : 16, m = (1 << w) - 1;
+    for (int i = threadIdx.x; i < entries * 8; i += kThreads) {  // 16 bytes each
+        const int e = i >> 3;
+        const uint32_t a = level(e & m) | level(e >> w & m) << 16;
+        const uint32_t b = wide ? level(e >> (2 * w) & m) | level(e >> (3 * w) & m) << 16 : a;
+        sts128(smem_u32(dst) + i * 16, a, b, a, b);
+    }
+}
+
+// Expander warps: keys into tensor memory, values into shared memory, and the rows' norms for softmax.
+template <int N, int NG, int W, bool KEYS>
+__device__ __forceinline__ void expand_tile(const TreeParams &p, Shared &sh, uint8_t *smem, uint32_t tmem, uint32_t codes, uint32_t tab, int buf, int row,
+                                            int q, const float (&ratio)[2], const uint32_t (&flip)[2], bool two) {
+    using L = Plan<N, NG>;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        if (g == 1 && !two) break;
+        uint32_t t[8];
+        if (NG == 2) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = KEYS ? p.tk[j] : j < 4 ? p.tv[j] : p.tv[j] ^ flip[g];
+        }
+        const __half2 r2 = __float2half2_rn(ratio[g]);
+        const uint32_t from = codes + g * W * kTile * 16;
+        uint32_t next[W];
+        load_quarter<W>(from, row, 0, next);
 #pragma unroll 1
-    for (int i = 0; i < L::kDepth; ++i) fetch();
-    int rs = 0;
-#pragma unroll 1
-    for (long long i = 0; i < tiles; ++i) {
-        const int b = (int)(i & 1);
-        const uint32_t par = (uint32_t)(i >> 1) & 1;
-        cp_wait<L::kDepth - 1>();
-        const uint32_t ring = ring0 + rs * L::kRing, norm = norm0 + rs * L::kNorm;
-        const uint32_t o0 = odd >> rs & 1;
-        const uint32_t w0 = lds32(norm + row * 4);
-        float n0 = norm_value(w0, o0), n1 = 0.0f;
-        const bool none = !(valid >> rs & 1);
-        const bool two = NG == 2 && (has2 >> rs & 1);
-        if (NG == 2 && two) n1 = norm_value(lds32(norm + (kTile + row) * 4), o0 ^ 1);
-        // Two groups with norms n0, n1: the product takes the larger one, the other group's levels are scaled by their ratio.
-        float nn = n0, ratio[2] = {1.0f, 1.0f};
-        uint32_t flip[2] = {0, 0};
-        if (KEYS) {
-            if (NG == 2 && two) {
-                nn = fmaxf(fabsf(n0), fabsf(n1));
-                ratio[0] = n0 / nn, ratio[1] = n1 / nn;
-            }
-        } else {
-            nn = fabsf(n0);
-            if (n0 < 0.0f) flip[0] = 0x80808080u;  // a negative norm turns its levels round
-            if (NG == 2 && two) {
-                if (n1 < 0.0f) flip[1] = 0x80808080u;
-                nn = fmaxf(nn, fabsf(n1));
-                ratio[0] = fabsf(n0) / nn, ratio[1] = fabsf(n1) / nn;
-            }
-        }
-        if (NG == 2 && two) {
-            const bool odd_norm = !(fabsf(n0) <= 65504.0f && fabsf(n1) <= 65504.0f);
-            if (odd_norm) nn = __int_as_float(0x7FC00000);  // the row is lost for who attends it, and only for them
+        for (int h = 0; h < 4; ++h) {
+            uint32_t r[16], c[W];
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
-                if (!(fabsf(ratio[g]) <= 1.0f)) ratio[g] = odd_norm ? 1.0f : 0.0f;  // 0/0: both norms are zero
-        }
-        wait(sh, &sh.s_empty[b], par ^ 1, p.status, 0x47490001u);
-        if (KEYS) {
-            sh.scal[b][0][row] = none ? 0.0f : nn;
-        } else {
-            // a norm of zero counts in the denominator: 2^-40 stands for it, far below the smallest fp16 norm
-            const float safe = nn == 0.0f ? 0x1p-40f : nn;
-            sh.scal[b][1][row] = none ? -INFINITY : nn <= 65504.0f ? log2f(safe) : __int_as_float(0x7FC00000);
-            sh.scal[b][2][row] = !none && nn <= 65504.0f ? 1.0f / safe : 0.0f;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.sc_full[b]);
-        const int vb = KEYS || L::kVBuf == 2 ? b : 0;
-        const uint32_t vpar = KEYS || L::kVBuf == 2 ? par : (uint32_t)(i & 1);
-        if (KEYS) {
-            wait(sh, &sh.k_empty[b], par ^ 1, p.status, 0x47490002u);
-            fence_after();
-        } else {
-            wait(sh, &sh.v_empty[vb], vpar ^ 1, p.status, 0x47490003u);
-        }
+            for (int j = 0; j < W; ++j) c[j] = next[j];
+            load_quarter<W>(from, row, min(h + 1, 3), next);
+            if (NG == 1) {
+                lookup_quarter<N, W>(c, tab, r);
+                if (!KEYS) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            if (g == 1 && !two) break;
-            uint32_t t[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) t[j] = KEYS || j < 4 ? tab[j] : tab[j] ^ flip[g];
-            uint32_t c[4 * W];
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const uint4 v = lds128(ring + ((g * 4 + j) * kTile + row) * 16);
-                c[4 * j] = v.x, c[4 * j + 1] = v.y, c[4 * j + 2] = v.z, c[4 * j + 3] = v.w;
-            }
-            const __half2 r2 = __float2half2_rn(ratio[g]);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t r[16];
-                expand_quarter<W>(c + h * W, t, r);
-                if (NG == 2) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&r[j]), r2);
-                        r[j] = *reinterpret_cast<uint32_t *>(&x);
-                    }
+                    for (int j = 0; j < 16; ++j) r[j] ^= flip[0];
                 }
-                if (KEYS) {
-                    tmem_st16(sh.tmem + ((uint32_t)(32 * q) << 16) + L::cK + (b * NG + g) * 64 + h * 16, r);
-                } else {
-                    // row `row` of the tile: two 64-wide segments of swizzled 16-byte chunks
-                    const uint32_t base = smem_u32(smem + L::oV) + (vb * NG + g) * L::kVBytes + (h >> 1) * (kTile * 128) +
-                                          (row >> 3) * 1024 + (row & 7) * 128;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        sts128(base + ((((h & 1) * 4 + j) ^ (row & 7)) << 4), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                }
-            }
-        }
-        if (KEYS) {
-            wait_st();
-            fence_before();
-        } else {
-            fence_async();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(KEYS ? &sh.k_full[b] : &sh.v_full[vb]);
-        // The products. The second one of a tile is issued an expansion later, when its weights are there, but at
-        // once where the item's part ends, for its partials wait for it.
-        if (q == 0) {
-            const bool first = starts >> rs & 1;
-            if (KEYS) {
-                if (first) {
-                    wait(sh, &sh.z_full, zpar, p.status, 0x47490006u);
-                    zpar ^= 1;
-                }
-                issue_scores<N, NG>(p, sh, smem, i, two);
             } else {
-                if (owed) issue_sums<N, NG>(p, sh, smem, i - 1, first_b, two_b);
-                owed = !(ends >> rs & 1);
-                if (!owed) issue_sums<N, NG>(p, sh, smem, i, first, two);
-                first_b = first, two_b = two;
+                expand_quarter<W>(c, t, r);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&r[j]), r2);
+                    r[j] = *reinterpret_cast<const uint32_t *>(&x);
+                }
             }
-            __syncwarp();
+            if (KEYS) {
+                tmem_st16(tmem + ((uint32_t)(32 * q) << 16) + L::cK + (buf * NG + g) * 64 + h * 16, r);
+            } else {
+                // row `row` of the tile: two 64-wide segments of swizzled 16-byte chunks
+                const uint32_t base = smem_u32(smem + L::oV) + (buf * NG + g) * L::kVBytes + (h >> 1) * (kTile * 128) + (row >> 3) * 1024 +
+                                      (row & 7) * 128;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sts128(base + ((((h & 1) * 4 + j) ^ (row & 7)) << 4), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            }
         }
-        rs = rs + 1 == L::kDepth ? 0 : rs + 1;
-        fetch();
     }
-    if (q == 0) {  // MMAs in flight finish before tensor memory is freed
-        mma_commit(&sh.drain[KEYS]);
-        for (unsigned k = 0; k < kSpin; ++k)
-            if (mbar_try(&sh.drain[KEYS], 0)) break;
-        __syncwarp();
-    }
-    cp_wait<0>();
 }
 
 template <int N, int NG, bool KEYS>
-__device__ void expand_any(const TreeParams &p, Shared &sh, uint8_t *smem, int row, int q, int lane) {
+__device__ __forceinline__ void expand_any(const TreeParams &p, Shared &sh, uint8_t *smem, uint32_t tmem, uint32_t codes, uint32_t tab, int buf, int row,
+                                           int q, const float (&ratio)[2], const uint32_t (&flip)[2], bool two) {
     switch (KEYS ? p.wk : p.wv) {
-    case 2: expand_role<N, NG, KEYS, 2>(p, sh, smem, row, q, lane); break;
-    case 3: expand_role<N, NG, KEYS, 3>(p, sh, smem, row, q, lane); break;
-    default: expand_role<N, NG, KEYS, 4>(p, sh, smem, row, q, lane); break;
+    case 2: expand_tile<N, NG, 2, KEYS>(p, sh, smem, tmem, codes, tab, buf, row, q, ratio, flip, two); break;
+    case 3: expand_tile<N, NG, 3, KEYS>(p, sh, smem, tmem, codes, tab, buf, row, q, ratio, flip, two); break;
+    default: expand_tile<N, NG, 4, KEYS>(p, sh, smem, tmem, codes, tab, buf, row, q, ratio, flip, two); break;
+    }
+}
+
+// The norm of a side's row, and for two groups of norms n0, n1 the larger one with each group's ratio to it, by which its levels
+// are scaled. Ratios stay finite whatever the norms, so that a lost row reaches only who attends it.
+template <int NG>
+__device__ __forceinline__ float row_norm(uint32_t info, uint32_t norms, bool two, float (&ratio)[2]) {
+    const float n0 = norm_value(info, lds32(norms), 0, NG == 2 && two ? 1 : 0);
+    ratio[0] = ratio[1] = 1.0f;
+    if (NG == 1 || !two) return n0;
+    const float n1 = norm_value(info, lds32(norms + kTile * 4), 1, 1);
+    float nn = fmaxf(fabsf(n0), fabsf(n1));
+    const bool lost = !(fabsf(n0) <= 65504.0f && fabsf(n1) <= 65504.0f);
+    ratio[0] = n0 / nn, ratio[1] = n1 / nn;
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+        if (!(fabsf(ratio[g]) <= 1.0f)) ratio[g] = lost ? 1.0f : 0.0f;  // 0 / 0: both norms are zero
+    return lost ? __int_as_float(0x7FC00000) : nn;
+}
+
+template <int N, int NG, bool KEYS, bool VALUES>
+__device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, int row, int q, int lane) {
+    using L = Plan<N, NG>;
+    Cursor c = sh.start;
+    const int tiles = uniform(c.left);
+    const uint32_t tmem = uniform(sh.tmem), ring = smem_u32(smem) + p.o_ring;
+    auto place = [&](int w) { return w == 2 && wide_two(N) ? (lane & 15) * 8 : lane * 4; };
+    const uint32_t tab_k = smem_u32(smem) + L::oTab + place(p.wk), tab_v = smem_u32(smem) + p.o_tab_v + place(p.wv);
+    int st = 0;
+    uint32_t rpar = 0;
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+        const int b = i & 1, vb = L::kVBuf == 2 ? b : 0;
+        const uint32_t par = (uint32_t)(i >> 1) & 1;
+        const bool two_k = NG == 2 && p.unit[c.u].ngk == 2, two_v = NG == 2 && p.unit[c.u].ngv == 2;
+        if (NG == 2) c.advance(p, N);
+        wait(sh, &sh.ring_full[st], rpar, p.status, 0x4749000Fu);
+        const uint32_t kc = ring + st * p.stage, vc = kc + Stage<NG>::codes(p.wk), info = vc + Stage<NG>::codes(p.wv);
+        const uint32_t nrm = info + Stage<NG>::kInfo;
+        wait(sh, &sh.s_empty[b], par ^ 1, p.status, 0x47490001u);
+        float ratio_k[2], ratio_v[2];
+        uint32_t flip[2] = {0, 0};
+        if (KEYS) {
+            const uint32_t word = lds32(info + row * 4);
+            const float n = row_norm<NG>(word, nrm + row * 4, two_k, ratio_k);
+            sh.scal[b][0][row] = word & 1 ? n : 0.0f;
+        }
+        if (VALUES) {
+            const uint32_t word = lds32(info + (kTile + row) * 4);
+            float n = row_norm<NG>(word, nrm + (NG * kTile + row) * 4, two_v, ratio_v);
+            if (NG == 1 || !two_v) {
+                if (n < 0.0f) flip[0] = NG == 1 ? 0x80008000u : 0x80808080u;  // a negative norm turns its levels round
+                n = fabsf(n);
+            }
+            // a norm of zero counts in the denominator: 2^-40 stands for it, far below the smallest fp16 norm
+            const float safe = n == 0.0f ? 0x1p-40f : n;
+            const bool lost = !(n <= 65504.0f);
+            sh.scal[b][1][row] = !(word & 1) ? -INFINITY : lost ? __int_as_float(0x7FC00000) : log2f(safe);
+            sh.scal[b][2][row] = (word & 1) && !lost ? 1.0f / safe : 0.0f;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.sc_full[b]);
+        if (KEYS) {
+            wait(sh, &sh.k_empty[b], par ^ 1, p.status, 0x47490002u);
+            fence_after();
+            expand_any<N, NG, true>(p, sh, smem, tmem, kc, tab_k, b, row, q, ratio_k, flip, two_k);
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.k_full[b]);
+        }
+        if (VALUES) {
+            wait(sh, &sh.v_empty[vb], (L::kVBuf == 2 ? par : (uint32_t)(i & 1)) ^ 1, p.status, 0x47490003u);
+            expand_any<N, NG, false>(p, sh, smem, tmem, vc, tab_v, vb, row, q, ratio_v, flip, two_v);
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.v_full[vb]);
+        }
+        if (lane == 0) mbar_arrive(&sh.ring_empty[st]);
+        if (++st == p.depth) st = 0, rpar ^= 1;
     }
 }
 
@@ -745,65 +869,60 @@ __device__ __forceinline__ float load_q(const TreeParams &p, int64_t at) {
 }
 
 // Rotated queries of an item's columns into shared memory (the K-major B operand), scaled by one power of two so that
-// fp16 holds them whatever their size; returns what takes the scale back out of the logits.
+// fp16 holds them whatever their size (a coordinate is at most the sum of the query's magnitudes); returns what takes the
+// scale back out of the logits.
 template <int N, int NG>
 __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, const Cursor &c, int warp, int lane) {
     using L = Plan<N, NG>;
-    const TreeUnit &u = p.unit[c.u];
+    const TreeUnit u = p.unit[c.u];
     const int rows = u.nh * p.per, cols = min(N, c.n * rows - c.c * N);
-    float z[N / 8][NG][4], top = 0.0f;
+    // coordinates 4 * lane .. of group g of a column's query, placed at its head's elements of the cache row
+    auto load = [&](int col, int g, float (&z)[4]) {
+        const int at = c.c * N + col, node = at / rows, r = at - node * rows, h = u.h0 + r / p.per;
+        const int64_t src = (int64_t)(c.first + node) * p.t.q_stride_t + (int64_t)(u.h0 * p.per + r) * p.t.q_stride_h;
+        const int d0 = (u.gk + g) * kGroup + 4 * lane - h * p.dk;
 #pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-        const int col = warp + 8 * i;
+        for (int j = 0; j < 4; ++j) z[j] = d0 + j >= 0 && d0 + j < p.dk ? load_q(p, src + d0 + j) : 0.0f;
+    };
+    float top = 0.0f;
+#pragma unroll 2
+    for (int col = warp; col < cols; col += L::kSoft) {
+        float sum = 0.0f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[i][g][j] = 0.0f;
-            if (col < cols && g < u.ngk) {
-                const int at = c.c * N + col, node = at / rows, r = at - node * rows, h = u.h0 + r / p.per;
-                const int64_t src = (int64_t)(c.first + node) * p.t.q_stride_t + (int64_t)(u.h0 * p.per + r) * p.t.q_stride_h;
-                const int d0 = (u.gk + g) * kGroup + 4 * lane - h * p.dk;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (d0 + j >= 0 && d0 + j < p.dk) z[i][g][j] = load_q(p, src + d0 + j);
-            }
+            if (g >= u.ngk) break;
+            float z[4];
+            load(col, g, z);
+            sum += (fabsf(z[0]) + fabsf(z[1])) + (fabsf(z[2]) + fabsf(z[3]));
         }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (sum <= 3e38f) top = fmaxf(top, sum);  // a column that is not finite does not scale the others
     }
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i)
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            fwht(z[i][g], lane);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float a = fabsf(z[i][g][j]);
-                if (a <= 3e38f) top = fmaxf(top, a);  // a lost column does not scale the others
-            }
-        }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     if (lane == 0) atomicMax(&sh.zmax, __float_as_int(top));
-    bar_sync(1, kSoftThreads);
-    // largest coordinate between 2^13 and 2^14; the exponent is held where both powers of two are normal
-    const int ex = max(-110, min(110, ((sh.zmax >> 23) & 255) - 127 - 13));
+    bar_sync(1, 32 * L::kSoft);
+    // the largest sum between 2^14 and 2^15; the exponent is held where both powers of two are normal
+    const int ex = max(-110, min(110, ((sh.zmax >> 23) & 255) - 127 - 14));
     const float down = __int_as_float((127 - ex) << 23);
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-        const int col = warp + 8 * i;
+#pragma unroll 2
+    for (int col = warp; col < N; col += L::kSoft) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
+            float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (col < cols && g < u.ngk) load(col, g, z);
+            fwht(z, lane);
             const uint32_t base = smem_u32(smem + L::oZ) + g * L::kZBytes + (col >> 3) * 1024 + (col & 7) * 128;
             auto put = [&](int pos, float x, float y) {
                 const __half2 v = __floats2half2_rn(x * down, y * down);
                 sts32(base + (pos >> 6) * (N * 128) + ((((pos & 63) >> 3) ^ (col & 7)) << 4) + (pos & 7) * 2,
                       *reinterpret_cast<const uint32_t *>(&v));
             };
-            if (p.wk == 2) {
-                put(position_of(4 * lane, 2), z[i][g][0], z[i][g][2]);
-                put(position_of(4 * lane + 1, 2), z[i][g][1], z[i][g][3]);
+            if (NG == 2 && p.wk == 2) {
+                put(position_of(4 * lane, 2), z[0], z[2]);
+                put(position_of(4 * lane + 1, 2), z[1], z[3]);
             } else {
-                put(4 * lane, z[i][g][0], z[i][g][1]);
-                put(4 * lane + 2, z[i][g][2], z[i][g][3]);
+                put(4 * lane, z[0], z[1]);
+                put(4 * lane + 2, z[2], z[3]);
             }
         }
     }
@@ -812,9 +931,9 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
 
 // Who attends drafted token j, as bits over the item's columns.
 template <int N>
-__device__ void gather_mask(const TreeParams &p, Shared &sh, const Cursor &c, int warp, int lane) {
+__device__ void gather_mask(const TreeParams &p, Shared &sh, const Cursor &c, int warp, int warps, int lane) {
     const int rows = p.unit[c.u].nh * p.per, jw = (c.n + 31) / 32;
-    for (int k = warp; k < jw * ((N + 31) / 32); k += 8) {
+    for (int k = warp; k < jw * ((N + 31) / 32); k += warps) {
         const int cw = k / jw, j0 = (k - cw * jw) * 32, node = (c.c * N + cw * 32 + lane) / rows;
         uint32_t w = 0;
         if (node < c.n) {
@@ -837,22 +956,75 @@ __device__ __forceinline__ int ordered(float x) {  // integers in the order of t
 }
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
 
+// Raises the references of columns cx .. cx + X - 1 whose largest logit of this tile (columns in tensor memory at ts, this
+// thread's cache row) passes the weights' range; the factors for what was summed before go to sh.f. All four warps of
+// the warpgroup; true if any was raised. Kept out of the loop's straight line: it runs in the first tile and rarely after.
+template <int N, int X>
+__device__ __noinline__ bool raise(Shared &sh, uint32_t ts, int cx, float nk, float ln, uint32_t see, int warp, int lane) {
+    const int wg = warp >> 2, row = 32 * (warp & 3) + lane;
+    float mine = 0.0f;
+#pragma unroll 1
+    for (int k = 0; k < X; k += 8) {
+        float d[8];
+        tmem_ld<8>(ts + k, d);
+        wait_ld<8>(d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float t = see >> (k + j) & 1 ? fmaf(d[j], nk, ln) : -INFINITY;
+            const float x = unordered(__reduce_max_sync(0xFFFFFFFFu, ordered(fmaxf(t, -INFINITY))));
+            if (lane == k + j) mine = x;
+        }
+    }
+    if (lane < X) sh.wmax[warp][lane] = mine;
+    bar_sync(2 + wg, 128);
+    bool raised = false;
+    if (row < X) {
+        const float old = -sh.minus_m[cx + row];
+        float x = sh.wmax[4 * wg][row];
+#pragma unroll
+        for (int k = 1; k < 4; ++k) x = fmaxf(x, sh.wmax[4 * wg + k][row]);
+        raised = x > old + kRaise;
+        sh.f[cx + row] = raised ? ex2(old - x) : 1.0f;
+        if (raised) sh.minus_m[cx + row] = -x;
+    }
+    return bar_or(2 + wg, 128, raised);
+}
+
+// Scales the running sums of columns cx .. cx + X - 1 by the factors of a raise.
+__device__ __noinline__ void scale_sums(Shared &sh, uint32_t to, int n, int groups, int cx, int X) {
+#pragma unroll 1
+    for (int g = 0; g < groups; ++g) {
+#pragma unroll 1
+        for (int k = 0; k < X; k += 8) {
+            float o[8];
+            tmem_ld<8>(to + g * n + cx + k, o);
+            wait_ld<8>(o);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] *= sh.f[cx + k + j];
+            tmem_st8(to + g * n + cx + k, o);
+        }
+    }
+    wait_st();
+}
+
 template <int N, int NG>
 __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int warp, int lane) {
     using L = Plan<N, NG>;
-    constexpr int NC = N / 2;                  // columns of this warpgroup
+    constexpr int NC = N / L::kSoftWG;         // columns of this warpgroup
+    constexpr int kSoftThreads = 32 * L::kSoft;
     constexpr int X = NC < 32 ? NC : 32;       // columns per tensor memory load
     const int wg = warp >> 2, q = warp & 3, row = 32 * q + lane, c0 = wg * NC;
     const uint32_t tm = sh.tmem + ((uint32_t)(32 * q) << 16);
     Cursor c = sh.start;
-    long long i = 0, done = sh.w0;  // tiles done by this block; of all blocks
+    int i = 0;
+    long long done = sh.w0;  // tiles of the blocks before and of this one so far
     bool more = true;
     while (more) {
         // ------------------------------------------------ one item's part --
         bar_sync(1, kSoftThreads);  // the item before is finished: zmax, m, mask may be written
         if (warp == 0 && lane == 0) sh.zmax = 0;
-        if (lane + 32 * q < NC) sh.m[c0 + lane + 32 * q] = kNoMax;
-        gather_mask<N>(p, sh, c, warp, lane);
+        if (row < NC) sh.minus_m[c0 + row] = -kNoMax;
+        gather_mask<N>(p, sh, c, warp, L::kSoft, lane);
         bar_sync(1, kSoftThreads);
         const float mult = rotate_queries<N, NG>(p, sh, smem, c, warp, lane);
         fence_async();
@@ -864,13 +1036,13 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
         const int i0 = (c.s * p.n_units + c.u) * p.ncol_max + c.c;
         if (c.tile == 0 && warp == 0 && lane == 0)
             p.rec[i0] = make_int2(slot, run_of(sh.total, p.grid, done + c.ntiles - 1) - (int)blockIdx.x + 1);
-        const int count = (int)min((long long)(c.ntiles - c.tile), c.left);
-        float l[NC];
+        const int count = min(c.ntiles - c.tile, c.left);
+        F2 l[NC / 2];
 #pragma unroll
-        for (int k = 0; k < NC; ++k) l[k] = 0.0f;
+        for (int k = 0; k < NC / 2; ++k) l[k] = f2(0.0f, 0.0f);
 #pragma unroll 1
         for (int it = 0; it < count; ++it, ++i) {
-            const int b = (int)(i & 1);
+            const int b = i & 1;
             const uint32_t par = (uint32_t)(i >> 1) & 1;
             const int tok = (c.tile + it) * kTile;
             const bool masked = tok + kTile > c.ctx;  // the tile holds drafted tokens
@@ -882,6 +1054,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
             }
             wait(sh, &sh.sc_full[b], par, p.status, 0x47490009u);
             const float nk = sh.scal[b][0][row] * mult, ln = sh.scal[b][1][row], inv = sh.scal[b][2][row];
+            const F2 nk2 = f2(nk, nk), ln2 = f2(ln, ln), inv2 = f2(inv, inv);
             wait(sh, &sh.s_full[b], par, p.status, 0x4749000Au);
             fence_after();
             // Column by column in halves of X: the denominators of all columns and the logits of one half fit the registers.
@@ -890,75 +1063,37 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
                 float d[X];
                 const int cx = c0 + hf;
                 const uint32_t ts = tm + L::cS + b * N + cx;
-                auto logits = [&]() {  // d = log2 of the weights, before the reference
+                bool raised = false;
+#pragma unroll 1
+                for (int pass = 0;; ++pass) {
                     tmem_ld<X>(ts, d);
                     wait_ld<X>(d);
+                    float top = kNoMax;
+#pragma unroll
+                    for (int k = 0; k < X; k += 4) {  // d = log2 of the weights
+                        const float4 m = *reinterpret_cast<const float4 *>(&sh.minus_m[cx + k]);
+                        f2_get(f2_add(f2_fma(f2(d[k], d[k + 1]), nk2, ln2), f2(m.x, m.y)), d[k], d[k + 1]);
+                        f2_get(f2_add(f2_fma(f2(d[k + 2], d[k + 3]), nk2, ln2), f2(m.z, m.w)), d[k + 2], d[k + 3]);
+                    }
                     if (masked) {
 #pragma unroll
-                        for (int k = 0; k < X; ++k) {
-                            const float x = fmaf(d[k], nk, ln);
-                            d[k] = see[hf / 32] >> k & 1 ? x : -INFINITY;
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < X; ++k) d[k] = fmaf(d[k], nk, ln);
+                        for (int k = 0; k < X; ++k) d[k] = see[hf / 32] >> k & 1 ? d[k] : -INFINITY;
                     }
-                };
-                auto minus_reference = [&]() {
 #pragma unroll
-                    for (int k = 0; k < X; k += 4) {
-                        const float4 m = *reinterpret_cast<const float4 *>(&sh.m[cx + k]);
-                        d[k] -= m.x, d[k + 1] -= m.y, d[k + 2] -= m.z, d[k + 3] -= m.w;
+                    for (int k = 0; k < X; k += 2) top = max3(top, d[k], d[k + 1]);
+                    if (!bar_or(2 + wg, 128, top > kRaise) || pass) break;
+                    raised = raise<N, X>(sh, ts, cx, nk, ln, masked ? see[hf / 32] : 0xFFFFFFFFu, warp, lane);
+                }
+                if (raised) {
+#pragma unroll
+                    for (int k = 0; k < X; k += 2) {
+                        const float2 f = *reinterpret_cast<const float2 *>(&sh.f[cx + k]);
+                        l[(hf + k) / 2] = f2_mul(l[(hf + k) / 2], f2(f.x, f.y));
                     }
-                };
-                logits();
-                minus_reference();
-                float top = d[0];
-#pragma unroll
-                for (int k = 1; k < X; ++k) top = fmaxf(top, d[k]);
-                if (bar_or(2 + wg, 128, top > kRaise)) {
-                    // ---------------------------------- raise references --
-                    logits();
-                    float mine = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < X; ++k) {
-                        const float x = unordered(__reduce_max_sync(0xFFFFFFFFu, ordered(fmaxf(d[k], -INFINITY))));
-                        if (lane == k) mine = x;
-                    }
-                    if (lane < X) sh.wmax[warp][lane] = mine;
-                    bar_sync(2 + wg, 128);
-                    bool raised = false;
-                    if (row < X) {
-                        const float old = sh.m[cx + row];
-                        float x = sh.wmax[4 * wg][row];
-#pragma unroll
-                        for (int k = 1; k < 4; ++k) x = fmaxf(x, sh.wmax[4 * wg + k][row]);
-                        raised = x > old + kRaise;
-                        sh.f[cx + row] = raised ? ex2(old - x) : 1.0f;
-                        if (raised) sh.m[cx + row] = x;
-                    }
-                    raised = bar_or(2 + wg, 128, raised);
-                    minus_reference();
-                    if (raised) {
-#pragma unroll
-                        for (int k = 0; k < X; ++k) l[hf + k] *= sh.f[cx + k];
-                        if (it) {  // the first tile's product does not accumulate
-                            wait(sh, &sh.p_empty[b ^ 1], (uint32_t)((i - 1) >> 1) & 1, p.status, 0x4749000Bu);
-                            fence_after();
-                            for (int g = 0; g < u.ngv; ++g) {
-#pragma unroll 1
-                                for (int k = 0; k < X; k += 8) {
-                                    float o[8];
-                                    const uint32_t to = tm + L::cO + g * N + cx + k;
-                                    tmem_ld<8>(to, o);
-                                    wait_ld<8>(o);
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) o[j] *= sh.f[cx + k + j];
-                                    tmem_st8(to, o);
-                                }
-                            }
-                            wait_st();
-                        }
+                    if (it) {  // the first tile's product does not accumulate
+                        wait(sh, &sh.p_empty, (uint32_t)(i - 1) & 1, p.status, 0x4749000Bu);
+                        fence_after();
+                        scale_sums(sh, tm + L::cO, N, u.ngv, cx, X);
                     }
                 }
                 if (hf + X == NC) {
@@ -966,17 +1101,16 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.s_empty[b]);
                 }
-                if (hf == 0) wait(sh, &sh.p_empty[b], par ^ 1, p.status, 0x4749000Cu);
+                if (hf == 0) wait(sh, &sh.p_empty, (uint32_t)(i & 1) ^ 1, p.status, 0x4749000Cu);
                 // weights in fp16: cache row `row`, columns cx .. cx + X - 1 (the MN-major B operand)
-                const uint32_t pb = smem_u32(smem + L::oP) + b * L::kPBytes + (cx >> 6) * (kTile * 128) + (row >> 3) * 1024 + (row & 7) * 128;
+                const uint32_t pb = smem_u32(smem + L::oP) + (cx >> 6) * (kTile * 128) + (row >> 3) * 1024 + (row & 7) * 128;
 #pragma unroll
                 for (int k = 0; k < X; k += 8) {
                     uint32_t h[4];
 #pragma unroll
                     for (int j = 0; j < 8; j += 2) {
                         const float x = ex2(d[k + j]), y = ex2(d[k + j + 1]);
-                        l[hf + k + j] = fmaf(x, inv, l[hf + k + j]);
-                        l[hf + k + j + 1] = fmaf(y, inv, l[hf + k + j + 1]);
+                        l[(hf + k + j) / 2] = f2_fma(f2(x, y), inv2, l[(hf + k + j) / 2]);
                         const __half2 v = __floats2half2_rn(x, y);
                         h[j >> 1] = *reinterpret_cast<const uint32_t *>(&v);
                     }
@@ -985,27 +1119,42 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
             }
             fence_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[b]);
+            if (lane == 0) mbar_arrive(&sh.p_full);
         }
         // ------------------------------------------------- the item's partials --
 #pragma unroll
-        for (int k = 0; k < NC; ++k) {
-            float x = l[k];
+        for (int hf = 0; hf < NC; hf += X) {
+            float v[X];
 #pragma unroll
-            for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-            if (lane == 0) sh.lsum[warp][k] = x;
+            for (int k = 0; k < X; k += 2) f2_get(l[(hf + k) / 2], v[k], v[k + 1]);
+            // sums over the lanes: each step halves the columns a lane carries, so lane k ends with column k
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                if (o >= X) {
+#pragma unroll
+                    for (int k = 0; k < X; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < o; ++k) {
+                        const bool up = lane & o;
+                        const float send = up ? v[k] : v[k + o], keep = up ? v[k + o] : v[k];
+                        v[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+                    }
+                }
+            }
+            if (lane < X) sh.lsum[warp][hf + lane] = v[0];
         }
         bar_sync(2 + wg, 128);
         if (row < NC && c0 + row < cols) {
             const float x = sh.lsum[4 * wg][row] + sh.lsum[4 * wg + 1][row] + (sh.lsum[4 * wg + 2][row] + sh.lsum[4 * wg + 3][row]);
-            p.ml[(size_t)slot * N + c0 + row] = make_float2(sh.m[c0 + row], x);
+            p.ml[(size_t)slot * N + c0 + row] = make_float2(-sh.minus_m[c0 + row], x);
         }
-        wait(sh, &sh.p_empty[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1, p.status, 0x4749000Du);
+        wait(sh, &sh.p_empty, (uint32_t)(i - 1) & 1, p.status, 0x4749000Du);
         fence_after();
-        const int nat = natural_of(row, p.wv);
+        const int nat = NG == 2 ? natural_of(row, p.wv) : row;
         for (int g = 0; g < u.ngv; ++g) {
             float *out = p.part + ((size_t)slot * NG + g) * N * kGroup + nat;
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < NC; k += 8) {
                 float o[8];
                 tmem_ld<8>(tm + L::cO + g * N + c0 + k, o);
@@ -1028,53 +1177,64 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     Shared &sh = *reinterpret_cast<Shared *>(smem + L::oShared);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (tid == 0) {
         sh.abort = 0;
         sh.bad = 0;
+#pragma unroll 1
+        for (int i = 0; i < p.depth; ++i) {
+            mbar_init(&sh.ring_full[i], 128);
+            mbar_init(&sh.ring_empty[i], L::kExp);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.k_full[i], 4);
             mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.v_full[i], 4);
             mbar_init(&sh.v_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_empty[i], 8);
-            mbar_init(&sh.p_full[i], 8);
-            mbar_init(&sh.p_empty[i], 1);
-            mbar_init(&sh.sc_full[i], 8);
+            mbar_init(&sh.s_empty[i], L::kSoft);
+            mbar_init(&sh.sc_full[i], L::kExp);
         }
-        mbar_init(&sh.z_full, 8);
-        mbar_init(&sh.drain[0], 1);
-        mbar_init(&sh.drain[1], 1);
+        mbar_init(&sh.p_full, L::kSoft);
+        mbar_init(&sh.p_empty, 1);
+        mbar_init(&sh.z_full, L::kSoft);
+        mbar_init(&sh.drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (NG == 1) {
+        fill_table(smem + L::oTab, p.tk, p.wk, p.wk == 2 && wide_two(N));
+        if (p.o_tab_v != L::oTab) fill_table(smem + p.o_tab_v, p.tv, p.wv, p.wv == 2 && wide_two(N));
     }
     __syncthreads();
     const bool work = find_run<N>(p, sh);  // uniform
     if (blockIdx.x == 0 && tid == 0 && sh.bad) atomicOr(p.status, kStatusIndex);
     if (!work) return;
-    if (warp == 8) {
+    if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sh.tmem)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
     }
     fence_before();
     __syncthreads();
     fence_after();
-    // A softmax thread of many columns keeps logits and denominators in registers: the expanders give theirs up.
-    // 256 (kSoft + kExp) = 512 x 128, what the block was launched with.
-    if (warp < 8) {
-        if (N >= 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(L::kSoft));
+    // A softmax thread of many columns keeps logits and denominators in registers: the others give theirs up.
+    if (warp < L::kSoft) {
+        if (L::kSoftWG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(L::kSoftRegs));
         softmax_role<N, NG>(p, sh, smem, warp, lane);
-    } else if (warp < 12) {
-        if (N >= 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kExp));
-        expand_any<N, NG, true>(p, sh, smem, tid - 256, warp & 3, lane);
+    } else if (warp < L::kSoft + L::kExp) {
+        if (L::kSoftWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kExpRegs));
+        const int row = 32 * (warp & 3) + lane;
+        if (L::kExpWG == 1) expand_role<N, NG, true, true>(p, sh, smem, row, warp & 3, lane);
+        else if (warp < L::kSoft + 4) expand_role<N, NG, true, false>(p, sh, smem, row, warp & 3, lane);
+        else expand_role<N, NG, false, true>(p, sh, smem, row, warp & 3, lane);
     } else {
-        if (N >= 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kExp));
-        expand_any<N, NG, false>(p, sh, smem, tid - 384, warp & 3, lane);
+        if (L::kSoftWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kRestRegs));
+        if (warp == 12) issue_role<N, NG>(p, sh, smem);
+        else if (warp < 15) fetch_role<N, NG>(p, sh, smem, tid - 13 * 32);
     }
     fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 12) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(sh.tmem), "r"(512));
     }
@@ -1182,6 +1342,12 @@ Shape shape_of(const cq_kv_geom &g, int n_seqs, int max_nodes, TreeUnit *u) {
     s.N = 16;
     while (s.N < top && s.N < most) s.N *= 2;
     if (s.ng == 2 && s.N == 32) s.N = 64;
+    // 128 columns leave room for one large level table, or for two where a stage of codes is small
+    const bool same = g.k_bits == g.v_bits && std::equal(g.k_codebook, g.k_codebook + levels_of(g.k_bits), g.v_codebook);
+    const int wk = width_of(g.k_bits), wv = width_of(g.v_bits);
+    if (s.N == 128 && Plan<128, 1>::oTab + table_bytes(wk, 128) + (same ? 0 : table_bytes(wv, 128)) + 2 * Stage<1>::bytes(wk, wv) >
+                          Plan<128, 1>::kLimit)
+        s.N = 64;
     s.ncol_max = std::max(1, (most + s.N - 1) / s.N);
     s.items = (size_t)n_seqs * s.n_units * s.ncol_max;
     s.slots = s.items + sm_count();
@@ -1206,11 +1372,32 @@ float byte_table(const float *lv, uint32_t *t) {
     return std::ldexp(1.0f, e);
 }
 
+// Shared memory behind the fixed part: level tables, then as many ring stages as fit. False if fewer than two do.
 template <int N, int NG>
-int launch_main(const TreeParams &p, cudaStream_t st) {
-    const int rc = ensure_smem(reinterpret_cast<const void *>(tree_kernel<N, NG>), Plan<N, NG>::kSmem);
+bool lay_out(TreeParams &p) {
+    using L = Plan<N, NG>;
+    int at = L::oTab;
+    p.o_tab_v = at;
+    if (NG == 1) {
+        const bool same = p.wk == p.wv && std::equal(p.tk, p.tk + 8, p.tv);
+        at += table_bytes(p.wk, N);
+        if (!same) {
+            p.o_tab_v = at;
+            at += table_bytes(p.wv, N);
+        }
+    }
+    p.o_ring = at;
+    p.stage = Stage<NG>::bytes(p.wk, p.wv);
+    p.depth = std::min(kMaxDepth, (L::kLimit - at) / p.stage);
+    return p.depth >= 2;
+}
+
+template <int N, int NG>
+int launch_main(TreeParams &p, cudaStream_t st) {
+    if (!lay_out<N, NG>(p)) return set_error(CQ_ERR_SHAPE, "no room for the level tables");
+    const int rc = ensure_smem(reinterpret_cast<const void *>(tree_kernel<N, NG>), Plan<N, NG>::kLimit + 1024);
     if (rc) return rc;
-    tree_kernel<N, NG><<<p.grid, kThreads, Plan<N, NG>::kSmem, st>>>(p);
+    tree_kernel<N, NG><<<p.grid, kThreads, p.o_ring + p.depth * p.stage + 1024, st>>>(p);
     return CQ_OK;
 }
 
