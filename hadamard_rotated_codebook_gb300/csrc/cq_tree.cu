@@ -62,8 +62,10 @@ struct TreeParams {
     uint32_t tk[8], tv[8];  // level tables: low bytes of 16 fp16 levels, then high bytes
     float k_mult, v_mult;   // scale * log2(e) / sqrt(128) * 2^(table exponent); 2^(table exponent) / sqrt(128)
     int n_units, hq, per, dk, dv, wk, wv, kgroups, vgroups;
-    int depth, stage, o_tab_v, o_ring;  // ring stages and their bytes; offsets behind the key table's
+    int depth, stage;        // ring stages and their bytes
+    uint32_t tab_k, tab_v;   // shared-memory addresses of the level tables
     uint32_t div_mul, div_shift;  // t / block_size = t * div_mul >> div_shift
+    bool vec_q;      // a column's query is whole runs of 16 elements on 16-byte boundaries
     int rows;        // most query heads of a unit
     int ncol_max;    // column tiles of a request with max_nodes tokens
     int grid;
@@ -451,14 +453,17 @@ struct Plan {
     static constexpr int kPBytes = kTile * (N <= 64 ? 128 : 256);
     static constexpr int kZBytes = N * 256;                    // one group
     static constexpr int oV = 0, oP = oV + kVBuf * NG * kVBytes, oZ = oP + kPBytes, oShared = oZ + NG * kZBytes;
-    static constexpr int oTab = oShared + ((int)sizeof(Shared) + 127) / 128 * 128;
-    static constexpr int kLimit = 232448 - 1024;               // a block's shared memory, less the alignment of its start
+    static constexpr int oRing = oShared + ((int)sizeof(Shared) + 127) / 128 * 128;
     // registers of the roles where softmax takes two warpgroups: 256 kSoftRegs + 128 (kExpRegs + kRestRegs) = 512 x 128
     static constexpr int kSoftRegs = 168, kExpRegs = 104, kRestRegs = 72;
     // TMEM columns
     static constexpr int cK = 0, cS = 2 * NG * 64, cO = cS + 2 * N;
     static_assert(cO + NG * N <= 512, "tensor memory");
 };
+
+// A block's shared memory as addresses: the first kilobyte is the system's. The tables lie at the top, each aligned to its
+// size, so that an entry's address is put together by one logical operation.
+constexpr int kSmemFirst = 1024, kSmemLast = 232448 + 1024, kTabTop = kSmemLast / 32768 * 32768;
 
 // Level tables in shared memory (one group per row): entry e at e * 128 bytes, repeated for every lane so that no two lanes of a
 // warp meet in a bank. A code pair gives one fp16 pair (3 and 4 bits, and 2 bits where space is short), a byte of two-bit
@@ -532,46 +537,45 @@ __device__ __forceinline__ void fetch_side(const Side &s, uint32_t r, size_t all
 
 template <int N, int NG>
 __device__ void fetch_role(const TreeParams &p, Shared &sh, uint8_t *smem, int lane) {
+    using L = Plan<N, NG>;
     Cursor c = sh.start;
     const int tiles = uniform(c.left);
-    const uint32_t ring = smem_u32(smem) + p.o_ring;
-    RowAt r[2] = {row_at(p, c, lane), row_at(p, c, lane + 64)};
+    const uint32_t ring = smem_u32(smem) + L::oRing;
+    RowAt next = row_at(p, c, lane);
     int st = 0, unit = c.u;
     uint32_t par = 1;
     Side sk = side_of<true>(p, unit), sv = side_of<false>(p, unit);
     const size_t all_k = (size_t)p.t.cap * sk.groups, all_v = (size_t)p.t.cap * sv.groups;
 #pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
-        if (c.u != unit) {
-            unit = c.u;
+    for (int i = 0; i < 2 * tiles; ++i) {  // half a tile at a time
+        const int half = i & 1;
+        const RowAt now = next;
+        const int u = c.u;
+        if (half) c.advance(p, N);
+        next = row_at(p, c, lane + 64 * (half ^ 1));
+        if (u != unit) {
+            unit = u;
             sk = side_of<true>(p, unit), sv = side_of<false>(p, unit);
         }
-        c.advance(p, N);
-        wait(sh, &sh.ring_empty[st], par, p.status, 0x4749000Eu);
-        const uint32_t kc = ring + st * p.stage + lane * 16, vc = kc + Stage<NG>::codes(p.wk);
-        const uint32_t info = vc + Stage<NG>::codes(p.wv) - lane * 12, nrm = info + Stage<NG>::kInfo;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const RowAt now = r[k];
-            r[k] = row_at(p, c, lane + 64 * k);
-            const long long at = (long long)now.blk * p.t.block_size + now.off;
-            bool ok = now.ok;
-            if (ok && (now.blk < 0 || at >= p.t.cap)) {
-                ok = false;
-                atomicOr(p.status, kStatusIndex);
-            }
-            if (ok) {
-                fetch_side<NG>(sk, (uint32_t)at, all_k, kc + 1024 * k, info + 256 * k, nrm + 256 * k);
-                fetch_side<NG>(sv, (uint32_t)at, all_v, vc + 1024 * k, info + 256 * k + kTile * 4, nrm + 256 * k + NG * kTile * 4);
-            } else {
-                sts32(info + 256 * k, 0);
-                sts32(info + 256 * k + kTile * 4, 0);
-            }
+        if (!half) wait(sh, &sh.ring_empty[st], par, p.status, 0x4749000Eu);
+        const uint32_t kc = ring + st * p.stage + (lane + 64 * half) * 16, vc = kc + Stage<NG>::codes(p.wk);
+        const uint32_t info = vc + Stage<NG>::codes(p.wv) - (lane + 64 * half) * 12, nrm = info + Stage<NG>::kInfo;
+        const long long at = (long long)now.blk * p.t.block_size + now.off;
+        const bool ok = now.ok && now.blk >= 0 && at < p.t.cap;
+        if (ok) {
+            fetch_side<NG>(sk, (uint32_t)at, all_k, kc, info, nrm);
+            fetch_side<NG>(sv, (uint32_t)at, all_v, vc, info + kTile * 4, nrm + NG * kTile * 4);
+        } else {
+            sts32(info, 0);
+            sts32(info + kTile * 4, 0);
+            if (now.ok) atomicOr(p.status, kStatusIndex);
         }
-        // two arrivals a lane: one when its copies have landed, one for what it stored itself
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(&sh.ring_full[st])) : "memory");
-        mbar_arrive(&sh.ring_full[st]);
-        if (++st == p.depth) st = 0, par ^= 1;
+        if (half) {
+            // two arrivals a lane: one when its copies have landed, one for what it stored itself
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(&sh.ring_full[st])) : "memory");
+            mbar_arrive(&sh.ring_full[st]);
+            if (++st == p.depth) st = 0, par ^= 1;
+        }
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
 }
@@ -596,7 +600,7 @@ __device__ __forceinline__ void issue_scores(const TreeParams &p, Shared &sh, ui
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if (g == 1 && !two) break;
-#pragma unroll 2
+#pragma unroll 1
         for (int k = 0; k < 8; ++k)
             mma_ts(tmem + L::cS + b * N, tmem + L::cK + (b * NG + g) * 64 + 8 * k,
                    dz + (uint64_t)((g * L::kZBytes + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), idesc_f16(128, N, 0, 0), (g | k) != 0);
@@ -617,7 +621,7 @@ __device__ __forceinline__ void issue_sums(const TreeParams &p, Shared &sh, uint
     for (int g = 0; g < NG; ++g) {
         if (g == 1 && !two) break;
         const uint64_t dv = desc_sw128(smem_u32(smem + L::oV) + (vb * NG + g) * L::kVBytes, kTile * 128);
-#pragma unroll 2
+#pragma unroll 1
         for (int k = 0; k < 8; ++k)  // 16 cache rows: two atoms
             mma_ss(tmem + L::cO + g * N, dv + (uint64_t)(k * 2048 >> 4), dp + (uint64_t)(k * 2048 >> 4), idesc_f16(128, N, 1, 1),
                    !first || k);
@@ -670,13 +674,13 @@ __device__ __forceinline__ void load_quarter(uint32_t codes, int row, int h, uin
 
 // 32 codes in words c as 16 fp16 pairs in their order, from the table at `tab` (plus this lane's place in a row).
 template <int N, int W>
-__device__ __forceinline__ void lookup_quarter(const uint32_t *c, uint32_t tab, uint32_t (&r)[16]) {
+__device__ __forceinline__ void lookup_quarter(const uint32_t (&c)[W], uint32_t tab, uint32_t (&r)[16]) {
     if (W == 2 && wide_two(N)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t x = c[j / 4];
             const int s = 8 * (j & 3) - 7;
-            const uint32_t a = tab + ((s < 0 ? x << 7 : x >> (s < 0 ? 0 : s)) & 0x7F80u);
+            const uint32_t a = tab | ((s < 0 ? x << 7 : x >> (s < 0 ? 0 : s)) & 0x7F80u);
             asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(r[2 * j]), "=r"(r[2 * j + 1]) : "r"(a));
         }
     } else {
@@ -686,43 +690,47 @@ __device__ __forceinline__ void lookup_quarter(const uint32_t *c, uint32_t tab, 
         for (int j = 0; j < 16; ++j) {
             const int at = kBits * j, w = at / 32, s = at % 32;  // the pair's bits: from bit s of word w
             uint32_t x;
-            if (s + kBits > 32) x = __funnelshift_r(c[w], c[w + 1], s) << 7;
+            if (s + kBits > 32) x = __funnelshift_r(c[w], c[w + 1 < W ? w + 1 : w], s) << 7;
             else x = s < 7 ? c[w] << (7 - s) : c[w] >> (s - 7);
-            asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(r[j]) : "r"(tab + (x & kMask)));
+            asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(r[j]) : "r"(tab | (x & kMask)));
         }
     }
 }
 
 // Fills a table (all threads); t: the levels' bytes as in TreeParams.
-__device__ void fill_table(uint8_t *dst, const uint32_t (&t)[8], int w, bool wide) {
+__device__ void fill_table(uint32_t dst, const uint32_t (&t)[8], int w, bool wide) {
     auto level = [&](int q) -> uint32_t {
         const uint32_t lo = t[q >> 2] >> (8 * (q & 3)) & 255u, hi = t[4 + (q >> 2)] >> (8 * (q & 3)) & 255u;
         return lo | hi << 8;
     };
     const int entries = w == 4 || wide ? 256 : w == 3 ? 64 : 16, m = (1 << w) - 1;
+#pragma unroll 1
     for (int i = threadIdx.x; i < entries * 8; i += kThreads) {  // 16 bytes each
         const int e = i >> 3;
         const uint32_t a = level(e & m) | level(e >> w & m) << 16;
         const uint32_t b = wide ? level(e >> (2 * w) & m) | level(e >> (3 * w) & m) << 16 : a;
-        sts128(smem_u32(dst) + i * 16, a, b, a, b);
+        sts128(dst + i * 16, a, b, a, b);
     }
 }
 
-// Expander warps: keys into tensor memory, values into shared memory, and the rows' norms for softmax.
-template <int N, int NG, int W, bool KEYS>
-__device__ __forceinline__ void expand_tile(const TreeParams &p, Shared &sh, uint8_t *smem, uint32_t tmem, uint32_t codes, uint32_t tab, int buf, int row,
-                                            int q, const float (&ratio)[2], const uint32_t (&flip)[2], bool two) {
+// Expander warps: keys into tensor memory, values into shared memory, and the rows' norms for softmax. One code for both sides.
+template <int N, int NG, int W>
+__device__ __forceinline__ void expand_tile(const TreeParams &p, uint8_t *smem, uint32_t tmem, bool keys, uint32_t codes, uint32_t tab, int buf, int row,
+                                            int q, const float (&ratio)[2], uint32_t flip, bool two) {
     using L = Plan<N, NG>;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        if (g == 1 && !two) break;
+#pragma unroll 1
+    for (int g = 0; g < (two ? 2 : 1); ++g) {
         uint32_t t[8];
         if (NG == 2) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) t[j] = KEYS ? p.tk[j] : j < 4 ? p.tv[j] : p.tv[j] ^ flip[g];
+            for (int j = 0; j < 8; ++j) t[j] = keys ? p.tk[j] : j < 4 ? p.tv[j] : p.tv[j] ^ (flip & 0x80808080u);
         }
-        const __half2 r2 = __float2half2_rn(ratio[g]);
+        const __half2 r2 = __float2half2_rn(NG == 2 && g ? ratio[1] : ratio[0]);
+        const bool turned = NG == 1 && __any_sync(0xFFFFFFFFu, flip != 0);
         const uint32_t from = codes + g * W * kTile * 16;
+        const uint32_t to_k = tmem + ((uint32_t)(32 * q) << 16) + L::cK + (buf * NG + g) * 64;
+        // row `row` of the tile: two 64-wide segments of swizzled 16-byte chunks
+        const uint32_t to_v = smem_u32(smem + L::oV) + (buf * NG + g) * L::kVBytes + (row >> 3) * 1024 + (row & 7) * 128;
         uint32_t next[W];
         load_quarter<W>(from, row, 0, next);
 #pragma unroll 1
@@ -733,10 +741,6 @@ __device__ __forceinline__ void expand_tile(const TreeParams &p, Shared &sh, uin
             load_quarter<W>(from, row, min(h + 1, 3), next);
             if (NG == 1) {
                 lookup_quarter<N, W>(c, tab, r);
-                if (!KEYS) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) r[j] ^= flip[0];
-                }
             } else {
                 expand_quarter<W>(c, t, r);
 #pragma unroll
@@ -745,27 +749,20 @@ __device__ __forceinline__ void expand_tile(const TreeParams &p, Shared &sh, uin
                     r[j] = *reinterpret_cast<const uint32_t *>(&x);
                 }
             }
-            if (KEYS) {
-                tmem_st16(tmem + ((uint32_t)(32 * q) << 16) + L::cK + (buf * NG + g) * 64 + h * 16, r);
+            if (keys) {
+                tmem_st16(to_k + h * 16, r);
             } else {
-                // row `row` of the tile: two 64-wide segments of swizzled 16-byte chunks
-                const uint32_t base = smem_u32(smem + L::oV) + (buf * NG + g) * L::kVBytes + (h >> 1) * (kTile * 128) + (row >> 3) * 1024 +
-                                      (row & 7) * 128;
+                const uint32_t base = to_v + (h >> 1) * (kTile * 128);
+                if (NG == 1 && __builtin_expect(turned, 0)) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 16; ++j) r[j] ^= flip;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
                     sts128(base + ((((h & 1) * 4 + j) ^ (row & 7)) << 4), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                }
             }
         }
-    }
-}
-
-template <int N, int NG, bool KEYS>
-__device__ __forceinline__ void expand_any(const TreeParams &p, Shared &sh, uint8_t *smem, uint32_t tmem, uint32_t codes, uint32_t tab, int buf, int row,
-                                           int q, const float (&ratio)[2], const uint32_t (&flip)[2], bool two) {
-    switch (KEYS ? p.wk : p.wv) {
-    case 2: expand_tile<N, NG, 2, KEYS>(p, sh, smem, tmem, codes, tab, buf, row, q, ratio, flip, two); break;
-    case 3: expand_tile<N, NG, 3, KEYS>(p, sh, smem, tmem, codes, tab, buf, row, q, ratio, flip, two); break;
-    default: expand_tile<N, NG, 4, KEYS>(p, sh, smem, tmem, codes, tab, buf, row, q, ratio, flip, two); break;
     }
 }
 
@@ -786,63 +783,70 @@ __device__ __forceinline__ float row_norm(uint32_t info, uint32_t norms, bool tw
     return lost ? __int_as_float(0x7FC00000) : nn;
 }
 
-template <int N, int NG, bool KEYS, bool VALUES>
-__device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, int row, int q, int lane) {
+// Sides side0 .. side0 + sides - 1 (0: keys, 1: values).
+template <int N, int NG>
+__device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, int side0, int sides, int row, int q, int lane) {
     using L = Plan<N, NG>;
     Cursor c = sh.start;
     const int tiles = uniform(c.left);
-    const uint32_t tmem = uniform(sh.tmem), ring = smem_u32(smem) + p.o_ring;
-    auto place = [&](int w) { return w == 2 && wide_two(N) ? (lane & 15) * 8 : lane * 4; };
-    const uint32_t tab_k = smem_u32(smem) + L::oTab + place(p.wk), tab_v = smem_u32(smem) + p.o_tab_v + place(p.wv);
+    const uint32_t tmem = uniform(sh.tmem), ring = smem_u32(smem) + L::oRing;
     int st = 0;
     uint32_t rpar = 0;
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
-        const int b = i & 1, vb = L::kVBuf == 2 ? b : 0;
+        const int b = i & 1;
         const uint32_t par = (uint32_t)(i >> 1) & 1;
-        const bool two_k = NG == 2 && p.unit[c.u].ngk == 2, two_v = NG == 2 && p.unit[c.u].ngv == 2;
-        if (NG == 2) c.advance(p, N);
+        bool two[2] = {false, false};
+        if (NG == 2) {
+            two[0] = p.unit[c.u].ngk == 2, two[1] = p.unit[c.u].ngv == 2;
+            c.advance(p, N);
+        }
+        float ratio[2][2];
+        uint32_t flip = 0;
         wait(sh, &sh.ring_full[st], rpar, p.status, 0x4749000Fu);
-        const uint32_t kc = ring + st * p.stage, vc = kc + Stage<NG>::codes(p.wk), info = vc + Stage<NG>::codes(p.wv);
+        const uint32_t codes = ring + st * p.stage, info = codes + Stage<NG>::codes(p.wk) + Stage<NG>::codes(p.wv);
         const uint32_t nrm = info + Stage<NG>::kInfo;
         wait(sh, &sh.s_empty[b], par ^ 1, p.status, 0x47490001u);
-        float ratio_k[2], ratio_v[2];
-        uint32_t flip[2] = {0, 0};
-        if (KEYS) {
+        if (side0 == 0) {
             const uint32_t word = lds32(info + row * 4);
-            const float n = row_norm<NG>(word, nrm + row * 4, two_k, ratio_k);
+            const float n = row_norm<NG>(word, nrm + row * 4, two[0], ratio[0]);
             sh.scal[b][0][row] = word & 1 ? n : 0.0f;
         }
-        if (VALUES) {
+        if (side0 + sides == 2) {
             const uint32_t word = lds32(info + (kTile + row) * 4);
-            float n = row_norm<NG>(word, nrm + (NG * kTile + row) * 4, two_v, ratio_v);
-            if (NG == 1 || !two_v) {
-                if (n < 0.0f) flip[0] = NG == 1 ? 0x80008000u : 0x80808080u;  // a negative norm turns its levels round
+            float n = row_norm<NG>(word, nrm + (NG * kTile + row) * 4, two[1], ratio[1]);
+            if (!two[1]) {
+                if (n < 0.0f) flip = 0x80008000u;  // a negative norm turns its levels round
+                if (NG == 2) flip |= flip >> 8;    // byte tables: the high bytes' signs
                 n = fabsf(n);
             }
             // a norm of zero counts in the denominator: 2^-40 stands for it, far below the smallest fp16 norm
             const float safe = n == 0.0f ? 0x1p-40f : n;
             const bool lost = !(n <= 65504.0f);
-            sh.scal[b][1][row] = !(word & 1) ? -INFINITY : lost ? __int_as_float(0x7FC00000) : log2f(safe);
-            sh.scal[b][2][row] = (word & 1) && !lost ? 1.0f / safe : 0.0f;
+            sh.scal[b][1][row] = !(word & 1) ? -INFINITY : lost ? __int_as_float(0x7FC00000) : __log2f(safe);
+            sh.scal[b][2][row] = (word & 1) && !lost ? __fdividef(1.0f, safe) : 0.0f;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sc_full[b]);
-        if (KEYS) {
-            wait(sh, &sh.k_empty[b], par ^ 1, p.status, 0x47490002u);
+#pragma unroll 1
+        for (int s = side0; s < side0 + sides; ++s) {
+            const bool keys = s == 0;
+            const int buf = keys || L::kVBuf == 2 ? b : 0, w = keys ? p.wk : p.wv;
+            uint64_t *full = keys ? &sh.k_full[buf] : &sh.v_full[buf];
+            wait(sh, keys ? &sh.k_empty[buf] : &sh.v_empty[buf], (keys || L::kVBuf == 2 ? par : (uint32_t)(i & 1)) ^ 1, p.status, 0x47490002u);
             fence_after();
-            expand_any<N, NG, true>(p, sh, smem, tmem, kc, tab_k, b, row, q, ratio_k, flip, two_k);
+            const uint32_t from = keys ? codes : codes + Stage<NG>::codes(p.wk);
+            const uint32_t tab = (keys ? p.tab_k : p.tab_v) | (w == 2 && wide_two(N) ? (lane & 15) * 8 : lane * 4);
+            const float rt[2] = {keys ? ratio[0][0] : ratio[1][0], keys ? ratio[0][1] : ratio[1][1]};
+            const bool tw = keys ? two[0] : two[1];
+            if (w == 2) expand_tile<N, NG, 2>(p, smem, tmem, keys, from, tab, buf, row, q, rt, flip, tw);
+            else if (w == 3) expand_tile<N, NG, 3>(p, smem, tmem, keys, from, tab, buf, row, q, rt, flip, tw);
+            else expand_tile<N, NG, 4>(p, smem, tmem, keys, from, tab, buf, row, q, rt, flip, tw);
             wait_st();
             fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.k_full[b]);
-        }
-        if (VALUES) {
-            wait(sh, &sh.v_empty[vb], (L::kVBuf == 2 ? par : (uint32_t)(i & 1)) ^ 1, p.status, 0x47490003u);
-            expand_any<N, NG, false>(p, sh, smem, tmem, vc, tab_v, vb, row, q, ratio_v, flip, two_v);
             fence_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.v_full[vb]);
+            if (lane == 0) mbar_arrive(full);
         }
         if (lane == 0) mbar_arrive(&sh.ring_empty[st]);
         if (++st == p.depth) st = 0, rpar ^= 1;
@@ -869,7 +873,8 @@ __device__ __forceinline__ float load_q(const TreeParams &p, int64_t at) {
 }
 
 // Rotated queries of an item's columns into shared memory (the K-major B operand), scaled by one power of two so that
-// fp16 holds them whatever their size (a coordinate is at most the sum of the query's magnitudes); returns what takes the
+// fp16 holds them whatever their size (a coordinate is at most the sum of the query's magnitudes, and that at most 8 or 64
+// times a lane's largest share of it); returns what takes the
 // scale back out of the logits.
 template <int N, int NG>
 __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, const Cursor &c, int warp, int lane) {
@@ -884,27 +889,91 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[j] = d0 + j >= 0 && d0 + j < p.dk ? load_q(p, src + d0 + j) : 0.0f;
     };
-    float top = 0.0f;
-#pragma unroll 2
-    for (int col = warp; col < cols; col += L::kSoft) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            if (g >= u.ngk) break;
-            float z[4];
-            load(col, g, z);
-            sum += (fabsf(z[0]) + fabsf(z[1])) + (fabsf(z[2]) + fabsf(z[3]));
+    // Eight lanes to a column, 16 elements each, where runs of 16 lie in one head and on 16-byte boundaries; else a
+    // warp to a column.
+    const int sub = lane & 7, slot = warp * 4 + (lane >> 3);
+    auto load16 = [&](int col, float (&z)[16]) {
+        const int at = c.c * N + col, node = at / rows, r = at - node * rows, h = u.h0 + r / p.per;
+        const int d0 = u.gk * kGroup + 16 * sub - h * p.dk;
+        const int64_t src = (int64_t)(c.first + node) * p.t.q_stride_t + (int64_t)(u.h0 * p.per + r) * p.t.q_stride_h + d0;
+        uint4 v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        if (col < cols && d0 >= 0 && d0 < p.dk) {
+            const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.t.q) + src);
+            v[0] = from[0], v[1] = from[1];
         }
+        const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (sum <= 3e38f) top = fmaxf(top, sum);  // a column that is not finite does not scale the others
+        for (int j = 0; j < 8; ++j) {
+            if (p.t.dtype == CQ_T_F16) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+                z[2 * j] = x.x, z[2 * j + 1] = x.y;
+            } else {
+                z[2 * j] = __uint_as_float(w[j] << 16), z[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        }
+    };
+    const bool fast = NG == 1 && p.vec_q;
+    float top = 0.0f;
+    if (fast) {
+#pragma unroll 1
+        for (int col = slot; col < cols; col += 4 * L::kSoft) {
+            float z[16], sum = 0.0f;
+            load16(col, z);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum += fabsf(z[j]);
+            if (sum <= 1e36f) top = fmaxf(top, 8.0f * sum);  // what is not finite does not scale the others
+        }
+    } else {
+#pragma unroll 1
+        for (int col = warp; col < cols; col += L::kSoft) {
+            for (int g = 0; g < u.ngk; ++g) {
+                float z[4];
+                load(col, g, z);
+                const float sum = (fabsf(z[0]) + fabsf(z[1])) + (fabsf(z[2]) + fabsf(z[3]));
+                if (sum <= 1e36f) top = fmaxf(top, 64.0f * sum);
+            }
+        }
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     if (lane == 0) atomicMax(&sh.zmax, __float_as_int(top));
     bar_sync(1, 32 * L::kSoft);
-    // the largest sum between 2^14 and 2^15; the exponent is held where both powers of two are normal
+    // the bound between 2^14 and 2^15; the exponent is held where both powers of two are normal
     const int ex = max(-110, min(110, ((sh.zmax >> 23) & 255) - 127 - 14));
     const float down = __int_as_float((127 - ex) << 23);
-#pragma unroll 2
+    if (fast) {
+#pragma unroll 1
+        for (int col = slot; col < N; col += 4 * L::kSoft) {
+            float z[16];
+            load16(col, z);
+#pragma unroll
+            for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (!(j & h)) {
+                        const float x = z[j], y = z[j + h];
+                        z[j] = x + y, z[j + h] = x - y;
+                    }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float y = __shfl_xor_sync(0xFFFFFFFFu, z[j], o);
+                    z[j] = (sub & o) ? y - z[j] : z[j] + y;
+                }
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const __half2 v = __floats2half2_rn(z[2 * j] * down, z[2 * j + 1] * down);
+                w[j] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+            const uint32_t base = smem_u32(smem + L::oZ) + (sub >> 2) * (N * 128) + (col >> 3) * 1024 + (col & 7) * 128;
+            sts128(base + (((2 * (sub & 3)) ^ (col & 7)) << 4), w[0], w[1], w[2], w[3]);
+            sts128(base + (((2 * (sub & 3) + 1) ^ (col & 7)) << 4), w[4], w[5], w[6], w[7]);
+        }
+        return p.k_mult * __int_as_float((127 + ex) << 23);
+    }
+#pragma unroll 1
     for (int col = warp; col < N; col += L::kSoft) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -1075,7 +1144,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
                         f2_get(f2_add(f2_fma(f2(d[k], d[k + 1]), nk2, ln2), f2(m.x, m.y)), d[k], d[k + 1]);
                         f2_get(f2_add(f2_fma(f2(d[k + 2], d[k + 3]), nk2, ln2), f2(m.z, m.w)), d[k + 2], d[k + 3]);
                     }
-                    if (masked) {
+                    if (__builtin_expect(masked, 0)) {
 #pragma unroll
                         for (int k = 0; k < X; ++k) d[k] = see[hf / 32] >> k & 1 ? d[k] : -INFINITY;
                     }
@@ -1084,7 +1153,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
                     if (!bar_or(2 + wg, 128, top > kRaise) || pass) break;
                     raised = raise<N, X>(sh, ts, cx, nk, ln, masked ? see[hf / 32] : 0xFFFFFFFFu, warp, lane);
                 }
-                if (raised) {
+                if (__builtin_expect(raised, 0)) {
 #pragma unroll
                     for (int k = 0; k < X; k += 2) {
                         const float2 f = *reinterpret_cast<const float2 *>(&sh.f[cx + k]);
@@ -1174,11 +1243,14 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
 template <int N, int NG>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
     using L = Plan<N, NG>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     Shared &sh = *reinterpret_cast<Shared *>(smem + L::oShared);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (smem_u32(smem) != kSmemFirst) {  // the tables' addresses count on it
+        if (tid == 0) atomicOr(p.status, 0x47490010u);
+        return;
+    }
     if (tid == 0) {
         sh.abort = 0;
         sh.bad = 0;
@@ -1203,8 +1275,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (NG == 1) {
-        fill_table(smem + L::oTab, p.tk, p.wk, p.wk == 2 && wide_two(N));
-        if (p.o_tab_v != L::oTab) fill_table(smem + p.o_tab_v, p.tv, p.wv, p.wv == 2 && wide_two(N));
+        fill_table(p.tab_k, p.tk, p.wk, p.wk == 2 && wide_two(N));
+        if (p.tab_v != p.tab_k) fill_table(p.tab_v, p.tv, p.wv, p.wv == 2 && wide_two(N));
     }
     __syncthreads();
     const bool work = find_run<N>(p, sh);  // uniform
@@ -1224,9 +1296,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     } else if (warp < L::kSoft + L::kExp) {
         if (L::kSoftWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kExpRegs));
         const int row = 32 * (warp & 3) + lane;
-        if (L::kExpWG == 1) expand_role<N, NG, true, true>(p, sh, smem, row, warp & 3, lane);
-        else if (warp < L::kSoft + 4) expand_role<N, NG, true, false>(p, sh, smem, row, warp & 3, lane);
-        else expand_role<N, NG, false, true>(p, sh, smem, row, warp & 3, lane);
+        const int side0 = L::kExpWG == 1 || warp < L::kSoft + 4 ? 0 : 1;
+        expand_role<N, NG>(p, sh, smem, side0, L::kExpWG == 1 ? 2 : 1, row, warp & 3, lane);
     } else {
         if (L::kSoftWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kRestRegs));
         if (warp == 12) issue_role<N, NG>(p, sh, smem);
@@ -1323,6 +1394,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------------- host --
+// Level tables at the top, the larger one first; the ring has what is left behind the fixed part. Its stages, or 0 where fewer
+// than two fit.
+template <int N, int NG>
+int lay_out(int wk, int wv, bool same, uint32_t &tab_k, uint32_t &tab_v) {
+    int end = kSmemLast;
+    tab_k = tab_v = 0;
+    if (NG == 1) {
+        auto place = [&](int w, int top) { return top - table_bytes(w, N) & -table_bytes(w, N); };
+        const bool k_first = table_bytes(wk, N) >= table_bytes(wv, N);
+        const int a = place(k_first ? wk : wv, kTabTop), b = same ? a : place(k_first ? wv : wk, a);
+        tab_k = k_first ? a : b;
+        tab_v = k_first ? b : a;
+        end = b;
+    }
+    const int depth = std::min(kMaxDepth, (end - kSmemFirst - Plan<N, NG>::oRing) / Stage<NG>::bytes(wk, wv));
+    return depth >= 2 ? depth : 0;
+}
+
 struct Shape {
     int n_units, ng, rows, N, ncol_max;
     size_t slots, items;
@@ -1344,10 +1433,8 @@ Shape shape_of(const cq_kv_geom &g, int n_seqs, int max_nodes, TreeUnit *u) {
     if (s.ng == 2 && s.N == 32) s.N = 64;
     // 128 columns leave room for one large level table, or for two where a stage of codes is small
     const bool same = g.k_bits == g.v_bits && std::equal(g.k_codebook, g.k_codebook + levels_of(g.k_bits), g.v_codebook);
-    const int wk = width_of(g.k_bits), wv = width_of(g.v_bits);
-    if (s.N == 128 && Plan<128, 1>::oTab + table_bytes(wk, 128) + (same ? 0 : table_bytes(wv, 128)) + 2 * Stage<1>::bytes(wk, wv) >
-                          Plan<128, 1>::kLimit)
-        s.N = 64;
+    uint32_t tk, tv;
+    if (s.N == 128 && !lay_out<128, 1>(width_of(g.k_bits), width_of(g.v_bits), same, tk, tv)) s.N = 64;
     s.ncol_max = std::max(1, (most + s.N - 1) / s.N);
     s.items = (size_t)n_seqs * s.n_units * s.ncol_max;
     s.slots = s.items + sm_count();
@@ -1372,32 +1459,14 @@ float byte_table(const float *lv, uint32_t *t) {
     return std::ldexp(1.0f, e);
 }
 
-// Shared memory behind the fixed part: level tables, then as many ring stages as fit. False if fewer than two do.
-template <int N, int NG>
-bool lay_out(TreeParams &p) {
-    using L = Plan<N, NG>;
-    int at = L::oTab;
-    p.o_tab_v = at;
-    if (NG == 1) {
-        const bool same = p.wk == p.wv && std::equal(p.tk, p.tk + 8, p.tv);
-        at += table_bytes(p.wk, N);
-        if (!same) {
-            p.o_tab_v = at;
-            at += table_bytes(p.wv, N);
-        }
-    }
-    p.o_ring = at;
-    p.stage = Stage<NG>::bytes(p.wk, p.wv);
-    p.depth = std::min(kMaxDepth, (L::kLimit - at) / p.stage);
-    return p.depth >= 2;
-}
-
 template <int N, int NG>
 int launch_main(TreeParams &p, cudaStream_t st) {
-    if (!lay_out<N, NG>(p)) return set_error(CQ_ERR_SHAPE, "no room for the level tables");
-    const int rc = ensure_smem(reinterpret_cast<const void *>(tree_kernel<N, NG>), Plan<N, NG>::kLimit + 1024);
+    p.stage = Stage<NG>::bytes(p.wk, p.wv);
+    p.depth = lay_out<N, NG>(p.wk, p.wv, p.wk == p.wv && std::equal(p.tk, p.tk + 8, p.tv), p.tab_k, p.tab_v);
+    if (!p.depth) return set_error(CQ_ERR_SHAPE, "no room for the level tables");
+    const int rc = ensure_smem(reinterpret_cast<const void *>(tree_kernel<N, NG>), kSmemLast - kSmemFirst);
     if (rc) return rc;
-    tree_kernel<N, NG><<<p.grid, kThreads, p.o_ring + p.depth * p.stage + 1024, st>>>(p);
+    tree_kernel<N, NG><<<p.grid, kThreads, kSmemLast - kSmemFirst, st>>>(p);
     return CQ_OK;
 }
 
@@ -1420,6 +1489,7 @@ int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float 
     p.hq = g.n_q_heads, p.per = g.n_q_heads / g.n_kv_heads, p.dk = g.head_dim_k, p.dv = g.head_dim_v;
     p.wk = width_of(g.k_bits), p.wv = width_of(g.v_bits);
     p.kgroups = in_padded(g.n_kv_heads * p.dk) / kGroup, p.vgroups = in_padded(g.n_kv_heads * p.dv) / kGroup;
+    p.vec_q = p.dk % 16 == 0 && (reinterpret_cast<uintptr_t>(t.q) & 15) == 0 && t.q_stride_t % 8 == 0 && t.q_stride_h % 8 == 0;
     // t / block_size for t < 2^31: a product with 2^(31 + l) / block_size rounded up, 2^l >= block_size
     int l = 0;
     while (l < 31 && (1u << l) < (unsigned)t.block_size) ++l;
