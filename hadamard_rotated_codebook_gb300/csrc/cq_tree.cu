@@ -24,10 +24,9 @@
 // lengths are read on the device, and the longest request cannot hold the launch up. Each run leaves
 // unrotated partial sums; a second kernel joins them, rotates and writes o.
 //
-// Roles of the 16 warps. Softmax: one or two warpgroups (N of 64 and more), each with its share of the columns; they
-// also rotate the queries and write the partials. Expansion: a thread per cache row turns its codes into fp16 levels, keys
-// into TMEM (the A operand) and values into shared memory, in two warpgroups where the columns are few and
-// in one where softmax needs the registers. One warp issues the MMAs, two fetch codes, norms and block numbers
+// Roles of the 16 or 20 warps. Softmax: one or two warpgroups (N of 64 and more), each with its share of the columns; they
+// also rotate the queries and write the partials. Expansion: a warpgroup each for keys and values, in which a thread turns its
+// cache row's codes into fp16 levels, keys into TMEM (the A operand) and values into shared memory. One warp issues the MMAs, two fetch codes, norms and block numbers
 // into a ring some tiles ahead.
 // Every wait is bounded: when one gives up, the flag s_abort makes all later waits return at once and every role
 // runs through its remaining tiles without waiting, so that the block's barriers stay matched.
@@ -45,7 +44,7 @@ namespace cq {
 namespace {
 
 constexpr int kTile = 128;        // cache rows per tile
-constexpr int kThreads = 512;
+constexpr int kMaxThreads = 640;
 constexpr int kMaxDepth = 8;      // stages of the ring of codes
 constexpr unsigned kSpin = 1u << 20;   // polls of up to ~1 us
 constexpr float kNoMax = -1e30f;       // reference of a column that has attended nothing yet
@@ -304,8 +303,8 @@ struct Shared {
     int zmax;
     int bad;
     long long total, w0;          // all tiles; this block's first one
-    long long scan_t[kThreads / 32];
-    long long scan_i[kThreads / 32];
+    long long scan_t[kMaxThreads / 32];
+    long long scan_i[kMaxThreads / 32];
     Cursor start;
     float scal[2][3][kTile];      // per tile buffer: n_k, log2 n_v, 1 / n_v
     alignas(16) float minus_m[128];  // column references, negated (read four at a time)
@@ -327,7 +326,7 @@ __device__ __forceinline__ void wait(Shared &sh, uint64_t *bar, uint32_t parity,
 }
 
 // Fills sh.start with this block's first tile and sh.total; false if it has none.
-template <int N>
+template <int N, int kThreads>
 __device__ bool find_run(const TreeParams &p, Shared &sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kW = kThreads / 32;
@@ -446,16 +445,17 @@ __device__ __forceinline__ void expand_quarter(const uint32_t *c, const uint32_t
 // ---------------------------------------------------------------- the kernel --
 template <int N, int NG>
 struct Plan {
-    static constexpr int kSoftWG = N >= 64 ? 2 : 1, kExpWG = 3 - kSoftWG;  // warpgroups
-    static constexpr int kSoft = 4 * kSoftWG, kExp = 4 * kExpWG;            // warps; then the issuer, two fetchers, one idle
+    static constexpr int kSoftWG = N >= 64 ? 2 : 1;              // warpgroups of softmax
+    static constexpr int kSoft = 4 * kSoftWG, kExp = 8;         // warps; then the issuer, two fetchers, one idle
+    static constexpr int kThreads = 32 * (kSoft + kExp + 4);
     static constexpr int kVBuf = NG == 1 ? 2 : 1;
     static constexpr int kVBytes = 2 * kTile * 128;            // one group's values: 128 rows x 128 fp16
     static constexpr int kPBytes = kTile * (N <= 64 ? 128 : 256);
     static constexpr int kZBytes = N * 256;                    // one group
     static constexpr int oV = 0, oP = oV + kVBuf * NG * kVBytes, oZ = oP + kPBytes, oShared = oZ + NG * kZBytes;
     static constexpr int oRing = oShared + ((int)sizeof(Shared) + 127) / 128 * 128;
-    // registers of the roles where softmax takes two warpgroups: 256 kSoftRegs + 128 (kExpRegs + kRestRegs) = 512 x 128
-    static constexpr int kSoftRegs = 168, kExpRegs = 104, kRestRegs = 72;
+    // registers of the roles where softmax takes two warpgroups: 256 (kSoftRegs + kExpRegs) + 128 kRestRegs <= 640 x 96
+    static constexpr int kSoftRegs = N == 128 ? 144 : 128, kExpRegs = N == 128 ? 64 : 72, kRestRegs = N == 128 ? 64 : 80;
     // TMEM columns
     static constexpr int cK = 0, cS = 2 * NG * 64, cO = cS + 2 * N;
     static_assert(cO + NG * N <= 512, "tensor memory");
@@ -681,7 +681,7 @@ __device__ __forceinline__ void lookup_quarter(const uint32_t (&c)[W], uint32_t 
             const uint32_t x = c[j / 4];
             const int s = 8 * (j & 3) - 7;
             const uint32_t a = tab | ((s < 0 ? x << 7 : x >> (s < 0 ? 0 : s)) & 0x7F80u);
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(r[2 * j]), "=r"(r[2 * j + 1]) : "r"(a));
+            asm("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(r[2 * j]), "=r"(r[2 * j + 1]) : "r"(a));
         }
     } else {
         constexpr int kBits = 2 * W;
@@ -692,7 +692,7 @@ __device__ __forceinline__ void lookup_quarter(const uint32_t (&c)[W], uint32_t 
             uint32_t x;
             if (s + kBits > 32) x = __funnelshift_r(c[w], c[w + 1 < W ? w + 1 : w], s) << 7;
             else x = s < 7 ? c[w] << (7 - s) : c[w] >> (s - 7);
-            asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(r[j]) : "r"(tab | (x & kMask)));
+            asm("ld.shared.u32 %0, [%1];\n" : "=r"(r[j]) : "r"(tab | (x & kMask)));  // the tables never change
         }
     }
 }
@@ -705,7 +705,7 @@ __device__ void fill_table(uint32_t dst, const uint32_t (&t)[8], int w, bool wid
     };
     const int entries = w == 4 || wide ? 256 : w == 3 ? 64 : 16, m = (1 << w) - 1;
 #pragma unroll 1
-    for (int i = threadIdx.x; i < entries * 8; i += kThreads) {  // 16 bytes each
+    for (int i = threadIdx.x; i < entries * 8; i += blockDim.x) {  // 16 bytes each
         const int e = i >> 3;
         const uint32_t a = level(e & m) | level(e >> w & m) << 16;
         const uint32_t b = wide ? level(e >> (2 * w) & m) | level(e >> (3 * w) & m) << 16 : a;
@@ -733,7 +733,7 @@ __device__ __forceinline__ void expand_tile(const TreeParams &p, uint8_t *smem, 
         const uint32_t to_v = smem_u32(smem + L::oV) + (buf * NG + g) * L::kVBytes + (row >> 3) * 1024 + (row & 7) * 128;
         uint32_t next[W];
         load_quarter<W>(from, row, 0, next);
-#pragma unroll 1
+#pragma unroll
         for (int h = 0; h < 4; ++h) {
             uint32_t r[16], c[W];
 #pragma unroll
@@ -783,72 +783,65 @@ __device__ __forceinline__ float row_norm(uint32_t info, uint32_t norms, bool tw
     return lost ? __int_as_float(0x7FC00000) : nn;
 }
 
-// Sides side0 .. side0 + sides - 1 (0: keys, 1: values).
 template <int N, int NG>
-__device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, int side0, int sides, int row, int q, int lane) {
+__device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, bool keys, int row, int q, int lane) {
     using L = Plan<N, NG>;
     Cursor c = sh.start;
-    const int tiles = uniform(c.left);
+    const int tiles = uniform(c.left), w = keys ? p.wk : p.wv;
     const uint32_t tmem = uniform(sh.tmem), ring = smem_u32(smem) + L::oRing;
+    const uint32_t tab = (keys ? p.tab_k : p.tab_v) | (w == 2 && wide_two(N) ? (lane & 15) * 8 : lane * 4);
     int st = 0;
     uint32_t rpar = 0;
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
-        const int b = i & 1;
+        const int b = i & 1, buf = keys || L::kVBuf == 2 ? b : 0;
         const uint32_t par = (uint32_t)(i >> 1) & 1;
-        bool two[2] = {false, false};
+        bool two = false;
         if (NG == 2) {
-            two[0] = p.unit[c.u].ngk == 2, two[1] = p.unit[c.u].ngv == 2;
+            two = (keys ? p.unit[c.u].ngk : p.unit[c.u].ngv) == 2;
             c.advance(p, N);
         }
-        float ratio[2][2];
+        float ratio[2];
         uint32_t flip = 0;
+        const uint32_t codes = ring + st * p.stage, info = codes + Stage<NG>::codes(p.wk) + Stage<NG>::codes(p.wv) + (keys ? 0 : kTile * 4);
+        const uint32_t nrm = info + Stage<NG>::kInfo + (keys ? 0 : (NG - 1) * kTile * 4);
         wait(sh, &sh.ring_full[st], rpar, p.status, 0x4749000Fu);
-        const uint32_t codes = ring + st * p.stage, info = codes + Stage<NG>::codes(p.wk) + Stage<NG>::codes(p.wv);
-        const uint32_t nrm = info + Stage<NG>::kInfo;
-        wait(sh, &sh.s_empty[b], par ^ 1, p.status, 0x47490001u);
-        if (side0 == 0) {
-            const uint32_t word = lds32(info + row * 4);
-            const float n = row_norm<NG>(word, nrm + row * 4, two[0], ratio[0]);
-            sh.scal[b][0][row] = word & 1 ? n : 0.0f;
-        }
-        if (side0 + sides == 2) {
-            const uint32_t word = lds32(info + (kTile + row) * 4);
-            float n = row_norm<NG>(word, nrm + (NG * kTile + row) * 4, two[1], ratio[1]);
-            if (!two[1]) {
+        const uint32_t word = lds32(info + row * 4);
+        float n = row_norm<NG>(word, nrm + row * 4, two, ratio);
+        if (!keys) {
+            if (!two) {
                 if (n < 0.0f) flip = 0x80008000u;  // a negative norm turns its levels round
                 if (NG == 2) flip |= flip >> 8;    // byte tables: the high bytes' signs
                 n = fabsf(n);
             }
-            // a norm of zero counts in the denominator: 2^-40 stands for it, far below the smallest fp16 norm
-            const float safe = n == 0.0f ? 0x1p-40f : n;
-            const bool lost = !(n <= 65504.0f);
-            sh.scal[b][1][row] = !(word & 1) ? -INFINITY : lost ? __int_as_float(0x7FC00000) : __log2f(safe);
-            sh.scal[b][2][row] = (word & 1) && !lost ? __fdividef(1.0f, safe) : 0.0f;
+        }
+        // a norm of zero counts in the denominator: 2^-40 stands for it, far below the smallest fp16 norm
+        const float safe = n == 0.0f ? 0x1p-40f : n;
+        const bool lost = !(n <= 65504.0f), real = word & 1;
+        const float ln = lost ? __int_as_float(0x7FC00000) : __log2f(safe), inv = lost ? 0.0f : __fdividef(1.0f, safe);
+        wait(sh, &sh.s_empty[b], par ^ 1, p.status, 0x47490001u);
+        if (keys) {
+            sh.scal[b][0][row] = real ? n : 0.0f;
+        } else {
+            sh.scal[b][1][row] = real ? ln : -INFINITY;
+            sh.scal[b][2][row] = real ? inv : 0.0f;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sc_full[b]);
-#pragma unroll 1
-        for (int s = side0; s < side0 + sides; ++s) {
-            const bool keys = s == 0;
-            const int buf = keys || L::kVBuf == 2 ? b : 0, w = keys ? p.wk : p.wv;
-            uint64_t *full = keys ? &sh.k_full[buf] : &sh.v_full[buf];
-            wait(sh, keys ? &sh.k_empty[buf] : &sh.v_empty[buf], (keys || L::kVBuf == 2 ? par : (uint32_t)(i & 1)) ^ 1, p.status, 0x47490002u);
-            fence_after();
-            const uint32_t from = keys ? codes : codes + Stage<NG>::codes(p.wk);
-            const uint32_t tab = (keys ? p.tab_k : p.tab_v) | (w == 2 && wide_two(N) ? (lane & 15) * 8 : lane * 4);
-            const float rt[2] = {keys ? ratio[0][0] : ratio[1][0], keys ? ratio[0][1] : ratio[1][1]};
-            const bool tw = keys ? two[0] : two[1];
-            if (w == 2) expand_tile<N, NG, 2>(p, smem, tmem, keys, from, tab, buf, row, q, rt, flip, tw);
-            else if (w == 3) expand_tile<N, NG, 3>(p, smem, tmem, keys, from, tab, buf, row, q, rt, flip, tw);
-            else expand_tile<N, NG, 4>(p, smem, tmem, keys, from, tab, buf, row, q, rt, flip, tw);
-            wait_st();
-            fence_before();
-            fence_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full);
+        wait(sh, keys ? &sh.k_empty[buf] : &sh.v_empty[buf], (keys || L::kVBuf == 2 ? par : (uint32_t)(i & 1)) ^ 1, p.status, 0x47490002u);
+        fence_after();
+        const uint32_t from = keys ? codes : codes + Stage<NG>::codes(p.wk);
+        if (w == 2) expand_tile<N, NG, 2>(p, smem, tmem, keys, from, tab, buf, row, q, ratio, flip, two);
+        else if (w == 3) expand_tile<N, NG, 3>(p, smem, tmem, keys, from, tab, buf, row, q, ratio, flip, two);
+        else expand_tile<N, NG, 4>(p, smem, tmem, keys, from, tab, buf, row, q, ratio, flip, two);
+        wait_st();
+        fence_before();
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(keys ? &sh.k_full[buf] : &sh.v_full[buf]);
+            mbar_arrive(&sh.ring_empty[st]);
         }
-        if (lane == 0) mbar_arrive(&sh.ring_empty[st]);
         if (++st == p.depth) st = 0, rpar ^= 1;
     }
 }
@@ -1241,9 +1234,10 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
 }
 
 template <int N, int NG>
-__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(Plan<N, NG>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
     using L = Plan<N, NG>;
     extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr int kIssuer = L::kSoft + L::kExp;
     Shared &sh = *reinterpret_cast<Shared *>(smem + L::oShared);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -1279,10 +1273,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (p.tab_v != p.tab_k) fill_table(p.tab_v, p.tv, p.wv, p.wv == 2 && wide_two(N));
     }
     __syncthreads();
-    const bool work = find_run<N>(p, sh);  // uniform
+    const bool work = find_run<N, L::kThreads>(p, sh);  // uniform
     if (blockIdx.x == 0 && tid == 0 && sh.bad) atomicOr(p.status, kStatusIndex);
     if (!work) return;
-    if (warp == 12) {
+    if (warp == kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sh.tmem)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
     }
@@ -1296,16 +1290,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     } else if (warp < L::kSoft + L::kExp) {
         if (L::kSoftWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kExpRegs));
         const int row = 32 * (warp & 3) + lane;
-        const int side0 = L::kExpWG == 1 || warp < L::kSoft + 4 ? 0 : 1;
-        expand_role<N, NG>(p, sh, smem, side0, L::kExpWG == 1 ? 2 : 1, row, warp & 3, lane);
+        expand_role<N, NG>(p, sh, smem, warp < L::kSoft + 4, row, warp & 3, lane);
     } else {
         if (L::kSoftWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kRestRegs));
-        if (warp == 12) issue_role<N, NG>(p, sh, smem);
-        else if (warp < 15) fetch_role<N, NG>(p, sh, smem, tid - 13 * 32);
+        if (warp == kIssuer) issue_role<N, NG>(p, sh, smem);
+        else if (warp < kIssuer + 3) fetch_role<N, NG>(p, sh, smem, tid - 32 * (kIssuer + 1));
     }
     fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kIssuer) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(sh.tmem), "r"(512));
     }
@@ -1466,7 +1459,7 @@ int launch_main(TreeParams &p, cudaStream_t st) {
     if (!p.depth) return set_error(CQ_ERR_SHAPE, "no room for the level tables");
     const int rc = ensure_smem(reinterpret_cast<const void *>(tree_kernel<N, NG>), kSmemLast - kSmemFirst);
     if (rc) return rc;
-    tree_kernel<N, NG><<<p.grid, kThreads, kSmemLast - kSmemFirst, st>>>(p);
+    tree_kernel<N, NG><<<p.grid, Plan<N, NG>::kThreads, kSmemLast - kSmemFirst, st>>>(p);
     return CQ_OK;
 }
 
