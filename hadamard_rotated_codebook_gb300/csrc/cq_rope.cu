@@ -3,7 +3,7 @@
 //   y = x / sqrt(mean(x^2) + eps) * (offset + w);   (y_a, y_b) rotated by t = position * inv_freq[pair]
 //
 // A head vector is a set of head_dim/2 pairs (a, b). A group of G lanes (a
-// power of two, 4 pairs a lane) owns one head: a lane keeps the pairs it
+// power of two; a lane has 4 pairs, or 8 of a 16-bit type: 16-byte loads) owns one head: a lane keeps the pairs it
 // rotates in registers, so the norm is one shuffle reduction over the group and the
 // rotation needs no exchange at all. The pairs of a lane are the same for every
 // head, and a warp takes several heads of one token, so each angle is
@@ -30,8 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPairs = 4;  // pairs a lane owns
-constexpr int kBatch = 4;  // heads in flight per lane group
+constexpr int kBatch = 4;   // heads in flight per lane group
 
 struct RopeParams {
     const void *q, *k;
@@ -48,21 +47,20 @@ struct RopeParams {
     uint64_t rates[128];
 };
 
-template <typename T> struct Vec4;
-template <> struct Vec4<float> { using V = float4; };
-template <> struct Vec4<__half> { using V = uint2; };
-template <> struct Vec4<__nv_bfloat16> { using V = uint2; };
-
-__device__ __forceinline__ void unpack(float4 v, float *x, const float *) {
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+// N consecutive elements as registers: N * sizeof(T) bytes, 8 or 16.
+template <int BYTES> struct Raw;
+template <> struct Raw<8> { using V = uint2; };
+template <> struct Raw<16> { using V = uint4; };
+__device__ __forceinline__ float to_f32(uint32_t v, int half, const __half *) {
+    return __half2float(__ushort_as_half((unsigned short)(half ? v >> 16 : v)));
 }
-__device__ __forceinline__ void unpack(uint2 v, float *x, const __half *) {
-    const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&v.x)), b = __half22float2(*reinterpret_cast<__half2 *>(&v.y));
-    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
-}
-__device__ __forceinline__ void unpack(uint2 v, float *x, const __nv_bfloat16 *) {
-    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+__device__ __forceinline__ float to_f32(uint32_t v, int half, const __nv_bfloat16 *) { return __uint_as_float(half ? v & 0xFFFF0000u : v << 16); }
+__device__ __forceinline__ float to_f32(uint32_t v, int, const float *) { return __uint_as_float(v); }
+template <typename T, int N, typename V>
+__device__ __forceinline__ void unpack(const V &v, float *x) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(&v);
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = sizeof(T) == 4 ? to_f32(w[j], 0, (const T *)nullptr) : to_f32(w[j / 2], j & 1, (const T *)nullptr);
 }
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -73,18 +71,28 @@ __device__ __forceinline__ void store1(void *base, int64_t off, int type, float 
     else if (type == CQ_T_F16) static_cast<__half *>(base)[off] = __float2half_rn(v);
     else static_cast<__nv_bfloat16 *>(base)[off] = __float2bfloat16_rn(v);
 }
-__device__ __forceinline__ void store4(void *base, int64_t off, int type, const float *v) {
+// N consecutive elements, N * size bytes a multiple of 8.
+template <int N>
+__device__ __forceinline__ void store_run(void *base, int64_t off, int type, const float *v) {
     if (type == CQ_T_F32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(base) + off) = make_float4(v[0], v[1], v[2], v[3]);
-    } else if (type == CQ_T_F16) {
-        const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
-        *reinterpret_cast<uint2 *>(static_cast<__half *>(base) + off) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-    } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(base) + off) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+#pragma unroll
+        for (int j = 0; j < N; j += 4) __stcs(reinterpret_cast<float4 *>(static_cast<float *>(base) + off + j), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+        return;
     }
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+        if (type == CQ_T_F16) {
+            const __half2 a = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t *>(&a);
+        } else {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t *>(&a);
+        }
+    }
+    uint16_t *dst = static_cast<uint16_t *>(base) + off;
+    if (N == 8) __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(w[0], w[1], w[N / 2 - 2], w[N / 2 - 1]));
+    else __stcs(reinterpret_cast<uint2 *>(dst), make_uint2(w[0], w[1]));
 }
 
 // Element offsets of the two members of pair p.
@@ -96,62 +104,65 @@ __device__ __forceinline__ int2 pair_at(int p, int d, int rot, bool il) {
     return make_int2(rot + t, rot + t + ((d - rot) >> 1));
 }
 
-// VEC: every lane's pairs are two aligned runs of four elements (`A` and `B`: of
-// adjacent pairs where IL, else of the first and of the second members).
-template <typename T, bool IL, bool VEC>
+// P pairs a lane. VEC: they are two aligned runs of P elements (`A` and `B`: of adjacent pairs where IL, else of the first and
+// of the second members).
+template <typename T, int P, bool IL, bool VEC>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
-    using V = typename Vec4<T>::V;
+    using V = typename Raw<VEC ? P * (int)sizeof(T) : 16>::V;
     __shared__ uint64_t s_rate[128];
+    __shared__ __align__(16) float s_w[2][256];  // offset + weight of queries and keys
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid < 128) s_rate[tid] = tid < (p.rot >> 1) ? p.rates[tid] : 0;  // a pair past rot_dim turns by zero
+    for (int i = tid; i < 2 * p.d; i += kThreads) {
+        const int k = i >= p.d, e = i - k * p.d;
+        const float *w = k ? p.wk : p.wq;
+        s_w[k][e] = p.offset + (w ? w[e] : 1.0f);
+    }
     __syncthreads();
     const int g = 1 << p.log_g, sub = lane & (g - 1), slot = lane >> p.log_g, slots = 32 >> p.log_g;
-    const int p0 = sub * kPairs, half_d = p.d >> 1;
+    const int p0 = sub * P, half_d = p.d >> 1;
     const bool live = p0 < half_d;
-    int at[2 * kPairs];  // element offsets: pair j is at[j], at[kPairs + j] (VEC: at[0] and at[kPairs] start the runs)
+    int at[2 * P];  // element offsets: pair j is at[j], at[P + j] (VEC: at[0] and at[P] start the runs)
     if (VEC && IL) {
-        at[0] = 2 * p0, at[kPairs] = 2 * p0 + 4;
+        at[0] = 2 * p0, at[P] = 2 * p0 + P;
     } else if (VEC) {
-        const int2 o = pair_at(p0, p.d, p.rot, false);
-        at[0] = o.x, at[kPairs] = o.y;
+        const int2 o = pair_at(min(p0, half_d - P), p.d, p.rot, false);
+        at[0] = o.x, at[P] = o.y;
     } else {
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
+        for (int j = 0; j < P; ++j) {
             const int2 o = pair_at(min(p0 + j, half_d - 1), p.d, p.rot, IL);
-            at[j] = o.x, at[kPairs + j] = o.y;
+            at[j] = o.x, at[P + j] = o.y;
         }
     }
-    // element offset of register x[i]; registers hold first members, then second ones (VEC && IL: the run itself)
-    auto elem = [&](int i) { return VEC ? at[i & kPairs] + (i & (kPairs - 1)) : at[i]; };
+    // registers hold first members, then second ones (VEC && IL: the run itself)
     const long long tasks = (long long)p.tokens * p.chunks;
     for (long long task = (long long)blockIdx.x * kWarps + warp; task < tasks; task += (long long)gridDim.x * kWarps) {
         const int t = (int)(task / p.chunks), c = (int)(task - (long long)t * p.chunks);
-        float cs[kPairs], sn[kPairs];
+        const int h1 = min(p.heads, (c + 1) * p.chunk);
+        float cs[P], sn[P];
         const uint64_t pos = p.rot ? (uint64_t)(int64_t)p.pos[t] : 0;
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
+        for (int j = 0; j < P; ++j) {
             const uint64_t turn = pos * s_rate[min(p0 + j, 127)];
             sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn[j], &cs[j]);
         }
-        const int h1 = min(p.heads, (c + 1) * p.chunk);
         for (int hb = c * p.chunk; hb < h1; hb += kBatch * slots) {
-            float x[kBatch][2 * kPairs];
+            V raw[kBatch][2];
+            float x[2 * P];
+            auto source = [&](int h) {
+                const bool is_q = h < p.hq;
+                return static_cast<const T *>(is_q ? p.q : p.k) + (is_q ? t * p.q_st + h * p.q_sh : t * p.k_st + (h - p.hq) * p.k_sh);
+            };
+            if (VEC) {
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                const int h = hb + b * slots + slot;
-#pragma unroll
-                for (int i = 0; i < 2 * kPairs; ++i) x[b][i] = 0.0f;
-                if (h < h1 && live) {
-                    const bool is_q = h < p.hq;
-                    const T *src = static_cast<const T *>(is_q ? p.q : p.k) +
-                                   (is_q ? t * p.q_st + h * p.q_sh : t * p.k_st + (h - p.hq) * p.k_sh);
-                    if (VEC) {
-                        unpack(*reinterpret_cast<const V *>(src + at[0]), &x[b][0], (const T *)nullptr);
-                        unpack(*reinterpret_cast<const V *>(src + at[kPairs]), &x[b][kPairs], (const T *)nullptr);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kPairs; ++j)
-                            if (p0 + j < half_d) x[b][j] = to_f(src[at[j]]), x[b][kPairs + j] = to_f(src[at[kPairs + j]]);
+                for (int b = 0; b < kBatch; ++b) {
+                    const int h = hb + b * slots + slot;
+                    raw[b][0] = raw[b][1] = V{};
+                    if (h < h1 && live) {
+                        const T *src = source(h);
+                        raw[b][0] = __ldcs(reinterpret_cast<const V *>(src + at[0]));
+                        raw[b][1] = __ldcs(reinterpret_cast<const V *>(src + at[P]));
                     }
                 }
             }
@@ -159,36 +170,48 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
             for (int b = 0; b < kBatch; ++b) {
                 if (hb + b * slots >= h1) break;  // uniform: the shuffles below take all lanes
                 const int h = hb + b * slots + slot;
+                if (VEC) {
+                    unpack<T, P>(raw[b][0], &x[0]);
+                    unpack<T, P>(raw[b][1], &x[P]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2 * P; ++i) x[i] = 0.0f;
+                    if (h < h1 && live) {
+                        const T *src = source(h);
+#pragma unroll
+                        for (int j = 0; j < P; ++j)
+                            if (p0 + j < half_d) x[j] = to_f(src[at[j]]), x[P + j] = to_f(src[at[P + j]]);
+                    }
+                }
                 float s = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 2 * kPairs; ++i) s = fmaf(x[b][i], x[b][i], s);
+                for (int i = 0; i < 2 * P; ++i) s = fmaf(x[i], x[i], s);
                 for (int o = g >> 1; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
                 if (h >= h1 || !live) continue;
                 const bool is_q = h < p.hq;
                 const float inv = rsqrtf(fmaf(s, p.inv_d, p.eps));
-                const float *w = is_q ? p.wq : p.wk;
-                float y[2 * kPairs];
+                const float *w = s_w[!is_q];
 #pragma unroll
-                for (int i = 0; i < 2 * kPairs; ++i) y[i] = x[b][i] * inv * (w ? p.offset + w[elem(i)] : p.offset + 1.0f);
+                for (int i = 0; i < 2 * P; ++i) x[i] = x[i] * inv * w[VEC ? at[i / P * P] + i % P : at[i]];
 #pragma unroll
-                for (int j = 0; j < kPairs; ++j) {
-                    const int a = VEC && IL ? 2 * j : j, e = VEC && IL ? 2 * j + 1 : kPairs + j;
-                    const float u = y[a], v = y[e];
-                    y[a] = u * cs[j] - v * sn[j];
-                    y[e] = v * cs[j] + u * sn[j];
+                for (int j = 0; j < P; ++j) {
+                    const int a = VEC && IL ? 2 * j : j, e = VEC && IL ? 2 * j + 1 : P + j;
+                    const float u = x[a], v = x[e];
+                    x[a] = u * cs[j] - v * sn[j];
+                    x[e] = v * cs[j] + u * sn[j];
                 }
                 void *dst = is_q ? p.qo : p.ko;
                 const int type = is_q ? p.q_type : p.k_type;
                 const int64_t base = is_q ? t * p.qo_st + h * p.qo_sh : t * p.ko_st + (h - p.hq) * p.ko_sh;
                 if (VEC) {
-                    store4(dst, base + at[0], type, &y[0]);
-                    store4(dst, base + at[kPairs], type, &y[kPairs]);
+                    store_run<P>(dst, base + at[0], type, &x[0]);
+                    store_run<P>(dst, base + at[P], type, &x[P]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < kPairs; ++j)
+                    for (int j = 0; j < P; ++j)
                         if (p0 + j < half_d) {
-                            store1(dst, base + at[j], type, y[j]);
-                            store1(dst, base + at[kPairs + j], type, y[kPairs + j]);
+                            store1(dst, base + at[j], type, x[j]);
+                            store1(dst, base + at[P + j], type, x[P + j]);
                         }
                 }
             }
@@ -198,12 +221,17 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
 
 int size_of(int type) { return type == CQ_T_F32 ? 4 : 2; }
 
+template <typename T, int P>
+void launch_p(const RopeParams &p, bool il, bool vec, int grid, cudaStream_t st) {
+    if (il && vec) qk_norm_rope_kernel<T, P, true, true><<<grid, kThreads, 0, st>>>(p);
+    else if (vec) qk_norm_rope_kernel<T, P, false, true><<<grid, kThreads, 0, st>>>(p);
+    else if (il) qk_norm_rope_kernel<T, 4, true, false><<<grid, kThreads, 0, st>>>(p);
+    else qk_norm_rope_kernel<T, 4, false, false><<<grid, kThreads, 0, st>>>(p);
+}
 template <typename T>
-void launch_t(const RopeParams &p, bool il, bool vec, int grid, cudaStream_t st) {
-    if (il && vec) qk_norm_rope_kernel<T, true, true><<<grid, kThreads, 0, st>>>(p);
-    else if (il) qk_norm_rope_kernel<T, true, false><<<grid, kThreads, 0, st>>>(p);
-    else if (vec) qk_norm_rope_kernel<T, false, true><<<grid, kThreads, 0, st>>>(p);
-    else qk_norm_rope_kernel<T, false, false><<<grid, kThreads, 0, st>>>(p);
+void launch_t(const RopeParams &p, int pairs, bool il, bool vec, int grid, cudaStream_t st) {
+    if (sizeof(T) == 2 && pairs == 8) launch_p<T, sizeof(T) == 2 ? 8 : 4>(p, il, vec, grid, st);
+    else launch_p<T, 4>(p, il, vec, grid, st);
 }
 
 }  // namespace
@@ -220,19 +248,25 @@ int launch_qk_norm_rope(const cq_qk_desc &d, void *stream) {
     p.q_type = d.q_out_dtype, p.k_type = d.k_out_dtype;
     p.eps = d.eps, p.offset = d.weight_offset, p.inv_d = 1.0f / (float)d.head_dim;
     for (int i = 0; i < d.rot_dim / 2; ++i) p.rates[i] = d.rates[i];
-    const int lanes = (d.head_dim / 2 + kPairs - 1) / kPairs;
+    // Runs of P elements need every offset of a run to be a multiple of P: 8 of a 16-bit type, else 4, else single elements.
+    const bool il = d.interleaved != 0;
+    auto fits = [&](int P) {
+        bool ok = il ? d.head_dim % (2 * P) == 0 : (d.rot_dim / 2) % P == 0 && (d.head_dim - d.rot_dim) / 2 % P == 0;
+        auto runs = [&](const void *b, int64_t st, int64_t sh, int type, int heads) {
+            const int bytes = std::min(16, P * size_of(type));
+            ok = ok && (!heads || (reinterpret_cast<uintptr_t>(b) % bytes == 0 && st * size_of(type) % bytes == 0 && sh * size_of(type) % bytes == 0));
+        };
+        runs(p.q, p.q_st, p.q_sh, d.in_dtype, d.n_q_heads);
+        runs(p.k, p.k_st, p.k_sh, d.in_dtype, d.n_kv_heads);
+        runs(p.qo, p.qo_st, p.qo_sh, p.q_type, d.n_q_heads);
+        runs(p.ko, p.ko_st, p.ko_sh, p.k_type, d.n_kv_heads);
+        return ok;
+    };
+    const int pairs = d.in_dtype != CQ_T_F32 && fits(8) ? 8 : 4;
+    const bool vec = pairs == 8 || fits(4);
+    const int lanes = (d.head_dim / 2 + pairs - 1) / pairs;
     p.log_g = 0;
     while ((1 << p.log_g) < lanes) ++p.log_g;
-    // Runs of four elements need every offset of a run to be a multiple of four.
-    const bool il = d.interleaved != 0;
-    bool vec = il ? d.head_dim % 8 == 0 : (d.rot_dim / 2) % 4 == 0 && (d.head_dim - d.rot_dim) / 2 % 4 == 0;
-    auto runs = [&](const void *b, int64_t st, int64_t sh, int type, int heads) {
-        vec = vec && (!heads || ((reinterpret_cast<uintptr_t>(b) % (4 * size_of(type)) == 0) && st % 4 == 0 && sh % 4 == 0));
-    };
-    runs(p.q, p.q_st, p.q_sh, d.in_dtype, d.n_q_heads);
-    runs(p.k, p.k_st, p.k_sh, d.in_dtype, d.n_kv_heads);
-    runs(p.qo, p.qo_st, p.qo_sh, p.q_type, d.n_q_heads);
-    runs(p.ko, p.ko_st, p.ko_sh, p.k_type, d.n_kv_heads);
     // A warp takes as many of a token's heads as still leave every SM 32 warps.
     const int slots = 32 >> p.log_g, sms = sm_count();
     p.chunk = slots;
@@ -241,9 +275,9 @@ int launch_qk_norm_rope(const cq_qk_desc &d, void *stream) {
     const long long blocks = ((long long)p.tokens * p.chunks + kWarps - 1) / kWarps;
     const int grid = (int)std::min<long long>(blocks, 8LL * sms);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (d.in_dtype == CQ_T_F32) launch_t<float>(p, il, vec, grid, st);
-    else if (d.in_dtype == CQ_T_F16) launch_t<__half>(p, il, vec, grid, st);
-    else launch_t<__nv_bfloat16>(p, il, vec, grid, st);
+    if (d.in_dtype == CQ_T_F32) launch_t<float>(p, 4, il, vec, grid, st);
+    else if (d.in_dtype == CQ_T_F16) launch_t<__half>(p, pairs, il, vec, grid, st);
+    else launch_t<__nv_bfloat16>(p, pairs, il, vec, grid, st);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(CQ_ERR_CUDA, "norm and rotation launch: %s", cudaGetErrorString(e));
     return CQ_OK;
