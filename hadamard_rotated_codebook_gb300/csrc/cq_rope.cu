@@ -107,7 +107,7 @@ __device__ __forceinline__ int2 pair_at(int p, int d, int rot, bool il) {
 // P pairs a lane. VEC: they are two aligned runs of P elements (`A` and `B`: of adjacent pairs where IL, else of the first and
 // of the second members).
 template <typename T, int P, bool IL, bool VEC>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
     using V = typename Raw<VEC ? P * (int)sizeof(T) : 16>::V;
     __shared__ uint64_t s_rate[128];
     __shared__ __align__(16) float s_w[2][256];  // offset + weight of queries and keys

@@ -25,6 +25,8 @@ from ._capi import CQ_T_BF16, CQ_T_F16, CQ_T_F32, KvGeom, KvStep, KvTree, QkDesc
 _TYPE = {torch.float32: CQ_T_F32, torch.float16: CQ_T_F16, torch.bfloat16: CQ_T_BF16}
 _load = _capi.load
 _stay = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (  # the handle without a Stream object around it
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _type(t: torch.Tensor, name: str) -> int:
@@ -51,21 +53,30 @@ def _i32(t: torch.Tensor, name: str, n: int, device) -> int:
     return t.data_ptr()
 
 
-def _heads(t: torch.Tensor, name: str, device):
-    """[tokens, heads, width] with a contiguous last dimension; other strides are free."""
+def _heads(t: torch.Tensor, name: str, device, out: bool = False):
+    """[tokens, heads, width] with a contiguous last dimension; other strides
+    are free, but an output's elements must not share memory. Returns the shape
+    and the first two strides."""
     _dev(t, name, device)
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (shape[2] > 1 and stride[2] != 1):
         raise ValueError(f"{name} must be [tokens, heads, width] with a contiguous last dimension, "
-                         f"got {tuple(t.shape)} strides {t.stride()}")
-    return t.shape
+                         f"got {tuple(shape)} strides {stride}")
+    n, h, d = shape
+    st, sh, _ = stride
+    if out and n * h * d and not ((h == 1 or sh >= d) and (n == 1 or st >= (h - 1) * sh + d)
+                                  or (n == 1 or st >= d) and (h == 1 or sh >= (n - 1) * st + d)):
+        raise ValueError(f"{name} overlaps itself: shape {tuple(shape)}, strides {stride}")
+    return n, h, d, st, sh
 
 
-def _distinct(t: torch.Tensor, name: str) -> None:
-    """An output's elements must not share memory."""
-    (n, h, d), (st, sh, _) = t.shape, t.stride()
-    if t.numel() and not ((h == 1 or sh >= d) and (n == 1 or st >= (h - 1) * sh + d)
-                          or (n == 1 or st >= d) and (h == 1 or sh >= (n - 1) * st + d)):
-        raise ValueError(f"{name} overlaps itself: shape {tuple(t.shape)}, strides {t.stride()}")
+def _weight(w: Optional[torch.Tensor], name: str, d: int, device):
+    if w is None:
+        return None
+    _dev(w, name, device)
+    if w.dtype != torch.float32 or w.shape != (d,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous float32 [{d}], got {w.dtype} {tuple(w.shape)}")
+    return w.data_ptr()
 
 
 def _table(t: torch.Tensor, n_seqs: int, device) -> int:
@@ -81,8 +92,11 @@ def _table(t: torch.Tensor, n_seqs: int, device) -> int:
 
 def _call(device, fn, *args) -> None:
     """Calls fn(*args, stream) with `device` current."""
-    with (_stay if device.index == torch.cuda.current_device() else torch.cuda.device(device)):
-        code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if device.index == torch.cuda.current_device():
+        code = fn(*args, _raw_stream(device.index))
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, _raw_stream(device.index))
     if code:
         check(code)
 
@@ -119,31 +133,24 @@ def cq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, r
     [d] (None: ones). Returns (q_out, k_out); outputs may be given, may have
     another type than the input, and may be the inputs themselves."""
     dev = q.device
-    (n, hq, d), (nk, hkv, dk) = _heads(q, "q", dev), _heads(k, "k", dev)
-    if n != nk or d != dk or q.dtype != k.dtype:
-        raise ValueError(f"q {tuple(q.shape)} {q.dtype} and k {tuple(k.shape)} {k.dtype} do not belong together")
+    n, hq, d, qt, qh = _heads(q, "q", dev)
+    nk, hkv, dk, kt, kh = _heads(k, "k", dev)
+    dtype = q.dtype
+    if n != nk or d != dk or k.dtype != dtype:
+        raise ValueError(f"q {tuple(q.shape)} {dtype} and k {tuple(k.shape)} {k.dtype} do not belong together")
     if not isinstance(rates, np.ndarray) or rates.dtype != np.uint64 or not rates.flags.c_contiguous:
         raise TypeError("rates must be the array cq_rope_init returned")
     if q_out is None:
-        q_out = torch.empty((n, hq, d), dtype=q_dtype or q.dtype, device=dev)
+        q_out = torch.empty((n, hq, d), dtype=q_dtype or dtype, device=dev)
     if k_out is None:
-        k_out = torch.empty((n, hkv, d), dtype=k_dtype or k.dtype, device=dev)
-    if tuple(_heads(q_out, "q_out", dev)) != (n, hq, d) or tuple(_heads(k_out, "k_out", dev)) != (n, hkv, d):
+        k_out = torch.empty((n, hkv, d), dtype=k_dtype or dtype, device=dev)
+    qn, qc, qd, qot, qoh = _heads(q_out, "q_out", dev, True)
+    kn, kc, kd, kot, koh = _heads(k_out, "k_out", dev, True)
+    if qn != n or kn != n or qc != hq or kc != hkv or qd != d or kd != d:
         raise ValueError(f"outputs {tuple(q_out.shape)}, {tuple(k_out.shape)} for inputs {tuple(q.shape)}, {tuple(k.shape)}")
-    _distinct(q_out, "q_out")
-    _distinct(k_out, "k_out")
-    w = []
-    for x, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if x is not None:
-            _dev(x, name, dev)
-            if x.dtype != torch.float32 or x.shape != (d,) or not x.is_contiguous():
-                raise ValueError(f"{name} must be contiguous float32 [{d}], got {x.dtype} {tuple(x.shape)}")
-            x = x.data_ptr()
-        w.append(x)
-    desc = QkDesc(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), w[0], w[1],
-                  _i32(positions, "positions", n, dev), rates.ctypes.data,
-                  q.stride(0), q.stride(1), k.stride(0), k.stride(1),
-                  q_out.stride(0), q_out.stride(1), k_out.stride(0), k_out.stride(1),
+    desc = QkDesc(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+                  _weight(q_weight, "q_weight", d, dev), _weight(k_weight, "k_weight", d, dev),
+                  _i32(positions, "positions", n, dev), rates.ctypes.data, qt, qh, kt, kh, qot, qoh, kot, koh,
                   _type(q, "q"), _type(q_out, "q_out"), _type(k_out, "k_out"),
                   n, hq, hkv, d, 2 * rates.size, interleaved, eps, weight_offset)
     _call(dev, _load().cq_qk_norm_rope, desc)
@@ -264,17 +271,16 @@ def cq_kv_tree_attend(geom: KvGeometry, q: torch.Tensor, k_cache: torch.Tensor, 
     request has more than ``max_nodes`` (up to 256). Returns o [nodes, Hq,
     head_dim_v] of q's type; a token that attends nothing gets zeros."""
     dev = q.device
-    n, hq, dk = _heads(q, "q", dev)
+    n, hq, dk, qt, qh = _heads(q, "q", dev)
     if hq != geom.n_q_heads or dk != geom.head_dim_k:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected [nodes, {geom.n_q_heads}, {geom.head_dim_k}]")
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"q must be float16 or bfloat16, got {q.dtype}")
     if o is None:
         o = torch.empty((n, hq, geom.head_dim_v), dtype=q.dtype, device=dev)
-    elif tuple(_heads(o, "o", dev)) != (n, hq, geom.head_dim_v) or o.dtype != q.dtype:
+    on, oc, od, ot, oh = _heads(o, "o", dev, True)
+    if on != n or oc != hq or od != geom.head_dim_v or o.dtype != q.dtype:
         raise ValueError(f"o must be {q.dtype} [{n}, {hq}, {geom.head_dim_v}], got {o.dtype} {tuple(o.shape)}")
-    else:
-        _distinct(o, "o")
     n_seqs = context_lens.numel()
     geom.check_caches(k_cache, v_cache, cap, dev)
     words = 0
@@ -290,7 +296,7 @@ def cq_kv_tree_attend(geom: KvGeometry, q: torch.Tensor, k_cache: torch.Tensor, 
                   mask.data_ptr() if mask is not None else None, q.data_ptr(), o.data_ptr(),
                   ws.data_ptr() if size else None, size,
                   block_table.stride(0) if n_seqs > 1 else block_table.shape[1],
-                  q.stride(0), q.stride(1), o.stride(0), o.stride(1),
+                  qt, qh, ot, oh,
                   cap, block_table.shape[1], block_size, n_seqs, n, max_nodes, words, _TYPE[q.dtype])
     _call(dev, _load().cq_kv_tree_attend, geom.c, tree)
     return o
