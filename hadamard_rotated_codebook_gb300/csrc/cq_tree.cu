@@ -44,7 +44,7 @@ namespace cq {
 namespace {
 
 constexpr int kTile = 128;        // cache rows per tile
-constexpr int kMaxThreads = 640;
+constexpr int kMaxThreads = 768;
 constexpr int kMaxDepth = 8;      // stages of the ring of codes
 constexpr unsigned kSpin = 1u << 20;   // polls of up to ~1 us
 constexpr float kNoMax = -1e30f;       // reference of a column that has attended nothing yet
@@ -446,7 +446,9 @@ __device__ __forceinline__ void expand_quarter(const uint32_t *c, const uint32_t
 template <int N, int NG>
 struct Plan {
     static constexpr int kSoftWG = N >= 64 ? 2 : 1;              // warpgroups of softmax
-    static constexpr int kSoft = 4 * kSoftWG, kExp = 8;         // warps; then the issuer, two fetchers, one idle
+    // Two expander warpgroups a side take turns at the tiles where softmax leaves the registers: an expansion is mostly latency.
+    static constexpr int kTurns = N == 16 && NG == 1 ? 2 : 1;
+    static constexpr int kSoft = 4 * kSoftWG, kExp = 8 * kTurns;  // warps; then the issuer, two fetchers, one idle
     static constexpr int kThreads = 32 * (kSoft + kExp + 4);
     static constexpr int kVBuf = NG == 1 ? 2 : 1;
     static constexpr int kVBytes = 2 * kTile * 128;            // one group's values: 128 rows x 128 fp16
@@ -784,16 +786,16 @@ __device__ __forceinline__ float row_norm(uint32_t info, uint32_t norms, bool tw
 }
 
 template <int N, int NG>
-__device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, bool keys, int row, int q, int lane) {
+__device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, int turn, bool keys, int row, int q, int lane) {
     using L = Plan<N, NG>;
     Cursor c = sh.start;
     const int tiles = uniform(c.left), w = keys ? p.wk : p.wv;
     const uint32_t tmem = uniform(sh.tmem), ring = smem_u32(smem) + L::oRing;
     const uint32_t tab = (keys ? p.tab_k : p.tab_v) | (w == 2 && wide_two(N) ? (lane & 15) * 8 : lane * 4);
-    int st = 0;
+    int st = turn;
     uint32_t rpar = 0;
 #pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
+    for (int i = turn; i < tiles; i += L::kTurns) {
         const int b = i & 1, buf = keys || L::kVBuf == 2 ? b : 0;
         const uint32_t par = (uint32_t)(i >> 1) & 1;
         bool two = false;
@@ -842,7 +844,8 @@ __device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, bool
             mbar_arrive(keys ? &sh.k_full[buf] : &sh.v_full[buf]);
             mbar_arrive(&sh.ring_empty[st]);
         }
-        if (++st == p.depth) st = 0, rpar ^= 1;
+        st += L::kTurns;
+        if (st >= p.depth) st -= p.depth, rpar ^= 1;
     }
 }
 
@@ -865,15 +868,47 @@ __device__ __forceinline__ float load_q(const TreeParams &p, int64_t at) {
                                  : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.t.q)[at]);
 }
 
-// Rotated queries of an item's columns into shared memory (the K-major B operand), scaled by one power of two so that
-// fp16 holds them whatever their size (a coordinate is at most the sum of the query's magnitudes, and that at most 8 or 64
-// times a lane's largest share of it); returns what takes the
-// scale back out of the logits.
+// The queries of an item's columns. Eight lanes take a column, 16 elements each, where runs of 16 lie in one head and on 16-byte
+// boundaries (`vec_q`): stash_queries starts their copies into the buffer of the weights, idle between two
+// items, while the partials of the item before are written, and each lane reads back its own. Else a warp takes a column
+// and reads it twice.
+template <int N, int NG>
+__device__ __forceinline__ uint32_t stash_at(uint8_t *smem, int i, int warp, int lane) {
+    using L = Plan<N, NG>;
+    return smem_u32(smem + L::oP) + ((i * L::kSoft + warp) * 32 + lane) * 32;
+}
+template <int N, int NG>
+__device__ __forceinline__ void stash_queries(const TreeParams &p, uint8_t *smem, const Cursor &c, int warp, int lane) {
+    using L = Plan<N, NG>;
+    if (NG == 2 || !p.vec_q) return;
+    const int rows = p.unit[c.u].nh * p.per, h0 = p.unit[c.u].h0, cols = min(N, c.n * rows - c.c * N);
+    const int g0 = p.unit[c.u].gk * kGroup + 16 * (lane & 7);
+#pragma unroll 1
+    for (int i = 0; i < N / (4 * L::kSoft); ++i) {
+        const int col = warp * 4 + (lane >> 3) + i * 4 * L::kSoft;
+        const int at = c.c * N + col, node = at / rows, r = at - node * rows, d0 = g0 - (h0 + r / p.per) * p.dk;
+        const uint32_t to = stash_at<N, NG>(smem, i, warp, lane);
+        if (col < cols && d0 >= 0 && d0 < p.dk) {
+            const __half *from = static_cast<const __half *>(p.t.q) + (int64_t)(c.first + node) * p.t.q_stride_t +
+                                 (int64_t)(h0 * p.per + r) * p.t.q_stride_h + d0;
+            cp_async16(to, from);
+            cp_async16(to + 16, from + 8);
+        } else {
+            sts128(to, 0, 0, 0, 0);
+            sts128(to + 16, 0, 0, 0, 0);
+        }
+    }
+}
+
+// The rotated queries into shared memory (the K-major B operand), scaled by one power of two so that fp16 holds them whatever their
+// size (a coordinate is at most the sum of the query's 128 or fewer magnitudes); returns what takes the scale back out
+// of the logits.
 template <int N, int NG>
 __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, const Cursor &c, int warp, int lane) {
     using L = Plan<N, NG>;
     const TreeUnit u = p.unit[c.u];
     const int rows = u.nh * p.per, cols = min(N, c.n * rows - c.c * N);
+    const bool fast = NG == 1 && p.vec_q, half = p.t.dtype == CQ_T_F16;
     // coordinates 4 * lane .. of group g of a column's query, placed at its head's elements of the cache row
     auto load = [&](int col, int g, float (&z)[4]) {
         const int at = c.c * N + col, node = at / rows, r = at - node * rows, h = u.h0 + r / p.per;
@@ -882,48 +917,33 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[j] = d0 + j >= 0 && d0 + j < p.dk ? load_q(p, src + d0 + j) : 0.0f;
     };
-    // Eight lanes to a column, 16 elements each, where runs of 16 lie in one head and on 16-byte boundaries; else a
-    // warp to a column.
-    const int sub = lane & 7, slot = warp * 4 + (lane >> 3);
-    auto load16 = [&](int col, float (&z)[16]) {
-        const int at = c.c * N + col, node = at / rows, r = at - node * rows, h = u.h0 + r / p.per;
-        const int d0 = u.gk * kGroup + 16 * sub - h * p.dk;
-        const int64_t src = (int64_t)(c.first + node) * p.t.q_stride_t + (int64_t)(u.h0 * p.per + r) * p.t.q_stride_h + d0;
-        uint4 v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        if (col < cols && d0 >= 0 && d0 < p.dk) {
-            const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.t.q) + src);
-            v[0] = from[0], v[1] = from[1];
-        }
-        const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (p.t.dtype == CQ_T_F16) {
-                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-                z[2 * j] = x.x, z[2 * j + 1] = x.y;
-            } else {
-                z[2 * j] = __uint_as_float(w[j] << 16), z[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-            }
-        }
-    };
-    const bool fast = NG == 1 && p.vec_q;
+    // the largest finite magnitude: what is not finite does not scale the others
     float top = 0.0f;
     if (fast) {
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
+        const uint32_t inf = half ? 0x7C00u : 0x7F80u;
+        uint32_t most = 0;  // magnitudes of a 16-bit type are ordered as integers
 #pragma unroll 1
-        for (int col = slot; col < cols; col += 4 * L::kSoft) {
-            float z[16], sum = 0.0f;
-            load16(col, z);
+        for (int i = 0; i < 2 * N / (4 * L::kSoft); ++i) {
+            const uint4 v = lds128(stash_at<N, NG>(smem, i >> 1, warp, lane) + (i & 1) * 16);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum += fabsf(z[j]);
-            if (sum <= 1e36f) top = fmaxf(top, 8.0f * sum);  // what is not finite does not scale the others
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a = w[j] & 0x7FFFu, b = w[j] >> 16 & 0x7FFFu;
+                most = max(most, max(a < inf ? a : 0u, b < inf ? b : 0u));
+            }
         }
+        top = half ? __half2float(__ushort_as_half((unsigned short)most)) : __uint_as_float(most << 16);
     } else {
 #pragma unroll 1
         for (int col = warp; col < cols; col += L::kSoft) {
+#pragma unroll 1
             for (int g = 0; g < u.ngk; ++g) {
                 float z[4];
                 load(col, g, z);
-                const float sum = (fabsf(z[0]) + fabsf(z[1])) + (fabsf(z[2]) + fabsf(z[3]));
-                if (sum <= 1e36f) top = fmaxf(top, 64.0f * sum);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (fabsf(z[j]) <= 3.4e38f) top = fmaxf(top, fabsf(z[j]));
             }
         }
     }
@@ -931,14 +951,24 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     if (lane == 0) atomicMax(&sh.zmax, __float_as_int(top));
     bar_sync(1, 32 * L::kSoft);
-    // the bound between 2^14 and 2^15; the exponent is held where both powers of two are normal
-    const int ex = max(-110, min(110, ((sh.zmax >> 23) & 255) - 127 - 14));
+    // the largest magnitude between 2^7 and 2^8, a sum of 128 of them below 2^15; the exponent is held where both powers of
+    // two are normal
+    const int ex = max(-110, min(120, ((sh.zmax >> 23) & 255) - 127 - 7));
     const float down = __int_as_float((127 - ex) << 23);
     if (fast) {
 #pragma unroll 1
-        for (int col = slot; col < N; col += 4 * L::kSoft) {
+        for (int i = 0; i < N / (4 * L::kSoft); ++i) {
+            const int sub = lane & 7, col = warp * 4 + (lane >> 3) + i * 4 * L::kSoft;
+            const uint32_t from = stash_at<N, NG>(smem, i, warp, lane);
+            const uint4 v0 = lds128(from), v1 = lds128(from + 16);
+            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
             float z[16];
-            load16(col, z);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+                z[2 * j] = (half ? x.x : __uint_as_float(w[j] << 16)) * down;
+                z[2 * j + 1] = (half ? x.y : __uint_as_float(w[j] & 0xFFFF0000u)) * down;
+            }
 #pragma unroll
             for (int h = 1; h < 16; h <<= 1)
 #pragma unroll
@@ -947,35 +977,34 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
                         const float x = z[j], y = z[j + h];
                         z[j] = x + y, z[j + h] = x - y;
                     }
+#pragma unroll 1
+            for (int o = 1; o < 8; o <<= 1) {
+                const float sign = (sub & o) ? -1.0f : 1.0f;
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float y = __shfl_xor_sync(0xFFFFFFFFu, z[j], o);
-                    z[j] = (sub & o) ? y - z[j] : z[j] + y;
-                }
-            uint32_t w[8];
+                for (int j = 0; j < 16; ++j) z[j] = fmaf(z[j], sign, __shfl_xor_sync(0xFFFFFFFFu, z[j], o));
+            }
+            uint32_t h2[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const __half2 v = __floats2half2_rn(z[2 * j] * down, z[2 * j + 1] * down);
-                w[j] = *reinterpret_cast<const uint32_t *>(&v);
+                const __half2 v = __floats2half2_rn(z[2 * j], z[2 * j + 1]);
+                h2[j] = *reinterpret_cast<const uint32_t *>(&v);
             }
             const uint32_t base = smem_u32(smem + L::oZ) + (sub >> 2) * (N * 128) + (col >> 3) * 1024 + (col & 7) * 128;
-            sts128(base + (((2 * (sub & 3)) ^ (col & 7)) << 4), w[0], w[1], w[2], w[3]);
-            sts128(base + (((2 * (sub & 3) + 1) ^ (col & 7)) << 4), w[4], w[5], w[6], w[7]);
+            sts128(base + (((2 * (sub & 3)) ^ (col & 7)) << 4), h2[0], h2[1], h2[2], h2[3]);
+            sts128(base + (((2 * (sub & 3) + 1) ^ (col & 7)) << 4), h2[4], h2[5], h2[6], h2[7]);
         }
-        return p.k_mult * __int_as_float((127 + ex) << 23);
-    }
+    } else {
 #pragma unroll 1
-    for (int col = warp; col < N; col += L::kSoft) {
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int k = warp * NG; k < N * NG; k += k % NG == NG - 1 ? (L::kSoft - 1) * NG + 1 : 1) {
+            const int col = k / NG, g = k % NG;
             float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             if (col < cols && g < u.ngk) load(col, g, z);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] *= down;
             fwht(z, lane);
             const uint32_t base = smem_u32(smem + L::oZ) + g * L::kZBytes + (col >> 3) * 1024 + (col & 7) * 128;
             auto put = [&](int pos, float x, float y) {
-                const __half2 v = __floats2half2_rn(x * down, y * down);
+                const __half2 v = __floats2half2_rn(x, y);
                 sts32(base + (pos >> 6) * (N * 128) + ((((pos & 63) >> 3) ^ (col & 7)) << 4) + (pos & 7) * 2,
                       *reinterpret_cast<const uint32_t *>(&v));
             };
@@ -1081,6 +1110,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
     int i = 0;
     long long done = sh.w0;  // tiles of the blocks before and of this one so far
     bool more = true;
+    stash_queries<N, NG>(p, smem, c, warp, lane);
     while (more) {
         // ------------------------------------------------ one item's part --
         bar_sync(1, kSoftThreads);  // the item before is finished: zmax, m, mask may be written
@@ -1211,13 +1241,19 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
             const float x = sh.lsum[4 * wg][row] + sh.lsum[4 * wg + 1][row] + (sh.lsum[4 * wg + 2][row] + sh.lsum[4 * wg + 3][row]);
             p.ml[(size_t)slot * N + c0 + row] = make_float2(-sh.minus_m[c0 + row], x);
         }
+        done += count;
+        c.left -= count;
+        more = c.left > 0;
+        if (more) c.next_item(p, N);
         wait(sh, &sh.p_empty, (uint32_t)(i - 1) & 1, p.status, 0x4749000Du);
         fence_after();
+        if (more) stash_queries<N, NG>(p, smem, c, warp, lane);
         const int nat = NG == 2 ? natural_of(row, p.wv) : row;
         for (int g = 0; g < u.ngv; ++g) {
             float *out = p.part + ((size_t)slot * NG + g) * N * kGroup + nat;
 #pragma unroll 1
             for (int k = 0; k < NC; k += 8) {
+                if (c0 + k >= cols) break;
                 float o[8];
                 tmem_ld<8>(tm + L::cO + g * N + c0 + k, o);
                 wait_ld<8>(o);
@@ -1226,10 +1262,6 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
                     if (c0 + k + j < cols) out[(size_t)(c0 + k + j) * kGroup] = o[j];
             }
         }
-        done += count;
-        c.left -= count;
-        more = c.left > 0;
-        if (more) c.next_item(p, N);
     }
 }
 
@@ -1251,7 +1283,7 @@ __global__ void __launch_bounds__(Plan<N, NG>::kThreads, 1) tree_kernel(const __
 #pragma unroll 1
         for (int i = 0; i < p.depth; ++i) {
             mbar_init(&sh.ring_full[i], 128);
-            mbar_init(&sh.ring_empty[i], L::kExp);
+            mbar_init(&sh.ring_empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.k_full[i], 4);
@@ -1260,7 +1292,7 @@ __global__ void __launch_bounds__(Plan<N, NG>::kThreads, 1) tree_kernel(const __
             mbar_init(&sh.v_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.s_empty[i], L::kSoft);
-            mbar_init(&sh.sc_full[i], L::kExp);
+            mbar_init(&sh.sc_full[i], 8);
         }
         mbar_init(&sh.p_full, L::kSoft);
         mbar_init(&sh.p_empty, 1);
@@ -1290,7 +1322,8 @@ __global__ void __launch_bounds__(Plan<N, NG>::kThreads, 1) tree_kernel(const __
     } else if (warp < L::kSoft + L::kExp) {
         if (L::kSoftWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kExpRegs));
         const int row = 32 * (warp & 3) + lane;
-        expand_role<N, NG>(p, sh, smem, warp < L::kSoft + 4, row, warp & 3, lane);
+        const int group = (warp - L::kSoft) >> 2;
+        expand_role<N, NG>(p, sh, smem, group >> 1, !(group & 1), row, warp & 3, lane);
     } else {
         if (L::kSoftWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kRestRegs));
         if (warp == kIssuer) issue_role<N, NG>(p, sh, smem);
@@ -1330,42 +1363,48 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
         for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[g][j] = 0.0f;
-        // the largest reference first (small loads), then the weighted sum in part order
-        for (int a = lane; a < rec.y; a += 32) M = fmaxf(M, p.ml[(size_t)(rec.x + a) * N + col].x);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+        // weighted sums in part order, rescaled where a part has a larger reference: all loads are independent
 #pragma unroll 4
         for (int a = many ? warp : 0; a < rec.y; a += many ? kJoinWarps : 1) {
             const float2 ml = p.ml[(size_t)(rec.x + a) * N + col];
-            const float w = ex2(ml.x - M);
-            sum = fmaf(ml.y, w, sum);
+            float4 v[NG];
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                if (g < u.ngv) v[g] = *reinterpret_cast<const float4 *>(p.part + (((size_t)(rec.x + a) * NG + g) * N + col) * kGroup + 4 * lane);
+            const float top = fmaxf(M, ml.x), f = ex2(M - top), w = ex2(ml.x - top);
+            M = top;
+            sum = fmaf(ml.y, w, sum * f);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 if (g >= u.ngv) break;
-                const float4 v = *reinterpret_cast<const float4 *>(p.part + (((size_t)(rec.x + a) * NG + g) * N + col) * kGroup + 4 * lane);
-                acc[g][0] = fmaf(v.x, w, acc[g][0]), acc[g][1] = fmaf(v.y, w, acc[g][1]);
-                acc[g][2] = fmaf(v.z, w, acc[g][2]), acc[g][3] = fmaf(v.w, w, acc[g][3]);
+                acc[g][0] = fmaf(v[g].x, w, acc[g][0] * f), acc[g][1] = fmaf(v[g].y, w, acc[g][1] * f);
+                acc[g][2] = fmaf(v[g].z, w, acc[g][2] * f), acc[g][3] = fmaf(v[g].w, w, acc[g][3] * f);
             }
         }
-        if (many) {  // uniform in the block
+        if (many) {  // uniform in the block: the warps' sums meet in warp 0
             __syncthreads();
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s_acc[warp][g][4 * lane + j] = acc[g][j];
-            if (lane == 0) s_ml[warp] = make_float2(0.0f, sum);
+            if (lane == 0) s_ml[warp] = make_float2(M, sum);
             __syncthreads();
             if (warp) continue;
+            float top = kNoMax;
+            for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_ml[w].x);
             sum = 0.0f;
-            for (int w = 0; w < kJoinWarps; ++w) sum += s_ml[w].y;
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float x = 0.0f;
-                    for (int w = 0; w < kJoinWarps; ++w) x += s_acc[w][g][4 * lane + j];
-                    acc[g][j] = x;
-                }
+                for (int j = 0; j < 4; ++j) acc[g][j] = 0.0f;
+            for (int w = 0; w < kJoinWarps; ++w) {
+                const float f = ex2(s_ml[w].x - top);
+                sum = fmaf(s_ml[w].y, f, sum);
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[g][j] = fmaf(s_acc[w][g][4 * lane + j], f, acc[g][j]);
+            }
         }
         const int at = ct * N + col, node = at / rows, r = at - node * rows, h = u.h0 + r / p.per;
         const float f = sum == 0.0f ? 0.0f : p.v_mult / sum;  // zero: a token that attends nothing
@@ -1511,8 +1550,8 @@ int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float 
         rc = s.N == 16 ? launch_main<16, 2>(p, st) : launch_main<64, 2>(p, st);
     }
     if (rc) return rc;
-    // a block per column where there are few, eight columns otherwise
-    const int cg = s.N == 16 ? 1 : 8;
+    // a block per column where that still fills the GPU with less than a few blocks per SM, a warp per column otherwise
+    const int cg = s.items * s.N <= 4 * (size_t)p.grid ? 1 : std::min(s.N, 32);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)s.items, (unsigned)(s.N / cg));
     cfg.blockDim = dim3(32 * kJoinWarps);
