@@ -17,7 +17,7 @@
 //   w[c][t] = 2^(x log2(e) + log2 n_v[t] - m[c]),  o = H sum_t w levels / sum_t w / n_v[t].
 // w is what the second product takes in fp16 (one rounding of 2^-11); with the reference m from the
 // column's own largest w it neither over- nor underflows whatever the size of the norms. m rises only when a
-// column's w would pass 2^8 (the accumulators are then scaled, which is rare after the first tile); columns
+// column's w would pass 2^15 (the accumulators are then scaled, which is rare after the first tile); columns
 // decide for themselves, so a column's bits do not depend on the others.
 //
 // Split. The tiles of all (request, unit, column tile) items in one row are cut into equal runs, one per SM:
@@ -44,11 +44,11 @@ namespace cq {
 namespace {
 
 constexpr int kTile = 128;        // cache rows per tile
-constexpr int kMaxThreads = 768;
+constexpr int kMaxThreads = 640;
 constexpr int kMaxDepth = 8;      // stages of the ring of codes
 constexpr unsigned kSpin = 1u << 20;   // polls of up to ~1 us
 constexpr float kNoMax = -1e30f;       // reference of a column that has attended nothing yet
-constexpr float kRaise = 8.0f;         // log2 of the largest weight before a reference is raised
+constexpr float kRaise = 15.0f;         // log2 of the largest weight before a reference is raised (fp16 ends below 2^16)
 constexpr float kInvSqrt128 = 0.08838834764831845f;
 
 struct TreeParams {
@@ -446,9 +446,7 @@ __device__ __forceinline__ void expand_quarter(const uint32_t *c, const uint32_t
 template <int N, int NG>
 struct Plan {
     static constexpr int kSoftWG = N >= 64 ? 2 : 1;              // warpgroups of softmax
-    // Two expander warpgroups a side take turns at the tiles where softmax leaves the registers: an expansion is mostly latency.
-    static constexpr int kTurns = N == 16 && NG == 1 ? 2 : 1;
-    static constexpr int kSoft = 4 * kSoftWG, kExp = 8 * kTurns;  // warps; then the issuer, two fetchers, one idle
+    static constexpr int kSoft = 4 * kSoftWG, kExp = 8;         // warps; then the issuer, two fetchers, one idle
     static constexpr int kThreads = 32 * (kSoft + kExp + 4);
     static constexpr int kVBuf = NG == 1 ? 2 : 1;
     static constexpr int kVBytes = 2 * kTile * 128;            // one group's values: 128 rows x 128 fp16
@@ -543,22 +541,26 @@ __device__ void fetch_role(const TreeParams &p, Shared &sh, uint8_t *smem, int l
     Cursor c = sh.start;
     const int tiles = uniform(c.left);
     const uint32_t ring = smem_u32(smem) + L::oRing;
-    RowAt next = row_at(p, c, lane);
-    int st = 0, unit = c.u;
+    // block numbers of the next two halves; the cursor is a tile ahead of the copies
+    RowAt next = row_at(p, c, lane), after = row_at(p, c, lane + 64);
+    int st = 0, unit = c.u, unit_next = c.u;
     uint32_t par = 1;
     Side sk = side_of<true>(p, unit), sv = side_of<false>(p, unit);
     const size_t all_k = (size_t)p.t.cap * sk.groups, all_v = (size_t)p.t.cap * sv.groups;
 #pragma unroll 1
     for (int i = 0; i < 2 * tiles; ++i) {  // half a tile at a time
         const int half = i & 1;
-        const RowAt now = next;
-        const int u = c.u;
-        if (half) c.advance(p, N);
-        next = row_at(p, c, lane + 64 * (half ^ 1));
-        if (u != unit) {
-            unit = u;
-            sk = side_of<true>(p, unit), sv = side_of<false>(p, unit);
+        if (!half) {
+            if (unit_next != unit) {
+                unit = unit_next;
+                sk = side_of<true>(p, unit), sv = side_of<false>(p, unit);
+            }
+            c.advance(p, N);
+            unit_next = c.u;
         }
+        const RowAt now = next;
+        next = after;
+        after = row_at(p, c, lane + 64 * half);
         if (!half) wait(sh, &sh.ring_empty[st], par, p.status, 0x4749000Eu);
         const uint32_t kc = ring + st * p.stage + (lane + 64 * half) * 16, vc = kc + Stage<NG>::codes(p.wk);
         const uint32_t info = vc + Stage<NG>::codes(p.wv) - (lane + 64 * half) * 12, nrm = info + Stage<NG>::kInfo;
@@ -786,16 +788,16 @@ __device__ __forceinline__ float row_norm(uint32_t info, uint32_t norms, bool tw
 }
 
 template <int N, int NG>
-__device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, int turn, bool keys, int row, int q, int lane) {
+__device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, bool keys, int row, int q, int lane) {
     using L = Plan<N, NG>;
     Cursor c = sh.start;
     const int tiles = uniform(c.left), w = keys ? p.wk : p.wv;
     const uint32_t tmem = uniform(sh.tmem), ring = smem_u32(smem) + L::oRing;
     const uint32_t tab = (keys ? p.tab_k : p.tab_v) | (w == 2 && wide_two(N) ? (lane & 15) * 8 : lane * 4);
-    int st = turn;
+    int st = 0;
     uint32_t rpar = 0;
 #pragma unroll 1
-    for (int i = turn; i < tiles; i += L::kTurns) {
+    for (int i = 0; i < tiles; ++i) {
         const int b = i & 1, buf = keys || L::kVBuf == 2 ? b : 0;
         const uint32_t par = (uint32_t)(i >> 1) & 1;
         bool two = false;
@@ -844,8 +846,7 @@ __device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, int 
             mbar_arrive(keys ? &sh.k_full[buf] : &sh.v_full[buf]);
             mbar_arrive(&sh.ring_empty[st]);
         }
-        st += L::kTurns;
-        if (st >= p.depth) st -= p.depth, rpar ^= 1;
+        if (++st == p.depth) st = 0, rpar ^= 1;
     }
 }
 
@@ -1322,8 +1323,7 @@ __global__ void __launch_bounds__(Plan<N, NG>::kThreads, 1) tree_kernel(const __
     } else if (warp < L::kSoft + L::kExp) {
         if (L::kSoftWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kExpRegs));
         const int row = 32 * (warp & 3) + lane;
-        const int group = (warp - L::kSoft) >> 2;
-        expand_role<N, NG>(p, sh, smem, group >> 1, !(group & 1), row, warp & 3, lane);
+        expand_role<N, NG>(p, sh, smem, warp < L::kSoft + 4, row, warp & 3, lane);
     } else {
         if (L::kSoftWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kRestRegs));
         if (warp == kIssuer) issue_role<N, NG>(p, sh, smem);

@@ -335,7 +335,7 @@ def _tree_mask(nodes, rng, words, empty=False):
 
 
 def _check_attend(C, geom, kb, vb, ctx, nodes, bs=16, dtype=F16, masked=True, empty=False, seed=0, poison=True, scale=None,
-                  lo=1.0, hi=8.0, q_scale=1.0, max_nodes=None, words=None):
+                  lo=1.0, hi=8.0, q_scale=1.0, max_nodes=None, words=None, contiguous=False):
     hq, hkv, dk, dv = geom
     rng = np.random.RandomState(seed)
     pages = [-(-(c + n) // bs) for c, n in zip(ctx, nodes)]
@@ -366,6 +366,8 @@ def _check_attend(C, geom, kb, vb, ctx, nodes, bs=16, dtype=F16, masked=True, em
             R.split_blob(blob, cap, w, b)[1][~used] = np.nan
     big = torch.randn(total, hq + 1, dk + 3, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed)) * q_scale
     q = big.to(dtype)[:, 1:, 2:2 + dk]
+    if contiguous:
+        q = q.contiguous()
     out = torch.full((total, hq, dv + 5), 7.0, dtype=dtype, device="cuda")
     scale = 1.0 / math.sqrt(dk) if scale is None else scale
     cbk, cbv = O.analytic_codebook(kb), O.analytic_codebook(vb)
@@ -384,6 +386,14 @@ def _check_attend(C, geom, kb, vb, ctx, nodes, bs=16, dtype=F16, masked=True, em
     assert np.isfinite(got).all()
     assert (err <= tol).all(), f"worst error/tolerance {np.max(err / np.maximum(tol, 1e-300)):.3g}"
     return got, float(np.max(err / np.maximum(tol, 1e-300))) if total else 0.0
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("geom", [(12, 2, 48, 64), (8, 4, 64, 64), (8, 2, 128, 128), (6, 6, 80, 80), (4, 1, 256, 256), (6, 3, 40, 24), (1, 1, 16, 16)])
+@pytest.mark.parametrize("nodes", [[1], [2, 0, 5], [33, 3]])
+def test_attend_contiguous_queries(C, dtype, geom, nodes):
+    """Queries on vector boundaries, as they come from cq_qk_norm_rope; each request's context spans several blocks."""
+    _check_attend(C, geom, 4, 2, ctx=[300 + 7 * i for i in range(len(nodes))], nodes=nodes, dtype=dtype, contiguous=True, seed=sum(geom))
 
 
 GEOMS = [(12, 2, 48, 64), (8, 4, 64, 64), (8, 2, 128, 128), (4, 1, 256, 256), (6, 6, 80, 80), (6, 3, 40, 24), (16, 1, 128, 64),
