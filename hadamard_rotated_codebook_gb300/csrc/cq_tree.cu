@@ -285,14 +285,17 @@ struct Cursor {
     }
 };
 
+// a / b for 0 <= a < 2^53 and a quotient far below 2^22 times smaller than 2^53 / b: rounding cannot reach the next integer.
+__device__ __forceinline__ long long floor_div(long long a, long long b) { return (long long)floor((double)a / (double)b); }
+
 // Run b of `grid` blocks; with fewer tiles than blocks the first `total` blocks take one each, so that the parts of an
 // item are consecutive blocks.
 __device__ __forceinline__ long long run_start(long long total, int grid, int b) {
-    const long long n = min(total, (long long)grid);
-    return b < n ? total * b / n : total;
+    const int n = (int)min(total, (long long)grid);
+    return b < n ? floor_div(total * b, n) : total;
 }
 __device__ __forceinline__ int run_of(long long total, int grid, long long tile) {
-    return (int)(((tile + 1) * min(total, (long long)grid) - 1) / total);
+    return (int)floor_div((tile + 1) * min(total, (long long)grid) - 1, total);
 }
 
 struct Shared {
@@ -347,6 +350,7 @@ __device__ bool find_run(const TreeParams &p, Shared &sh) {
     if (lane == 0) sh.scan_t[warp] = t;
     __syncthreads();
     long long total = 0;
+#pragma unroll 1
     for (int w = 0; w < kW; ++w) total += sh.scan_t[w];
     __syncthreads();
     const long long w0 = run_start(total, p.grid, blockIdx.x), w1 = run_start(total, p.grid, blockIdx.x + 1);
@@ -365,6 +369,7 @@ __device__ bool find_run(const TreeParams &p, Shared &sh) {
         if (lane == 31) sh.scan_t[warp] = ia, sh.scan_i[warp] = ib;
         __syncthreads();
         long long ba = ct, bb = ci;
+#pragma unroll 1
         for (int w = 0; w < kW; ++w) {
             if (w < warp) ba += sh.scan_t[w], bb += sh.scan_i[w];
             ct += sh.scan_t[w], ci += sh.scan_i[w];
@@ -1364,7 +1369,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[g][j] = 0.0f;
         // weighted sums in part order, rescaled where a part has a larger reference: all loads are independent
-#pragma unroll 4
+#pragma unroll 2
         for (int a = many ? warp : 0; a < rec.y; a += many ? kJoinWarps : 1) {
             const float2 ml = p.ml[(size_t)(rec.x + a) * N + col];
             float4 v[NG];
@@ -1550,8 +1555,10 @@ int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float 
         rc = s.N == 16 ? launch_main<16, 2>(p, st) : launch_main<64, 2>(p, st);
     }
     if (rc) return rc;
-    // a block per column where that still fills the GPU with less than a few blocks per SM, a warp per column otherwise
-    const int cg = s.items * s.N <= 4 * (size_t)p.grid ? 1 : std::min(s.N, 32);
+    // A block per column where they are few (its warps share long rows of parts), a warp per column otherwise: one for each while
+    // that is a few blocks per SM, four columns after another beyond (a block is mostly latency: 36 against 26 us for 65536).
+    const size_t columns = s.items * s.N;
+    const int cg = columns <= 4 * (size_t)p.grid ? 1 : columns <= 128 * (size_t)p.grid ? 8 : std::min(s.N, 32);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)s.items, (unsigned)(s.N / cg));
     cfg.blockDim = dim3(32 * kJoinWarps);
