@@ -285,17 +285,15 @@ struct Cursor {
     }
 };
 
-// a / b for 0 <= a < 2^53 and a quotient far below 2^22 times smaller than 2^53 / b: rounding cannot reach the next integer.
-__device__ __forceinline__ long long floor_div(long long a, long long b) { return (long long)floor((double)a / (double)b); }
-
 // Run b of `grid` blocks; with fewer tiles than blocks the first `total` blocks take one each, so that the parts of an
 // item are consecutive blocks.
 __device__ __forceinline__ long long run_start(long long total, int grid, int b) {
     const int n = (int)min(total, (long long)grid);
-    return b < n ? floor_div(total * b, n) : total;
+    if (b >= n) return total;
+    return total < 1 << 21 ? (unsigned)total * (unsigned)b / (unsigned)n : total * b / n;  // grid < 2^11: a short division
 }
 __device__ __forceinline__ int run_of(long long total, int grid, long long tile) {
-    return (int)floor_div((tile + 1) * min(total, (long long)grid) - 1, total);
+    return (int)(((tile + 1) * min(total, (long long)grid) - 1) / total);
 }
 
 struct Shared {
@@ -305,7 +303,7 @@ struct Shared {
     volatile int abort;
     int zmax;
     int bad;
-    long long total, w0;          // all tiles; this block's first one
+    long long total, run[2];      // all tiles; this block's first one and the next block's
     long long scan_t[kMaxThreads / 32];
     long long scan_i[kMaxThreads / 32];
     Cursor start;
@@ -334,63 +332,76 @@ __device__ bool find_run(const TreeParams &p, Shared &sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kW = kThreads / 32;
     auto tiles_and_items = [&](int s, long long &t, long long &i) {
+        t = i = 0;
+        if (s >= p.t.n_seqs) return;
         const Seq q = seq_at(p, s);
         if (q.bad) sh.bad = 1;
         i = (long long)p.n_units * cols_of(p, q.n, N);
         t = q.n ? i * tiles_of(q.len) : 0;
     };
-    long long t = 0;
-    for (int s = tid; s < p.t.n_seqs; s += kThreads) {
-        long long a, b;
-        tiles_and_items(s, a, b);
-        t += a;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    if (lane == 0) sh.scan_t[warp] = t;
-    __syncthreads();
-    long long total = 0;
+    // Inclusive sums of a and b up to this thread, and of all threads.
+    auto scan = [&](long long a, long long b, long long &ia, long long &ib, long long &all_a, long long &all_b) {
+        ia = a, ib = b;
 #pragma unroll 1
-    for (int w = 0; w < kW; ++w) total += sh.scan_t[w];
-    __syncthreads();
-    const long long w0 = run_start(total, p.grid, blockIdx.x), w1 = run_start(total, p.grid, blockIdx.x + 1);
-    if (tid == 0) sh.total = total, sh.w0 = w0;
-    if (w0 >= w1) return false;
-    long long ct = 0, ci = 0;  // tiles and items before the chunk
-    for (int base = 0; base < p.t.n_seqs; base += kThreads) {
-        long long a = 0, b = 0;
-        if (base + tid < p.t.n_seqs) tiles_and_items(base + tid, a, b);
-        long long ia = a, ib = b;
-#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long ua = __shfl_up_sync(0xFFFFFFFFu, ia, o), ub = __shfl_up_sync(0xFFFFFFFFu, ib, o);
             if (lane >= o) ia += ua, ib += ub;
         }
+        __syncthreads();
         if (lane == 31) sh.scan_t[warp] = ia, sh.scan_i[warp] = ib;
         __syncthreads();
-        long long ba = ct, bb = ci;
+        long long wa = lane < kW ? sh.scan_t[lane] : 0, wb = lane < kW ? sh.scan_i[lane] : 0;
 #pragma unroll 1
-        for (int w = 0; w < kW; ++w) {
-            if (w < warp) ba += sh.scan_t[w], bb += sh.scan_i[w];
-            ct += sh.scan_t[w], ci += sh.scan_i[w];
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long ua = __shfl_up_sync(0xFFFFFFFFu, wa, o), ub = __shfl_up_sync(0xFFFFFFFFu, wb, o);
+            if (lane >= o) wa += ua, wb += ub;
         }
-        const long long t0 = ba + ia - a;
+        all_a = __shfl_sync(0xFFFFFFFFu, wa, 31), all_b = __shfl_sync(0xFFFFFFFFu, wb, 31);
+        const long long pa = __shfl_sync(0xFFFFFFFFu, wa, max(warp - 1, 0)), pb = __shfl_sync(0xFFFFFFFFu, wb, max(warp - 1, 0));
+        if (warp) ia += pa, ib += pb;
+    };
+    // The sum over all requests; those of the first chunk are kept.
+    long long a, b, ia, ib, all_a, all_b, total = 0;
+    tiles_and_items(tid, a, b);
+    for (int s = tid + kThreads; s < p.t.n_seqs; s += kThreads) {
+        long long x, y;
+        tiles_and_items(s, x, y);
+        total += x;
+    }
+    if (p.t.n_seqs > kThreads) {  // uniform
+        scan(total, 0, ia, ib, all_a, all_b);
+        total = all_a;
+    }
+    scan(a, b, ia, ib, all_a, all_b);
+    total += all_a;
+    if (tid < 2) sh.run[tid] = run_start(total, p.grid, blockIdx.x + tid);
+    if (tid == 0) sh.total = total;
+    __syncthreads();
+    const long long w0 = sh.run[0], w1 = sh.run[1];
+    if (w0 >= w1) return false;
+    long long ct = 0, ci = 0;  // tiles and items before the chunk
+    for (int base = 0;;) {
+        const long long t0 = ct + ia - a;
         if (a && t0 <= w0 && w0 < t0 + a) {  // exactly one thread
             Cursor c;
             c.s = base + tid;
             c.take(p, N);
             const long long off = w0 - t0;
-            const int it = (int)(off / c.ntiles);
+            const int it = off < 1ll << 32 ? (int)((unsigned)off / (unsigned)c.ntiles) : (int)(off / c.ntiles);
             c.tile = (int)(off - (long long)it * c.ntiles);
             c.u = it / c.ncol;
             c.c = it - c.u * c.ncol;
-            c.item = (int)(bb + ib - b) + it;
+            c.item = (int)(ci + ib - b) + it;
             c.left = (int)(w1 - w0);
             sh.start = c;
         }
-        __syncthreads();
-        if (ct > w0) break;  // uniform
+        ct += all_a, ci += all_b;
+        base += kThreads;
+        if (ct > w0 || base >= p.t.n_seqs) break;  // uniform
+        tiles_and_items(base + tid, a, b);
+        scan(a, b, ia, ib, all_a, all_b);
     }
+    __syncthreads();
     return true;
 }
 
@@ -708,16 +719,19 @@ __device__ __forceinline__ void lookup_quarter(const uint32_t (&c)[W], uint32_t 
 
 // Fills a table (all threads); t: the levels' bytes as in TreeParams.
 __device__ void fill_table(uint32_t dst, const uint32_t (&t)[8], int w, bool wide) {
-    auto level = [&](int q) -> uint32_t {
-        const uint32_t lo = t[q >> 2] >> (8 * (q & 3)) & 255u, hi = t[4 + (q >> 2)] >> (8 * (q & 3)) & 255u;
-        return lo | hi << 8;
-    };
-    const int entries = w == 4 || wide ? 256 : w == 3 ? 64 : 16, m = (1 << w) - 1;
+    const int entries = w == 4 || wide ? 256 : w == 3 ? 64 : 16;
 #pragma unroll 1
     for (int i = threadIdx.x; i < entries * 8; i += blockDim.x) {  // 16 bytes each
-        const int e = i >> 3;
-        const uint32_t a = level(e & m) | level(e >> w & m) << 16;
-        const uint32_t b = wide ? level(e >> (2 * w) & m) | level(e >> (3 * w) & m) << 16 : a;
+        const uint32_t e = i >> 3;
+        uint32_t r[8], a, b;
+        if (w == 2) {  // pairs of codes 0 and 2, .. of 1 and 3, ..
+            expand_w2(e, t, r);
+            a = prmt(r[0], r[4], 0x5410), b = wide ? prmt(r[0], r[4], 0x7632) : a;
+        } else {
+            if (w == 3) expand_w3(e, t, r);
+            else expand_w4(e, t, r);
+            a = b = r[0];
+        }
         sts128(dst + i * 16, a, b, a, b);
     }
 }
@@ -968,31 +982,39 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
             const uint32_t from = stash_at<N, NG>(smem, i, warp, lane);
             const uint4 v0 = lds128(from), v1 = lds128(from + 16);
             const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-            float z[16];
+            F2 z[8];  // elements 2 j and 2 j + 1
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-                z[2 * j] = (half ? x.x : __uint_as_float(w[j] << 16)) * down;
-                z[2 * j + 1] = (half ? x.y : __uint_as_float(w[j] & 0xFFFF0000u)) * down;
+                const float a = half ? x.x : __uint_as_float(w[j] << 16), b = half ? x.y : __uint_as_float(w[j] & 0xFFFF0000u);
+                z[j] = f2_mul(f2(a + b, a - b), f2(down, down));
             }
+            const F2 minus = f2(-1.0f, -1.0f);
 #pragma unroll
-            for (int h = 1; h < 16; h <<= 1)
+            for (int h = 1; h < 8; h <<= 1)
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                for (int j = 0; j < 8; ++j)
                     if (!(j & h)) {
-                        const float x = z[j], y = z[j + h];
-                        z[j] = x + y, z[j + h] = x - y;
+                        const F2 x = z[j], y = z[j + h];
+                        z[j] = f2_add(x, y), z[j + h] = f2_fma(y, minus, x);
                     }
 #pragma unroll 1
             for (int o = 1; o < 8; o <<= 1) {
                 const float sign = (sub & o) ? -1.0f : 1.0f;
+                const F2 s2 = f2(sign, sign);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) z[j] = fmaf(z[j], sign, __shfl_xor_sync(0xFFFFFFFFu, z[j], o));
+                for (int j = 0; j < 8; ++j) {
+                    float x, y;
+                    f2_get(z[j], x, y);
+                    z[j] = f2_fma(z[j], s2, f2(__shfl_xor_sync(0xFFFFFFFFu, x, o), __shfl_xor_sync(0xFFFFFFFFu, y, o)));
+                }
             }
             uint32_t h2[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const __half2 v = __floats2half2_rn(z[2 * j], z[2 * j + 1]);
+                float x, y;
+                f2_get(z[j], x, y);
+                const __half2 v = __floats2half2_rn(x, y);
                 h2[j] = *reinterpret_cast<const uint32_t *>(&v);
             }
             const uint32_t base = smem_u32(smem + L::oZ) + (sub >> 2) * (N * 128) + (col >> 3) * 1024 + (col & 7) * 128;
@@ -1047,11 +1069,11 @@ __device__ void gather_mask(const TreeParams &p, Shared &sh, const Cursor &c, in
     }
 }
 
-__device__ __forceinline__ int ordered(float x) {  // integers in the order of the floats
-    const int i = __float_as_int(x);
-    return i ^ ((i >> 31) & 0x7FFFFFFF);
+__device__ __forceinline__ float warp_max(float x) {  // NaNs count as nothing
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;\n" : "=f"(r) : "f"(x));
+    return r;
 }
-__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
 
 // Raises the references of columns cx .. cx + X - 1 whose largest logit of this tile (columns in tensor memory at ts, this
 // thread's cache row) passes the weights' range; the factors for what was summed before go to sh.f. All four warps of
@@ -1068,7 +1090,7 @@ __device__ __noinline__ bool raise(Shared &sh, uint32_t ts, int cx, float nk, fl
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float t = see >> (k + j) & 1 ? fmaf(d[j], nk, ln) : -INFINITY;
-            const float x = unordered(__reduce_max_sync(0xFFFFFFFFu, ordered(fmaxf(t, -INFINITY))));
+            const float x = warp_max(fmaxf(t, -INFINITY));
             if (lane == k + j) mine = x;
         }
     }
@@ -1085,6 +1107,26 @@ __device__ __noinline__ bool raise(Shared &sh, uint32_t ts, int cx, float nk, fl
         if (raised) sh.minus_m[cx + row] = -x;
     }
     return bar_or(2 + wg, 128, raised);
+}
+
+// The first references of an item's part: the largest finite logits of the tile's first 32 cache rows, by their warp alone. With
+// 2^15 above them that holds nearly always, and costs the other warps a barrier.
+template <int X>
+__device__ __noinline__ void seed(Shared &sh, uint32_t ts, int cx, float nk, float ln, uint32_t see, int lane) {
+    float mine = kNoMax;
+#pragma unroll 1
+    for (int k = 0; k < X; k += 8) {
+        float d[8];
+        tmem_ld<8>(ts + k, d);
+        wait_ld<8>(d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float t = fmaf(d[j], nk, ln);
+            const float x = warp_max((see >> (k + j) & 1) && t < 1e30f ? t : kNoMax);
+            if (lane == k + j) mine = x;
+        }
+    }
+    if (lane < X) sh.minus_m[cx + lane] = -fmaxf(mine, kNoMax);
 }
 
 // Scales the running sums of columns cx .. cx + X - 1 by the factors of a raise.
@@ -1114,7 +1156,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
     const uint32_t tm = sh.tmem + ((uint32_t)(32 * q) << 16);
     Cursor c = sh.start;
     int i = 0;
-    long long done = sh.w0;  // tiles of the blocks before and of this one so far
+    long long done = sh.run[0];  // tiles of the blocks before and of this one so far
     bool more = true;
     stash_queries<N, NG>(p, smem, c, warp, lane);
     while (more) {
@@ -1162,6 +1204,10 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
                 const int cx = c0 + hf;
                 const uint32_t ts = tm + L::cS + b * N + cx;
                 bool raised = false;
+                if (__builtin_expect(it == 0, 0)) {
+                    if (q == 0) seed<X>(sh, ts, cx, nk, ln, masked ? see[hf / 32] : 0xFFFFFFFFu, lane);
+                    bar_sync(2 + wg, 128);
+                }
 #pragma unroll 1
                 for (int pass = 0;; ++pass) {
                     tmem_ld<X>(ts, d);
