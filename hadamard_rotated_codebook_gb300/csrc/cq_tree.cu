@@ -59,7 +59,7 @@ struct TreeParams {
     float2 *ml;      // [slot][N] reference and denominator
     int2 *rec;       // [item] first slot and number of parts
     uint32_t tk[8], tv[8];  // level tables: low bytes of 16 fp16 levels, then high bytes
-    float k_mult, v_mult;   // scale * log2(e) / sqrt(128) * 2^(table exponent); 2^(table exponent) / sqrt(128)
+    float k_mult, v_mult;   // scale * log2(e) / sqrt(128) / (table scale); 1 / sqrt(128) / (table scale)
     int n_units, hq, per, dk, dv, wk, wv, kgroups, vgroups;
     int depth, stage;        // ring stages and their bytes
     uint32_t tab_k, tab_v;   // shared-memory addresses of the level tables
@@ -1526,20 +1526,51 @@ Shape shape_of(const cq_kv_geom &g, int n_seqs, int max_nodes, TreeUnit *u) {
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
-// Level tables as bytes, scaled by a power of two into [1, 2); returns that power.
+// Level tables as bytes, scaled so that the largest level lies in [1, 4) and the levels' relative errors in fp16 are small: of 256
+// scales the one whose worst error is least (two magnitudes are then off by 2^-16 or so instead of 2^-12, eight by
+// 2^-13). Returns what takes the scale out again. The search is a pure function of the levels; a thread keeps
+// its last results, by content.
 float byte_table(const float *lv, uint32_t *t) {
+    struct Found {
+        float lv[16];
+        uint32_t t[8];
+        float back;
+    };
+    static thread_local Found found[4];
+    static thread_local int filled = 0, next = 0;
+    for (int i = 0; i < filled; ++i)
+        if (std::equal(lv, lv + 16, found[i].lv)) {
+            std::copy(found[i].t, found[i].t + 8, t);
+            return found[i].back;
+        }
+    Found f;
+    std::copy(lv, lv + 16, f.lv);
     float top = 0.0f;
     for (int i = 0; i < 16; ++i) top = std::max(top, std::fabs(lv[i]));
     int e = 0;
     if (top > 0.0f) std::frexp(top, &e), --e;
-    for (int i = 0; i < 8; ++i) t[i] = 0;
-    for (int i = 0; i < 16; ++i) {
-        const __half h = __float2half_rn(std::ldexp(lv[i], -e));
-        const uint32_t b = __half_as_ushort(h);
-        t[i / 4] |= (b & 255u) << (8 * (i & 3));
-        t[4 + i / 4] |= (b >> 8) << (8 * (i & 3));
+    double best = 1e30, scale = 1.0;
+    for (int k = 0; k < 256 && top > 0.0f; ++k) {
+        const double s = std::ldexp(1.0 + k / 256.0, -e);
+        double worst = 0.0;
+        for (int i = 0; i < 16; ++i) {
+            const double x = lv[i] * s;
+            if (x != 0.0) worst = std::max(worst, std::fabs(__half2float(__float2half_rn((float)x)) / x - 1.0));
+        }
+        if (worst < best) best = worst, scale = s;
     }
-    return std::ldexp(1.0f, e);
+    for (int i = 0; i < 8; ++i) f.t[i] = 0;
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t b = __half_as_ushort(__float2half_rn((float)(lv[i] * scale)));
+        f.t[i / 4] |= (b & 255u) << (8 * (i & 3));
+        f.t[4 + i / 4] |= (b >> 8) << (8 * (i & 3));
+    }
+    f.back = (float)(1.0 / scale);
+    found[next] = f;
+    next = (next + 1) % 4;
+    filled = std::min(filled + 1, 4);
+    std::copy(f.t, f.t + 8, t);
+    return f.back;
 }
 
 template <int N, int NG>
