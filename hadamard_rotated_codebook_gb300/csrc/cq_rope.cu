@@ -183,10 +183,16 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const __grid_
                             if (p0 + j < half_d) x[j] = to_f(src[at[j]]), x[P + j] = to_f(src[at[P + j]]);
                     }
                 }
-                float s = 0.0f;
+                // squares pair by pair, four pairs to a partial sum, neighbours first: the same bits for every P and layout
+                float part[P / 4];
 #pragma unroll
-                for (int i = 0; i < 2 * P; ++i) s = fmaf(x[i], x[i], s);
-                for (int o = g >> 1; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+                for (int j = 0; j < P; ++j) {
+                    const int m = VEC && IL ? 2 * j : j, e = VEC && IL ? 2 * j + 1 : P + j;
+                    part[j / 4] = fmaf(x[e], x[e], fmaf(x[m], x[m], j % 4 ? part[j / 4] : 0.0f));
+                }
+                float s = part[0];
+                if (P == 8) s += part[P / 4 - 1];
+                for (int o = 1; o < g; o <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
                 if (h >= h1 || !live) continue;
                 const bool is_q = h < p.hq;
                 const float inv = rsqrtf(fmaf(s, p.inv_d, p.eps));

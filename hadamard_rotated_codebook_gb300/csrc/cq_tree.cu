@@ -464,11 +464,15 @@ struct Plan {
     static constexpr int kSoftWG = N >= 64 ? 2 : 1;              // warpgroups of softmax
     static constexpr int kSoft = 4 * kSoftWG, kExp = 8;         // warps; then the issuer, two fetchers, one idle
     static constexpr int kThreads = 32 * (kSoft + kExp + 4);
+    static constexpr int kIssue = N <= 32 ? 4 : 1;               // MMAs in line: with few columns the issuer is the slowest role
     static constexpr int kVBuf = NG == 1 ? 2 : 1;
     static constexpr int kVBytes = 2 * kTile * 128;            // one group's values: 128 rows x 128 fp16
     static constexpr int kPBytes = kTile * (N <= 64 ? 128 : 256);
     static constexpr int kZBytes = N * 256;                    // one group
-    static constexpr int oV = 0, oP = oV + kVBuf * NG * kVBytes, oZ = oP + kPBytes, oShared = oZ + NG * kZBytes;
+    // Queries of a 16-bit type come rotated as a sum of two fp16 terms while there is room (and tensor work to spare): one term
+    // would be the largest part of an fp16 result's error. bf16 results do not show it.
+    static constexpr int kZTerms = N <= 64 && NG == 1 ? 2 : 1;
+    static constexpr int oV = 0, oP = oV + kVBuf * NG * kVBytes, oZ = oP + kPBytes, oShared = oZ + NG * kZTerms * kZBytes;
     static constexpr int oRing = oShared + ((int)sizeof(Shared) + 127) / 128 * 128;
     // registers of the roles where softmax takes two warpgroups: 256 (kSoftRegs + kExpRegs) + 128 kRestRegs <= 640 x 96
     static constexpr int kSoftRegs = N == 128 ? 144 : 128, kExpRegs = N == 128 ? 64 : 72, kRestRegs = N == 128 ? 64 : 80;
@@ -620,10 +624,16 @@ __device__ __forceinline__ void issue_scores(const TreeParams &p, Shared &sh, ui
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if (g == 1 && !two) break;
-#pragma unroll 1
+#pragma unroll L::kIssue
         for (int k = 0; k < 8; ++k)
             mma_ts(tmem + L::cS + b * N, tmem + L::cK + (b * NG + g) * 64 + 8 * k,
                    dz + (uint64_t)((g * L::kZBytes + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), idesc_f16(128, N, 0, 0), (g | k) != 0);
+    }
+    if (L::kZTerms == 2 && p.t.dtype == CQ_T_F16) {  // the second term of the queries
+#pragma unroll L::kIssue
+        for (int k = 0; k < 8; ++k)
+            mma_ts(tmem + L::cS + b * N, tmem + L::cK + b * 64 + 8 * k,
+                   dz + (uint64_t)((L::kZBytes + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), idesc_f16(128, N, 0, 0), 1);
     }
     mma_commit(&sh.k_empty[b]);
     mma_commit(&sh.s_full[b]);
@@ -641,7 +651,7 @@ __device__ __forceinline__ void issue_sums(const TreeParams &p, Shared &sh, uint
     for (int g = 0; g < NG; ++g) {
         if (g == 1 && !two) break;
         const uint64_t dv = desc_sw128(smem_u32(smem + L::oV) + (vb * NG + g) * L::kVBytes, kTile * 128);
-#pragma unroll 1
+#pragma unroll L::kIssue
         for (int k = 0; k < 8; ++k)  // 16 cache rows: two atoms
             mma_ss(tmem + L::cO + g * N, dv + (uint64_t)(k * 2048 >> 4), dp + (uint64_t)(k * 2048 >> 4), idesc_f16(128, N, 1, 1),
                    !first || k);
@@ -1020,6 +1030,18 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
             const uint32_t base = smem_u32(smem + L::oZ) + (sub >> 2) * (N * 128) + (col >> 3) * 1024 + (col & 7) * 128;
             sts128(base + (((2 * (sub & 3)) ^ (col & 7)) << 4), h2[0], h2[1], h2[2], h2[3]);
             sts128(base + (((2 * (sub & 3) + 1) ^ (col & 7)) << 4), h2[4], h2[5], h2[6], h2[7]);
+            if (L::kZTerms == 2 && half) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float x, y;
+                    f2_get(z[j], x, y);
+                    const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&h2[j]));
+                    const __half2 v = __floats2half2_rn(x - hi.x, y - hi.y);
+                    h2[j] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+                sts128(base + L::kZBytes + (((2 * (sub & 3)) ^ (col & 7)) << 4), h2[0], h2[1], h2[2], h2[3]);
+                sts128(base + L::kZBytes + (((2 * (sub & 3) + 1) ^ (col & 7)) << 4), h2[4], h2[5], h2[6], h2[7]);
+            }
         }
     } else {
 #pragma unroll 1
@@ -1033,8 +1055,13 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
             const uint32_t base = smem_u32(smem + L::oZ) + g * L::kZBytes + (col >> 3) * 1024 + (col & 7) * 128;
             auto put = [&](int pos, float x, float y) {
                 const __half2 v = __floats2half2_rn(x, y);
-                sts32(base + (pos >> 6) * (N * 128) + ((((pos & 63) >> 3) ^ (col & 7)) << 4) + (pos & 7) * 2,
-                      *reinterpret_cast<const uint32_t *>(&v));
+                const uint32_t to = base + (pos >> 6) * (N * 128) + ((((pos & 63) >> 3) ^ (col & 7)) << 4) + (pos & 7) * 2;
+                sts32(to, *reinterpret_cast<const uint32_t *>(&v));
+                if (L::kZTerms == 2) {
+                    const float2 hi = __half22float2(v);
+                    const __half2 l = __floats2half2_rn(x - hi.x, y - hi.y);
+                    sts32(to + L::kZBytes, *reinterpret_cast<const uint32_t *>(&l));
+                }
             };
             if (NG == 2 && p.wk == 2) {
                 put(position_of(4 * lane, 2), z[0], z[2]);
