@@ -16,20 +16,33 @@
 // Exponents. The norm of a value row goes into the exponent:
 //   w[c][t] = 2^(x log2(e) + log2 n_v[t] - m[c]),  o = H sum_t w levels / sum_t w / n_v[t].
 // w is what the second product takes in fp16 (one rounding of 2^-11); with the reference m from the
-// column's own largest w it neither over- nor underflows whatever the size of the norms. m rises only when a
-// column's w would pass 2^15 (the accumulators are then scaled, which is rare after the first tile); columns
-// decide for themselves, so a column's bits do not depend on the others.
+// column's own logits it neither over- nor underflows whatever the size of the norms. m starts at the
+// largest logit of 32 rows and rises when a column's w would pass 2^15 (the accumulators are then
+// scaled, which is rare: at 2^8 it cost 5 to 9%); columns decide for themselves, so a column's bits do
+// not depend on the others.
 //
-// Split. The tiles of all (request, unit, column tile) items in one row are cut into equal runs, one per SM:
-// lengths are read on the device, and the longest request cannot hold the launch up. Each run leaves
+// Split. The tiles of all (request, unit, column tile) items in one row are cut into equal runs, one per
+// SM: lengths are read on the device, and the longest request cannot hold the launch up. Each run leaves
 // unrotated partial sums; a second kernel joins them, rotates and writes o.
 //
-// Roles of the 16 or 20 warps. Softmax: one or two warpgroups (N of 64 and more), each with its share of the columns; they
-// also rotate the queries and write the partials. Expansion: a warpgroup each for keys and values, in which a thread turns its
-// cache row's codes into fp16 levels, keys into TMEM (the A operand) and values into shared memory. One warp issues the MMAs, two fetch codes, norms and block numbers
-// into a ring some tiles ahead.
-// Every wait is bounded: when one gives up, the flag s_abort makes all later waits return at once and every role
-// runs through its remaining tiles without waiting, so that the block's barriers stay matched.
+// Roles of the 16 or 20 warps. Softmax: one warpgroup, or two with half the columns each (N of 64 and
+// more); they also rotate the queries and write the partials. Expansion: a warpgroup each for keys and
+// values, in which a thread turns its cache row's codes into fp16 levels, keys into TMEM (the A operand)
+// and values into shared memory. One warp issues the MMAs, two fetch codes, norms and block numbers into
+// a ring some tiles ahead. Every wait is bounded: when one gives up, the flag `abort` makes all later
+// waits return at once and every role runs through its remaining tiles without waiting, so that the
+// block's barriers stay matched.
+//
+// What bounds it. Neither memory (8 to 18% of the copy rate) nor the tensor pipe (19 to 35% of the dense
+// rate at 128 columns): a tile of 16 columns takes about 2000 cycles and one of 128 about 2900, made of
+// the latencies of five roles that hand each other buffers, with 46 to 49% of the issue slots used and
+// shared memory busy for 50 to 65% of the time. An item (a request, unit and column tile) costs another
+// 15000 to 20000 cycles to begin and end. Measured: 256 requests of 8000 tokens, 12 heads on 2 of 48/64, 2 bits,
+// one token each, 117 us; 32 requests of 2000 to 8000 tokens with trees of 40 to 64, 32 heads on 8 of 128, 4 bits,
+// 355 us; one of 131071 tokens with a tree of 64, the same heads, 2 bits, 209 us.
+// Tried and slower: both sides or the keys alone looked up by byte permutes instead of tables
+// (server 355 -> 495 us: the integer pipe runs at half rate), two expander warpgroups a side, two softmax
+// streams or eight fetchers for 16 columns (117 -> 120 to 145 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -310,8 +323,7 @@ struct Shared {
     float scal[2][3][kTile];      // per tile buffer: n_k, log2 n_v, 1 / n_v
     alignas(16) float minus_m[128];  // column references, negated (read four at a time)
     alignas(16) float f[128];        // factors of the last raise
-    float wmax[8][32];            // column maxima of a softmax warp
-    float lsum[8][64];
+    float by_warp[8][64];         // column maxima of a softmax warp in a raise, denominators at an item's end
     uint32_t mask[CQ_TREE_MAX_NODES][4];  // columns (bits) that attend drafted token j
 };
 
@@ -617,9 +629,9 @@ __device__ __forceinline__ void issue_scores(const TreeParams &p, Shared &sh, ui
     const int b = i & 1;
     const uint32_t par = (uint32_t)(i >> 1) & 1;
     const uint64_t dz = desc_sw128(smem_u32(smem + L::oZ), 16);
-    __syncwarp();
     wait(sh, &sh.k_full[b], par, p.status, 0x47490004u);
     wait(sh, &sh.s_empty[b], par ^ 1, p.status, 0x47490005u);
+    __syncwarp();
     fence_after();
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -1121,14 +1133,14 @@ __device__ __noinline__ bool raise(Shared &sh, uint32_t ts, int cx, float nk, fl
             if (lane == k + j) mine = x;
         }
     }
-    if (lane < X) sh.wmax[warp][lane] = mine;
+    if (lane < X) sh.by_warp[warp][lane] = mine;
     bar_sync(2 + wg, 128);
     bool raised = false;
     if (row < X) {
         const float old = -sh.minus_m[cx + row];
-        float x = sh.wmax[4 * wg][row];
+        float x = sh.by_warp[4 * wg][row];
 #pragma unroll
-        for (int k = 1; k < 4; ++k) x = fmaxf(x, sh.wmax[4 * wg + k][row]);
+        for (int k = 1; k < 4; ++k) x = fmaxf(x, sh.by_warp[4 * wg + k][row]);
         raised = x > old + kRaise;
         sh.f[cx + row] = raised ? ex2(old - x) : 1.0f;
         if (raised) sh.minus_m[cx + row] = -x;
@@ -1313,11 +1325,11 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
                     }
                 }
             }
-            if (lane < X) sh.lsum[warp][hf + lane] = v[0];
+            if (lane < X) sh.by_warp[warp][hf + lane] = v[0];
         }
         bar_sync(2 + wg, 128);
         if (row < NC && c0 + row < cols) {
-            const float x = sh.lsum[4 * wg][row] + sh.lsum[4 * wg + 1][row] + (sh.lsum[4 * wg + 2][row] + sh.lsum[4 * wg + 3][row]);
+            const float x = sh.by_warp[4 * wg][row] + sh.by_warp[4 * wg + 1][row] + (sh.by_warp[4 * wg + 2][row] + sh.by_warp[4 * wg + 3][row]);
             p.ml[(size_t)slot * N + c0 + row] = make_float2(-sh.minus_m[c0 + row], x);
         }
         done += count;
@@ -1430,8 +1442,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     const Seq q = seq_at(p, s);
     const TreeUnit &u = p.unit[ui];
     const int rows = u.nh * p.per, cols = min(N, q.n * rows - ct * N), first = blockIdx.y * CG;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");  // every block: what follows this kernel also follows the one before it
     if (first >= cols) return;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const int2 rec = p.rec[item];
     const bool many = rec.y > kFewParts;
     for (int k = many ? 0 : warp; k < CG && first + k < cols; k += many ? 1 : kJoinWarps) {
@@ -1521,6 +1533,10 @@ int lay_out(int wk, int wv, bool same, uint32_t &tab_k, uint32_t &tab_v) {
     const int depth = std::min(kMaxDepth, (end - kSmemFirst - Plan<N, NG>::oRing) / Stage<NG>::bytes(wk, wv));
     return depth >= 2 ? depth : 0;
 }
+
+// Two four-bit tables leave 64 columns two stages (and 128 columns one: shape_of then takes 64).
+static_assert((kTabTop - 2 * table_bytes(4, 64) - kSmemFirst - Plan<64, 1>::oRing) / Stage<1>::bytes(4, 4) >= 2, "stages");
+static_assert((kSmemLast - kSmemFirst - Plan<64, 2>::oRing) / Stage<2>::bytes(4, 4) >= 2, "stages");
 
 struct Shape {
     int n_units, ng, rows, N, ncol_max;

@@ -335,7 +335,7 @@ def _tree_mask(nodes, rng, words, empty=False):
 
 
 def _check_attend(C, geom, kb, vb, ctx, nodes, bs=16, dtype=F16, masked=True, empty=False, seed=0, poison=True, scale=None,
-                  lo=1.0, hi=8.0, q_scale=1.0, max_nodes=None, words=None, contiguous=False):
+                  lo=1.0, hi=8.0, q_scale=1.0, max_nodes=None, words=None, contiguous=False, books=None):
     hq, hkv, dk, dv = geom
     rng = np.random.RandomState(seed)
     pages = [-(-(c + n) // bs) for c, n in zip(ctx, nodes)]
@@ -370,7 +370,7 @@ def _check_attend(C, geom, kb, vb, ctx, nodes, bs=16, dtype=F16, masked=True, em
         q = q.contiguous()
     out = torch.full((total, hq, dv + 5), 7.0, dtype=dtype, device="cuda")
     scale = 1.0 / math.sqrt(dk) if scale is None else scale
-    cbk, cbv = O.analytic_codebook(kb), O.analytic_codebook(vb)
+    cbk, cbv = books or (O.analytic_codebook(kb), O.analytic_codebook(vb))
     g = C.cq_kv_geometry(hq, hkv, dk, dv, kb, vb, cbk, cbv, scale)
     C.cq_kv_tree_attend(g, q, torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), cap, _i32(table), bs, _i32(ctx), _i32(cu),
                         torch.from_numpy(mask).cuda() if masked else None, most, o=out[..., 2:2 + dv])
@@ -426,6 +426,37 @@ def test_attend_without_context(C, masked):
     got, _ = _check_attend(C, (8, 4, 64, 64), 4, 4, ctx=[0, 0, 0], nodes=[33, 1, 130], masked=masked, empty=masked)
     if masked:
         assert (got[32] == 0).all() and (got[33] == 0).all() and (got[-1] == 0).all()
+
+
+@pytest.mark.parametrize("kb,vb", [(4, 4), (2, 4), (4, 2), (3, 3), (2, 2)])
+@pytest.mark.parametrize("nodes", [[3], [40, 2]])
+def test_attend_own_codebooks(C, kb, vb, nodes):
+    """Codebooks that are not symmetric, differ between keys and values, and are of another size than the
+    analytic ones: two large level tables leave less room for the columns of a large tree."""
+    rng = np.random.RandomState(kb + vb)
+    books = tuple((np.sort(rng.uniform(-1, 1, 2 ** b)) * s + 0.01 * s).astype(np.float32) for b, s in ((kb, 0.3), (vb, 40.0)))
+    _check_attend(C, (8, 2, 128, 128), kb, vb, ctx=[250, 3][:len(nodes)], nodes=nodes, dtype=BF16, books=books, seed=kb)
+    _check_attend(C, (8, 4, 64, 64), kb, vb, ctx=[250, 3][:len(nodes)], nodes=nodes, dtype=F16, books=books, seed=vb, contiguous=True)
+
+
+def test_attend_negative_norms(C):
+    """A norm below zero turns its row round; the formula holds for it as for any other."""
+    _check_attend(C, (8, 4, 64, 64), 4, 3, ctx=[150], nodes=[5], lo=-4.0, hi=4.0)
+    _check_attend(C, (4, 1, 256, 256), 2, 4, ctx=[150], nodes=[5], lo=-4.0, hi=4.0)
+    _check_attend(C, (4, 1, 128, 128), 3, 2, ctx=[150], nodes=[33], lo=-4.0, hi=4.0)
+
+
+def test_attend_all_requests_empty(C):
+    """No drafted tokens at all: nothing is written, nothing is reported."""
+    cb = O.analytic_codebook(2)
+    g = C.cq_kv_geometry(4, 2, 48, 64, 2, 2, cb, cb, 0.125)
+    kc, vc = (torch.from_numpy(_blob(64, w, 2, np.random.RandomState(i))).cuda() for i, w in ((1, 96), (2, 128)))
+    o = torch.full((3, 4, 64), 5.0, dtype=F16, device="cuda")
+    C.cq_kv_tree_attend(g, torch.zeros(3, 4, 48, dtype=F16, device="cuda"), kc, vc, 64, _i32([[0, 1], [2, 3]]), 16, _i32([20, 7]),
+                        _i32([0, 0, 0]), None, 3, o=o)
+    torch.cuda.synchronize()
+    assert (o == 5).all()
+    C.cq_device_status()
 
 
 def test_attend_causal_chunk(C):
