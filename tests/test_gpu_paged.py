@@ -722,3 +722,13 @@ def test_results_do_not_depend_on_the_run(C):
     first = C.cq_kv_tree_attend(*args)
     for _ in range(20):
         assert torch.equal(C.cq_kv_tree_attend(*args), first)
+
+
+def test_example_tree_gives_what_single_tokens_give():
+    """The example's layer: the verified path of a tree against the same tokens one
+    at a time. Both attend the same cache rows in another order: fp16 roundings of
+    the attention (2^-10), and at most one step of the int8 quantisation behind it
+    (1/127 of the largest element), of which few elements take one."""
+    from examples import verify_drafts
+    worst, accepted, _ = verify_drafts.run(requests=3, context=40, nodes=9, steps=3)
+    assert accepted >= 9 and worst < 2 ** -10 + 1 / 127
