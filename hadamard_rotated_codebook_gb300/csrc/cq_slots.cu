@@ -5,26 +5,31 @@
 // with r > m * max(n, 1e-12) (a tie falls to the lower level).
 //
 // Eight lanes own a group, 16 consecutive coordinates each: four stages of the
-// transform in registers, three by shuffles, and a warp stores four groups' codes as
-// whole words. A code is found by binary search (2 to 4 steps, the midpoints in shared
-// memory as a heap: at most 8 different words a step, never two in a bank).
+// transform in registers (two coordinates to an instruction), three by shuffles, and a warp
+// stores four groups' codes as whole words. A code is looked up: [-1, 1] is cut into 128
+// cells of equal width with at most one midpoint each, and a cell holds that midpoint (or the
+// nearest) and the code below it, so that one comparison decides. The table is repeated 16
+// times in shared memory, so that no two lanes of half a warp meet in a bank. Codebooks whose
+// midpoints lie too close for that are searched instead, over the midpoints as a heap.
 //
 // Decisions are those of exact arithmetic. In fp32 the seven stages and the
 // scaling are off by at most 8 roundings of 2^-24 of n (every partial sum is at most
-// n after scaling), 1/n by 7 and the quotient by 1: 16 in all, under 1e-6. The two
-// midpoints next to a coordinate lie on its search path, so the path tells whether it
-// is within 1e-6 of one; then, or where n lies within 1e-6 of a border between two fp16
-// values, those coordinates and the norm are computed again in fp64. For Gaussian rows that is
-// about 1% of the groups, and mostly one coordinate of them, so its sum is taken directly (the
-// transform of the whole group in fp64, at this GPU's sixty-fourth of the fp32 rate, would cost as
-// much as all the rest).
+// n after scaling), 1/n by 7 and the quotient by 1: 16 in all, under 1e-6. No midpoint
+// lies within 1/64 of a cell of its edge, so the cell's own midpoint (or the two next to a
+// coordinate on its search path) tells whether it is within 1e-6 of one; then, or where n lies
+// within 1e-6 of a border between two fp16 values, those coordinates and the norm are computed
+// again in fp64. For Gaussian rows that is about 1% of the groups, and mostly one coordinate of
+// them, so its sum is taken directly (the transform of the whole group in fp64, at this GPU's
+// sixty-fourth of the fp32 rate, would cost as much as all the rest).
 //
-// Bound by instructions (150 a group at four bits, 100 at three), not by memory.
+// Bound by instructions, not by memory: 8190 rows of 8 heads of 128 in bf16, four and three bits: see the figures at the
+// launcher.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "cq_paged.h"
 
@@ -34,6 +39,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr float kNear = 1e-6f;
+constexpr int kCells = 132;              // 64 to a unit, over [-1, 1] and a margin
+constexpr int kCopies = 16;
+constexpr int kTable = kCells * kCopies;  // entries of 8 bytes
 constexpr float kInvSqrt128 = 0.08838834764831845f;
 
 struct SideParams {
@@ -44,7 +52,11 @@ struct SideParams {
     int width, groups, bits;
     bool vec;            // rows start on 16-byte boundaries
     long long warps;     // of four groups each
+    bool cells;          // the cell table holds this codebook
     float heap[16];      // midpoints as a search heap: node 1 the middle one, children of k at 2k and 2k + 1
+    float offset;        // cell of u: the integer part of 64 u + offset - 2^16
+    float cell_mid[kCells];
+    uint8_t cell_code[kCells];
     double mid[15];
 };
 
@@ -58,6 +70,32 @@ struct SlotParams {
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Two fp32 operations in one instruction.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void f2_get(F2 a, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
 
 // 16 consecutive elements, zero past `have`.
 template <typename T>
@@ -116,7 +154,7 @@ __device__ __noinline__ void decide(const SideParams &s, const T *src, int have,
 }
 
 template <int LEVELS, typename T>
-__device__ __forceinline__ void encode(const SlotParams &p, const SideParams &s, const float *heap, long long warp_task, int lane) {
+__device__ __forceinline__ void encode(const SlotParams &p, const SideParams &s, const float2 *table, long long warp_task, int lane) {
     constexpr int W = LEVELS == 16 ? 4 : LEVELS == 8 ? 3 : 2;
     const int sub = lane & 7;
     const long long task = warp_task * 4 + (lane >> 3);
@@ -133,61 +171,97 @@ __device__ __forceinline__ void encode(const SlotParams &p, const SideParams &s,
     if (!__any_sync(0xFFFFFFFFu, live)) return;
     const int k0 = g * kGroup + 16 * sub, have = live ? s.width - k0 : 0;
     const T *src = static_cast<const T *>(s.rows) + i * s.stride + k0;
-    float x[16], n2 = 0.0f;
+    float x[16];
     load16(src, have, s.vec, x);
+    F2 z[8], q2 = f2(0.0f, 0.0f);  // elements 2 j and 2 j + 1
 #pragma unroll
-    for (int j = 0; j < 16; ++j) n2 = fmaf(x[j], x[j], n2);
+    for (int j = 0; j < 8; ++j) {
+        const F2 v = f2(x[2 * j], x[2 * j + 1]);
+        q2 = f2_fma(v, v, q2);
+        z[j] = f2(x[2 * j] + x[2 * j + 1], x[2 * j] - x[2 * j + 1]);
+    }
+    float n2, other;
+    f2_get(q2, n2, other);
+    n2 += other;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) n2 += __shfl_xor_sync(0xFFFFFFFFu, n2, o);
+    const F2 minus = f2(-1.0f, -1.0f);
 #pragma unroll
-    for (int h = 1; h < 16; h <<= 1)
+    for (int h = 1; h < 8; h <<= 1)
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < 8; ++j)
             if (!(j & h)) {
-                const float a = x[j], b = x[j + h];
-                x[j] = a + b, x[j + h] = a - b;
+                const F2 a = z[j], b = z[j + h];
+                z[j] = f2_add(a, b), z[j + h] = f2_fma(b, minus, a);
             }
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
         const float sign = (sub & o) ? -1.0f : 1.0f;
+        const F2 s2 = f2(sign, sign);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = fmaf(x[j], sign, __shfl_xor_sync(0xFFFFFFFFu, x[j], o));
+        for (int j = 0; j < 8; ++j) {
+            float a, b;
+            f2_get(z[j], a, b);
+            z[j] = f2_fma(z[j], s2, f2(__shfl_xor_sync(0xFFFFFFFFu, a, o), __shfl_xor_sync(0xFFFFFFFFu, b, o)));
+        }
     }
     const float n = sqrtf(n2), scale = kInvSqrt128 / fmaxf(n, 1e-12f);
-    unsigned near = 0;
-    uint64_t codes = 0;
-    const float first = heap[1];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const float u = x[j] * scale;
-        int c;
-        float dist;
-        if (LEVELS == 3) {
-            const float a = u - heap[1], b = u - heap[2];
-            c = ((a > 0.0f) + (b > 0.0f) - 1) & 3;
-            dist = fminf(fabsf(a), fabsf(b));
-        } else {
-            float d = u - first;
-            dist = fabsf(d);
-            int k = d > 0.0f ? 3 : 2;
-#pragma unroll
-            for (int l = 1; l < W; ++l) {
-                d = u - heap[k];
-                dist = fminf(dist, fabsf(d));
-                k = 2 * k + (d > 0.0f);
-            }
-            c = k - LEVELS;
-        }
-        near |= (unsigned)(dist <= kNear) << j;
-        codes |= (uint64_t)(unsigned)c << (j * W);
+    for (int j = 0; j < 8; ++j) {
+        f2_get(f2_mul(z[j], f2(scale, scale)), x[2 * j], x[2 * j + 1]);
     }
+    unsigned near = 0;
+    uint32_t word[2] = {0, 0};  // codes: 16 W bits, the second half from bit 8 W on
+    if (s.cells) {
+        // 64 u + offset behind 2^16: the sum has seven bits of fraction, so its bits 7 to 14 are the cell, and masked in place
+        // the byte offset of the cell's 16 entries of 8 bytes. What is not a number ends in the last cell.
+        const char *mine = reinterpret_cast<const char *>(table) + (lane & (kCopies - 1)) * 8;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float at = fminf(fmaf(x[j], 64.0f, s.offset), 65536.0f + (kCells - 1));
+            const float2 e = *reinterpret_cast<const float2 *>(mine + (__float_as_uint(at) & 0x7F80u));
+            const float d = x[j] - e.x;
+            unsigned c = __float_as_uint(e.y) + (d > 0.0f);
+            if (LEVELS == 3) c = (c - 1) & 3;
+            word[j / 8] |= c << (j % 8 * W);
+            near |= (unsigned)(fabsf(d) <= kNear) << j;
+        }
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < 16; ++j) {
+            float u = x[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) u = i == j ? x[i] : u;
+            unsigned c;
+            float dist;
+            if (LEVELS == 3) {
+                const float a = u - s.heap[1], b = u - s.heap[2];
+                c = ((a > 0.0f) + (b > 0.0f) - 1) & 3;
+                dist = fminf(fabsf(a), fabsf(b));
+            } else {
+                unsigned k = 1;
+                dist = 4.0f;
+#pragma unroll 1
+                for (int l = 0; l < W; ++l) {
+                    const float d = u - s.heap[k];
+                    dist = fminf(dist, fabsf(d));
+                    k = 2 * k + (d > 0.0f);
+                }
+                c = k - LEVELS;
+            }
+            if (j < 8) word[0] |= c << (j * W);
+            else word[1] |= c << ((j - 8) * W);
+            near |= (unsigned)(dist <= kNear) << j;
+        }
+    }
+    uint64_t codes = word[0] | (uint64_t)word[1] << (8 * W);
     __half norm = __float2half_rn(n);
     bool wild = n2 < 1e-30f || n2 > 1e30f;  // a sum of squares that fp32 may not hold
     if (__any_sync(0xFFFFFFFFu, wild)) {
         // a group of zeros is decided as it stands (every coordinate is exactly zero); else every coordinate again
         bool nonzero = false;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) nonzero |= x[j] != 0.0f;
+        for (int j = 0; j < 16; ++j) nonzero |= !(x[j] == 0.0f);
         nonzero = __ballot_sync(0xFFFFFFFFu, nonzero) >> (lane & 24) & 0xFFu;
         if (wild) near = nonzero ? 0xFFFFu : 0u;
     }
@@ -210,25 +284,55 @@ __device__ __forceinline__ void encode(const SlotParams &p, const SideParams &s,
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv_write_slots_kernel(const __grid_constant__ SlotParams p) {
-    __shared__ float heap[2][16];
+    extern __shared__ float2 s_table[];
     const int tid = threadIdx.x, lane = tid & 31;
-    if (tid < 32) heap[tid >> 4][tid & 15] = p.side[tid >> 4].heap[tid & 15];
+    for (int i = tid; i < 2 * kTable; i += kThreads) {
+        const SideParams &s = p.side[i >= kTable];
+        const int cell = (i >= kTable ? i - kTable : i) / kCopies;
+        s_table[i] = make_float2(s.cell_mid[cell], __uint_as_float(s.cell_code[cell]));
+    }
     __syncthreads();
     const long long all = p.side[0].warps + p.side[1].warps;
     for (long long t = (long long)blockIdx.x * kWarps + (tid >> 5); t < all; t += (long long)gridDim.x * kWarps) {
         const int which = t >= p.side[0].warps;
         const SideParams &s = p.side[which];
         const long long task = which ? t - p.side[0].warps : t;
+        const float2 *table = s_table + which * kTable;
         switch (s.bits) {
-        case 2: encode<4, T>(p, s, heap[which], task, lane); break;
-        case 3: encode<8, T>(p, s, heap[which], task, lane); break;
-        case 4: encode<16, T>(p, s, heap[which], task, lane); break;
-        default: encode<3, T>(p, s, heap[which], task, lane); break;
+        case 2: encode<4, T>(p, s, table, task, lane); break;
+        case 3: encode<8, T>(p, s, table, task, lane); break;
+        case 4: encode<16, T>(p, s, table, task, lane); break;
+        default: encode<3, T>(p, s, table, task, lane); break;
         }
     }
 }
 
 }  // namespace
+
+// The cells of a codebook: an offset of the grid for which every cell has at most one midpoint and none lies within 1/64 of a
+// cell of an edge (the cell of a coordinate is found to 1/128), looked for among 64. False if there is none.
+static bool find_cells(const double *mid, int n, SideParams &s) {
+    int at[15];
+    for (int k = 0; k < 64; ++k) {
+        const double offset = 65.0 + k / 64.0;  // -1 lies in cell 1, 1 in cell 130 at most
+        bool ok = true;
+        for (int l = 0; l < n && ok; ++l) {
+            const double v = std::min(std::max(64.0 * mid[l] + offset, -1.5), kCells + 0.5);  // what no coordinate reaches: outside
+            at[l] = (int)std::floor(v);
+            const double in = v - at[l];
+            if (at[l] >= 0 && at[l] < kCells) ok = in > 1.0 / 64 && in < 63.0 / 64 && (!l || at[l] != at[l - 1]);
+        }
+        if (!ok) continue;
+        s.offset = (float)(65536.0 + offset);
+        for (int c = 0, l = 0; c < kCells; ++c) {
+            while (l < n && at[l] < c) ++l;  // midpoints below the cell
+            s.cell_mid[c] = l < n && at[l] == c ? (float)mid[l] : 8.0f;  // 8: none here, and no coordinate is near it
+            s.cell_code[c] = (uint8_t)l;
+        }
+        return true;
+    }
+    return false;
+}
 
 int launch_kv_write_slots(const SlotSide side[2], int cap, int dtype, const int32_t *slots, int n, void *stream) {
     SlotParams p;
@@ -246,6 +350,7 @@ int launch_kv_write_slots(const SlotSide side[2], int cap, int dtype, const int3
         const int levels = levels_of(a.bits);
         for (int l = 0; l < 16; ++l) s.heap[l] = 0.0f;
         for (int l = 0; l + 1 < levels; ++l) s.mid[l] = 0.5 * ((double)a.codebook[l] + (double)a.codebook[l + 1]);
+        s.cells = find_cells(s.mid, levels - 1, s);
         if (levels == 3) {
             s.heap[1] = (float)s.mid[0], s.heap[2] = (float)s.mid[1];
         } else {
@@ -259,11 +364,11 @@ int launch_kv_write_slots(const SlotSide side[2], int cap, int dtype, const int3
     p.status = device_status_ptr();
     if (!p.status) return set_error(CQ_ERR_CUDA, "no device status word");
     const long long blocks = (p.side[0].warps + p.side[1].warps + kWarps - 1) / kWarps;
-    const int grid = (int)std::min<long long>(blocks, 8LL * sm_count());
+    const int grid = (int)std::min<long long>(blocks, 4LL * sm_count()), smem = 2 * kTable * (int)sizeof(float2);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == CQ_T_F32) kv_write_slots_kernel<float><<<grid, kThreads, 0, st>>>(p);
-    else if (dtype == CQ_T_F16) kv_write_slots_kernel<__half><<<grid, kThreads, 0, st>>>(p);
-    else kv_write_slots_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(p);
+    if (dtype == CQ_T_F32) kv_write_slots_kernel<float><<<grid, kThreads, smem, st>>>(p);
+    else if (dtype == CQ_T_F16) kv_write_slots_kernel<__half><<<grid, kThreads, smem, st>>>(p);
+    else kv_write_slots_kernel<__nv_bfloat16><<<grid, kThreads, smem, st>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(CQ_ERR_CUDA, "slot write launch: %s", cudaGetErrorString(e));
     return CQ_OK;

@@ -270,6 +270,43 @@ def test_write_slots_borders(C, bits):
     _check_write(C, 1, 128, 128, bits, bits, F32, x, x.flip(0).contiguous(), list(range(len(rows))), len(rows) + 3)
 
 
+def test_write_slots_other_codebooks(C):
+    """Codebooks that are not symmetric, with midpoints closer than a cell of the lookup, past the largest
+    coordinate, and on round numbers."""
+    rng = np.random.RandomState(0)
+    x = torch.randn(64, 300, device="cuda")
+    books = [np.sort(rng.uniform(-0.3, 0.3, 16)), 0.001 * np.arange(16) - 0.004, np.linspace(-3, 3, 16), np.linspace(-0.25, 0.25, 16),
+             np.concatenate([np.linspace(-0.2, 0.2, 15), [9.0]])]
+    for cb in books:
+        cb = cb.astype(np.float32)
+        g = C.cq_kv_geometry(1, 1, 300, 300, 4, 4, cb, cb[::-1] * -1, 1.0)
+        blobs = [torch.zeros(C.cq_packed_bytes(64, 300, 128, 4), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        C.cq_kv_write_slots(g, *blobs, 64, x, x, _i32(np.arange(64)))
+        for blob, book in zip(blobs, (cb, cb[::-1] * -1)):
+            codes, norms = R.encode(_np(x), 4, book)
+            gc, gn = R.split_blob(blob.cpu().numpy(), 64, 300, 4)
+            np.testing.assert_array_equal(gc, R.pack(codes, 4))
+            np.testing.assert_array_equal(gn.view(np.uint16), norms.view(np.uint16))
+
+
+def test_write_slots_non_finite_rows(C):
+    """A row with a NaN or an infinity gets a norm that is not finite and reaches no other row."""
+    x = torch.randn(9, 128, device="cuda")
+    bad = x.clone()
+    bad[2, 5], bad[4, 0], bad[6, 9] = math.nan, math.inf, -math.inf
+    cb = O.analytic_codebook(4)
+    g = C.cq_kv_geometry(1, 1, 128, 128, 4, 4, cb, cb, 1.0)
+    out = []
+    for rows in (x, bad):
+        blobs = [torch.zeros(C.cq_packed_bytes(9, 128, 128, 4), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        C.cq_kv_write_slots(g, *blobs, 9, rows, rows, _i32(np.arange(9)))
+        out.append(R.split_blob(blobs[0].cpu().numpy(), 9, 128, 4))
+    keep = [0, 1, 3, 5, 7, 8]
+    np.testing.assert_array_equal(out[0][0][keep], out[1][0][keep])
+    np.testing.assert_array_equal(out[0][1][keep], out[1][1][keep])
+    assert not np.isfinite(out[1][1][[2, 4, 6]].astype(np.float32)).any()
+
+
 def test_write_slots_matches_kv_write(C):
     """Away from borders it is cq_kv_write: the same bytes for ordinary rows."""
     x, y = torch.randn(50, 96, device="cuda"), torch.randn(50, 128, device="cuda")
