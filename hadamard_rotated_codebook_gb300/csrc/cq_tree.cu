@@ -50,6 +50,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <cstring>
 
 #include "cq_paged.h"
 
@@ -471,25 +472,27 @@ __device__ __forceinline__ void expand_quarter(const uint32_t *c, const uint32_t
 }
 
 // ---------------------------------------------------------------- the kernel --
-template <int N, int NG>
+template <int N, int NG, int ZT>
 struct Plan {
     static constexpr int kSoftWG = N >= 64 ? 2 : 1;              // warpgroups of softmax
     static constexpr int kSoft = 4 * kSoftWG, kExp = 8;         // warps; then the issuer, two fetchers, one idle
     static constexpr int kThreads = 32 * (kSoft + kExp + 4);
     static constexpr int kIssue = N <= 32 ? 4 : 1;               // MMAs in line: with few columns the issuer is the slowest role
-    static constexpr int kVBuf = NG == 1 ? 2 : 1;
+    static constexpr int kVBuf = NG == 1 && !(N == 128 && ZT == 2) ? 2 : 1;
     static constexpr int kVBytes = 2 * kTile * 128;            // one group's values: 128 rows x 128 fp16
     static constexpr int kPBytes = kTile * (N <= 64 ? 128 : 256);
     static constexpr int kZBytes = N * 256;                    // one group
-    // Queries of a 16-bit type come rotated as a sum of two fp16 terms while there is room (and tensor work to spare): one term
-    // would be the largest part of an fp16 result's error. bf16 results do not show it.
-    static constexpr int kZTerms = N <= 64 && NG == 1 ? 2 : 1;
-    static constexpr int oV = 0, oP = oV + kVBuf * NG * kVBytes, oZ = oP + kPBytes, oShared = oZ + NG * kZTerms * kZBytes;
-    static constexpr int oRing = oShared + ((int)sizeof(Shared) + 127) / 128 * 128;
+    // ZT: fp16 queries come rotated as a sum of two fp16 terms: one term would be the largest part of an fp16 result's error
+    // (0.00048 against the 0.0002 of the result's own rounding). bf16 results do not show it. At 128 columns the second
+    // term takes the place of the second buffer of values, in a kernel of its own.
+    static constexpr int oV = 0, oP = oV + kVBuf * NG * kVBytes, oZ = oP + kPBytes, oShared = oZ + NG * ZT * kZBytes;
+    static constexpr int oRatio = oShared + ((int)sizeof(Shared) + 127) / 128 * 128;  // per tile buffer and group: a row's key norms over the larger
+    static constexpr int oRing = oRatio + (NG == 2 ? 2 * NG * kTile * 4 : 0);
     // registers of the roles where softmax takes two warpgroups: 256 (kSoftRegs + kExpRegs) + 128 kRestRegs <= 640 x 96
     static constexpr int kSoftRegs = N == 128 ? 144 : 128, kExpRegs = N == 128 ? 64 : 72, kRestRegs = N == 128 ? 64 : 80;
     // TMEM columns
-    static constexpr int cK = 0, cS = 2 * NG * 64, cO = cS + 2 * N;
+    static constexpr int kKBuf = NG == 2 && N == 64 ? 1 : 2;     // 512 columns hold no second buffer of keys then
+    static constexpr int cK = 0, cS = kKBuf * NG * 64, cO = cS + 2 * NG * N;
     static_assert(cO + NG * N <= 512, "tensor memory");
 };
 
@@ -567,9 +570,9 @@ __device__ __forceinline__ void fetch_side(const Side &s, uint32_t r, size_t all
     sts32(info, word);
 }
 
-template <int N, int NG>
+template <int N, int NG, int ZT>
 __device__ void fetch_role(const TreeParams &p, Shared &sh, uint8_t *smem, int lane) {
-    using L = Plan<N, NG>;
+    using L = Plan<N, NG, ZT>;
     Cursor c = sh.start;
     const int tiles = uniform(c.left);
     const uint32_t ring = smem_u32(smem) + L::oRing;
@@ -623,36 +626,35 @@ __device__ __forceinline__ float norm_value(uint32_t info, uint32_t word, int g,
 }
 
 // The two products of tile i, issued by one warp. `first`: the tile starts its item's part.
-template <int N, int NG>
+template <int N, int NG, int ZT>
 __device__ __forceinline__ void issue_scores(const TreeParams &p, Shared &sh, uint8_t *smem, uint32_t tmem, int i, bool two) {
-    using L = Plan<N, NG>;
-    const int b = i & 1;
+    using L = Plan<N, NG, ZT>;
+    const int b = i & 1, kb = L::kKBuf == 2 ? b : 0;
     const uint32_t par = (uint32_t)(i >> 1) & 1;
     const uint64_t dz = desc_sw128(smem_u32(smem + L::oZ), 16);
-    wait(sh, &sh.k_full[b], par, p.status, 0x47490004u);
+    wait(sh, &sh.k_full[kb], L::kKBuf == 2 ? par : (uint32_t)(i & 1), p.status, 0x47490004u);
     wait(sh, &sh.s_empty[b], par ^ 1, p.status, 0x47490005u);
     __syncwarp();
     fence_after();
+    // two groups keep their scores apart: their norms are ratios for softmax, which multiplies in fp32
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         if (g == 1 && !two) break;
+#pragma unroll
+        for (int t = 0; t < ZT; ++t) {
+            if (t == 1 && N < 128 && p.t.dtype != CQ_T_F16) break;  // the second term of the queries
 #pragma unroll L::kIssue
-        for (int k = 0; k < 8; ++k)
-            mma_ts(tmem + L::cS + b * N, tmem + L::cK + (b * NG + g) * 64 + 8 * k,
-                   dz + (uint64_t)((g * L::kZBytes + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), idesc_f16(128, N, 0, 0), (g | k) != 0);
+            for (int k = 0; k < 8; ++k)
+                mma_ts(tmem + L::cS + (b * NG + g) * N, tmem + L::cK + (kb * NG + g) * 64 + 8 * k,
+                       dz + (uint64_t)(((t * NG + g) * L::kZBytes + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), idesc_f16(128, N, 0, 0), (t | k) != 0);
+        }
     }
-    if (L::kZTerms == 2 && p.t.dtype == CQ_T_F16) {  // the second term of the queries
-#pragma unroll L::kIssue
-        for (int k = 0; k < 8; ++k)
-            mma_ts(tmem + L::cS + b * N, tmem + L::cK + b * 64 + 8 * k,
-                   dz + (uint64_t)((L::kZBytes + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), idesc_f16(128, N, 0, 0), 1);
-    }
-    mma_commit(&sh.k_empty[b]);
+    mma_commit(&sh.k_empty[kb]);
     mma_commit(&sh.s_full[b]);
 }
-template <int N, int NG>
+template <int N, int NG, int ZT>
 __device__ __forceinline__ void issue_sums(const TreeParams &p, Shared &sh, uint8_t *smem, uint32_t tmem, int i, bool first, bool two) {
-    using L = Plan<N, NG>;
+    using L = Plan<N, NG, ZT>;
     const int vb = L::kVBuf == 2 ? i & 1 : 0;
     wait(sh, &sh.v_full[vb], L::kVBuf == 2 ? (uint32_t)(i >> 1) & 1 : (uint32_t)(i & 1), p.status, 0x47490007u);
     wait(sh, &sh.p_full, (uint32_t)(i & 1), p.status, 0x47490008u);
@@ -672,7 +674,7 @@ __device__ __forceinline__ void issue_sums(const TreeParams &p, Shared &sh, uint
     mma_commit(&sh.p_empty);
 }
 
-template <int N, int NG>
+template <int N, int NG, int ZT>
 __device__ void issue_role(const TreeParams &p, Shared &sh, uint8_t *smem) {
     Cursor c = sh.start;
     const uint32_t tmem = uniform(sh.tmem);
@@ -685,13 +687,13 @@ __device__ void issue_role(const TreeParams &p, Shared &sh, uint8_t *smem) {
         if (next_first) {
             wait(sh, &sh.z_full, zpar, p.status, 0x47490006u);
             zpar ^= 1;
-            issue_scores<N, NG>(p, sh, smem, tmem, i, two_k);
+            issue_scores<N, NG, ZT>(p, sh, smem, tmem, i, two_k);
         }
         first = next_first;
         const bool more = c.advance(p, N);
         next_first = uniform(!more || c.tile == 0);
-        if (!next_first) issue_scores<N, NG>(p, sh, smem, tmem, i + 1, two_k);  // while softmax works on tile i
-        issue_sums<N, NG>(p, sh, smem, tmem, i, first, two_v);
+        if (!next_first) issue_scores<N, NG, ZT>(p, sh, smem, tmem, i + 1, two_k);  // while softmax works on tile i
+        issue_sums<N, NG, ZT>(p, sh, smem, tmem, i, first, two_v);
     }
     mma_commit(&sh.drain);  // MMAs in flight finish before tensor memory is freed
     for (unsigned k = 0; k < kSpin; ++k)
@@ -759,10 +761,10 @@ __device__ void fill_table(uint32_t dst, const uint32_t (&t)[8], int w, bool wid
 }
 
 // Expander warps: keys into tensor memory, values into shared memory, and the rows' norms for softmax. One code for both sides.
-template <int N, int NG, int W>
+template <int N, int NG, int ZT, int W>
 __device__ __forceinline__ void expand_tile(const TreeParams &p, uint8_t *smem, uint32_t tmem, bool keys, uint32_t codes, uint32_t tab, int buf, int row,
                                             int q, const float (&ratio)[2], uint32_t flip, bool two) {
-    using L = Plan<N, NG>;
+    using L = Plan<N, NG, ZT>;
 #pragma unroll 1
     for (int g = 0; g < (two ? 2 : 1); ++g) {
         uint32_t t[8];
@@ -770,7 +772,9 @@ __device__ __forceinline__ void expand_tile(const TreeParams &p, uint8_t *smem, 
 #pragma unroll
             for (int j = 0; j < 8; ++j) t[j] = keys ? p.tk[j] : j < 4 ? p.tv[j] : p.tv[j] ^ (flip & 0x80808080u);
         }
-        const __half2 r2 = __float2half2_rn(NG == 2 && g ? ratio[1] : ratio[0]);
+        // the ratio as two fp16 terms: what is left is the product's one rounding
+        const float ratio_g = NG == 2 && g ? ratio[1] : ratio[0];
+        const __half2 r2 = __float2half2_rn(ratio_g), r2_low = __float2half2_rn(ratio_g - __low2float(r2));
         const bool turned = NG == 1 && __any_sync(0xFFFFFFFFu, flip != 0);
         const uint32_t from = codes + g * W * kTile * 16;
         const uint32_t to_k = tmem + ((uint32_t)(32 * q) << 16) + L::cK + (buf * NG + g) * 64;
@@ -790,7 +794,7 @@ __device__ __forceinline__ void expand_tile(const TreeParams &p, uint8_t *smem, 
                 expand_quarter<W>(c, t, r);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&r[j]), r2);
+                    const __half2 l = *reinterpret_cast<__half2 *>(&r[j]), x = __hfma2(l, r2, __hmul2(l, r2_low));
                     r[j] = *reinterpret_cast<const uint32_t *>(&x);
                 }
             }
@@ -828,9 +832,9 @@ __device__ __forceinline__ float row_norm(uint32_t info, uint32_t norms, bool tw
     return lost ? __int_as_float(0x7FC00000) : nn;
 }
 
-template <int N, int NG>
+template <int N, int NG, int ZT>
 __device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, bool keys, int row, int q, int lane) {
-    using L = Plan<N, NG>;
+    using L = Plan<N, NG, ZT>;
     Cursor c = sh.start;
     const int tiles = uniform(c.left), w = keys ? p.wk : p.wv;
     const uint32_t tmem = uniform(sh.tmem), ring = smem_u32(smem) + L::oRing;
@@ -839,7 +843,8 @@ __device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, bool
     uint32_t rpar = 0;
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
-        const int b = i & 1, buf = keys || L::kVBuf == 2 ? b : 0;
+        const bool twice = (keys ? L::kKBuf : L::kVBuf) == 2;
+        const int b = i & 1, buf = twice ? b : 0;
         const uint32_t par = (uint32_t)(i >> 1) & 1;
         bool two = false;
         if (NG == 2) {
@@ -867,18 +872,24 @@ __device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, bool
         wait(sh, &sh.s_empty[b], par ^ 1, p.status, 0x47490001u);
         if (keys) {
             sh.scal[b][0][row] = real ? n : 0.0f;
+            if (NG == 2) {  // softmax applies the ratios of the keys, in fp32
+                const uint32_t to = smem_u32(smem + L::oRatio) + (b * 2 * kTile + row) * 4;
+                sts32(to, __float_as_uint(ratio[0]));
+                sts32(to + kTile * 4, __float_as_uint(ratio[1]));
+                ratio[0] = ratio[1] = 1.0f;
+            }
         } else {
             sh.scal[b][1][row] = real ? ln : -INFINITY;
             sh.scal[b][2][row] = real ? inv : 0.0f;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sc_full[b]);
-        wait(sh, keys ? &sh.k_empty[buf] : &sh.v_empty[buf], (keys || L::kVBuf == 2 ? par : (uint32_t)(i & 1)) ^ 1, p.status, 0x47490002u);
+        wait(sh, keys ? &sh.k_empty[buf] : &sh.v_empty[buf], (twice ? par : (uint32_t)(i & 1)) ^ 1, p.status, 0x47490002u);
         fence_after();
         const uint32_t from = keys ? codes : codes + Stage<NG>::codes(p.wk);
-        if (w == 2) expand_tile<N, NG, 2>(p, smem, tmem, keys, from, tab, buf, row, q, ratio, flip, two);
-        else if (w == 3) expand_tile<N, NG, 3>(p, smem, tmem, keys, from, tab, buf, row, q, ratio, flip, two);
-        else expand_tile<N, NG, 4>(p, smem, tmem, keys, from, tab, buf, row, q, ratio, flip, two);
+        if (w == 2) expand_tile<N, NG, ZT, 2>(p, smem, tmem, keys, from, tab, buf, row, q, ratio, flip, two);
+        else if (w == 3) expand_tile<N, NG, ZT, 3>(p, smem, tmem, keys, from, tab, buf, row, q, ratio, flip, two);
+        else expand_tile<N, NG, ZT, 4>(p, smem, tmem, keys, from, tab, buf, row, q, ratio, flip, two);
         wait_st();
         fence_before();
         fence_async();
@@ -914,14 +925,14 @@ __device__ __forceinline__ float load_q(const TreeParams &p, int64_t at) {
 // boundaries (`vec_q`): stash_queries starts their copies into the buffer of the weights, idle between two
 // items, while the partials of the item before are written, and each lane reads back its own. Else a warp takes a column
 // and reads it twice.
-template <int N, int NG>
+template <int N, int NG, int ZT>
 __device__ __forceinline__ uint32_t stash_at(uint8_t *smem, int i, int warp, int lane) {
-    using L = Plan<N, NG>;
+    using L = Plan<N, NG, ZT>;
     return smem_u32(smem + L::oP) + ((i * L::kSoft + warp) * 32 + lane) * 32;
 }
-template <int N, int NG>
+template <int N, int NG, int ZT>
 __device__ __forceinline__ void stash_queries(const TreeParams &p, uint8_t *smem, const Cursor &c, int warp, int lane) {
-    using L = Plan<N, NG>;
+    using L = Plan<N, NG, ZT>;
     if (NG == 2 || !p.vec_q) return;
     const int rows = p.unit[c.u].nh * p.per, h0 = p.unit[c.u].h0, cols = min(N, c.n * rows - c.c * N);
     const int g0 = p.unit[c.u].gk * kGroup + 16 * (lane & 7);
@@ -929,7 +940,7 @@ __device__ __forceinline__ void stash_queries(const TreeParams &p, uint8_t *smem
     for (int i = 0; i < N / (4 * L::kSoft); ++i) {
         const int col = warp * 4 + (lane >> 3) + i * 4 * L::kSoft;
         const int at = c.c * N + col, node = at / rows, r = at - node * rows, d0 = g0 - (h0 + r / p.per) * p.dk;
-        const uint32_t to = stash_at<N, NG>(smem, i, warp, lane);
+        const uint32_t to = stash_at<N, NG, ZT>(smem, i, warp, lane);
         if (col < cols && d0 >= 0 && d0 < p.dk) {
             const __half *from = static_cast<const __half *>(p.t.q) + (int64_t)(c.first + node) * p.t.q_stride_t +
                                  (int64_t)(h0 * p.per + r) * p.t.q_stride_h + d0;
@@ -945,9 +956,9 @@ __device__ __forceinline__ void stash_queries(const TreeParams &p, uint8_t *smem
 // The rotated queries into shared memory (the K-major B operand), scaled by one power of two so that fp16 holds them whatever their
 // size (a coordinate is at most the sum of the query's 128 or fewer magnitudes); returns what takes the scale back out
 // of the logits.
-template <int N, int NG>
+template <int N, int NG, int ZT>
 __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, const Cursor &c, int warp, int lane) {
-    using L = Plan<N, NG>;
+    using L = Plan<N, NG, ZT>;
     const TreeUnit u = p.unit[c.u];
     const int rows = u.nh * p.per, cols = min(N, c.n * rows - c.c * N);
     const bool fast = NG == 1 && p.vec_q, half = p.t.dtype == CQ_T_F16;
@@ -967,7 +978,7 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
         uint32_t most = 0;  // magnitudes of a 16-bit type are ordered as integers
 #pragma unroll 1
         for (int i = 0; i < 2 * N / (4 * L::kSoft); ++i) {
-            const uint4 v = lds128(stash_at<N, NG>(smem, i >> 1, warp, lane) + (i & 1) * 16);
+            const uint4 v = lds128(stash_at<N, NG, ZT>(smem, i >> 1, warp, lane) + (i & 1) * 16);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -1001,7 +1012,7 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
 #pragma unroll 1
         for (int i = 0; i < N / (4 * L::kSoft); ++i) {
             const int sub = lane & 7, col = warp * 4 + (lane >> 3) + i * 4 * L::kSoft;
-            const uint32_t from = stash_at<N, NG>(smem, i, warp, lane);
+            const uint32_t from = stash_at<N, NG, ZT>(smem, i, warp, lane);
             const uint4 v0 = lds128(from), v1 = lds128(from + 16);
             const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
             F2 z[8];  // elements 2 j and 2 j + 1
@@ -1042,7 +1053,7 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
             const uint32_t base = smem_u32(smem + L::oZ) + (sub >> 2) * (N * 128) + (col >> 3) * 1024 + (col & 7) * 128;
             sts128(base + (((2 * (sub & 3)) ^ (col & 7)) << 4), h2[0], h2[1], h2[2], h2[3]);
             sts128(base + (((2 * (sub & 3) + 1) ^ (col & 7)) << 4), h2[4], h2[5], h2[6], h2[7]);
-            if (L::kZTerms == 2 && half) {
+            if (ZT == 2 && half) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float x, y;
@@ -1069,10 +1080,10 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
                 const __half2 v = __floats2half2_rn(x, y);
                 const uint32_t to = base + (pos >> 6) * (N * 128) + ((((pos & 63) >> 3) ^ (col & 7)) << 4) + (pos & 7) * 2;
                 sts32(to, *reinterpret_cast<const uint32_t *>(&v));
-                if (L::kZTerms == 2) {
+                if (ZT == 2 && half) {
                     const float2 hi = __half22float2(v);
                     const __half2 l = __floats2half2_rn(x - hi.x, y - hi.y);
-                    sts32(to + L::kZBytes, *reinterpret_cast<const uint32_t *>(&l));
+                    sts32(to + NG * L::kZBytes, *reinterpret_cast<const uint32_t *>(&l));
                 }
             };
             if (NG == 2 && p.wk == 2) {
@@ -1114,18 +1125,34 @@ __device__ __forceinline__ float warp_max(float x) {  // NaNs count as nothing
     return r;
 }
 
+// Scores of X columns for this thread's cache row; with two groups their sum in the ratio r0 : r1 of the row's norms.
+template <int N, int NG, int X>
+__device__ __forceinline__ void load_scores(uint32_t ts, float (&d)[X], float r0, float r1, bool two) {
+    tmem_ld<X>(ts, d);
+    wait_ld<X>(d);
+    if (NG == 2 && two) {
+#pragma unroll
+        for (int k = 0; k < X; k += 8) {
+            float e[8];
+            tmem_ld<8>(ts + N + k, e);
+            wait_ld<8>(e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[k + j] = fmaf(e[j], r1, d[k + j] * r0);
+        }
+    }
+}
+
 // Raises the references of columns cx .. cx + X - 1 whose largest logit of this tile (columns in tensor memory at ts, this
 // thread's cache row) passes the weights' range; the factors for what was summed before go to sh.f. All four warps of
 // the warpgroup; true if any was raised. Kept out of the loop's straight line: it runs in the first tile and rarely after.
-template <int N, int X>
-__device__ __noinline__ bool raise(Shared &sh, uint32_t ts, int cx, float nk, float ln, uint32_t see, int warp, int lane) {
+template <int N, int NG, int X>
+__device__ __noinline__ bool raise(Shared &sh, uint32_t ts, int cx, float nk, float ln, float r0, float r1, bool two, uint32_t see, int warp, int lane) {
     const int wg = warp >> 2, row = 32 * (warp & 3) + lane;
     float mine = 0.0f;
 #pragma unroll 1
     for (int k = 0; k < X; k += 8) {
         float d[8];
-        tmem_ld<8>(ts + k, d);
-        wait_ld<8>(d);
+        load_scores<N, NG, 8>(ts + k, d, r0, r1, two);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float t = see >> (k + j) & 1 ? fmaf(d[j], nk, ln) : -INFINITY;
@@ -1150,14 +1177,13 @@ __device__ __noinline__ bool raise(Shared &sh, uint32_t ts, int cx, float nk, fl
 
 // The first references of an item's part: the largest finite logits of the tile's first 32 cache rows, by their warp alone. With
 // 2^15 above them that holds nearly always, and costs the other warps a barrier.
-template <int X>
-__device__ __noinline__ void seed(Shared &sh, uint32_t ts, int cx, float nk, float ln, uint32_t see, int lane) {
+template <int N, int NG, int X>
+__device__ __noinline__ void seed(Shared &sh, uint32_t ts, int cx, float nk, float ln, float r0, float r1, bool two, uint32_t see, int lane) {
     float mine = kNoMax;
 #pragma unroll 1
     for (int k = 0; k < X; k += 8) {
         float d[8];
-        tmem_ld<8>(ts + k, d);
-        wait_ld<8>(d);
+        load_scores<N, NG, 8>(ts + k, d, r0, r1, two);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float t = fmaf(d[j], nk, ln);
@@ -1185,9 +1211,9 @@ __device__ __noinline__ void scale_sums(Shared &sh, uint32_t to, int n, int grou
     wait_st();
 }
 
-template <int N, int NG>
+template <int N, int NG, int ZT>
 __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int warp, int lane) {
-    using L = Plan<N, NG>;
+    using L = Plan<N, NG, ZT>;
     constexpr int NC = N / L::kSoftWG;         // columns of this warpgroup
     constexpr int kSoftThreads = 32 * L::kSoft;
     constexpr int X = NC < 32 ? NC : 32;       // columns per tensor memory load
@@ -1197,7 +1223,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
     int i = 0;
     long long done = sh.run[0];  // tiles of the blocks before and of this one so far
     bool more = true;
-    stash_queries<N, NG>(p, smem, c, warp, lane);
+    stash_queries<N, NG, ZT>(p, smem, c, warp, lane);
     while (more) {
         // ------------------------------------------------ one item's part --
         bar_sync(1, kSoftThreads);  // the item before is finished: zmax, m, mask may be written
@@ -1205,7 +1231,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
         if (row < NC) sh.minus_m[c0 + row] = -kNoMax;
         gather_mask<N>(p, sh, c, warp, L::kSoft, lane);
         bar_sync(1, kSoftThreads);
-        const float mult = rotate_queries<N, NG>(p, sh, smem, c, warp, lane);
+        const float mult = rotate_queries<N, NG, ZT>(p, sh, smem, c, warp, lane);
         fence_async();
         fence_before();  // tensor memory reads of the item before
         __syncwarp();
@@ -1216,6 +1242,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
         if (c.tile == 0 && warp == 0 && lane == 0)
             p.rec[i0] = make_int2(slot, run_of(sh.total, p.grid, done + c.ntiles - 1) - (int)blockIdx.x + 1);
         const int count = min(c.ntiles - c.tile, c.left);
+        const bool two = NG == 2 && u.ngk == 2;
         F2 l[NC / 2];
 #pragma unroll
         for (int k = 0; k < NC / 2; ++k) l[k] = f2(0.0f, 0.0f);
@@ -1233,6 +1260,11 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
             }
             wait(sh, &sh.sc_full[b], par, p.status, 0x47490009u);
             const float nk = sh.scal[b][0][row] * mult, ln = sh.scal[b][1][row], inv = sh.scal[b][2][row];
+            float r0 = 1.0f, r1 = 0.0f;
+            if (NG == 2) {
+                const uint32_t from = smem_u32(smem + L::oRatio) + (b * 2 * kTile + row) * 4;
+                r0 = __uint_as_float(lds32(from)), r1 = __uint_as_float(lds32(from + kTile * 4));
+            }
             const F2 nk2 = f2(nk, nk), ln2 = f2(ln, ln), inv2 = f2(inv, inv);
             wait(sh, &sh.s_full[b], par, p.status, 0x4749000Au);
             fence_after();
@@ -1241,16 +1273,15 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
             for (int hf = 0; hf < NC; hf += X) {
                 float d[X];
                 const int cx = c0 + hf;
-                const uint32_t ts = tm + L::cS + b * N + cx;
+                const uint32_t ts = tm + L::cS + b * NG * N + cx;
                 bool raised = false;
                 if (__builtin_expect(it == 0, 0)) {
-                    if (q == 0) seed<X>(sh, ts, cx, nk, ln, masked ? see[hf / 32] : 0xFFFFFFFFu, lane);
+                    if (q == 0) seed<N, NG, X>(sh, ts, cx, nk, ln, r0, r1, two, masked ? see[hf / 32] : 0xFFFFFFFFu, lane);
                     bar_sync(2 + wg, 128);
                 }
 #pragma unroll 1
                 for (int pass = 0;; ++pass) {
-                    tmem_ld<X>(ts, d);
-                    wait_ld<X>(d);
+                    load_scores<N, NG, X>(ts, d, r0, r1, two);
                     float top = kNoMax;
 #pragma unroll
                     for (int k = 0; k < X; k += 4) {  // d = log2 of the weights
@@ -1265,7 +1296,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
 #pragma unroll
                     for (int k = 0; k < X; k += 2) top = max3(top, d[k], d[k + 1]);
                     if (!bar_or(2 + wg, 128, top > kRaise) || pass) break;
-                    raised = raise<N, X>(sh, ts, cx, nk, ln, masked ? see[hf / 32] : 0xFFFFFFFFu, warp, lane);
+                    raised = raise<N, NG, X>(sh, ts, cx, nk, ln, r0, r1, two, masked ? see[hf / 32] : 0xFFFFFFFFu, warp, lane);
                 }
                 if (__builtin_expect(raised, 0)) {
 #pragma unroll
@@ -1338,7 +1369,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
         if (more) c.next_item(p, N);
         wait(sh, &sh.p_empty, (uint32_t)(i - 1) & 1, p.status, 0x4749000Du);
         fence_after();
-        if (more) stash_queries<N, NG>(p, smem, c, warp, lane);
+        if (more) stash_queries<N, NG, ZT>(p, smem, c, warp, lane);
         const int nat = NG == 2 ? natural_of(row, p.wv) : row;
         for (int g = 0; g < u.ngv; ++g) {
             float *out = p.part + ((size_t)slot * NG + g) * N * kGroup + nat;
@@ -1356,9 +1387,9 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
     }
 }
 
-template <int N, int NG>
-__global__ void __launch_bounds__(Plan<N, NG>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
-    using L = Plan<N, NG>;
+template <int N, int NG, int ZT>
+__global__ void __launch_bounds__(Plan<N, NG, ZT>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+    using L = Plan<N, NG, ZT>;
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr int kIssuer = L::kSoft + L::kExp;
     Shared &sh = *reinterpret_cast<Shared *>(smem + L::oShared);
@@ -1409,15 +1440,15 @@ __global__ void __launch_bounds__(Plan<N, NG>::kThreads, 1) tree_kernel(const __
     // A softmax thread of many columns keeps logits and denominators in registers: the others give theirs up.
     if (warp < L::kSoft) {
         if (L::kSoftWG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(L::kSoftRegs));
-        softmax_role<N, NG>(p, sh, smem, warp, lane);
+        softmax_role<N, NG, ZT>(p, sh, smem, warp, lane);
     } else if (warp < L::kSoft + L::kExp) {
         if (L::kSoftWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kExpRegs));
         const int row = 32 * (warp & 3) + lane;
-        expand_role<N, NG>(p, sh, smem, warp < L::kSoft + 4, row, warp & 3, lane);
+        expand_role<N, NG, ZT>(p, sh, smem, warp < L::kSoft + 4, row, warp & 3, lane);
     } else {
         if (L::kSoftWG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(L::kRestRegs));
-        if (warp == kIssuer) issue_role<N, NG>(p, sh, smem);
-        else if (warp < kIssuer + 3) fetch_role<N, NG>(p, sh, smem, tid - 32 * (kIssuer + 1));
+        if (warp == kIssuer) issue_role<N, NG, ZT>(p, sh, smem);
+        else if (warp < kIssuer + 3) fetch_role<N, NG, ZT>(p, sh, smem, tid - 32 * (kIssuer + 1));
     }
     fence_before();
     __syncthreads();
@@ -1518,7 +1549,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 // ---------------------------------------------------------------------- host --
 // Level tables at the top, the larger one first; the ring has what is left behind the fixed part. Its stages, or 0 where fewer
 // than two fit.
-template <int N, int NG>
+template <int N, int NG, int ZT>
 int lay_out(int wk, int wv, bool same, uint32_t &tab_k, uint32_t &tab_v) {
     int end = kSmemLast;
     tab_k = tab_v = 0;
@@ -1530,13 +1561,14 @@ int lay_out(int wk, int wv, bool same, uint32_t &tab_k, uint32_t &tab_v) {
         tab_v = k_first ? b : a;
         end = b;
     }
-    const int depth = std::min(kMaxDepth, (end - kSmemFirst - Plan<N, NG>::oRing) / Stage<NG>::bytes(wk, wv));
+    const int depth = std::min(kMaxDepth, (end - kSmemFirst - Plan<N, NG, ZT>::oRing) / Stage<NG>::bytes(wk, wv));
     return depth >= 2 ? depth : 0;
 }
 
 // Two four-bit tables leave 64 columns two stages (and 128 columns one: shape_of then takes 64).
-static_assert((kTabTop - 2 * table_bytes(4, 64) - kSmemFirst - Plan<64, 1>::oRing) / Stage<1>::bytes(4, 4) >= 2, "stages");
-static_assert((kSmemLast - kSmemFirst - Plan<64, 2>::oRing) / Stage<2>::bytes(4, 4) >= 2, "stages");
+static_assert((kTabTop - 2 * table_bytes(4, 64) - kSmemFirst - Plan<64, 1, 2>::oRing) / Stage<1>::bytes(4, 4) >= 2, "stages");
+static_assert(Plan<128, 1, 2>::oRing == Plan<128, 1, 1>::oRing, "one layout for both kernels of 128 columns");
+static_assert((kSmemLast - kSmemFirst - Plan<64, 2, 2>::oRing) / Stage<2>::bytes(4, 4) >= 2, "stages");
 
 struct Shape {
     int n_units, ng, rows, N, ncol_max;
@@ -1560,7 +1592,7 @@ Shape shape_of(const cq_kv_geom &g, int n_seqs, int max_nodes, TreeUnit *u) {
     // 128 columns leave room for one large level table, or for two where a stage of codes is small
     const bool same = g.k_bits == g.v_bits && std::equal(g.k_codebook, g.k_codebook + levels_of(g.k_bits), g.v_codebook);
     uint32_t tk, tv;
-    if (s.N == 128 && !lay_out<128, 1>(width_of(g.k_bits), width_of(g.v_bits), same, tk, tv)) s.N = 64;
+    if (s.N == 128 && !lay_out<128, 1, 1>(width_of(g.k_bits), width_of(g.v_bits), same, tk, tv)) s.N = 64;
     s.ncol_max = std::max(1, (most + s.N - 1) / s.N);
     s.items = (size_t)n_seqs * s.n_units * s.ncol_max;
     s.slots = s.items + sm_count();
@@ -1569,10 +1601,19 @@ Shape shape_of(const cq_kv_geom &g, int n_seqs, int max_nodes, TreeUnit *u) {
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
-// Level tables as bytes, scaled so that the largest level lies in [1, 4) and the levels' relative errors in fp16 are small: of 256
-// scales the one whose worst error is least (two magnitudes are then off by 2^-16 or so instead of 2^-12, eight by
-// 2^-13). Returns what takes the scale out again. The search is a pure function of the levels; a thread keeps
-// its last results, by content.
+// What rounding x to fp16 leaves, for normal fp16 values: ties to even, by the bits.
+float round_f16(float x) {
+    uint32_t u;
+    std::memcpy(&u, &x, 4);
+    u = (u + 0xFFFu + (u >> 13 & 1)) & ~0x1FFFu;
+    std::memcpy(&x, &u, 4);
+    return x;
+}
+
+// Level tables as bytes. The levels are scaled so that the largest lies in [1, 4) and fp16 holds them well: of 4096 scales the
+// one with the least sum of squared errors, after the part that all levels share is taken out again with the
+// scale (eight magnitudes are then off by 2^-15 or so instead of 2^-12; with 256 scales half as well). Returns what takes the scale out.
+// The search is a pure function of the levels; a thread keeps its last results, by content.
 float byte_table(const float *lv, uint32_t *t) {
     struct Found {
         float lv[16];
@@ -1588,19 +1629,27 @@ float byte_table(const float *lv, uint32_t *t) {
         }
     Found f;
     std::copy(lv, lv + 16, f.lv);
-    float top = 0.0f;
-    for (int i = 0; i < 16; ++i) top = std::max(top, std::fabs(lv[i]));
+    float mag[16], top = 0.0f;  // the distinct magnitudes
+    int n = 0;
+    for (int i = 0; i < 16; ++i) {
+        const float m = std::fabs(lv[i]);
+        top = std::max(top, m);
+        if (m != 0.0f && std::find(mag, mag + n, m) == mag + n) mag[n++] = m;
+    }
     int e = 0;
     if (top > 0.0f) std::frexp(top, &e), --e;
-    double best = 1e30, scale = 1.0;
-    for (int k = 0; k < 256 && top > 0.0f; ++k) {
-        const double s = std::ldexp(1.0 + k / 256.0, -e);
-        double worst = 0.0;
-        for (int i = 0; i < 16; ++i) {
-            const double x = lv[i] * s;
-            if (x != 0.0) worst = std::max(worst, std::fabs(__half2float(__float2half_rn((float)x)) / x - 1.0));
+    double best = 1e300, scale = std::ldexp(1.0, -e), back = 1.0 / scale;
+    double xx = 0.0;
+    for (int i = 0; i < n; ++i) xx += (double)mag[i] * mag[i];
+    for (int k = 0; k < 4096 && n; ++k) {
+        const double s = std::ldexp(1.0 + k / 4096.0, -e);
+        double xh = 0.0, hh = 0.0;
+        for (int i = 0; i < n; ++i) {
+            const float h = round_f16((float)(mag[i] * s));
+            xh += (double)mag[i] * h, hh += (double)h * h;
         }
-        if (worst < best) best = worst, scale = s;
+        const double left = xx - xh * xh / hh;  // the least sum of (mag - factor * h)^2
+        if (left < best) best = left, scale = s, back = xh / hh;
     }
     for (int i = 0; i < 8; ++i) f.t[i] = 0;
     for (int i = 0; i < 16; ++i) {
@@ -1608,7 +1657,7 @@ float byte_table(const float *lv, uint32_t *t) {
         f.t[i / 4] |= (b & 255u) << (8 * (i & 3));
         f.t[4 + i / 4] |= (b >> 8) << (8 * (i & 3));
     }
-    f.back = (float)(1.0 / scale);
+    f.back = (float)back;
     found[next] = f;
     next = (next + 1) % 4;
     filled = std::min(filled + 1, 4);
@@ -1616,14 +1665,14 @@ float byte_table(const float *lv, uint32_t *t) {
     return f.back;
 }
 
-template <int N, int NG>
+template <int N, int NG, int ZT>
 int launch_main(TreeParams &p, cudaStream_t st) {
     p.stage = Stage<NG>::bytes(p.wk, p.wv);
-    p.depth = lay_out<N, NG>(p.wk, p.wv, p.wk == p.wv && std::equal(p.tk, p.tk + 8, p.tv), p.tab_k, p.tab_v);
+    p.depth = lay_out<N, NG, ZT>(p.wk, p.wv, p.wk == p.wv && std::equal(p.tk, p.tk + 8, p.tv), p.tab_k, p.tab_v);
     if (!p.depth) return set_error(CQ_ERR_SHAPE, "no room for the level tables");
-    const int rc = ensure_smem(reinterpret_cast<const void *>(tree_kernel<N, NG>), kSmemLast - kSmemFirst);
+    const int rc = ensure_smem(reinterpret_cast<const void *>(tree_kernel<N, NG, ZT>), kSmemLast - kSmemFirst);
     if (rc) return rc;
-    tree_kernel<N, NG><<<p.grid, Plan<N, NG>::kThreads, kSmemLast - kSmemFirst, st>>>(p);
+    tree_kernel<N, NG, ZT><<<p.grid, Plan<N, NG, ZT>::kThreads, kSmemLast - kSmemFirst, st>>>(p);
     return CQ_OK;
 }
 
@@ -1666,13 +1715,13 @@ int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float 
     int rc;
     if (s.ng == 1) {
         switch (s.N) {
-        case 16: rc = launch_main<16, 1>(p, st); break;
-        case 32: rc = launch_main<32, 1>(p, st); break;
-        case 64: rc = launch_main<64, 1>(p, st); break;
-        default: rc = launch_main<128, 1>(p, st); break;
+        case 16: rc = launch_main<16, 1, 2>(p, st); break;
+        case 32: rc = launch_main<32, 1, 2>(p, st); break;
+        case 64: rc = launch_main<64, 1, 2>(p, st); break;
+        default: rc = t.dtype == CQ_T_F16 ? launch_main<128, 1, 2>(p, st) : launch_main<128, 1, 1>(p, st); break;
         }
     } else {
-        rc = s.N == 16 ? launch_main<16, 2>(p, st) : launch_main<64, 2>(p, st);
+        rc = s.N == 16 ? launch_main<16, 2, 2>(p, st) : launch_main<64, 2, 2>(p, st);
     }
     if (rc) return rc;
     // A block per column where they are few (its warps share long rows of parts), a warp per column otherwise: one for each while
