@@ -21,6 +21,10 @@
 // scaled, which is rare: at 2^8 it cost 5 to 9%); columns decide for themselves, so a column's bits do
 // not depend on the others.
 //
+// Heads over two groups (a head of 96 or 256, say). Each group's levels are products of their own, and a row's two norms are
+// n and r0 n, r1 n with the larger of them n: the scores stay apart in tensor memory until softmax adds them in fp32, while
+// the values' levels are multiplied by their r in fp16, with one rounding.
+//
 // Split. The tiles of all (request, unit, column tile) items in one row are cut into equal runs, one per
 // SM: lengths are read on the device, and the longest request cannot hold the launch up. Each run leaves
 // unrotated partial sums; a second kernel joins them, rotates and writes o.
@@ -502,8 +506,8 @@ constexpr int kSmemFirst = 1024, kSmemLast = 232448 + 1024, kTabTop = kSmemLast 
 
 // Level tables in shared memory (one group per row): entry e at e * 128 bytes, repeated for every lane so that no two lanes of a
 // warp meet in a bank. A code pair gives one fp16 pair (3 and 4 bits, and 2 bits where space is short), a byte of two-bit
-// codes four levels. Against permutes of register tables (1.3 to 3.1 instructions a value on the half-rate
-// integer pipe, which bounded the kernel) a pair costs two integer instructions and a load.
+// codes four levels. A pair costs two integer instructions and a load; byte permutes of register tables, on the half-rate
+// integer pipe, bounded the kernel (407 -> 316 us and 903 -> 618 us for the long context and the server below, when this came).
 __host__ __device__ constexpr bool wide_two(int N) { return N <= 32; }
 __host__ __device__ constexpr int table_bytes(int w, int N) { return w == 4 || (w == 2 && wide_two(N)) ? 256 * 128 : w == 3 ? 64 * 128 : 16 * 128; }
 

@@ -527,9 +527,10 @@ size_t cq_kv_tree_workspace(const cq_kv_geom *geom, int n_seqs, int max_nodes);
  * of a prompt. A token that attends nothing gets o = 0. What a token does not
  * attend has no influence on it, whatever bytes the cache holds there; rows
  * past the drafted tokens are never read.
- * The caches are never expanded in memory; the arithmetic is that of
- * cq_kv_attend (fp16 levels and rotated queries on the tensor cores, fp32
- * logits, softmax and sums, probabilities times norms in fp16). Block numbers
+ * The caches are never expanded in memory. Levels and rotated queries go to
+ * the tensor cores in fp16 (an fp16 query as the sum of two fp16 values, a
+ * bf16 query as one), probabilities times norms in fp16; logits, softmax
+ * and sums are fp32. Block numbers
  * outside the cache, and lengths outside the given sizes, are skipped and
  * mark the device status word (CQ_ERR_INDEX). Every head must lie within two
  * groups of 128 of its cache row (all head widths up to 128, and 256).
