@@ -22,12 +22,14 @@
 // them, so its sum is taken directly (the transform of the whole group in fp64, at this GPU's
 // sixty-fourth of the fp32 rate, would cost as much as all the rest).
 //
-// Bound by instructions, not by memory: 8190 rows of 8 heads of 128 in bf16, four and three bits (41.2 MB), take 42 to 45 us,
-// 0.95 TB/s or 14% of the copy rate. 650 instructions go to four groups; issue slots are used to 60%, with 22 warps on an SM
-// (59 registers, 33 KB of tables a block), and the fp64 pipe of the exact decisions to 22% of the time. A step of 77 rows
-// takes 12 to 13 us, most of it setting the tables up and one pass through the code.
-// Slower or no faster: a warp to a group (92 us), a binary search for each code (47), loading a task ahead (42), 3, 5 or
-// 6 blocks per SM (43 to 49).
+// Bound by instructions, not by memory: 8190 rows of 8 heads of 128 in bf16, four and three bits (41.2 MB), take 36 us,
+// 1.16 TB/s or 17% of the copy rate. 650 instructions go to four groups; issue slots are used to 68%, with 27 warps on an SM
+// (59 registers, 33 KB of tables a block), and the fp64 pipe of the exact decisions to 23% of the time. A warp that
+// decides exactly takes half as long again as the others: dealing a block's tasks out as its warps come for them brought 45.7
+// to 35.6 us (before, SMs were busy 54000 to 86000 cycles). A step of 77 rows takes 12 to 13 us, most of it
+// setting the tables up and one pass through the code.
+// Slower or no faster: a warp to a group (92 us), a binary search for each code (47 against 42 then), loading a task ahead (42),
+// 3, 5 or 6 blocks per SM (43 to 49).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -125,7 +127,7 @@ template <typename T>
 __device__ __noinline__ void decide(const SideParams &s, const T *src, int have, int levels, unsigned near, uint64_t &codes, int w, __half &norm) {
     const int lane = threadIdx.x & 31, sub = lane & 7;
     double m2 = 0.0;
-#pragma unroll 1
+#pragma unroll 4
     for (int j = 0; j < 16; ++j) {
         const double x = j < have ? (double)to_f(src[j]) : 0.0;
         m2 = fma(x, x, m2);
@@ -140,7 +142,7 @@ __device__ __noinline__ void decide(const SideParams &s, const T *src, int have,
         const int owner = has ? __ffs(has) - 1 : 0;
         const int bit = __shfl_sync(0xFFFFFFFFu, __ffs(near) - 1, (lane & 24) + owner) & 15, k = 16 * owner + bit;
         double r = 0.0;
-#pragma unroll 1
+#pragma unroll 4
         for (int j = 0; j < 16; ++j) {
             const double x = j < have ? (double)to_f(src[j]) : 0.0;
             r += __popc(k & (16 * sub + j)) & 1 ? -x : x;
@@ -148,8 +150,11 @@ __device__ __noinline__ void decide(const SideParams &s, const T *src, int have,
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
         if (has && sub == owner) {
+            // midpoints more than 1e-5 below are counted in fp32, and the few that are left in fp64 (midpoints ascend)
+            const float u = (float)r / (float)border;
             int c = 0;
-            for (int l = 0; l < levels - 1; ++l) c += r > s.mid[l] * border;
+            for (int l = 0; l < levels - 1; ++l) c += (float)s.mid[l] < u - 1e-5f;
+            while (c < levels - 1 && r > s.mid[c] * border) ++c;
             if (levels == 3) c = (c - 1) & 3;
             codes = (codes & ~((uint64_t)((1 << w) - 1) << (bit * w))) | (uint64_t)c << (bit * w);
             near &= near - 1;
@@ -289,15 +294,23 @@ __device__ __forceinline__ void encode(const SlotParams &p, const SideParams &s,
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv_write_slots_kernel(const __grid_constant__ SlotParams p) {
     extern __shared__ float2 s_table[];
+    __shared__ int s_turn;
     const int tid = threadIdx.x, lane = tid & 31;
     for (int i = tid; i < 2 * kTable; i += kThreads) {
         const SideParams &s = p.side[i >= kTable];
         const int cell = (i >= kTable ? i - kTable : i) / kCopies;
         s_table[i] = make_float2(s.cell_mid[cell], __uint_as_float(s.cell_code[cell]));
     }
+    if (tid == 0) s_turn = 0;
     __syncthreads();
     const long long all = p.side[0].warps + p.side[1].warps;
-    for (long long t = (long long)blockIdx.x * kWarps + (tid >> 5); t < all; t += (long long)gridDim.x * kWarps) {
+    // The block's tasks are handed out as its warps come for them: exact decisions make some of them much longer.
+    for (;;) {
+        int turn;
+        if (lane == 0) turn = atomicAdd(&s_turn, 1);
+        turn = __shfl_sync(0xFFFFFFFFu, turn, 0);
+        const long long t = (long long)(turn >> 3) * gridDim.x * kWarps + (long long)blockIdx.x * kWarps + (turn & 7);
+        if (t >= all) break;
         const int which = t >= p.side[0].warps;
         const SideParams &s = p.side[which];
         const long long task = which ? t - p.side[0].warps : t;
