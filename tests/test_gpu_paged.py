@@ -372,7 +372,7 @@ def _tree_mask(nodes, rng, words, empty=False):
 
 
 def _check_attend(C, geom, kb, vb, ctx, nodes, bs=16, dtype=F16, masked=True, empty=False, seed=0, poison=True, scale=None,
-                  lo=1.0, hi=8.0, q_scale=1.0, max_nodes=None, words=None, contiguous=False, books=None):
+                  lo=1.0, hi=8.0, q_scale=1.0, max_nodes=None, words=None, contiguous=False, books=None, rms=None):
     hq, hkv, dk, dv = geom
     rng = np.random.RandomState(seed)
     pages = [-(-(c + n) // bs) for c, n in zip(ctx, nodes)]
@@ -422,6 +422,9 @@ def _check_attend(C, geom, kb, vb, ctx, nodes, bs=16, dtype=F16, masked=True, em
     err = np.abs(got - want)
     assert np.isfinite(got).all()
     assert (err <= tol).all(), f"worst error/tolerance {np.max(err / np.maximum(tol, 1e-300)):.3g}"
+    if rms is not None:
+        share = math.sqrt(np.mean(err ** 2) / np.mean(want ** 2))
+        assert share <= rms, f"{share:.2e} of the result's size, allowed {rms:.2e}"
     return got, float(np.max(err / np.maximum(tol, 1e-300))) if total else 0.0
 
 
@@ -509,6 +512,25 @@ def test_attend_long_context_in_parts(C):
 def test_attend_many_requests(C):
     rng = np.random.RandomState(0)
     _check_attend(C, (4, 2, 48, 64), 2, 2, ctx=rng.randint(0, 60, 700).tolist(), nodes=rng.randint(0, 3, 700).tolist(), max_nodes=8)
+
+
+def test_attend_many_uneven_requests(C):
+    """Lengths from nothing to several tiles: the runs of the thread blocks begin and end anywhere, and
+    the requests are more than a block's threads."""
+    rng = np.random.RandomState(1)
+    ctx = np.where(rng.rand(700) < 0.1, rng.randint(100, 900, 700), rng.randint(0, 40, 700))
+    _check_attend(C, (4, 2, 48, 64), 2, 3, ctx=ctx.tolist(), nodes=rng.randint(0, 3, 700).tolist())
+    _check_attend(C, (4, 1, 128, 128), 4, 2, ctx=ctx[:90].tolist(), nodes=rng.randint(0, 40, 90).tolist(), dtype=BF16)
+
+
+@pytest.mark.parametrize("geom", [(8, 4, 64, 64), (4, 1, 128, 128), (4, 1, 256, 256), (6, 6, 80, 80)])
+@pytest.mark.parametrize("bits", [(2, 2), (4, 4), (5, 3)])
+@pytest.mark.parametrize("nodes", [[3], [40]])
+def test_attend_fp16_precision(C, geom, bits, nodes):
+    """An fp16 result carries three roundings to fp16, of the weights, of the result and, where a head has two groups, of the
+    values of one: each of at most half a step, uniform, so 2^-11 / sqrt(3) of the value in the mean square, and sqrt(3)
+    times that together. (Queries in one fp16 term would add as much again.)"""
+    _check_attend(C, geom, *bits, ctx=[2500], nodes=nodes, contiguous=True, seed=geom[2] + bits[0], q_scale=1.5, rms=2.0 ** -11)
 
 
 def test_attend_peaked_flat_and_extreme_sizes(C):
