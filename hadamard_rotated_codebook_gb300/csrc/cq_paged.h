@@ -33,6 +33,9 @@ struct TreeUnit {
 // are too many.
 int tree_units(const cq_kv_geom &g, TreeUnit *u);
 
+// Whether the attention's shared-memory layout holds on a device that keeps `reserved` bytes of each block's shared memory for
+// itself: CQ_OK, or the error that the call returns before it launches anything.
+int tree_smem_check(int reserved);
 size_t tree_workspace(const cq_kv_geom &g, int n_seqs, int max_nodes);
 // lk, lv: level tables of the key and value codes (level_table).
 int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float *lk, const float *lv, void *stream);

@@ -167,6 +167,11 @@ int cq_kv_write_slots(const cq_kv_geom *g, uint8_t *k_cache, uint8_t *v_cache, i
     return launch_kv_write_slots(side, cap, dtype, slots, n, stream);
 }
 
+int cq_selftest_tree_smem(int reserved) {
+    clear_error();
+    return tree_smem_check(reserved);
+}
+
 size_t cq_kv_tree_workspace(const cq_kv_geom *g, int n_seqs, int max_nodes) {
     clear_error();
     TreeUnit u[kMaxUnits];

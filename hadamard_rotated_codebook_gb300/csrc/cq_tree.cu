@@ -53,6 +53,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -85,6 +86,7 @@ struct TreeParams {
     uint32_t div_mul, div_shift;  // t / block_size = t * div_mul >> div_shift
     bool vec_q;      // a column's query is whole runs of 16 elements on 16-byte boundaries
     int rows;        // most query heads of a unit
+    int slots;       // of part and ml
     int ncol_max;    // column tiles of a request with max_nodes tokens
     int grid;
 };
@@ -1418,7 +1420,7 @@ __global__ void __launch_bounds__(Plan<N, NG, ZT>::kThreads, 1) tree_kernel(cons
     Shared &sh = *reinterpret_cast<Shared *>(smem + L::oShared);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    if (smem_u32(smem) != kSmemFirst) {  // the tables' addresses count on it
+    if (smem_u32(smem) != kSmemFirst) {  // the tables' addresses count on it; the host has checked (smem_check)
         if (tid == 0) atomicOr(p.status, 0x47490010u);
         return;
     }
@@ -1498,7 +1500,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     const int rows = u.nh * p.per, cols = min(N, q.n * rows - ct * N), first = blockIdx.y * CG;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");  // every block: what follows this kernel also follows the one before it
     if (first >= cols) return;
-    const int2 rec = p.rec[item];
+    int2 rec = p.rec[item];
+    if (rec.x < 0 || rec.y < 0 || rec.x > p.slots - rec.y) rec.y = 0;  // an item that no block wrote
     const bool many = rec.y > kFewParts;
     for (int k = many ? 0 : warp; k < CG && first + k < cols; k += many ? 1 : kJoinWarps) {
         const int col = first + k;
@@ -1688,18 +1691,44 @@ float byte_table(const float *lv, uint32_t *t) {
     return f.back;
 }
 
+// Bytes at the start of a block's shared memory that the system keeps on the current device (cached per device), or -1.
+int reserved_smem() {
+    static std::atomic<int> cache[64];  // one more than the bytes
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return -1;
+    }
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess) {
+            cudaGetLastError();
+            return -1;
+        }
+        cache[dev].store(++n, std::memory_order_relaxed);  // every writer stores the same value
+    }
+    return n - 1;
+}
+
 template <int N, int NG, int ZT>
 int launch_main(TreeParams &p, cudaStream_t st) {
     p.stage = Stage<NG>::bytes(p.wk, p.wv);
     p.depth = lay_out<N, NG, ZT>(p.wk, p.wv, p.wk == p.wv && std::equal(p.tk, p.tk + 8, p.tv), p.tab_k, p.tab_v);
     if (!p.depth) return set_error(CQ_ERR_SHAPE, "no room for the level tables");
-    const int rc = ensure_smem(reinterpret_cast<const void *>(tree_kernel<N, NG, ZT>), kSmemLast - kSmemFirst);
+    int rc = tree_smem_check(reserved_smem());
+    if (rc) return rc;
+    rc = ensure_smem(reinterpret_cast<const void *>(tree_kernel<N, NG, ZT>), kSmemLast - kSmemFirst);
     if (rc) return rc;
     tree_kernel<N, NG, ZT><<<p.grid, Plan<N, NG, ZT>::kThreads, kSmemLast - kSmemFirst, st>>>(p);
     return CQ_OK;
 }
 
 }  // namespace
+
+int tree_smem_check(int reserved) {
+    if (reserved == kSmemFirst) return CQ_OK;
+    return set_error(CQ_ERR_CUDA, "tree attention counts on shared memory from byte %d on, and the system keeps %d bytes", kSmemFirst, reserved);
+}
 
 size_t tree_workspace(const cq_kv_geom &g, int n_seqs, int max_nodes) {
     if (!n_seqs || !max_nodes) return 0;
@@ -1725,6 +1754,7 @@ int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float 
     p.div_shift = 31 + l;
     p.div_mul = (uint32_t)(((1ull << (31 + l)) + (unsigned)t.block_size - 1) / (unsigned)t.block_size);
     if (!t.max_blocks) p.t.block_table = t.cu_nodes, p.t.table_stride = 0;  // no token is read, but entry 0 is
+    p.slots = (int)s.slots;
     p.rows = s.rows, p.ncol_max = s.ncol_max, p.grid = sm_count();
     p.status = device_status_ptr();
     if (!p.status) return set_error(CQ_ERR_CUDA, "no device status word");

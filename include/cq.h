@@ -562,6 +562,12 @@ int cq_selftest_wait_timeout(void *stream);
  * again. Errors: CQ_ERR_NOMEM, CQ_ERR_CUDA. */
 int cq_selftest_dirty_counters(void *stream);
 
+/* Diagnostic without a counterpart on the pages: what cq_kv_tree_attend
+ * answers, before it launches anything, on a device that keeps `reserved`
+ * bytes of each block's shared memory for itself (its kernel's addresses
+ * count on the 1024 of this GPU): CQ_OK or CQ_ERR_CUDA. */
+int cq_selftest_tree_smem(int reserved);
+
 /* -------------------------------------------------------- container -- */
 /*
  * Own .cact-shaped container (the pages disagree on the header: 196 bytes

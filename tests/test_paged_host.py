@@ -169,6 +169,17 @@ def test_kv_tree_attend_refuses(A, kw, code):
     assert lib.cq_last_error()
 
 
+@pytest.mark.parametrize("reserved", [-1, 0, 1023, 1025, 2048])
+def test_kv_tree_attend_refuses_another_shared_memory_layout(A, reserved):
+    """The kernel's addresses count on shared memory that starts behind 1024 bytes: a device that
+    keeps another number is refused on the host, so that the joining kernel never runs over parts
+    that no block wrote."""
+    lib = A.load()
+    assert lib.cq_selftest_tree_smem(1024) == 0
+    assert lib.cq_selftest_tree_smem(reserved) == A.CQ_ERR_CUDA
+    assert b"shared memory" in lib.cq_last_error()
+
+
 def test_host_tensors_are_refused(C):
     """The binding takes device tensors only, and says so before it calls the library."""
     import torch
