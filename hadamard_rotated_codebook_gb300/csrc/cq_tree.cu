@@ -21,6 +21,10 @@
 // scaled, which is rare: at 2^8 it cost 5 to 9%); columns decide for themselves, so a column's bits do
 // not depend on the others.
 //
+// Queries in fp16. Each column is rounded at the power of two of its own largest element (rotate_queries), so that a query of any
+// size leaves its tile mates' bits alone. The product then takes the columns at the tile's largest scale where that is exact for
+// all of them, and else as they are, in which case softmax first multiplies their scores by their powers of two (scale_scores).
+//
 // Heads over two groups (a head of 96 or 256, say). Each group's levels are products of their own, and a row's two norms are
 // n and r0 n, r1 n with the larger of them n: the scores stay apart in tensor memory until softmax adds them in fp32, while
 // the values' levels are multiplied by their r in fp16, with one rounding.
@@ -70,6 +74,9 @@ constexpr unsigned kSpin = 1u << 20;   // polls of up to ~1 us
 constexpr float kNoMax = -1e30f;       // reference of a column that has attended nothing yet
 constexpr float kRaise = 15.0f;         // log2 of the largest weight before a reference is raised (fp16 ends below 2^16)
 constexpr float kInvSqrt128 = 0.08838834764831845f;
+constexpr int kExLow = -110, kExHigh = 120;  // exponents of the queries' scales: both signs are normal powers of two
+constexpr int kNoEx = -128;                 // of a column that is zero
+constexpr int kGuard = 10;                   // a tile's columns share one scale where theirs are at most so many powers of two apart
 
 struct TreeParams {
     cq_kv_tree t;
@@ -327,7 +334,8 @@ struct Shared {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], sc_full[2], p_full, p_empty, z_full, drain;
     uint32_t tmem;
     volatile int abort;
-    int zmax;
+    int ztop, zlow;               // largest and smallest exponent among the item's columns
+    signed char zex[128];         // exponents of the columns' scales
     int bad;
     long long total, run[2];      // all places; this block's first one and the next block's
     long long first, edge[2];     // place of the first tile; tiles before this block's run and up to its end
@@ -978,11 +986,25 @@ __device__ __forceinline__ void stash_queries(const TreeParams &p, uint8_t *smem
     }
 }
 
-// The rotated queries into shared memory (the K-major B operand), scaled by one power of two so that fp16 holds them whatever their
-// size (a coordinate is at most the sum of the query's 128 or fewer magnitudes); returns what takes the scale back out
-// of the logits.
+__device__ __forceinline__ float power_of_two(int e) {  // -252 .. 254
+    return __int_as_float((127 + (e >> 1)) << 23) * __int_as_float((127 + e - (e >> 1)) << 23);
+}
+// Where the columns keep their own scales their scores are multiplied by 2^(own - wide_base): at most 2^90, and the powers of two
+// that leave fp32 belong to columns whose logits are then less than 2^-100 of another's.
+__device__ __forceinline__ int wide_base(int top) { return max(kExLow, top - 90); }
+// Exponent of the scale at which fp16 holds a column whose largest finite magnitude is `top`: it lies between 2^7 and 2^8 then, and
+// a sum of 128 of them below 2^15.
+__device__ __forceinline__ int exponent_of(float top) {
+    return top > 0.0f ? max(kExLow, min(kExHigh, ((__float_as_int(top) >> 23) & 255) - 127 - 7)) : kNoEx;
+}
+// A multiple of 2^(kGuard - 24), for which fp16 has kGuard powers of two to spare below: hi and lo terms of it stay what they are
+// when they are multiplied by 2^-kGuard or more. It moves a column by 2^-22 of its largest element at most.
+constexpr float kGrid = 1.5f * (1 << (kGuard - 1));
+
+// The rotated queries into shared memory (the K-major B operand), each column rounded to fp16 at its own scale, then brought to
+// the tile's (or left, `wide`, where the columns are too far apart); returns what takes the scale back out of the logits.
 template <int N, int NG, int ZT>
-__device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, const Cursor &c, int warp, int lane) {
+__device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, const Cursor &c, int warp, int lane, bool &wide) {
     using L = Plan<N, NG, ZT>;
     const TreeUnit u = p.unit[c.u];
     const int rows = u.nh * p.per, cols = min(N, c.n * rows - c.c * N);
@@ -995,44 +1017,58 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[j] = d0 + j >= 0 && d0 + j < p.dk ? load_q(p, src + d0 + j) : 0.0f;
     };
-    // the largest finite magnitude: what is not finite does not scale the others
-    float top = 0.0f;
+    // the columns' largest finite magnitudes (what is not finite scales nothing)
+    int top = kNoEx, low = -kNoEx;
     if (fast) {
         asm volatile("cp.async.wait_all;\n" ::: "memory");
         const uint32_t inf = half ? 0x7C00u : 0x7F80u;
-        uint32_t most = 0;  // magnitudes of a 16-bit type are ordered as integers
 #pragma unroll 1
-        for (int i = 0; i < 2 * N / (4 * L::kSoft); ++i) {
-            const uint4 v = lds128(stash_at<N, NG, ZT>(smem, i >> 1, warp, lane) + (i & 1) * 16);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < N / (4 * L::kSoft); ++i) {
+            const uint32_t from = stash_at<N, NG, ZT>(smem, i, warp, lane);
+            const uint4 v0 = lds128(from), v1 = lds128(from + 16);
+            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            uint32_t most = 0;  // magnitudes of a 16-bit type are ordered as integers
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const uint32_t a = w[j] & 0x7FFFu, b = w[j] >> 16 & 0x7FFFu;
                 most = max(most, max(a < inf ? a : 0u, b < inf ? b : 0u));
             }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+            const int ex = exponent_of(half ? __half2float(__ushort_as_half((unsigned short)most)) : __uint_as_float(most << 16));
+            if ((lane & 7) == 0) sh.zex[warp * 4 + (lane >> 3) + i * 4 * L::kSoft] = (signed char)ex;
+            top = max(top, ex), low = min(low, ex == kNoEx ? -kNoEx : ex);
         }
-        top = half ? __half2float(__ushort_as_half((unsigned short)most)) : __uint_as_float(most << 16);
+        top = __reduce_max_sync(0xFFFFFFFFu, top), low = __reduce_min_sync(0xFFFFFFFFu, low);
     } else {
 #pragma unroll 1
-        for (int col = warp; col < cols; col += L::kSoft) {
+        for (int col = warp; col < N; col += L::kSoft) {
+            float most = 0.0f;
 #pragma unroll 1
-            for (int g = 0; g < u.ngk; ++g) {
+            for (int g = 0; col < cols && g < u.ngk; ++g) {
                 float z[4];
                 load(col, g, z);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (fabsf(z[j]) <= 3.4e38f) top = fmaxf(top, fabsf(z[j]));
+                    if (fabsf(z[j]) <= 3.4e38f) most = fmaxf(most, fabsf(z[j]));
             }
+            const int ex = exponent_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most))));
+            if (lane == 0) sh.zex[col] = (signed char)ex;
+            top = max(top, ex), low = min(low, ex == kNoEx ? -kNoEx : ex);
         }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if (lane == 0) atomicMax(&sh.zmax, __float_as_int(top));
+    if (lane == 0) atomicMax(&sh.ztop, top), atomicMin(&sh.zlow, low);
     bar_sync(1, 32 * L::kSoft);
-    // the largest magnitude between 2^7 and 2^8, a sum of 128 of them below 2^15; the exponent is held where both powers of
-    // two are normal
-    const int ex = max(-110, min(120, ((sh.zmax >> 23) & 255) - 127 - 7));
-    const float down = __int_as_float((127 - ex) << 23);
+    top = sh.ztop == kNoEx ? 0 : sh.ztop;
+    wide = top - sh.zlow > kGuard;  // not where all columns are zero: 0 - 128
+    // a column's own scale, and from there to the tile's
+    auto own_of = [&](int col) { return sh.zex[col] == kNoEx ? top : sh.zex[col]; };
+    auto down_of = [&](int own) { return __int_as_float((127 - own) << 23); };
+    auto shift_of = [&](int own) { return __float2half2_rn(wide ? 1.0f : __int_as_float((127 + own - top) << 23)); };
+    auto scaled = [&](__half2 v, __half2 shift) {
+        const __half2 x = __hmul2(v, shift);
+        return *reinterpret_cast<const uint32_t *>(&x);
+    };
     if (fast) {
 #pragma unroll 1
         for (int i = 0; i < N / (4 * L::kSoft); ++i) {
@@ -1040,6 +1076,9 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
             const uint32_t from = stash_at<N, NG, ZT>(smem, i, warp, lane);
             const uint4 v0 = lds128(from), v1 = lds128(from + 16);
             const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            const int own = own_of(col);
+            const float down = down_of(own);
+            const __half2 shift = shift_of(own);
             F2 z[8];  // elements 2 j and 2 j + 1
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -1068,12 +1107,13 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
                 }
             }
             uint32_t h2[8];
+            const F2 grid = f2(kGrid, kGrid), back = f2(-kGrid, -kGrid);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
+                z[j] = f2_add(f2_add(z[j], grid), back);
                 float x, y;
                 f2_get(z[j], x, y);
-                const __half2 v = __floats2half2_rn(x, y);
-                h2[j] = *reinterpret_cast<const uint32_t *>(&v);
+                h2[j] = scaled(__floats2half2_rn(x, y), shift);
             }
             const uint32_t base = smem_u32(smem + L::oZ) + (sub >> 2) * (N * 128) + (col >> 3) * 1024 + (col & 7) * 128;
             sts128(base + (((2 * (sub & 3)) ^ (col & 7)) << 4), h2[0], h2[1], h2[2], h2[3]);
@@ -1083,9 +1123,8 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
                 for (int j = 0; j < 8; ++j) {
                     float x, y;
                     f2_get(z[j], x, y);
-                    const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&h2[j]));
-                    const __half2 v = __floats2half2_rn(x - hi.x, y - hi.y);
-                    h2[j] = *reinterpret_cast<const uint32_t *>(&v);
+                    const float2 hi = __half22float2(__floats2half2_rn(x, y));
+                    h2[j] = scaled(__floats2half2_rn(x - hi.x, y - hi.y), shift);
                 }
                 sts128(base + L::kZBytes + (((2 * (sub & 3)) ^ (col & 7)) << 4), h2[0], h2[1], h2[2], h2[3]);
                 sts128(base + L::kZBytes + (((2 * (sub & 3) + 1) ^ (col & 7)) << 4), h2[4], h2[5], h2[6], h2[7]);
@@ -1097,18 +1136,22 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
             const int col = k / NG, g = k % NG;
             float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             if (col < cols && g < u.ngk) load(col, g, z);
+            const int own = own_of(col);
+            const float down = down_of(own);
+            const __half2 shift = shift_of(own);
 #pragma unroll
             for (int j = 0; j < 4; ++j) z[j] *= down;
             fwht(z, lane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] = __fadd_rn(__fadd_rn(z[j], kGrid), -kGrid);
             const uint32_t base = smem_u32(smem + L::oZ) + g * L::kZBytes + (col >> 3) * 1024 + (col & 7) * 128;
             auto put = [&](int pos, float x, float y) {
                 const __half2 v = __floats2half2_rn(x, y);
                 const uint32_t to = base + (pos >> 6) * (N * 128) + ((((pos & 63) >> 3) ^ (col & 7)) << 4) + (pos & 7) * 2;
-                sts32(to, *reinterpret_cast<const uint32_t *>(&v));
+                sts32(to, scaled(v, shift));
                 if (ZT == 2 && half) {
                     const float2 hi = __half22float2(v);
-                    const __half2 l = __floats2half2_rn(x - hi.x, y - hi.y);
-                    sts32(to + NG * L::kZBytes, *reinterpret_cast<const uint32_t *>(&l));
+                    sts32(to + NG * L::kZBytes, scaled(__floats2half2_rn(x - hi.x, y - hi.y), shift));
                 }
             };
             if (NG == 2 && p.wk == 2) {
@@ -1120,7 +1163,7 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
             }
         }
     }
-    return p.k_mult * __int_as_float((127 + ex) << 23);
+    return p.k_mult * power_of_two(wide ? wide_base(top) : top);
 }
 
 // Who attends drafted token j, as bits over the item's columns.
@@ -1236,6 +1279,28 @@ __device__ __noinline__ void scale_sums(Shared &sh, uint32_t to, int n, int grou
     wait_st();
 }
 
+// Brings the scores of NC columns from c0 on (tensor memory at ts, a warp its own rows) from their own scales to one.
+template <int N, int NG, int NC>
+__device__ __noinline__ void scale_scores(Shared &sh, uint32_t ts, int c0, bool two) {
+    const int base = wide_base(sh.ztop);
+#pragma unroll 1
+    for (int g = 0; g < (NG == 2 && two ? 2 : 1); ++g) {
+#pragma unroll 1
+        for (int k = 0; k < NC; k += 8) {
+            float d[8];
+            tmem_ld<8>(ts + g * N + k, d);
+            wait_ld<8>(d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int ex = sh.zex[c0 + k + j];
+                d[j] *= ex == kNoEx ? 1.0f : power_of_two(ex - base);
+            }
+            tmem_st8(ts + g * N + k, d);
+        }
+    }
+    wait_st();
+}
+
 template <int N, int NG, int ZT>
 __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int warp, int lane) {
     using L = Plan<N, NG, ZT>;
@@ -1251,12 +1316,13 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
     stash_queries<N, NG, ZT>(p, smem, c, warp, lane);
     while (more) {
         // ------------------------------------------------ one item's part --
-        bar_sync(1, kSoftThreads);  // the item before is finished: zmax, m, mask may be written
-        if (warp == 0 && lane == 0) sh.zmax = 0;
+        bar_sync(1, kSoftThreads);  // the item before is finished: the exponents, m, mask may be written
+        if (warp == 0 && lane == 0) sh.ztop = kNoEx, sh.zlow = -kNoEx;
         if (row < NC) sh.minus_m[c0 + row] = -kNoMax;
         gather_mask<N>(p, sh, c, warp, L::kSoft, lane);
         bar_sync(1, kSoftThreads);
-        const float mult = rotate_queries<N, NG, ZT>(p, sh, smem, c, warp, lane);
+        bool wide;
+        const float mult = rotate_queries<N, NG, ZT>(p, sh, smem, c, warp, lane, wide);
         fence_async();
         fence_before();  // tensor memory reads of the item before
         __syncwarp();
@@ -1293,6 +1359,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
             const F2 nk2 = f2(nk, nk), ln2 = f2(ln, ln), inv2 = f2(inv, inv);
             wait(sh, &sh.s_full[b], par, p.status, 0x4749000Au);
             fence_after();
+            if (__builtin_expect(wide, 0)) scale_scores<N, NG, NC>(sh, tm + L::cS + b * NG * N + c0, c0, two);
             // Column by column in halves of X: the denominators of all columns and the logits of one half fit the registers.
 #pragma unroll
             for (int hf = 0; hf < NC; hf += X) {

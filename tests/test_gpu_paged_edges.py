@@ -1,0 +1,85 @@
+"""GPU tests of the paged cache's operators at the ends of their ranges: sizes far apart in one call, values past what
+fp32 squares hold, long contexts under one dominant row, lengths that leave 32 bits, waits that run out."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from tests import paged_reference as R
+from tests.test_gpu_paged import BF16, F16, _blob, _i32, _np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def C():
+    import hadamard_rotated_codebook_gb300 as pkg
+    return pkg
+
+
+class _Pool:
+    """One request of `ctx` cached and `n` drafted tokens, causal."""
+
+    def __init__(self, C, geom, bits, ctx, n, scale, seed=0, bs=32):
+        self.C, self.dims, self.bits, self.ctx, self.n, self.bs, self.scale = C, geom, bits, ctx, n, bs, scale
+        hq, hkv, dk, dv = geom
+        rng = np.random.RandomState(seed)
+        self.cap = (ctx + n + bs - 1) // bs * bs
+        self.kc, self.vc = _blob(self.cap, hkv * dk, bits, rng), _blob(self.cap, hkv * dv, bits, rng)
+        self.cb = O.analytic_codebook(bits)
+        self.g = C.cq_kv_geometry(hq, hkv, dk, dv, bits, bits, self.cb, self.cb, scale)
+        self.table = rng.permutation(self.cap // bs)[None]
+        self.q = torch.randn(n, hq, dk, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed))
+
+    def run(self, q):
+        kc, vc = (torch.from_numpy(x).cuda() for x in (self.kc, self.vc))
+        o = self.C.cq_kv_tree_attend(self.g, q, kc, vc, self.cap, _i32(self.table), self.bs, _i32([self.ctx]), _i32([0, self.n]), None, self.n)
+        torch.cuda.synchronize()
+        self.C.cq_device_status()
+        return o
+
+    def reference(self, q):
+        return R.attend(_np(q), self.kc, self.vc, self.cap, self.table, self.bs, [self.ctx], [0, self.n], lambda s, i, j: j <= i, self.dims,
+                        self.bits, self.bits, self.cb, self.cb, np.float64(np.float32(self.scale)))
+
+
+# whole runs of 16 and not, one group and two
+SPANS = [(4, 2, 64, 64), (6, 3, 40, 24), (8, 2, 128, 128), (6, 6, 80, 80), (4, 1, 256, 256)]
+
+
+@pytest.mark.parametrize("geom", SPANS)
+@pytest.mark.parametrize("n", [4, 40])
+@pytest.mark.parametrize("dtype,factor", [(BF16, 2.0 ** 28), (BF16, 1e12), (BF16, 1e30), (BF16, 6e37), (BF16, 1e-30), (F16, 2.0 ** 13), (F16, 2.0 ** -12)])
+def test_attend_a_query_of_another_size_leaves_its_tile_mates_alone(C, geom, n, dtype, factor):
+    """One token, and one head of another, are far larger (or smaller) than the rest of their column tile: every other
+    row has the bits that it has without them, and they have the bits that they have by themselves."""
+    pool = _Pool(C, geom, 4, 150, n, 0.125, seed=geom[2] + n)
+    q = pool.q.to(dtype)
+    odd = torch.zeros(n, geom[0], dtype=torch.bool, device="cuda")
+    odd[1] = odd[2, geom[0] - 1] = True
+    mixed = torch.where(odd[..., None], (q.float() * factor).to(dtype), q)
+    assert torch.isfinite(mixed).all()
+    a, b = pool.run(q), pool.run(mixed)
+    assert torch.equal(a[~odd], b[~odd])
+    alone = pool.run(torch.where(odd[..., None], mixed, torch.zeros_like(q)))
+    assert torch.equal(alone[odd].nan_to_num(7e4), b[odd].nan_to_num(7e4))
+
+
+@pytest.mark.parametrize("geom", SPANS)
+@pytest.mark.parametrize("scale", [0.125, 0.125 * 2.0 ** -40])
+def test_attend_queries_of_every_size_match_the_definition(C, geom, scale):
+    """Token i is 2^(5 i - 20) times as large: the logits of some or of others are of ordinary size, and the definition's
+    bound holds for each row by itself."""
+    n = 9
+    pool = _Pool(C, geom, 4, 150, n, scale, seed=geom[2])
+    size = 2.0 ** (5.0 * torch.arange(n, device="cuda") - 20) if scale > 1e-3 else 2.0 ** (5.0 * torch.arange(n, device="cuda"))
+    q = (pool.q * size[:, None, None]).to(BF16)
+    got = _np(pool.run(q))
+    with np.errstate(over="ignore", invalid="ignore"):
+        want, bound = pool.reference(q)
+        tol = bound + R.HALF_STEP["bfloat16"] * (np.abs(want) + bound) + R.TINY["bfloat16"]
+    tol = np.where(np.isnan(tol), np.inf, tol)  # logits past what the bound's exponential holds
+    assert np.isfinite(got).all() and (np.abs(got - want) <= tol).all()
+    assert np.isfinite(tol).mean() > 0.3
