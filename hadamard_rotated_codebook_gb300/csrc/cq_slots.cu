@@ -151,7 +151,7 @@ __device__ __noinline__ void decide(const SideParams &s, const T *src, int have,
         for (int o = 1; o < 8; o <<= 1) r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
         if (has && sub == owner) {
             // midpoints more than 1e-5 below are counted in fp32, and the few that are left in fp64 (midpoints ascend)
-            const float u = (float)r / (float)border;
+            const float u = border < 1e37 ? (float)r / (float)border : -INFINITY;  // past fp32 all are counted in fp64
             int c = 0;
             for (int l = 0; l < levels - 1; ++l) c += (float)s.mid[l] < u - 1e-5f;
             while (c < levels - 1 && r > s.mid[c] * border) ++c;
@@ -267,12 +267,13 @@ __device__ __forceinline__ void encode(const SlotParams &p, const SideParams &s,
     __half norm = __float2half_rn(n);
     bool wild = n2 < 1e-30f || n2 > 1e30f;  // a sum of squares that fp32 may not hold
     if (__any_sync(0xFFFFFFFFu, wild)) {
-        // a group of zeros is decided as it stands (every coordinate is exactly zero); else every coordinate again
+        // a group of zeros is decided as it stands (every coordinate is exactly zero); else every coordinate again. Where the sum
+        // of squares is too large, the coordinates above are zeros of an infinite scale and say nothing
         bool nonzero = false;
 #pragma unroll
         for (int j = 0; j < 16; ++j) nonzero |= !(x[j] == 0.0f);
         nonzero = __ballot_sync(0xFFFFFFFFu, nonzero) >> (lane & 24) & 0xFFu;
-        if (wild) near = nonzero ? 0xFFFFu : 0u;
+        if (wild) near = nonzero || n2 > 1e30f ? 0xFFFFu : 0u;
     }
     const bool edge = __half_as_ushort(__float2half_rn(n * (1.0f + kNear))) != __half_as_ushort(__float2half_rn(n * (1.0f - kNear)));
     if (!live) near = 0;

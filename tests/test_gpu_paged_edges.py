@@ -83,3 +83,28 @@ def test_attend_queries_of_every_size_match_the_definition(C, geom, scale):
     tol = np.where(np.isnan(tol), np.inf, tol)  # logits past what the bound's exponential holds
     assert np.isfinite(got).all() and (np.abs(got - want) <= tol).all()
     assert np.isfinite(tol).mean() > 0.3
+
+
+# ------------------------------------------------------------------------------------------------------- slot writes
+
+@pytest.mark.parametrize("bits", [2, 3, 4, 5])
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_write_slots_of_rows_whose_squares_leave_fp32(C, bits, dtype):
+    """Elements of 1e15 to 3e38: the sum of squares, the norm and then the sums of elements pass fp32. Codes are those of
+    exact arithmetic all the same, the norm is an infinity of fp16, and ordinary rows beside them keep their bytes."""
+    rng = np.random.RandomState(bits)
+    sizes = [1.0, 1e15, 3e18, 1e19, 2.0, 1e25, 1e30, 1e36, 0.5, 1e37]
+    rows = [rng.randn(256) * s for s in sizes] + [rng.uniform(-3.3e38, 3.3e38, 256), np.full(256, 3e38), np.full(256, -1e20), np.eye(256)[3] * 3e38,
+                                                  rng.choice([-1e30, 1e30], 256), np.concatenate([rng.randn(128), rng.randn(128) * 1e22])]
+    x = torch.from_numpy(np.array(rows, dtype=np.float32)).cuda().to(dtype)
+    assert torch.isfinite(x).all()
+    n, cap = len(rows), len(rows) + 2
+    cb = O.analytic_codebook(bits)
+    g = C.cq_kv_geometry(1, 1, 256, 256, bits, bits, cb, cb, 1.0)
+    blobs = [torch.zeros(C.cq_packed_bytes(cap, 256, 128, bits), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    C.cq_kv_write_slots(g, *blobs, cap, x, x, _i32(np.arange(n)))
+    codes, norms = R.encode(_np(x), bits, cb)
+    for blob in blobs:
+        gc, gn = R.split_blob(blob.cpu().numpy(), cap, 256, bits)
+        np.testing.assert_array_equal(gc[:n], R.pack(codes, R.width_of(bits)))
+        np.testing.assert_array_equal(gn[:n].view(np.uint16), norms.view(np.uint16))
