@@ -16,10 +16,17 @@
 // Exponents. The norm of a value row goes into the exponent:
 //   w[c][t] = 2^(x log2(e) + log2 n_v[t] - m[c]),  o = H sum_t w levels / sum_t w / n_v[t].
 // w is what the second product takes in fp16 (one rounding of 2^-11); with the reference m from the
-// column's own logits it neither over- nor underflows whatever the size of the norms. m starts at the
+// column's own logits it does not overflow whatever the size of the norms. m starts at the
 // largest logit of 32 rows and rises when a column's w would pass 2^15 (the accumulators are then
 // scaled, which is rare: at 2^8 it cost 5 to 9%); columns decide for themselves, so a column's bits do
 // not depend on the others.
+//
+// Small weights. A w below 2^-14 loses bits in fp16 and one below 2^-25 is nothing, and the tensor core, too, drops what lies
+// 2^-25 below its sum; the denominators keep them. One row far above all others would so cost a long context n 2^-25 of its result
+// (0.38% of 131071 rows measured). Every kChunk tiles a part therefore starts over from references and sums of its own and is
+// joined with what there was, in fp32: 16384 rows lose 2^-11 at most, one rounding of an fp16 result. It costs contexts of 65536 rows
+// 1 to 4% (32 requests; 6% for single tokens of heads over two groups) and shorter parts nothing. (References below the largest logit instead keep such weights too, but then they
+// rise often: 8 powers of two lower 314 -> 455 us for the server.)
 //
 // Queries in fp16. Each column is rounded at the power of two of its own largest element (rotate_queries), so that a query of any
 // size leaves its tile mates' bits alone. The product then takes the columns at the tile's largest scale where that is exact for
@@ -70,6 +77,7 @@ namespace {
 constexpr int kTile = 128;        // cache rows per tile
 constexpr int kMaxThreads = 640;
 constexpr int kMaxDepth = 8;      // stages of the ring of codes
+constexpr int kChunk = 128;       // tiles of an item that are summed from references of their own
 constexpr unsigned kSpin = 1u << 20;   // polls of up to ~1 us
 constexpr float kNoMax = -1e30f;       // reference of a column that has attended nothing yet
 constexpr float kRaise = 15.0f;         // log2 of the largest weight before a reference is raised (fp16 ends below 2^16)
@@ -709,7 +717,8 @@ __device__ void issue_role(const TreeParams &p, Shared &sh, uint8_t *smem) {
     const uint32_t tmem = uniform(sh.tmem);
     const int tiles = uniform(c.left);
     uint32_t zpar = 0;
-    bool first = true, next_first = true;  // tile i, tile i + 1 starts its item's part
+    bool next_first = true;  // tile i + 1 starts its item's part
+    int since = 0;           // tiles of this part before tile i
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
         const bool two_k = NG == 2 && uniform(p.unit[c.u].ngk == 2), two_v = NG == 2 && uniform(p.unit[c.u].ngv == 2);
@@ -717,8 +726,9 @@ __device__ void issue_role(const TreeParams &p, Shared &sh, uint8_t *smem) {
             wait(sh, &sh.z_full, zpar, p.status, 0x47490006u);
             zpar ^= 1;
             issue_scores<N, NG, ZT>(p, sh, smem, tmem, i, two_k);
+            since = 0;
         }
-        first = next_first;
+        const bool first = since++ % kChunk == 0;  // of a chunk
         const bool more = c.advance(p, N);
         next_first = uniform(!more || c.tile == 0);
         if (!next_first) issue_scores<N, NG, ZT>(p, sh, smem, tmem, i + 1, two_k);  // while softmax works on tile i
@@ -1301,6 +1311,29 @@ __device__ __noinline__ void scale_scores(Shared &sh, uint32_t ts, int c0, bool 
     wait_st();
 }
 
+// What a part has summed so far (reference and denominator `old`, the thread's own write) and a chunk's m and x, taken together,
+// with the factors for both sums.
+__device__ __noinline__ void join_references(float2 old, float &m, float &x, float &before, float &now) {
+    const float top = fmaxf(old.x, m);
+    before = ex2(old.x - top), now = ex2(m - top);
+    x = fmaf(x, now, old.y * before);
+    m = top;
+}
+// Likewise the sums of n columns from c0 on (tensor memory at ts, a thread its own value coordinate).
+__device__ __noinline__ void join_sums(Shared &sh, float *out, uint32_t ts, int c0, int n, int wg) {
+#pragma unroll 1
+    for (int k = 0; k < n; k += 8) {
+        float o[8], old[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) old[j] = k + j < n ? out[(size_t)(c0 + k + j) * kGroup] : 0.0f;
+        tmem_ld<8>(ts + c0 + k, o);
+        wait_ld<8>(o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (k + j < n) out[(size_t)(c0 + k + j) * kGroup] = fmaf(o[j], sh.f[c0 + k + j], old[j] * sh.by_warp[4 * wg][k + j]);
+    }
+}
+
 template <int N, int NG, int ZT>
 __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int warp, int lane) {
     using L = Plan<N, NG, ZT>;
@@ -1312,27 +1345,30 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
     Cursor c = sh.start;
     int i = 0;
     long long place = sh.first;  // of the tile to come
-    bool more = true;
+    bool more = true, again = false;  // again: a chunk of the same item's part
+    float mult = 0.0f;
+    bool wide = false;
     stash_queries<N, NG, ZT>(p, smem, c, warp, lane);
     while (more) {
-        // ------------------------------------------------ one item's part --
-        bar_sync(1, kSoftThreads);  // the item before is finished: the exponents, m, mask may be written
-        if (warp == 0 && lane == 0) sh.ztop = kNoEx, sh.zlow = -kNoEx;
-        if (row < NC) sh.minus_m[c0 + row] = -kNoMax;
-        gather_mask<N>(p, sh, c, warp, L::kSoft, lane);
-        bar_sync(1, kSoftThreads);
-        bool wide;
-        const float mult = rotate_queries<N, NG, ZT>(p, sh, smem, c, warp, lane, wide);
-        fence_async();
-        fence_before();  // tensor memory reads of the item before
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.z_full);
+        // ------------------------------------------ a chunk of an item's part --
         const TreeUnit u = p.unit[c.u];
         const int cols = min(N, c.n * u.nh * p.per - c.c * N), slot = blockIdx.x + c.item;
-        const int i0 = (c.s * p.n_units + c.u) * p.ncol_max + c.c;
-        if (c.tile == 0 && warp == 0 && lane == 0)
-            p.rec[i0] = make_int2(slot, run_of(sh.total, p.grid, place + c.ntiles - 1) - (int)blockIdx.x + 1);
-        const int count = min(c.ntiles - c.tile, c.left);
+        if (!again) {
+            bar_sync(1, kSoftThreads);  // the item before is finished: the exponents, m, mask may be written
+            if (warp == 0 && lane == 0) sh.ztop = kNoEx, sh.zlow = -kNoEx;
+            if (row < NC) sh.minus_m[c0 + row] = -kNoMax;
+            gather_mask<N>(p, sh, c, warp, L::kSoft, lane);
+            bar_sync(1, kSoftThreads);
+            mult = rotate_queries<N, NG, ZT>(p, sh, smem, c, warp, lane, wide);
+            fence_async();
+            fence_before();  // tensor memory reads of the item before
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.z_full);
+            const int i0 = (c.s * p.n_units + c.u) * p.ncol_max + c.c;
+            if (c.tile == 0 && warp == 0 && lane == 0)
+                p.rec[i0] = make_int2(slot, run_of(sh.total, p.grid, place + c.ntiles - 1) - (int)blockIdx.x + 1);
+        }
+        const int count = min(kChunk, min(c.ntiles - c.tile, c.left));
         const bool two = NG == 2 && u.ngk == 2;
         F2 l[NC / 2];
 #pragma unroll
@@ -1427,7 +1463,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_full);
         }
-        // ------------------------------------------------- the item's partials --
+        // ------------------------------------------------ the chunk's partials --
 #pragma unroll
         for (int hf = 0; hf < NC; hf += X) {
             float v[X];
@@ -1452,19 +1488,33 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
         }
         bar_sync(2 + wg, 128);
         if (row < NC && c0 + row < cols) {
-            const float x = sh.by_warp[4 * wg][row] + sh.by_warp[4 * wg + 1][row] + (sh.by_warp[4 * wg + 2][row] + sh.by_warp[4 * wg + 3][row]);
-            p.ml[(size_t)slot * N + c0 + row] = make_float2(-sh.minus_m[c0 + row], x);
+            float x = sh.by_warp[4 * wg][row] + sh.by_warp[4 * wg + 1][row] + (sh.by_warp[4 * wg + 2][row] + sh.by_warp[4 * wg + 3][row]);
+            float m = -sh.minus_m[c0 + row];
+            float2 *ml = &p.ml[(size_t)slot * N + c0 + row];
+            if (__builtin_expect(again, 0)) join_references(*ml, m, x, sh.by_warp[4 * wg][row], sh.f[c0 + row]);
+            *ml = make_float2(m, x);
         }
-        place += count + item_cost(N);  // where there is more, the next item starts
+        place += count;
         c.left -= count;
+        c.tile += count;
         more = c.left > 0;
-        if (more) c.next_item(p, N);
+        const bool merge = again;
+        again = more && c.tile < c.ntiles;
+        if (merge || again) bar_sync(2 + wg, 128);  // the factors; the references may be written again
+        if (more && !again) {
+            place += item_cost(N);
+            c.next_item(p, N);
+        }
         wait(sh, &sh.p_empty, (uint32_t)(i - 1) & 1, p.status, 0x4749000Du);
         fence_after();
-        if (more) stash_queries<N, NG, ZT>(p, smem, c, warp, lane);
+        if (more && !again) stash_queries<N, NG, ZT>(p, smem, c, warp, lane);
         const int nat = NG == 2 ? natural_of(row, p.wv) : row;
         for (int g = 0; g < u.ngv; ++g) {
             float *out = p.part + ((size_t)slot * NG + g) * N * kGroup + nat;
+            if (__builtin_expect(merge, 0)) {
+                join_sums(sh, out, tm + L::cO + g * N, c0, min(NC, cols - c0), wg);
+                continue;
+            }
 #pragma unroll 1
             for (int k = 0; k < NC; k += 8) {
                 if (c0 + k >= cols) break;

@@ -85,6 +85,41 @@ def test_attend_queries_of_every_size_match_the_definition(C, geom, scale):
     assert np.isfinite(tol).mean() > 0.3
 
 
+@pytest.mark.parametrize("where", [0, 40, 5000])
+@pytest.mark.parametrize("gap", [17.5, 22.3, 25.05])
+@pytest.mark.parametrize("n", [1, 40])
+def test_attend_rows_far_below_a_dominant_one_still_count(C, where, gap, n):
+    """131071 rows with 2^-gap times the weight of one row, which comes first, later or much later, in more requests than
+    thread blocks, so that one block has nearly all of a request. Together they are 0.4% to 70% of that row, against its
+    sign. Allowed in the 2-norm: one rounding of the result and one of the dominant weight, 2^-11 each, and a quarter of one
+    for levels, the others' weights and sums."""
+    seqs, ctx, d, bs = 160, 131071, 128, 1024
+    cap = (ctx + n + bs - 1) // bs * bs
+    cb = O.analytic_codebook(2)
+    rng = np.random.RandomState(where + n)
+    kc, vc = _blob(cap, d, 2, rng), _blob(cap, d, 2, rng)
+    kn, (vcodes, vn) = R.split_blob(kc, cap, d, 2)[1], R.split_blob(vc, cap, d, 2)
+    kn[:] = 0  # a logit of exactly zero
+    kn[where], vn[:] = 1.0, 1.0
+    vcodes[:] = vcodes[where]
+    vn[where] = -1.0
+    k0 = R.dequant(kc, cap, d, 2, cb, np.array([where]))[0][0]
+    q = torch.from_numpy(k0 / np.dot(k0, k0) * gap * math.log(2)).to(F16).cuda().expand(seqs * n, 1, d).contiguous()
+    g = C.cq_kv_geometry(1, 1, d, d, 2, 2, cb, cb, 1.0)
+    table = torch.arange(cap // bs, dtype=torch.int32, device="cuda").expand(seqs, -1).contiguous()
+    o = C.cq_kv_tree_attend(g, q, torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), cap, table, bs, _i32([ctx] * seqs),
+                            _i32(np.arange(seqs + 1) * n), None, n)
+    torch.cuda.synchronize()
+    C.cq_device_status()
+    top = np.exp(np.dot(_np(q[0, 0]), k0))
+    v = R.dequant(vc, cap, d, 2, cb, np.array([where]))[0][0]  # the others are its negative
+    rows = ctx + np.tile(np.arange(n), seqs)  # others that a token attends
+    want = v[None] * ((top - rows) / (top + rows))[:, None]
+    err = np.linalg.norm(_np(o[:, 0]) - want, axis=1) / np.linalg.norm(v)
+    print(f"worst {err.max() * 2048:.2f} of 2^-11")
+    assert (err <= 2.25 * 2.0 ** -11).all()
+
+
 # ------------------------------------------------------------------------------------------------------- slot writes
 
 @pytest.mark.parametrize("bits", [2, 3, 4, 5])
