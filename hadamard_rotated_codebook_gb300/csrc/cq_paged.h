@@ -38,6 +38,7 @@ int tree_units(const cq_kv_geom &g, TreeUnit *u);
 int tree_smem_check(int reserved);
 size_t tree_workspace(const cq_kv_geom &g, int n_seqs, int max_nodes);
 // lk, lv: level tables of the key and value codes (level_table).
-int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float *lk, const float *lv, void *stream);
+// give_up: nobody tells the products that the queries are there, and waits give up after a few polls (a self-test).
+int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float *lk, const float *lv, bool give_up, void *stream);
 
 }  // namespace cq

@@ -183,7 +183,7 @@ size_t cq_kv_tree_workspace(const cq_kv_geom *g, int n_seqs, int max_nodes) {
     return tree_workspace(*g, n_seqs, max_nodes);
 }
 
-int cq_kv_tree_attend(const cq_kv_geom *g, const cq_kv_tree *t, void *stream) {
+static int tree_attend(const cq_kv_geom *g, const cq_kv_tree *t, bool give_up, void *stream) {
     clear_error();
     TreeUnit u[kMaxUnits];
     int st = check_tree_geom(g, u);
@@ -213,7 +213,11 @@ int cq_kv_tree_attend(const cq_kv_geom *g, const cq_kv_tree *t, void *stream) {
     float lk[16], lv[16];
     level_table(g->k_bits, g->k_codebook, lk);
     level_table(g->v_bits, g->v_codebook, lv);
-    return launch_kv_tree_attend(*g, *t, lk, lv, stream);
+    return launch_kv_tree_attend(*g, *t, lk, lv, give_up, stream);
 }
+
+int cq_kv_tree_attend(const cq_kv_geom *g, const cq_kv_tree *t, void *stream) { return tree_attend(g, t, false, stream); }
+
+int cq_selftest_tree_timeout(const cq_kv_geom *g, const cq_kv_tree *t, void *stream) { return tree_attend(g, t, true, stream); }
 
 }  // extern "C"

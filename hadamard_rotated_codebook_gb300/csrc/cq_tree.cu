@@ -78,7 +78,7 @@ constexpr int kTile = 128;        // cache rows per tile
 constexpr int kMaxThreads = 640;
 constexpr int kMaxDepth = 8;      // stages of the ring of codes
 constexpr int kChunk = 128;       // tiles of an item that are summed from references of their own
-constexpr unsigned kSpin = 1u << 20;   // polls of up to ~1 us
+constexpr unsigned kSpin = 1u << 20;   // polls, each of which may last some microseconds
 constexpr float kNoMax = -1e30f;       // reference of a column that has attended nothing yet
 constexpr float kRaise = 15.0f;         // log2 of the largest weight before a reference is raised (fp16 ends below 2^16)
 constexpr float kInvSqrt128 = 0.08838834764831845f;
@@ -102,6 +102,7 @@ struct TreeParams {
     bool vec_q;      // a column's query is whole runs of 16 elements on 16-byte boundaries
     int rows;        // most query heads of a unit
     int slots;       // of part and ml
+    unsigned spin;   // polls before a wait gives up
     int ncol_max;    // column tiles of a request with max_nodes tokens
     int grid;
 };
@@ -359,11 +360,11 @@ struct Shared {
 
 // The roles' loops run side by side on an SM and have to fit its instruction cache together (where they did not, each role
 // waited for instructions most of the time): loops are kept rolled, and what runs once per item out of line.
-__device__ __forceinline__ void wait(Shared &sh, uint64_t *bar, uint32_t parity, unsigned int *status, unsigned code) {
+__device__ __forceinline__ void wait(const TreeParams &p, Shared &sh, uint64_t *bar, uint32_t parity, unsigned code) {
     const uint32_t b = smem_u32(bar);
     for (unsigned i = 0; !mbar_try(b, parity) && !sh.abort; ++i)
-        if (i >= kSpin) {
-            atomicOr(status, code);
+        if (i >= p.spin) {
+            atomicOr(p.status, code);
             sh.abort = 1;
         }
 }
@@ -633,7 +634,7 @@ __device__ void fetch_role(const TreeParams &p, Shared &sh, uint8_t *smem, int l
         const RowAt now = next;
         next = after;
         after = row_at(p, c, lane + 64 * half);
-        if (!half) wait(sh, &sh.ring_empty[st], par, p.status, 0x4749000Eu);
+        if (!half) wait(p, sh, &sh.ring_empty[st], par, 0x4749000Eu);
         const uint32_t kc = ring + st * p.stage + (lane + 64 * half) * 16, vc = kc + Stage<NG>::codes(p.wk);
         const uint32_t info = vc + Stage<NG>::codes(p.wv) - (lane + 64 * half) * 12, nrm = info + Stage<NG>::kInfo;
         const long long at = (long long)now.blk * p.t.block_size + now.off;
@@ -669,8 +670,8 @@ __device__ __forceinline__ void issue_scores(const TreeParams &p, Shared &sh, ui
     const int b = i & 1, kb = L::kKBuf == 2 ? b : 0;
     const uint32_t par = (uint32_t)(i >> 1) & 1;
     const uint64_t dz = desc_sw128(smem_u32(smem + L::oZ), 16);
-    wait(sh, &sh.k_full[kb], L::kKBuf == 2 ? par : (uint32_t)(i & 1), p.status, 0x47490004u);
-    wait(sh, &sh.s_empty[b], par ^ 1, p.status, 0x47490005u);
+    wait(p, sh, &sh.k_full[kb], L::kKBuf == 2 ? par : (uint32_t)(i & 1), 0x47490004u);
+    wait(p, sh, &sh.s_empty[b], par ^ 1, 0x47490005u);
     __syncwarp();
     fence_after();
     // two groups keep their scores apart: their norms are ratios for softmax, which multiplies in fp32
@@ -693,8 +694,8 @@ template <int N, int NG, int ZT>
 __device__ __forceinline__ void issue_sums(const TreeParams &p, Shared &sh, uint8_t *smem, uint32_t tmem, int i, bool first, bool two) {
     using L = Plan<N, NG, ZT>;
     const int vb = L::kVBuf == 2 ? i & 1 : 0;
-    wait(sh, &sh.v_full[vb], L::kVBuf == 2 ? (uint32_t)(i >> 1) & 1 : (uint32_t)(i & 1), p.status, 0x47490007u);
-    wait(sh, &sh.p_full, (uint32_t)(i & 1), p.status, 0x47490008u);
+    wait(p, sh, &sh.v_full[vb], L::kVBuf == 2 ? (uint32_t)(i >> 1) & 1 : (uint32_t)(i & 1), 0x47490007u);
+    wait(p, sh, &sh.p_full, (uint32_t)(i & 1), 0x47490008u);
     __syncwarp();
     fence_after();
     const uint64_t dp = desc_sw128(smem_u32(smem + L::oP), kTile * 128);
@@ -723,7 +724,7 @@ __device__ void issue_role(const TreeParams &p, Shared &sh, uint8_t *smem) {
     for (int i = 0; i < tiles; ++i) {
         const bool two_k = NG == 2 && uniform(p.unit[c.u].ngk == 2), two_v = NG == 2 && uniform(p.unit[c.u].ngv == 2);
         if (next_first) {
-            wait(sh, &sh.z_full, zpar, p.status, 0x47490006u);
+            wait(p, sh, &sh.z_full, zpar, 0x47490006u);
             zpar ^= 1;
             issue_scores<N, NG, ZT>(p, sh, smem, tmem, i, two_k);
             since = 0;
@@ -898,7 +899,7 @@ __device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, bool
         uint32_t flip = 0;
         const uint32_t codes = ring + st * p.stage, info = codes + Stage<NG>::codes(p.wk) + Stage<NG>::codes(p.wv) + (keys ? 0 : kTile * 4);
         const uint32_t nrm = info + Stage<NG>::kInfo + (keys ? 0 : (NG - 1) * kTile * 4);
-        wait(sh, &sh.ring_full[st], rpar, p.status, 0x4749000Fu);
+        wait(p, sh, &sh.ring_full[st], rpar, 0x4749000Fu);
         const uint32_t word = lds32(info + row * 4);
         float n = row_norm<NG>(word, nrm + row * 4, two, ratio);
         if (!keys) {
@@ -912,7 +913,7 @@ __device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, bool
         const float safe = n == 0.0f ? 0x1p-40f : n;
         const bool lost = !(n <= 65504.0f), real = word & 1;
         const float ln = lost ? __int_as_float(0x7FC00000) : __log2f(safe), inv = lost ? 0.0f : __fdividef(1.0f, safe);
-        wait(sh, &sh.s_empty[b], par ^ 1, p.status, 0x47490001u);
+        wait(p, sh, &sh.s_empty[b], par ^ 1, 0x47490001u);
         if (keys) {
             sh.scal[b][0][row] = real ? n : 0.0f;
             if (NG == 2) {  // softmax applies the ratios of the keys, in fp32
@@ -927,7 +928,7 @@ __device__ void expand_role(const TreeParams &p, Shared &sh, uint8_t *smem, bool
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sc_full[b]);
-        wait(sh, keys ? &sh.k_empty[buf] : &sh.v_empty[buf], (twice ? par : (uint32_t)(i & 1)) ^ 1, p.status, 0x47490002u);
+        wait(p, sh, keys ? &sh.k_empty[buf] : &sh.v_empty[buf], (twice ? par : (uint32_t)(i & 1)) ^ 1, 0x47490002u);
         fence_after();
         const uint32_t from = keys ? codes : codes + Stage<NG>::codes(p.wk);
         if (w == 2) expand_tile<N, NG, ZT, 2>(p, smem, tmem, keys, from, tab, buf, row, q, ratio, flip, two);
@@ -1363,7 +1364,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
             fence_async();
             fence_before();  // tensor memory reads of the item before
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.z_full);
+            if (lane == 0 && p.spin == kSpin) mbar_arrive(&sh.z_full);  // a self-test's products wait in vain
             const int i0 = (c.s * p.n_units + c.u) * p.ncol_max + c.c;
             if (c.tile == 0 && warp == 0 && lane == 0)
                 p.rec[i0] = make_int2(slot, run_of(sh.total, p.grid, place + c.ntiles - 1) - (int)blockIdx.x + 1);
@@ -1385,7 +1386,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
                 const int j = tok + row - c.ctx;
                 see[k] = j >= 0 && j < c.n ? sh.mask[j][(c0 + 32 * k) >> 5] >> (c0 & 31) : 0xFFFFFFFFu;
             }
-            wait(sh, &sh.sc_full[b], par, p.status, 0x47490009u);
+            wait(p, sh, &sh.sc_full[b], par, 0x47490009u);
             const float nk = sh.scal[b][0][row] * mult, ln = sh.scal[b][1][row], inv = sh.scal[b][2][row];
             float r0 = 1.0f, r1 = 0.0f;
             if (NG == 2) {
@@ -1393,7 +1394,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
                 r0 = __uint_as_float(lds32(from)), r1 = __uint_as_float(lds32(from + kTile * 4));
             }
             const F2 nk2 = f2(nk, nk), ln2 = f2(ln, ln), inv2 = f2(inv, inv);
-            wait(sh, &sh.s_full[b], par, p.status, 0x4749000Au);
+            wait(p, sh, &sh.s_full[b], par, 0x4749000Au);
             fence_after();
             if (__builtin_expect(wide, 0)) scale_scores<N, NG, NC>(sh, tm + L::cS + b * NG * N + c0, c0, two);
             // Column by column in halves of X: the denominators of all columns and the logits of one half fit the registers.
@@ -1433,7 +1434,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
                         l[(hf + k) / 2] = f2_mul(l[(hf + k) / 2], f2(f.x, f.y));
                     }
                     if (it) {  // the first tile's product does not accumulate
-                        wait(sh, &sh.p_empty, (uint32_t)(i - 1) & 1, p.status, 0x4749000Bu);
+                        wait(p, sh, &sh.p_empty, (uint32_t)(i - 1) & 1, 0x4749000Bu);
                         fence_after();
                         scale_sums(sh, tm + L::cO, N, u.ngv, cx, X);
                     }
@@ -1443,7 +1444,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.s_empty[b]);
                 }
-                if (hf == 0) wait(sh, &sh.p_empty, (uint32_t)(i & 1) ^ 1, p.status, 0x4749000Cu);
+                if (hf == 0) wait(p, sh, &sh.p_empty, (uint32_t)(i & 1) ^ 1, 0x4749000Cu);
                 // weights in fp16: cache row `row`, columns cx .. cx + X - 1 (the MN-major B operand)
                 const uint32_t pb = smem_u32(smem + L::oP) + (cx >> 6) * (kTile * 128) + (row >> 3) * 1024 + (row & 7) * 128;
 #pragma unroll
@@ -1505,7 +1506,7 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
             place += item_cost(N);
             c.next_item(p, N);
         }
-        wait(sh, &sh.p_empty, (uint32_t)(i - 1) & 1, p.status, 0x4749000Du);
+        wait(p, sh, &sh.p_empty, (uint32_t)(i - 1) & 1, 0x4749000Du);
         fence_after();
         if (more && !again) stash_queries<N, NG, ZT>(p, smem, c, warp, lane);
         const int nat = NG == 2 ? natural_of(row, p.wv) : row;
@@ -1854,7 +1855,7 @@ size_t tree_workspace(const cq_kv_geom &g, int n_seqs, int max_nodes) {
     return up16(s.items * sizeof(int2)) + up16(s.slots * s.N * sizeof(float2)) + s.slots * s.ng * s.N * kGroup * sizeof(float);
 }
 
-int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float *lk, const float *lv, void *stream) {
+int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float *lk, const float *lv, bool give_up, void *stream) {
     TreeParams p;
     const Shape s = shape_of(g, t.n_seqs, t.max_nodes, p.unit);
     if (s.slots > (size_t)INT_MAX / 2 || (s.N + 7) / 8 > 65535)
@@ -1872,6 +1873,7 @@ int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float 
     p.div_mul = (uint32_t)(((1ull << (31 + l)) + (unsigned)t.block_size - 1) / (unsigned)t.block_size);
     if (!t.max_blocks) p.t.block_table = t.cu_nodes, p.t.table_stride = 0;  // no token is read, but entry 0 is
     p.slots = (int)s.slots;
+    p.spin = give_up ? 4 : kSpin;
     p.rows = s.rows, p.ncol_max = s.ncol_max, p.grid = sm_count();
     p.status = device_status_ptr();
     if (!p.status) return set_error(CQ_ERR_CUDA, "no device status word");

@@ -568,6 +568,17 @@ int cq_selftest_dirty_counters(void *stream);
  * count on the 1024 of this GPU): CQ_OK or CQ_ERR_CUDA. */
 int cq_selftest_tree_smem(int reserved);
 
+/* Diagnostic without a counterpart on the pages: cq_kv_tree_attend whose
+ * products wait for queries that nobody announces, with waits that give up
+ * after a few polls, so that its kernel takes the path of a pipeline that has
+ * come to a stop: no role waits any more, products in flight are waited for
+ * (bounded), tensor memory is freed. o is written but holds
+ * nothing of use; a following cq_device_status reports CQ_ERR_TIMEOUT (code
+ * 0x4749....), and the next call works as ever. Errors: as for
+ * cq_kv_tree_attend. */
+int cq_selftest_tree_timeout(const cq_kv_geom *geom, const cq_kv_tree *t,
+                             void *stream);
+
 /* -------------------------------------------------------- container -- */
 /*
  * Own .cact-shaped container (the pages disagree on the header: 196 bytes

@@ -143,3 +143,23 @@ def test_write_slots_of_rows_whose_squares_leave_fp32(C, bits, dtype):
         gc, gn = R.split_blob(blob.cpu().numpy(), cap, 256, bits)
         np.testing.assert_array_equal(gc[:n], R.pack(codes, R.width_of(bits)))
         np.testing.assert_array_equal(gn[:n].view(np.uint16), norms.view(np.uint16))
+
+
+# ------------------------------------------------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("geom", [(4, 2, 64, 64), (8, 2, 128, 128), (6, 6, 80, 80), (4, 1, 256, 256)])
+@pytest.mark.parametrize("n", [1, 7, 40])
+def test_attend_waits_that_run_out_end_the_call_with_a_status(C, monkeypatch, geom, n):
+    """A wait that nothing ends gives up: every role runs through its tiles without waiting, the kernel ends, the host
+    reads CQ_ERR_TIMEOUT, and the next call gives what the one before gave."""
+    from hadamard_rotated_codebook_gb300 import _capi
+    lib = _capi.load()
+    pool = _Pool(C, geom, 4, 700, n, 0.125, seed=n)
+    q = pool.q.to(BF16)
+    want = pool.run(q)
+    with monkeypatch.context() as m:
+        m.setattr(lib, "cq_kv_tree_attend", lib.cq_selftest_tree_timeout)
+        with pytest.raises(C.CQError, match="0x4749"):
+            pool.run(q)
+    C.cq_device_status()
+    assert torch.equal(pool.run(q), want)
