@@ -34,7 +34,9 @@ struct PlanParams {
 struct Two {
     int a, b;
 };
-__device__ __forceinline__ Two operator+(Two x, Two y) { return {x.a + y.a, x.b + y.b}; }
+// Sums of lengths and blocks, held at 2^31 - 1: past that no token has a place, and the order of adding does not matter.
+__device__ __forceinline__ int held_sum(int x, int y) { return (int)min((unsigned)x + (unsigned)y, 0x7FFFFFFFu); }
+__device__ __forceinline__ Two operator+(Two x, Two y) { return {held_sum(x.a, y.a), held_sum(x.b, y.b)}; }
 
 __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const __grid_constant__ PlanParams p) {
     __shared__ int s_cu[kTile + 1], s_dem[kTile], s_len[kTile], s_held[kTile], s_extra[kTile];
@@ -78,7 +80,8 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const __grid_constant
             if (w < warp) before = before + s_warp[w];
             total = total + s_warp[w];
         }
-        Two run{before.a + inc.a - sum.a, before.b + inc.b - sum.b};
+        Two run{__shfl_up_sync(0xFFFFFFFFu, inc.a, 1), __shfl_up_sync(0xFFFFFFFFu, inc.b, 1)};
+        run = lane ? before + run : before;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int j = tid * kPer + i;
@@ -107,7 +110,9 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const __grid_constant
             const long long pos = (long long)s_len[lo] + (t - s_cu[lo]);
             const long long blk = pos / bs;
             int block = -1;
-            if (blk < s_held[lo]) {
+            if (pos > 0x7FFFFFFF) {
+                // no position, and no slot
+            } else if (blk < s_held[lo]) {
                 block = S.block_table[(base + lo) * S.table_stride + blk];
             } else if (blk < S.max_blocks) {
                 const long long at = (long long)n_free - 1 - s_dem[lo] - (blk - s_held[lo]);
@@ -116,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const __grid_constant
             const long long slot = block < 0 ? -1 : (long long)block * bs + (pos - blk * bs);
             if (slot < 0 || slot > 0x7FFFFFFF) bad = true;
             S.slots[t] = slot > 0x7FFFFFFF ? -1 : (int)slot;
-            S.positions[t] = (int)pos;
+            S.positions[t] = pos > 0x7FFFFFFF ? -1 : (int)pos;
             S.token_seq[t] = base + lo;
         }
         // the table entries of the blocks taken, a warp per request
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const __grid_constant
     }
     if (blockIdx.x == 0 && tid == 0) {
         S.cu_new[S.n_seqs] = carry.a;
-        S.n_free_out[0] = n_free - carry.b;
+        S.n_free_out[0] = (int)max((long long)n_free - carry.b, -0x80000000ll);
         bad |= carry.a > S.n_tokens;
     }
     if (bad) atomicOr(p.status, kStatusIndex);
@@ -153,8 +158,8 @@ int launch_kv_plan(const cq_kv_step &s, void *stream) {
     p.status = device_status_ptr();
     if (!p.status) return set_error(CQ_ERR_CUDA, "no device status word");
     // a token is a search and three stores: two tokens a thread, at most two blocks an SM
-    const int grid = std::max(1, std::min(2 * sm_count(), (s.n_tokens + 2 * kThreads - 1) / (2 * kThreads)));
-    p.per = (s.n_tokens + grid - 1) / grid;
+    const int grid = (int)std::max(1ll, std::min(2ll * sm_count(), ((long long)s.n_tokens + 2 * kThreads - 1) / (2 * kThreads)));
+    p.per = (int)(((long long)s.n_tokens + grid - 1) / grid);
     kv_plan_kernel<<<grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(CQ_ERR_CUDA, "plan launch: %s", cudaGetErrorString(e));

@@ -468,7 +468,8 @@ typedef struct cq_kv_step {
  * the next step passes the lengths after acceptance, held_out and n_free_out.
  * Where the stack runs out, or a table row would need more than max_blocks,
  * the missing blocks and their tokens' slots are -1; where the tokens do not
- * fit into n_tokens, the rest is dropped; each marks the device status word,
+ * fit into n_tokens, the rest is dropped; a position past 2^31 - 1 is -1, and
+ * so is its slot; sums in cu_new stay at 2^31 - 1. Each marks the device status word,
  * which a following cq_device_status reports as CQ_ERR_INDEX. n_free_out =
  * n_free minus the blocks asked for: negative by what is missing. Lengths
  * below zero count as zero. held_out and n_free_out must not be held and

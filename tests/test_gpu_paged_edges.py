@@ -145,6 +145,52 @@ def test_write_slots_of_rows_whose_squares_leave_fp32(C, bits, dtype):
         np.testing.assert_array_equal(gn[:n].view(np.uint16), norms.view(np.uint16))
 
 
+# ------------------------------------------------------------------------------------------------------------- plan
+
+TOP = 2 ** 31 - 1
+
+
+def _plan(C, lens, new, held, table, free, bs, room):
+    t = _i32(table)
+    out = C.cq_kv_plan(_i32(lens), _i32(new), _i32(held), t, _i32(free), _i32([len(free)]), bs, room)
+    torch.cuda.synchronize()
+    with pytest.raises(C.CQError):
+        C.cq_device_status()
+    C.cq_device_status()
+    return t.tolist(), {k: v.tolist() for k, v in out.items()}
+
+
+def test_plan_lengths_whose_sum_leaves_32_bits(C):
+    """Four requests of 2^30 new tokens: what fits into the slot map is planned, the rest is dropped and reported."""
+    table, out = _plan(C, [0] * 4, [2 ** 30] * 4, [0] * 4, [[-1, -1]] * 4, [3, 2, 1, 0], 2 ** 30, 8)
+    assert table == [[0, -1], [1, -1], [2, -1], [3, -1]] and out["held_out"] == [1] * 4 and out["n_free_out"] == [0]
+    assert out["cu_new"] == [0, 2 ** 30, TOP, TOP, TOP]
+    assert out["slots"] == out["positions"] == list(range(8)) and out["token_seq"] == [0] * 8
+    # over more than one chunk of requests
+    n = 1100
+    table, out = _plan(C, [0] * n, [2 ** 22] * n, [0] * n, [[-1]] * n, list(range(n))[::-1], 2 ** 22, 16)
+    assert table == [[i] for i in range(n)] and out["n_free_out"] == [0]
+    assert out["cu_new"] == [min(i * 2 ** 22, TOP) for i in range(n + 1)]
+    assert out["slots"] == out["positions"] == list(range(16)) and out["token_seq"] == [0] * 16
+
+
+def test_plan_positions_that_leave_32_bits(C):
+    table, out = _plan(C, [TOP - 2, 5], [5, 1], [2, 1], [[0, 1, -1], [1, -1, -1]], [7, 9], 2 ** 30, 7)
+    assert table == [[0, 1, 9], [1, -1, -1]] and out["held_out"] == [3, 1] and out["n_free_out"] == [1]
+    assert out["positions"] == [TOP - 2, TOP - 1, TOP, -1, -1, 5, -1]
+    assert out["slots"] == [TOP - 2, TOP - 1, TOP, -1, -1, 2 ** 30 + 5, -1]
+    assert out["token_seq"] == [0, 0, 0, 0, 0, 1, -1] and out["cu_new"] == [0, 5, 6]
+
+
+def test_plan_missing_blocks_stay_countable(C):
+    """A stack that is already below zero by all it can be: the count stays where it is."""
+    t = _i32([[-1, -1]])
+    out = C.cq_kv_plan(_i32([0]), _i32([20]), _i32([0]), t, _i32([4]), _i32([-(2 ** 31)]), 16, 20)
+    torch.cuda.synchronize()
+    assert out["n_free_out"].tolist() == [-(2 ** 31)] and t.tolist() == [[-1, -1]] and out["slots"].tolist() == [-1] * 20
+    with pytest.raises(C.CQError):
+        C.cq_device_status()
+
 # ------------------------------------------------------------------------------------------------- waits that run out
 
 @pytest.mark.parametrize("geom", [(4, 2, 64, 64), (8, 2, 128, 128), (6, 6, 80, 80), (4, 1, 256, 256)])
