@@ -197,3 +197,23 @@ def test_host_tensors_are_refused(C):
         C.cq_kv_tree_attend(g, x, x, x, 4, i, 16, i, i, None, 2)
     with pytest.raises(ValueError):
         C.cq_kv_geometry(4, 2, 48, 64, 3, 2, cb, cb, 0.1)  # four levels for three bits
+
+
+def test_sizes_past_32_bits_are_refused(C):
+    """They are cut to 32 bits on the way into the library: 2^32 + 16 would pass as 16."""
+    import torch
+    x, i = torch.zeros(2, 4, 8), torch.zeros(2, dtype=torch.int32)
+    wide = 2 ** 32
+    cb = np.array(CB2, dtype=np.float32)
+    g = C.cq_kv_geometry(4, 2, 48, 64, 2, 2, cb, cb, 0.1)
+    for call in (lambda: C.cq_rope_init(wide + 8),
+                 lambda: C.cq_kv_geometry(wide + 4, 2, 48, 64, 2, 2, cb, cb, 0.1), lambda: C.cq_kv_geometry(4, 2 - wide, 48, 64, 2, 2, cb, cb, 0.1),
+                 lambda: C.cq_kv_geometry(4, 2, wide + 48, 64, 2, 2, cb, cb, 0.1), lambda: C.cq_kv_geometry(4, 2, 48, wide + 64, 2, 2, cb, cb, 0.1),
+                 lambda: C.cq_kv_plan(i, i, i, torch.zeros(2, 2, dtype=torch.int32), i, i, wide + 16, 4),
+                 lambda: C.cq_kv_plan(i, i, i, torch.zeros(2, 2, dtype=torch.int32), i, i, 16, wide + 4),
+                 lambda: C.cq_kv_write_slots(g, x, x, wide + 4, torch.zeros(2, 96), torch.zeros(2, 128), i),
+                 lambda: C.cq_kv_tree_attend(g, x, x, x, wide + 4, i, 16, i, i, None, 2),
+                 lambda: C.cq_kv_tree_attend(g, x, x, x, 4, i, wide + 16, i, i, None, 2),
+                 lambda: C.cq_kv_tree_attend(g, x, x, x, 4, i, 16, i, i, None, wide + 2)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
