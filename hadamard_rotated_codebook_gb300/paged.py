@@ -280,8 +280,11 @@ def cq_kv_tree_attend(geom: KvGeometry, q: torch.Tensor, k_cache: torch.Tensor, 
     (positions 0 .. context_lens[s] - 1) and the drafted tokens j of its
     request (position context_lens[s] + j) whose bit j is set in row i of
     ``mask`` (int32 words, [nodes, words]); with mask None, tokens 0 .. i. No
-    request has more than ``max_nodes`` (up to 256). Returns o [nodes, Hq,
-    head_dim_v] of q's type; a token that attends nothing gets zeros."""
+    request has more than ``max_nodes`` (up to 256: a longer prompt takes several
+    calls). Returns o [nodes, Hq, head_dim_v] of q's type; a token that attends
+    nothing gets zeros. Rows that no request covers (padding behind the last one,
+    say) are not written: an o made by the call is uninitialised there, so give
+    one where such rows are read."""
     dev = q.device
     _int(cap, "cap"), _int(block_size, "block_size"), _int(max_nodes, "max_nodes")
     n, hq, dk, qt, qh = _heads(q, "q", dev)

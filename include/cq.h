@@ -525,7 +525,11 @@ size_t cq_kv_tree_workspace(const cq_kv_geom *geom, int n_seqs, int max_nodes);
  * j % 32 of mask[i][j / 32] is set (its ancestors and itself, for a tree).
  * Drafted token j stands in the cache at position context_lens[s] + j. With
  * mask NULL token i attends drafted tokens 0 .. i: a linear draft or a chunk
- * of a prompt. A token that attends nothing gets o = 0. What a token does not
+ * of a prompt, which is at most CQ_TREE_MAX_NODES long (a longer one takes
+ * several calls, each of which reads the context again). A token that attends
+ * nothing gets o = 0. Rows of q and o that no request covers (before
+ * cu_nodes[0], from cu_nodes[n_seqs] on, all of them where n_seqs or max_nodes
+ * is 0) are not read and keep what they hold. What a token does not
  * attend has no influence on it, whatever bytes the cache holds there; rows
  * past the drafted tokens are never read.
  * The caches are never expanded in memory. Levels and rotated queries go to

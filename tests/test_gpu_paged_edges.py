@@ -120,6 +120,26 @@ def test_attend_rows_far_below_a_dominant_one_still_count(C, where, gap, n):
     assert (err <= 2.25 * 2.0 ** -11).all()
 
 
+@pytest.mark.parametrize("n_seqs,most", [(2, 3), (0, 3), (2, 0)])
+def test_attend_rows_that_no_request_covers_keep_what_they_hold(C, n_seqs, most):
+    """Rows before the first request and behind the last one, as in a batch padded to a captured size."""
+    hq, hkv, d = 4, 2, 64
+    cb = O.analytic_codebook(4)
+    g = C.cq_kv_geometry(hq, hkv, d, d, 4, 4, cb, cb, 0.125)
+    kc, vc = (torch.from_numpy(_blob(64, hkv * d, 4, np.random.RandomState(i))).cuda() for i in (1, 2))
+    q = torch.randn(9, hq, d, device="cuda").to(F16)
+    q[:2], q[6:] = math.nan, math.nan  # rows that are not read either
+    o = torch.full((9, hq, d), 7.0, dtype=F16, device="cuda")
+    cu = _i32([2, 5, 6][:n_seqs + 1]) if most else _i32([2, 2, 2])
+    C.cq_kv_tree_attend(g, q, kc, vc, 64, _i32([[0, 1], [2, 3]]), 16, _i32([20, 7][:n_seqs]), cu, None, most, o=o)
+    torch.cuda.synchronize()
+    C.cq_device_status()
+    covered = slice(2, 6) if n_seqs and most else slice(0, 0)
+    keep = torch.ones(9, dtype=torch.bool)
+    keep[covered] = False
+    assert (o[keep.cuda()] == 7).all()
+    assert torch.isfinite(o).all() and (o[covered] != 7).any(-1).all()
+
 # ------------------------------------------------------------------------------------------------------- slot writes
 
 @pytest.mark.parametrize("bits", [2, 3, 4, 5])
