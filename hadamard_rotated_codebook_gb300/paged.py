@@ -29,11 +29,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (  # the h
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _int(x: int, name: str) -> int:
-    """The library's sizes are 32 bits wide, and ctypes cuts what is wider without a word."""
-    if not -0x80000000 <= x <= 0x7FFFFFFF:
-        raise ValueError(f"{name} must fit 32 bits, got {x}")
-    return x
+def _ints(**sizes) -> None:
+    """The library's sizes are 32 bits wide, and ctypes cuts what is wider without a word. (Calls come here where
+    the sizes or'ed together leave 31 bits; what is below zero is the library's to refuse.)"""
+    for name, x in sizes.items():
+        if not -0x80000000 <= x <= 0x7FFFFFFF:
+            raise ValueError(f"{name} must fit 32 bits, got {x}")
 
 
 def _type(t: torch.Tensor, name: str) -> int:
@@ -112,7 +113,8 @@ def cq_rope_init(rot_dim: int, theta: float = 10000.0, inv_freq=None) -> np.ndar
     """Rotation rates for cq_qk_norm_rope, made once per model: ``rot_dim / 2``
     64-bit fractions of a turn per position, of theta^(-2i/rot_dim) or of the
     given ``inv_freq`` (radians per position)."""
-    n = max(0, _int(rot_dim, "rot_dim") // 2)
+    _ints(rot_dim=rot_dim)
+    n = max(0, rot_dim // 2)
     rates = np.zeros(n, dtype=np.uint64)
     f = None
     if inv_freq is not None:
@@ -141,7 +143,8 @@ def cq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, r
     another type than the input, and may be the inputs themselves."""
     dev = q.device
     n, hq, d, qt, qh = _heads(q, "q", dev)
-    _int(n, "tokens")
+    if n >> 31:
+        _ints(tokens=n)
     nk, hkv, dk, kt, kh = _heads(k, "k", dev)
     dtype = q.dtype
     if n != nk or d != dk or k.dtype != dtype:
@@ -178,12 +181,14 @@ def cq_kv_plan(seq_lens: torch.Tensor, new_lens: torch.Tensor, held: torch.Tenso
     n_free_out, slots, positions, token_seq, cu_new (any of them may be given).
     Missing blocks and dropped tokens make a following cq_device_status raise."""
     dev = seq_lens.device
-    n = _int(seq_lens.numel(), "requests")
+    n = seq_lens.numel()
     if n_tokens is None:
         if slots is None:
             raise ValueError("give n_tokens or slots")
         n_tokens = slots.numel()
-    _int(n_tokens, "n_tokens"), _int(block_size, "block_size"), _int(free_list.numel(), "free_list's length")
+    n_free_max = free_list.numel()
+    if (n | n_tokens | block_size | n_free_max) >> 31:
+        _ints(requests=n, n_tokens=n_tokens, block_size=block_size, free_list=n_free_max)
 
     def out(t, m):
         return torch.empty(m, dtype=torch.int32, device=dev) if t is None else t
@@ -196,7 +201,7 @@ def cq_kv_plan(seq_lens: torch.Tensor, new_lens: torch.Tensor, held: torch.Tenso
                   _i32(slots, "slots", n_tokens, dev), _i32(positions, "positions", n_tokens, dev),
                   _i32(token_seq, "token_seq", n_tokens, dev), _i32(cu_new, "cu_new", n + 1, dev),
                   block_table.stride(0) if n > 1 else block_table.shape[1], n, block_table.shape[1], block_size,
-                  free_list.numel(), n_tokens)
+                  n_free_max, n_tokens)
     _call(dev, _load().cq_kv_plan, step)
     return {"held_out": held_out, "n_free_out": n_free_out, "slots": slots, "positions": positions,
             "token_seq": token_seq, "cu_new": cu_new}
@@ -207,8 +212,7 @@ class KvGeometry:
     logit scale, laid out once (see cq_kv_geometry)."""
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim_k, head_dim_v, k_bits, v_bits, k_codebook, v_codebook, scale):
-        for x, name in ((n_q_heads, "n_q_heads"), (n_kv_heads, "n_kv_heads"), (head_dim_k, "head_dim_k"), (head_dim_v, "head_dim_v")):
-            _int(x, name)
+        _ints(n_q_heads=n_q_heads, n_kv_heads=n_kv_heads, head_dim_k=head_dim_k, head_dim_v=head_dim_v)
         self._keep = _codebook_arg(k_codebook, k_bits), _codebook_arg(v_codebook, v_bits)
         self.n_q_heads, self.n_kv_heads = n_q_heads, n_kv_heads
         self.head_dim_k, self.head_dim_v = head_dim_k, head_dim_v
@@ -262,7 +266,8 @@ def cq_kv_write_slots(geom: KvGeometry, k_cache: torch.Tensor, v_cache: torch.Te
     head width]) into rows slots[i] of the two caches in one launch; -1 skips
     a row. Slots must be distinct; one outside the cache is skipped and makes a
     following cq_device_status raise."""
-    _int(cap, "cap")
+    if cap >> 31:
+        _ints(cap=cap)
     dev = k.device
     (n, ks), (nv, vs) = _rows(k, geom.k_width, "k", dev), _rows(v, geom.v_width, "v", dev)
     if n != nv or k.dtype != v.dtype:
@@ -286,7 +291,8 @@ def cq_kv_tree_attend(geom: KvGeometry, q: torch.Tensor, k_cache: torch.Tensor, 
     say) are not written: an o made by the call is uninitialised there, so give
     one where such rows are read."""
     dev = q.device
-    _int(cap, "cap"), _int(block_size, "block_size"), _int(max_nodes, "max_nodes")
+    if (cap | block_size | max_nodes) >> 31:
+        _ints(cap=cap, block_size=block_size, max_nodes=max_nodes)
     n, hq, dk, qt, qh = _heads(q, "q", dev)
     if hq != geom.n_q_heads or dk != geom.head_dim_k:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected [nodes, {geom.n_q_heads}, {geom.head_dim_k}]")
