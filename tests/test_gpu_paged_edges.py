@@ -120,6 +120,27 @@ def test_attend_rows_far_below_a_dominant_one_still_count(C, where, gap, n):
     assert (err <= 2.25 * 2.0 ** -11).all()
 
 
+@pytest.mark.parametrize("geom", [(4, 1, 64, 64), (2, 1, 128, 128), (1, 1, 256, 256), (3, 3, 80, 80)])
+@pytest.mark.parametrize("n", [1, 12, 40])
+@pytest.mark.parametrize("first,last", [(0.5, 24.0), (24.0, 0.5)])
+def test_attend_long_parts_are_joined_from_chunks(C, geom, n, first, last):
+    """More requests (over the same rows) than thread blocks, so that a block sums 20000 rows of one; key norms that grow or
+    shrink along the context, so that the chunks' references lie far apart."""
+    hq, hkv, dk, dv = geom
+    pool = _Pool(C, geom, 4, 20000, n, 0.25, seed=n + dk)
+    R.split_blob(pool.kc, pool.cap, hkv * dk, 4)[1][pool.table[0][np.arange(pool.cap) // pool.bs] * pool.bs + np.arange(pool.cap) % pool.bs] = \
+        np.linspace(first, last, pool.cap).astype(np.float16)[:, None]
+    seqs = 160
+    q = pool.q.to(F16)
+    o = C.cq_kv_tree_attend(pool.g, q.repeat(seqs, 1, 1), torch.from_numpy(pool.kc).cuda(), torch.from_numpy(pool.vc).cuda(), pool.cap,
+                            _i32(np.repeat(pool.table, seqs, 0)), pool.bs, _i32([pool.ctx] * seqs), _i32(np.arange(seqs + 1) * n), None, n)
+    torch.cuda.synchronize()
+    C.cq_device_status()
+    want, bound = pool.reference(q)
+    tol = bound + R.HALF_STEP["float16"] * (np.abs(want) + bound) + R.TINY["float16"]
+    err = np.abs(_np(o).reshape(seqs, n, hq, dv) - want)
+    assert (err <= tol).all(), f"worst error/tolerance {np.max(err / tol):.3g}"
+
 @pytest.mark.parametrize("n_seqs,most", [(2, 3), (0, 3), (2, 0)])
 def test_attend_rows_that_no_request_covers_keep_what_they_hold(C, n_seqs, most):
     """Rows before the first request and behind the last one, as in a batch padded to a captured size."""
