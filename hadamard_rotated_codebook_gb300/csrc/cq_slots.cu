@@ -12,19 +12,22 @@
 // times in shared memory, so that no two lanes of half a warp meet in a bank. Codebooks whose
 // midpoints lie too close for that are searched instead, over the midpoints as a heap.
 //
-// Decisions are those of exact arithmetic. In fp32 the seven stages and the
-// scaling are off by at most 8 roundings of 2^-24 of n (every partial sum is at most
-// n after scaling), 1/n by 7 and the quotient by 1: 16 in all, under 1e-6. No midpoint
+// Decisions are those of exact arithmetic. In fp32 the seven stages are off by at most 7 roundings
+// of 2^-24 of n (every partial sum is at most n after scaling), n by 7 of its own (12 of the sum of
+// squares, halved by the root, and the root's), and 1/sqrt(128), the quotient, the product and a
+// midpoint by one each: a coordinate next to midpoint m by 2^-24 (7 + 11 |m|) in all, the codebook's
+// margin (`near`: 4.6e-7 to 5.7e-7 for the analytic ones, 1.1e-6 for midpoints near 1). No midpoint
 // lies within 1/64 of a cell of its edge, so the cell's own midpoint (or the two next to a
-// coordinate on its search path) tells whether it is within 1e-6 of one; then, or where n lies
+// coordinate on its search path) tells whether it is within the margin of one; then, or where n lies
 // within 1e-6 of a border between two fp16 values, those coordinates and the norm are computed
 // again in fp64. For Gaussian rows that is about 1% of the groups, and mostly one coordinate of
 // them, so its sum is taken directly (the transform of the whole group in fp64, at this GPU's
 // sixty-fourth of the fp32 rate, would cost as much as all the rest).
 //
-// Bound by instructions, not by memory: 8190 rows of 8 heads of 128 in bf16, four and three bits (41.2 MB), take 36 us,
-// 1.16 TB/s or 17% of the copy rate. 650 instructions go to four groups; issue slots are used to 68%, with 27 warps on an SM
-// (59 registers, 33 KB of tables a block), and the fp64 pipe of the exact decisions to 23% of the time. A warp that
+// Bound by instructions, not by memory: 8190 rows of 8 heads of 128 in bf16, four and three bits (41.2 MB), take 35 us,
+// 1.18 TB/s or 17% of the copy rate. 650 instructions go to four groups; issue slots are used to 69%, with 27 warps on an SM
+// (58 registers, 33 KB of tables a block), and the fp64 pipe of the exact decisions to 15% of the time (25% at a margin of 1.1e-6
+// for every codebook: 36.7 us). A warp that
 // decides exactly takes half as long again as the others: dealing a block's tasks out as its warps come for them brought 45.7
 // to 35.6 us (before, SMs were busy 54000 to 86000 cycles). A step of 77 rows takes 12 to 13 us, most of it
 // setting the tables up and one pass through the code.
@@ -44,7 +47,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr float kNear = 1e-6f;
+constexpr float kNear = 1e-6f;           // of a norm: 8 roundings with that of the product
 constexpr int kCells = 132;              // 64 to a unit, over [-1, 1] and a margin
 constexpr int kCopies = 16;
 constexpr int kTable = kCells * kCopies;  // entries of 8 bytes
@@ -60,6 +63,7 @@ struct SideParams {
     long long warps;     // of four groups each
     bool cells;          // the cell table holds this codebook
     float heap[16];      // midpoints as a search heap: node 1 the middle one, children of k at 2k and 2k + 1
+    float near;          // how far fp32 may be from a coordinate next to a midpoint
     float offset;        // cell of u: the integer part of 64 u + offset - 2^16
     float cell_mid[kCells];
     uint8_t cell_code[kCells];
@@ -233,7 +237,7 @@ __device__ __forceinline__ void encode(const SlotParams &p, const SideParams &s,
             unsigned c = __float_as_uint(e.y) + (d > 0.0f);
             if (LEVELS == 3) c = (c - 1) & 3;
             word[j / 8] |= c << (j % 8 * W);
-            near |= (unsigned)(fabsf(d) <= kNear) << j;
+            near |= (unsigned)(fabsf(d) <= s.near) << j;
         }
     } else {
 #pragma unroll 1
@@ -260,7 +264,7 @@ __device__ __forceinline__ void encode(const SlotParams &p, const SideParams &s,
             }
             if (j < 8) word[0] |= c << (j * W);
             else word[1] |= c << ((j - 8) * W);
-            near |= (unsigned)(dist <= kNear) << j;
+            near |= (unsigned)(dist <= s.near) << j;
         }
     }
     uint64_t codes = word[0] | (uint64_t)word[1] << (8 * W);
@@ -368,6 +372,9 @@ int launch_kv_write_slots(const SlotSide side[2], int cap, int dtype, const int3
         const int levels = levels_of(a.bits);
         for (int l = 0; l < 16; ++l) s.heap[l] = 0.0f;
         for (int l = 0; l + 1 < levels; ++l) s.mid[l] = 0.5 * ((double)a.codebook[l] + (double)a.codebook[l + 1]);
+        double most = 0.0;  // the largest midpoint that a coordinate reaches
+        for (int l = 0; l + 1 < levels; ++l) most = std::max(most, std::min(1.0, std::fabs(s.mid[l])));
+        s.near = (float)(1.02 * std::ldexp(7.0 + 11.0 * most, -24));
         s.cells = find_cells(s.mid, levels - 1, s);
         if (levels == 3) {
             s.heap[1] = (float)s.mid[0], s.heap[2] = (float)s.mid[1];

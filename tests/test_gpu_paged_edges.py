@@ -186,6 +186,29 @@ def test_write_slots_of_rows_whose_squares_leave_fp32(C, bits, dtype):
         np.testing.assert_array_equal(gn[:n].view(np.uint16), norms.view(np.uint16))
 
 
+@pytest.mark.parametrize("book", [[-0.4, 0.2, 0.9, 0.98], [-1.01, -0.985, 0.95, 0.999], [-0.3, -0.1, 0.1, 0.3]])
+def test_write_slots_next_to_large_midpoints(C, book):
+    """Coordinates a few units of 2^-24 from midpoints of 0.04 to 0.9975, where fp32's error grows with the coordinate."""
+    cb = np.array(book, dtype=np.float32)
+    mids = (cb[1:].astype(np.float64) + cb[:-1].astype(np.float64)) / 2
+    rng = np.random.RandomState(int(abs(book[0]) * 100))
+    H, rows = R.hadamard(), []
+    for i in range(600):
+        m, k = mids[i % 3] * (1 + (i // 3 - 100) * 2.0 ** -25), rng.randint(128)
+        u = rng.randn(128) * np.exp(rng.randn(128))
+        u[k] = 0
+        u *= math.sqrt(1 - m * m) / np.linalg.norm(u)
+        u[k] = m
+        rows.append(u @ H * 2.0 ** rng.uniform(-8, 8))
+    x = torch.from_numpy(np.array(rows, dtype=np.float32)).cuda()
+    g = C.cq_kv_geometry(1, 1, 128, 128, 2, 2, cb, cb, 1.0)
+    blobs = [torch.zeros(C.cq_packed_bytes(600, 128, 128, 2), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    C.cq_kv_write_slots(g, *blobs, 600, x, x, _i32(np.arange(600)))
+    codes, norms = R.encode(_np(x), 2, cb)
+    gc, gn = R.split_blob(blobs[0].cpu().numpy(), 600, 128, 2)
+    np.testing.assert_array_equal(gc, R.pack(codes, 2))
+    np.testing.assert_array_equal(gn.view(np.uint16), norms.view(np.uint16))
+
 # ------------------------------------------------------------------------------------------------------------- plan
 
 TOP = 2 ** 31 - 1
