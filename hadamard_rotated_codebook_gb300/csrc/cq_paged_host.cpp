@@ -17,6 +17,20 @@ bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// x without its whole part as a 64-bit binary fraction, modulo 1.
+uint64_t fraction(double x) {
+    x -= std::trunc(x);
+    const uint64_t v = (uint64_t)(std::fabs(x) * 18446744073709551616.0);  // below 2^64: x is exact and below 1
+    return x < 0 ? 0 - v : v;
+}
+// f / (2 pi) modulo 1. The quotient in 64 bits alone is off by up to 2^-53 of itself, which a position of 10^9 makes more than
+// fp32's part in the angle; its remainder (2 pi in two doubles) brings the rest.
+uint64_t turns(double f) {
+    const double hi = 6.283185307179586, lo = 2.4492935982947064e-16;
+    const double q = f / hi;
+    return fraction(q) + fraction(std::fma(-q, lo, std::fma(-q, hi, f)) / hi);
+}
+
 // What the slot write and the attention need of a geometry.
 int check_cache_geom(const cq_kv_geom *g) {
     if (!g) return set_error(CQ_ERR_ARG, "null geometry");
@@ -84,14 +98,10 @@ int cq_rope_init(int rot_dim, double theta, const double *inv_freq, uint64_t *ra
     if (cap < (size_t)n) return set_error(CQ_ERR_ARG, "need room for %d rates, got %zu", n, cap);
     if (!inv_freq && !(std::isfinite(theta) && theta > 0))
         return set_error(CQ_ERR_ARG, "theta must be positive and finite");
-    const double two_pi = 6.283185307179586476925286766559;
     for (int i = 0; i < n; ++i) {
         const double f = inv_freq ? inv_freq[i] : std::pow(theta, -2.0 * i / rot_dim);
         if (!std::isfinite(f)) return set_error(CQ_ERR_ARG, "inv_freq[%d] is not finite", i);
-        double turns = f / two_pi;
-        turns -= std::floor(turns);  // whole turns change nothing
-        const double x = turns * 18446744073709551616.0;
-        rates[i] = x >= 18446744073709551616.0 ? 0 : (uint64_t)x;
+        rates[i] = turns(f);
     }
     return CQ_OK;
 }

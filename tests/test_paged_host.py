@@ -36,6 +36,23 @@ def test_rope_rates_are_fractions_of_a_turn(C):
     assert C.cq_rope_init(0).shape == (0,)
 
 
+def test_rope_rates_hold_all_their_bits(C):
+    """Against 2 pi in 60 digits: within two units of 2^-64, so that the largest position moves an angle by 2^-32 of a turn."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 120
+    two_pi = Decimal("6.28318530717958647692528676655900576839433879875021164194988918461563281257")
+    rng = np.random.RandomState(0)
+    freq = np.concatenate([[1.0, -1.0, 0.5, 1e-5, -1e-7, 6.283185307179586, 3.0, 1e-300, -1e-300, 0.0, 1000.0, -77.7],
+                           10000.0 ** -rng.rand(40), -(500000.0 ** -rng.rand(12))])
+    for at in range(0, len(freq), 32):
+        part = freq[at:at + 32]
+        rates = C.cq_rope_init(2 * len(part), inv_freq=part)
+        for f, r in zip(part, rates):
+            want = Decimal(float(f)) / two_pi * 2 ** 64
+            off = (Decimal(int(r)) - want) % 2 ** 64
+            assert min(off, 2 ** 64 - off) <= 2, f
+
+
 def test_rope_init_refuses(C, A):
     for kw in (dict(rot_dim=7), dict(rot_dim=258), dict(rot_dim=8, theta=0.0), dict(rot_dim=8, theta=math.inf),
                dict(rot_dim=4, inv_freq=[1.0, math.nan])):
