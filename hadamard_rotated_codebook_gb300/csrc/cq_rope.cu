@@ -17,8 +17,8 @@
 // which this GPU runs at a small fraction of its fp32 rate.
 //
 // The bound is memory: each element is read once and written once. 16383 tokens of 40 heads of 128 in bf16 (335 MB) take
-// 64.2 us, 5.2 TB/s or 77% of the copy rate; issue slots are used to two thirds and the shared-memory pipe (weights, staging of
-// loads and stores) to about half, with 24 warps on an SM. Small steps are a launch: 12 to 14 us through the Python
+// 63.7 us, 5.3 TB/s or 78% of the copy rate; issue slots are used to two thirds and the shared-memory pipe (weights, staging of
+// loads and stores) to about half, with 24 warps on an SM. Small steps are a launch: 13 to 18 us through the Python
 // binding, whose calls are what they cost: the kernel itself takes 5 to 6 from cold caches.
 // Tried and no faster: loads a batch of heads ahead (63.9 us), 4 blocks of 64 registers (66 to 83 us).
 #include <cuda_bf16.h>

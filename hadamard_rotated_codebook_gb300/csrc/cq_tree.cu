@@ -48,13 +48,14 @@
 // waits return at once and every role runs through its remaining tiles without waiting, so that the
 // block's barriers stay matched.
 //
-// What bounds it. Neither memory (9 to 18% of the copy rate) nor the tensor pipe (22 to 36% of the dense
+// What bounds it. Neither memory (18% of the copy rate for the decode batch below, which reads its caches once, 30% for the
+// server, whose column tiles read them again: 602 MB for 198) nor the tensor pipe (22 to 36% of the dense
 // rate at 128 columns): a tile of 16 columns takes about 2000 cycles and one of 128 about 3300, made of
-// the latencies of five roles that hand each other buffers, with 46 to 52% of the issue slots used and
-// shared memory busy for 46 to 65% of the time. An item (a request, unit and column tile) costs another
+// the latencies of five roles that hand each other buffers, with 46 to 51% of the issue slots used and
+// shared memory busy for 45 to 66% of the time. An item (a request, unit and column tile) costs another
 // 15000 to 20000 cycles to begin and end. Measured: 256 requests of 8000 tokens, 12 heads on 2 of 48/64, 2 bits,
 // one token each, 117 us; 32 requests of 2000 to 8000 tokens with trees of 40 to 64, 32 heads on 8 of 128, 4 bits,
-// 313 us; one of 131071 tokens with a tree of 64, the same heads, 2 bits, 203 us.
+// 316 us; one of 131071 tokens with a tree of 64, the same heads, 2 bits, 205 us.
 // Tried and slower: both sides or the keys alone looked up by byte permutes instead of tables (server 355 -> 495 us: the
 // integer pipe runs at half rate), two expander warpgroups a side, two softmax streams or eight fetchers for 16
 // columns (117 -> 120 to 145 us), leaving out the runs of 32 columns that a tree does not fill (203 -> 215 us and

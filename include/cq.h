@@ -332,12 +332,14 @@ int cq_kv_write(uint8_t *cache, int cap, int in, int bits,
                 const float *codebook, const float *rows, int t0, int n,
                 void *stream);
 
-/* Geometry shared by the sequences of one cq_kv_attend call (one layer). */
+/* Geometry shared by the sequences of one call (one layer). cq_kv_attend
+ * takes up to 16 query heads and cache rows of up to 512 elements; the calls
+ * over a paged cache below take up to 1024 and 65536. */
 typedef struct cq_kv_geom {
-    int n_q_heads;        /* 1..16, a multiple of n_kv_heads */
+    int n_q_heads;        /* a multiple of n_kv_heads */
     int n_kv_heads;       /* >= 1 */
-    int head_dim_k;       /* query/key head width; n_kv_heads*head_dim_k <= 512 */
-    int head_dim_v;       /* value head width;     n_kv_heads*head_dim_v <= 512 */
+    int head_dim_k;       /* query/key head width; a row has n_kv_heads*head_dim_k elements */
+    int head_dim_v;       /* value head width;     a row has n_kv_heads*head_dim_v elements */
     int k_bits, v_bits;   /* 2, 3, 4 or 5 (ternary) */
     const float *k_codebook, *v_codebook; /* host, cq_levels(bits) floats */
     float scale;          /* logit scale, typically 1/sqrt(head_dim_k) */
@@ -534,8 +536,11 @@ size_t cq_kv_tree_workspace(const cq_kv_geom *geom, int n_seqs, int max_nodes);
  * past the drafted tokens are never read.
  * The caches are never expanded in memory. Levels and rotated queries go to
  * the tensor cores in fp16 (an fp16 query as the sum of two fp16 values, a
- * bf16 query as one), probabilities times norms in fp16; logits, softmax
- * and sums are fp32. Block numbers
+ * bf16 query as one, each at a scale of its own), probabilities times norms
+ * in fp16 relative to the largest of at most 16384 rows, of which what lies
+ * below 2^-25 is lost; logits, softmax and sums are fp32. Where heads lie over
+ * two groups of a row, a norm that is not finite in one of them loses the row
+ * (NaN) to every head of either group that attends it. Block numbers
  * outside the cache, and lengths outside the given sizes, are skipped and
  * mark the device status word (CQ_ERR_INDEX). Every head must lie within two
  * groups of 128 of its cache row (all head widths up to 128, and 256).
@@ -546,7 +551,7 @@ int cq_kv_tree_attend(const cq_kv_geom *geom, const cq_kv_tree *t,
 
 /* Reads and clears the device-side status word (synchronises `stream`).
  * CQ_OK; CQ_ERR_TIMEOUT if a bounded wait gave up (results of that call are
- * invalid); CQ_ERR_INDEX if a gather met an index out of range (and no wait
+ * invalid); CQ_ERR_INDEX if a call met an index out of range (and no wait
  * gave up). */
 int cq_device_status(void *stream);
 
