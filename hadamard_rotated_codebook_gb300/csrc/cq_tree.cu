@@ -22,11 +22,11 @@
 // not depend on the others.
 //
 // Small weights. A w below 2^-14 loses bits in fp16 and one below 2^-25 is nothing, and the tensor core, too, drops what lies
-// 2^-25 below its sum; the denominators keep them. One row far above all others would so cost a long context n 2^-25 of its result
-// (0.38% of 131071 rows measured). Every kChunk tiles a part therefore starts over from references and sums of its own and is
-// joined with what there was, in fp32: 16384 rows lose 2^-11 at most, one rounding of an fp16 result. It costs contexts of 65536 rows
-// 1 to 4% (32 requests; 6% for single tokens of heads over two groups) and shorter parts nothing. (References below the largest logit instead keep such weights too, but then they
-// rise often: 8 powers of two lower 314 -> 455 us for the server.)
+// 2^-25 below its sum; the denominators keep them. One row far above all others would so cost a long context n 2^-25 of its
+// result (0.38% of 131071 rows measured). Every kChunk tiles a part therefore starts over from references and sums of its own
+// and is joined with what there was, in fp32: 16384 rows lose 2^-11 at most, one rounding of an fp16 result. It costs contexts
+// of 65536 rows 1 to 4% (32 requests; 6% for single tokens of heads over two groups) and shorter parts nothing. (References
+// below the largest logit keep such weights too, but rise often: 8 powers of two lower 314 -> 455 us for the server.)
 //
 // Queries in fp16. Each column is rounded at the power of two of its own largest element (rotate_queries), so that a query of any
 // size leaves its tile mates' bits alone. The product then takes the columns at the tile's largest scale where that is exact for
@@ -79,7 +79,7 @@ constexpr int kTile = 128;        // cache rows per tile
 constexpr int kMaxThreads = 640;
 constexpr int kMaxDepth = 8;      // stages of the ring of codes
 constexpr int kChunk = 128;       // tiles of an item that are summed from references of their own
-constexpr unsigned kSpin = 1u << 20;   // polls, each of which may last some microseconds
+constexpr unsigned kSpin = 1u << 20;   // polls of about 5 us each (measured)
 constexpr float kNoMax = -1e30f;       // reference of a column that has attended nothing yet
 constexpr float kRaise = 15.0f;         // log2 of the largest weight before a reference is raised (fp16 ends below 2^16)
 constexpr float kInvSqrt128 = 0.08838834764831845f;
