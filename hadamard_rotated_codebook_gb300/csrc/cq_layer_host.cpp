@@ -1,0 +1,84 @@
+// cq_layer_host.cpp -- host side of the block norm's and the adapters' entry points: argument checks, alignment.
+#include <cmath>
+#include <cstdint>
+
+#include "cq_layer.h"
+
+using namespace cq;
+
+namespace {
+
+bool is_float(int type) { return type >= CQ_T_F32 && type <= CQ_T_BF16; }
+bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int cq_block_norm(const cq_norm_desc *d, void *stream) {
+    clear_error();
+    if (!d) return set_error(CQ_ERR_ARG, "null descriptor");
+    if (!is_float(d->x_dtype) || !is_float(d->residual_dtype) || (!is_float(d->out_dtype) && d->out_dtype != CQ_T_I8))
+        return set_error(CQ_ERR_ARG, "unknown element types %d, %d, %d", d->x_dtype, d->residual_dtype, d->out_dtype);
+    if (d->n_tokens < 0) return set_error(CQ_ERR_SHAPE, "negative size");
+    if (d->width < 1 || d->width > CQ_NORM_MAX_WIDTH)
+        return set_error(CQ_ERR_SHAPE, "width must be 1..%d, got %d", CQ_NORM_MAX_WIDTH, d->width);
+    if (d->gate && d->gate_width != 1 && d->gate_width != d->width)
+        return set_error(CQ_ERR_SHAPE, "a gate has 1 or %d elements a token, got %d", d->width, d->gate_width);
+    if (d->gate_act < CQ_GATE_PLAIN || d->gate_act > CQ_GATE_SILU) return set_error(CQ_ERR_ARG, "unknown gate function %d", d->gate_act);
+    if (!(d->eps >= 0) || !std::isfinite(d->eps) || !std::isfinite(d->weight_offset) || !std::isfinite(d->branch_scale) ||
+        !std::isfinite(d->residual_scale))
+        return set_error(CQ_ERR_ARG, "eps must be finite and not negative, weight_offset and the scales finite");
+    if (d->n_tokens == 0) return CQ_OK;
+    if (!d->x || !d->out) return set_error(CQ_ERR_ARG, "null x or out");
+    if (d->out_dtype == CQ_T_I8 && !d->out_scale) return set_error(CQ_ERR_ARG, "int8 outputs need out_scale");
+    if (d->n_tokens > 1 && ((d->residual_out && d->residual_out_stride < d->width) || d->out_stride < d->width))
+        return set_error(CQ_ERR_SHAPE, "output rows of %d elements are %lld and %lld apart", d->width, (long long)d->residual_out_stride,
+                         (long long)d->out_stride);
+    return launch_block_norm(*d, stream);
+}
+
+int cq_lora_add(const cq_lora_desc *d, void *stream) {
+    clear_error();
+    if (!d) return set_error(CQ_ERR_ARG, "null descriptor");
+    if (d->w_dtype != CQ_T_F16 && d->w_dtype != CQ_T_BF16) return set_error(CQ_ERR_ARG, "weights are fp16 or bf16, got element type %d", d->w_dtype);
+    if (d->x_dtype != CQ_T_F32 && d->x_dtype != CQ_T_I8 && d->x_dtype != d->w_dtype)
+        return set_error(CQ_ERR_ARG, "activations are fp32, int8 or of the weights' type, got element type %d", d->x_dtype);
+    if (d->n_mats < 0 || d->n_mats > CQ_LORA_MAX_MATS)
+        return set_error(CQ_ERR_SHAPE, "at most %d matrices, got %d", CQ_LORA_MAX_MATS, d->n_mats);
+    if (d->n_tokens < 0 || d->n_seqs < 0 || d->n_adapters < 0) return set_error(CQ_ERR_SHAPE, "negative size");
+    if (d->in < 1) return set_error(CQ_ERR_SHAPE, "in must be at least 1, got %d", d->in);
+    if (d->rank < 1 || d->rank > CQ_LORA_MAX_RANK) return set_error(CQ_ERR_SHAPE, "rank must be 1..%d, got %d", CQ_LORA_MAX_RANK, d->rank);
+    for (int j = 0; j < d->n_mats; ++j)
+        if (d->out[j] < 1) return set_error(CQ_ERR_SHAPE, "out must be at least 1, got %d", d->out[j]);
+    if (d->n_mats == 0 || d->n_tokens == 0 || d->n_seqs == 0) return CQ_OK;
+    if (!d->x || !d->adapters || !d->cu_tokens) return set_error(CQ_ERR_ARG, "null x, adapters or cu_tokens");
+    if (d->x_dtype == CQ_T_I8 && !d->x_scale) return set_error(CQ_ERR_ARG, "int8 activations need x_scale");
+    for (int j = 0; j < d->n_mats; ++j) {
+        if (!d->y[j] || !d->y_out[j]) return set_error(CQ_ERR_ARG, "null y");
+        if (d->n_adapters && (!d->a[j] || !d->b[j])) return set_error(CQ_ERR_ARG, "null a or b");
+        if (d->n_tokens > 1 && d->y_out_stride[j] < d->out[j])
+            return set_error(CQ_ERR_SHAPE, "output rows of %d elements are %lld apart", d->out[j], (long long)d->y_out_stride[j]);
+        if (d->y[j] == d->y_out[j] && d->n_tokens > 1 && d->y_stride[j] != d->y_out_stride[j])
+            return set_error(CQ_ERR_SHAPE, "y is added to in place with rows %lld and %lld apart", (long long)d->y_stride[j],
+                             (long long)d->y_out_stride[j]);
+    }
+    LoraParams p;
+    p.d = *d;
+    p.cluster = 1;
+    p.status = device_status_ptr();
+    if (!p.status) return set_error(CQ_ERR_CUDA, "no device status word");
+    // Where 16-byte loads (8 of int8) and 16-byte accesses to y may be used; single elements elsewhere.
+    const int size = d->x_dtype == CQ_T_F32 ? 4 : d->x_dtype == CQ_T_I8 ? 1 : 2, run = d->x_dtype == CQ_T_I8 ? 8 : 16;
+    bool vec = d->in % 8 == 0 && aligned(d->x, run) && (d->n_tokens == 1 || d->x_stride * size % run == 0);
+    p.vec_b = d->rank % 4 == 0;
+    for (int j = 0; j < d->n_mats; ++j) {
+        vec = vec && aligned(d->a[j], 16);
+        p.vec_b = p.vec_b && aligned(d->b[j], 8);
+        p.vec_y[j] = d->out[j] % 4 == 0 && aligned(d->y[j], 16) && aligned(d->y_out[j], 16) &&
+                     (d->n_tokens == 1 || (d->y_stride[j] % 4 == 0 && d->y_out_stride[j] % 4 == 0));
+    }
+    return d->w_dtype == CQ_T_F16 ? launch_lora_f16(p, vec, stream) : launch_lora_bf16(p, vec, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,393 @@
+// cq_norm.cu -- a block's output onto the residual stream, and the next block's norm of the sum.
+//
+//   z = x / sqrt(mean(x^2) + eps) * (offset + wb)   (or x * (offset + wb), or x)
+//   r = residual_scale * res + branch_scale * act(gate) z
+//   y = r / sqrt(mean(r^2) + eps) * (offset + w),   or int8 codes of y with a scale per row
+//
+// A row's second mean needs all of r, so a row stays in registers: a team of lanes (a warp for rows of up to 1024
+// elements, else a block) owns a row, a lane has CH runs of 8 elements, and every element is read once and written
+// once. Teams walk over the rows; the rows to come are on their way into a ring in shared memory by bulk copies (one
+// instruction a tensor and row) while the reductions of this one wait on each other. Rows that are not whole 16-byte
+// units are read element by element instead. Which lane adds which element depends on the row's width alone, so a
+// row's bits depend neither on the other rows nor on how it is aligned.
+//
+// Codes: y_k = inv * t_k, t_k = r_k (offset + w_k). A product with one positive factor keeps the order of its values, so the
+// largest |y| is inv * max|t|, rounded, and the maximum is reduced together with the sum of squares. Scale and codes then
+// are those of cq_act_quant_int8 over the fp32 y, bit for bit.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "cq_layer.h"
+
+namespace cq {
+namespace {
+
+constexpr int kRun = 8;          // consecutive elements of a lane's run
+constexpr int kWarpRow = 1024;   // widest row that a warp takes alone
+constexpr int kWarpTeams = 4;    // such rows of a block
+constexpr int kMaxWarps = 16;    // of a block that takes a row
+constexpr int kMaxDepth = 4;
+constexpr unsigned kSpin = 1u << 20;
+constexpr int ring_bytes(int per_sm) { return 228 * 1024 / per_sm - 2048; }  // of a block: a kilobyte is the system's, less than one the barriers'
+static_assert(CQ_NORM_MAX_WIDTH <= 32 * kMaxWarps * 4 * kRun, "a block's lanes hold a row");
+static_assert(CQ_NORM_MAX_WIDTH * 12 <= ring_bytes(1), "a ring holds a row of each input in fp32");
+
+struct NormParams {
+    const void *x, *res, *gate;
+    const float *w, *wb;
+    void *sum, *y;
+    float *scale;
+    int64_t x_st, res_st, gate_st, sum_st, y_st;
+    int rows, d;
+    int x_type, res_type, y_type;
+    int act;
+    bool post, one_gate;  // one_gate: a gate per row
+    float eps, offset, branch, keep, inv_d;
+    unsigned int *status;
+    int depth;            // stages of a team's ring
+    int stage, at_res, at_gate;  // bytes of a stage; where its tensors begin
+};
+
+// A run as it comes from memory: 16 bytes of a 16-bit type, 32 of fp32.
+struct Raw {
+    uint4 a, b;
+};
+__device__ __forceinline__ float load_one(const void *base, int64_t off, int type) {
+    if (type == CQ_T_F32) return static_cast<const float *>(base)[off];
+    if (type == CQ_T_F16) return __half2float(static_cast<const __half *>(base)[off]);
+    return __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[off]);
+}
+__device__ __forceinline__ uint32_t pack_bits(float x, int type) {
+    return type == CQ_T_F16 ? (uint32_t)__half_as_ushort(__float2half_rn(x)) : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+// A run read element by element: n of its 8 exist.
+__device__ __forceinline__ void load_each(Raw &r, const void *base, int64_t off, int type, int n) {
+    uint32_t v[kRun];
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+        v[j] = 0;
+        if (j < n) v[j] = type == CQ_T_F32 ? static_cast<const uint32_t *>(base)[off + j] : static_cast<const uint16_t *>(base)[off + j];
+    }
+    if (type == CQ_T_F32) {
+        r.a = make_uint4(v[0], v[1], v[2], v[3]), r.b = make_uint4(v[4], v[5], v[6], v[7]);
+    } else {
+        r.a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        r.b = make_uint4(0, 0, 0, 0);
+    }
+}
+__device__ __forceinline__ void unpack(const Raw &r, int type, float (&v)[kRun]) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    if (type == CQ_T_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+    } else if (type == CQ_T_F16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+            v[2 * j] = f.x, v[2 * j + 1] = f.y;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_run(void *base, int64_t off, int type, const float (&v)[kRun], int n) {
+    if (!VEC) {
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) {
+            if (j >= n) continue;
+            if (type == CQ_T_F32) static_cast<float *>(base)[off + j] = v[j];
+            else static_cast<uint16_t *>(base)[off + j] = (uint16_t)pack_bits(v[j], type);
+        }
+        return;
+    }
+    if (type == CQ_T_F32) {
+        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + off);
+        p[0] = make_float4(v[0], v[1], v[2], v[3]);
+        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = pack_bits(v[2 * j], type) | pack_bits(v[2 * j + 1], type) << 16;
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + off) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <bool VEC>
+__device__ __forceinline__ void store_codes(int8_t *dst, const float (&v)[kRun], float step, int n) {
+    uint32_t q[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+        const float t = fminf(fmaxf(rintf(__fdiv_rn(v[j], step)), -128.0f), 127.0f);
+        q[j / 4] |= ((uint32_t)(int)t & 255u) << (8 * (j & 3));
+    }
+    if (VEC) {
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(q[0], q[1]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kRun; ++j)
+            if (j < n) dst[j] = (int8_t)(q[j / 4] >> (8 * (j & 3)));
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void load_weight(const float *w, int n, float (&t)[kRun]) {
+    if (VEC) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(w)), b = __ldg(reinterpret_cast<const float4 *>(w) + 1);
+        t[0] = a.x, t[1] = a.y, t[2] = a.z, t[3] = a.w, t[4] = b.x, t[5] = b.y, t[6] = b.z, t[7] = b.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) t[j] = j < n ? __ldg(w + j) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+__device__ __forceinline__ float open(float g, int act) {
+    return act == CQ_GATE_PLAIN ? g : act == CQ_GATE_SIGMOID ? sigmoid(g) : g * sigmoid(g);
+}
+
+// Sum of s and maximum of m over the team. Block teams: one barrier, the warps' parts in a buffer that alternates.
+template <bool WARP>
+__device__ __forceinline__ void reduce(float &s, float &m, bool with_max, float2 *buf) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (with_max) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    }
+    if (WARP) return;
+    const int warps = blockDim.x >> 5, part = threadIdx.x & (kMaxWarps - 1);
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(s, m);
+    __syncthreads();
+    const float2 v = part < warps ? buf[part] : make_float2(0.0f, 0.0f);  // both halves of a warp hold them all
+    s = v.x, m = v.y;
+#pragma unroll
+    for (int o = kMaxWarps / 2; o; o >>= 1) {
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (with_max) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    }
+}
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+// Starts the copies of a row into a stage of the ring (one lane).
+__device__ __forceinline__ void fetch_row(const NormParams &p, int64_t row, uint32_t to, uint32_t bar) {
+    const uint32_t nx = p.d * (p.x_type == CQ_T_F32 ? 4 : 2), nr = p.res ? p.d * (p.res_type == CQ_T_F32 ? 4 : 2) : 0;
+    const uint32_t ng = p.gate && !p.one_gate ? nx : 0;
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(nx + nr + ng) : "memory");
+    const int64_t size = p.x_type == CQ_T_F32 ? 4 : 2, rsize = p.res_type == CQ_T_F32 ? 4 : 2;
+    bulk(to, static_cast<const uint8_t *>(p.x) + row * p.x_st * size, nx, bar);
+    if (nr) bulk(to + p.at_res, static_cast<const uint8_t *>(p.res) + row * p.res_st * rsize, nr, bar);
+    if (ng) bulk(to + p.at_gate, static_cast<const uint8_t *>(p.gate) + row * p.gate_st * size, ng, bar);
+}
+// A copy that does not land within kSpin polls marks the status word; the block then runs on without waiting.
+__device__ __forceinline__ void wait(const NormParams &p, uint32_t bar, uint32_t parity, volatile int &abort) {
+    for (unsigned i = 0;; ++i) {
+        uint32_t ok;
+        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity), "r"(1000u)
+                     : "memory");
+        if (ok || abort) return;
+        if (i >= kSpin) {
+            atomicOr(p.status, 0x474A0001u);
+            abort = 1;
+            return;
+        }
+    }
+}
+__device__ __forceinline__ void take_run(Raw &r, uint32_t from, int type) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w) : "r"(from) : "memory");
+    if (type == CQ_T_F32)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(r.b.x), "=r"(r.b.y), "=r"(r.b.z), "=r"(r.b.w) : "r"(from + 16) : "memory");
+}
+
+// VEC: rows are whole runs on 16-byte boundaries and come through the ring.
+template <int CH, bool WARP, bool VEC, bool GATE>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : 32 * kMaxWarps) block_norm_kernel(const __grid_constant__ NormParams p) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float2 s_buf[4][kMaxWarps];
+    __shared__ uint64_t s_full[WARP ? kWarpTeams : 1][kMaxDepth];
+    __shared__ volatile int s_abort;
+    const int lanes = WARP ? 32 : blockDim.x, lane = WARP ? threadIdx.x & 31 : threadIdx.x, team = WARP ? threadIdx.x >> 5 : 0;
+    const int64_t teams = WARP ? gridDim.x * kWarpTeams : gridDim.x;
+    int64_t row = WARP ? blockIdx.x * kWarpTeams + team : blockIdx.x;
+    const uint32_t mine = smem_u32(ring) + team * p.depth * p.stage, full = smem_u32(s_full[team]);
+    if (VEC) {
+        if (threadIdx.x == 0) s_abort = 0;
+        if (lane == 0) {
+            for (int i = 0; i < p.depth; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(full + 8 * i));
+            asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+            for (int i = 0; i < p.depth && row + i * teams < p.rows; ++i) fetch_row(p, row + i * teams, mine + i * p.stage, full + 8 * i);
+        }
+        __syncthreads();
+    }
+    int st = 0;
+    uint32_t par = 0;
+#pragma unroll 1
+    for (int turn = 0; row < p.rows; row += teams, turn ^= 2) {
+        const uint32_t from = mine + st * p.stage;
+        if (VEC) wait(p, full + 8 * st, par, s_abort);
+        float v[CH][kRun], none = 0.0f, inv = 1.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = (c * lanes + lane) * kRun, n = p.d - e;
+            Raw r = {};
+            if (!VEC) load_each(r, p.x, row * p.x_st + e, p.x_type, n);
+            else if (n > 0) take_run(r, from + e * (p.x_type == CQ_T_F32 ? 4 : 2), p.x_type);
+            unpack(r, p.x_type, v[c]);
+        }
+        if (p.post) {
+            float s = 0.0f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int j = 0; j < kRun; ++j) s = fmaf(v[c][j], v[c][j], s);
+            reduce<WARP>(s, none, false, s_buf[turn]);
+            inv = rsqrtf(fmaf(s, p.inv_d, p.eps));
+        }
+        float s = 0.0f, top = 0.0f;
+        const float gate1 = GATE && p.one_gate ? open(load_one(p.gate, row * p.gate_st, p.x_type), p.act) : 1.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = (c * lanes + lane) * kRun, n = p.d - e;
+            if (n <= 0) continue;
+            Raw r = {};
+            float t[kRun];
+            if (p.wb) {
+                load_weight<VEC>(p.wb + e, n, t);
+#pragma unroll
+                for (int j = 0; j < kRun; ++j) v[c][j] = v[c][j] * inv * (p.offset + t[j]);
+            } else {
+                const float one = p.post ? p.offset + 1.0f : 1.0f;
+#pragma unroll
+                for (int j = 0; j < kRun; ++j) v[c][j] = v[c][j] * inv * one;
+            }
+            if (GATE && p.one_gate) {
+#pragma unroll
+                for (int j = 0; j < kRun; ++j) v[c][j] *= gate1;
+            } else if (GATE) {
+                if (VEC) take_run(r, from + p.at_gate + e * (p.x_type == CQ_T_F32 ? 4 : 2), p.x_type);
+                else load_each(r, p.gate, row * p.gate_st + e, p.x_type, n);
+                unpack(r, p.x_type, t);
+#pragma unroll
+                for (int j = 0; j < kRun; ++j) v[c][j] *= open(t[j], p.act);
+            }
+            if (p.res) {
+                if (VEC) take_run(r, from + p.at_res + e * (p.res_type == CQ_T_F32 ? 4 : 2), p.res_type);
+                else load_each(r, p.res, row * p.res_st + e, p.res_type, n);
+                unpack(r, p.res_type, t);
+            }
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) {
+                v[c][j] = p.res ? fmaf(p.keep, t[j], p.branch * v[c][j]) : p.branch * v[c][j];
+                if (!VEC && j >= n) v[c][j] = 0.0f;  // what is not there may have become no number (0 times an infinity)
+                s = fmaf(v[c][j], v[c][j], s);
+            }
+            if (p.sum) store_run<VEC>(p.sum, row * p.sum_st + e, p.res_type, v[c], n);
+            if (p.w) {
+                load_weight<VEC>(p.w + e, n, t);
+#pragma unroll
+                for (int j = 0; j < kRun; ++j) v[c][j] *= p.offset + t[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < kRun; ++j) v[c][j] *= p.offset + 1.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) top = fmaxf(top, fabsf(v[c][j]));
+        }
+        reduce<WARP>(s, top, p.scale != nullptr, s_buf[turn + 1]);  // every lane has read its part of the stage
+        if (VEC) {
+            const int64_t ahead = row + p.depth * teams;
+            if (lane == 0 && ahead < p.rows) fetch_row(p, ahead, from, full + 8 * st);
+            if (++st == p.depth) st = 0, par ^= 1;
+        }
+        inv = rsqrtf(fmaf(s, p.inv_d, p.eps));
+        const float most = top * inv, step = most > 0.0f ? __fdiv_rn(most, 127.0f) : 1.0f;
+        if (p.scale && lane == 0) p.scale[row] = step;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = (c * lanes + lane) * kRun, n = p.d - e;
+            if (n <= 0) continue;
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) v[c][j] *= inv;
+            if (p.scale) store_codes<VEC>(static_cast<int8_t *>(p.y) + row * p.y_st + e, v[c], step, n);
+            else store_run<VEC>(p.y, row * p.y_st + e, p.y_type, v[c], n);
+        }
+    }
+}
+
+template <int CH, bool WARP, bool VEC, bool GATE>
+int launch_k(const NormParams &p, int grid, int threads, cudaStream_t st) {
+    const size_t smem = VEC ? (size_t)p.stage * p.depth * (WARP ? kWarpTeams : 1) : 0;
+    auto k = block_norm_kernel<CH, WARP, VEC, GATE>;
+    if (smem > 32 * 1024) {
+        const int rc = ensure_smem(reinterpret_cast<const void *>(k), ring_bytes(1));
+        if (rc) return rc;
+    }
+    k<<<grid, threads, smem, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return set_error(CQ_ERR_CUDA, "block norm launch: %s", cudaGetErrorString(e));
+    return CQ_OK;
+}
+template <int CH, bool WARP>
+int launch_c(const NormParams &p, bool vec, int grid, int threads, cudaStream_t st) {
+    if (vec) return p.gate ? launch_k<CH, WARP, true, true>(p, grid, threads, st) : launch_k<CH, WARP, true, false>(p, grid, threads, st);
+    return p.gate ? launch_k<CH, WARP, false, true>(p, grid, threads, st) : launch_k<CH, WARP, false, false>(p, grid, threads, st);
+}
+
+int size_of(int type) { return type == CQ_T_F32 ? 4 : type == CQ_T_I8 ? 1 : 2; }
+
+}  // namespace
+
+int launch_block_norm(const cq_norm_desc &d, void *stream) {
+    NormParams p;
+    p.x = d.x, p.res = d.residual, p.gate = d.gate, p.w = d.weight, p.wb = d.branch_weight;
+    p.sum = d.residual_out, p.y = d.out, p.scale = d.out_dtype == CQ_T_I8 ? d.out_scale : nullptr;
+    p.x_st = d.x_stride, p.res_st = d.residual_stride, p.gate_st = d.gate_stride, p.sum_st = d.residual_out_stride, p.y_st = d.out_stride;
+    p.rows = d.n_tokens, p.d = d.width;
+    p.x_type = d.x_dtype, p.res_type = d.residual_dtype, p.y_type = d.out_dtype;
+    p.act = d.gate_act, p.post = d.post_norm != 0, p.one_gate = d.gate && d.gate_width == 1;
+    p.eps = d.eps, p.offset = d.weight_offset, p.branch = d.branch_scale, p.keep = d.residual_scale;
+    p.inv_d = 1.0f / (float)d.width;
+    p.status = device_status_ptr();
+    if (!p.status) return set_error(CQ_ERR_CUDA, "no device status word");
+    // Rows in bulk copies and 16-byte accesses (8 of int8) need every row to start on such a boundary.
+    bool vec = d.width % kRun == 0;
+    auto runs = [&](const void *b, int64_t st, int type) {
+        const int bytes = std::min(16, kRun * size_of(type));
+        vec = vec && (!b || (reinterpret_cast<uintptr_t>(b) % bytes == 0 && (d.n_tokens == 1 || st * size_of(type) % bytes == 0)));
+    };
+    runs(p.x, p.x_st, p.x_type);
+    runs(p.res, p.res_st, p.res_type);
+    if (!p.one_gate) runs(p.gate, p.gate_st, p.x_type);
+    runs(p.sum, p.sum_st, p.res_type);
+    runs(p.y, p.y_st, p.y_type);
+    runs(p.w, 0, CQ_T_F32);
+    runs(p.wb, 0, CQ_T_F32);
+    const int chunks = (d.width + kRun - 1) / kRun, sms = sm_count();
+    p.at_res = p.d * size_of(p.x_type);
+    p.at_gate = p.at_res + (p.res ? p.d * size_of(p.res_type) : 0);
+    p.stage = p.at_gate + (p.gate && !p.one_gate ? p.d * size_of(p.x_type) : 0);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (d.width <= kWarpRow) {
+        const int per_sm = 6;
+        p.depth = std::max(1, std::min(kMaxDepth, ring_bytes(per_sm) / kWarpTeams / p.stage));
+        const int grid = (int)std::min<long long>(((long long)p.rows + kWarpTeams - 1) / kWarpTeams, (long long)sms * per_sm);
+        if (chunks <= 32) return launch_c<1, true>(p, vec, grid, 32 * kWarpTeams, st);
+        if (chunks <= 64) return launch_c<2, true>(p, vec, grid, 32 * kWarpTeams, st);
+        return launch_c<4, true>(p, vec, grid, 32 * kWarpTeams, st);
+    }
+    const int ch = chunks <= 2 * 32 * kMaxWarps ? 2 : 4, threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
+    int per_sm = std::max(1, 1024 / threads);
+    while (per_sm > 1 && ring_bytes(per_sm) / p.stage < 3) --per_sm;
+    p.depth = std::max(1, std::min(kMaxDepth, ring_bytes(per_sm) / p.stage));
+    const int grid = std::min(p.rows, per_sm * sms);
+    return ch == 2 ? launch_c<2, false>(p, vec, grid, threads, st) : launch_c<4, false>(p, vec, grid, threads, st);
+}
+
+}  // namespace cq

@@ -398,6 +398,7 @@ int cq_kv_attend(const cq_kv_geom *geom, const cq_kv_seq *seqs, int n_seqs,
 #define CQ_T_F32 0
 #define CQ_T_F16 1
 #define CQ_T_BF16 2
+#define CQ_T_I8 3 /* only where an entry point says so */
 
 /* Position rotation rates for cq_qk_norm_rope: rates[i] is the part of a
  * turn by which one position rotates pair i, as a 64-bit binary fraction:
@@ -548,6 +549,98 @@ size_t cq_kv_tree_workspace(const cq_kv_geom *geom, int n_seqs, int max_nodes);
  * cq_device_status if a pipeline wait gave up. */
 int cq_kv_tree_attend(const cq_kv_geom *geom, const cq_kv_tree *t,
                       void *stream);
+
+/* --------------------------------------- a layer's other serving steps -- */
+/*
+ * What stands between the quantised products of a layer beside the cache: the
+ * residual stream with the blocks' norms, and the low-rank adapters of the
+ * requests of a batch. The pages have no counterpart.
+ */
+
+/* What becomes of a gate before it multiplies a branch. */
+#define CQ_GATE_PLAIN 0
+#define CQ_GATE_SIGMOID 1
+#define CQ_GATE_SILU 2 /* gate * sigmoid(gate) */
+
+/* Widest row of cq_block_norm. */
+#define CQ_NORM_MAX_WIDTH 16384
+
+/* One call of cq_block_norm; device memory. Strides are in elements between
+ * rows; a row is contiguous. */
+typedef struct cq_norm_desc {
+    const void *x;             /* [n_tokens][width], x_dtype: what a block gave */
+    const void *residual;      /* [n_tokens][width], residual_dtype; NULL: zeros */
+    const void *gate;          /* [n_tokens][gate_width], x_dtype; NULL: ones */
+    const float *branch_weight;/* [width]; NULL: no weight */
+    const float *weight;       /* [width]; NULL: ones */
+    void *residual_out;        /* [n_tokens][width], residual_dtype; NULL: not wanted */
+    void *out;                 /* [n_tokens][width], out_dtype */
+    float *out_scale;          /* [n_tokens] for CQ_T_I8, else ignored */
+    int64_t x_stride, residual_stride, gate_stride, residual_out_stride, out_stride;
+    int x_dtype, residual_dtype; /* CQ_T_F32, CQ_T_F16, CQ_T_BF16 */
+    int out_dtype;             /* one of these or CQ_T_I8 */
+    int n_tokens, width;       /* width 1..CQ_NORM_MAX_WIDTH */
+    int gate_width;            /* width, or 1: a gate per token */
+    int gate_act;              /* CQ_GATE_* */
+    int post_norm;             /* the branch has a norm of its own */
+    float branch_scale, residual_scale, eps, weight_offset;
+} cq_norm_desc;
+
+/* A block's output onto the residual stream, and the norm that the next block
+ * begins with, in one pass:
+ *   z = x / sqrt(mean(x^2) + eps) * (weight_offset + branch_weight)   if post_norm
+ *   z = x * (weight_offset + branch_weight)   if not (x without branch_weight)
+ *   r = residual_scale * residual + branch_scale * act(gate) * z
+ *   y = r / sqrt(mean(r^2) + eps) * (weight_offset + weight)
+ * in fp32, each output rounded once: y is the norm of the unrounded r. A
+ * missing weight of a norm counts as 1 (weight_offset is added to it too).
+ * With out_dtype CQ_T_I8 out holds the int8 codes of y and out_scale their
+ * scales, the bits of cq_act_quant_int8 over the fp32 y. residual_out may be
+ * residual itself and out may be x itself (same pointer, stride and type); an
+ * output must not overlap an input in another way, nor the other output.
+ * Errors: CQ_ERR_ARG, CQ_ERR_SHAPE, CQ_ERR_CUDA. */
+int cq_block_norm(const cq_norm_desc *d, void *stream);
+
+/* Largest rank and number of matrices of cq_lora_add. */
+#define CQ_LORA_MAX_RANK 256
+#define CQ_LORA_MAX_MATS 8
+
+/* One call of cq_lora_add; device memory unless marked. Strides are in
+ * elements between rows; a row is contiguous. */
+typedef struct cq_lora_desc {
+    const void *x;             /* [n_tokens][in], x_dtype */
+    const float *x_scale;      /* [n_tokens] for CQ_T_I8, else ignored */
+    const float *scales;       /* [n_adapters]; NULL: ones */
+    const int32_t *ranks;      /* [n_adapters] ranks in use of each adapter, 0..rank; NULL: rank */
+    const int32_t *adapters;   /* [n_seqs] each request's adapter, or -1 */
+    const int32_t *cu_tokens;  /* [n_seqs + 1] first token of each request */
+    const void *a[CQ_LORA_MAX_MATS]; /* [n_adapters][rank][in], w_dtype */
+    const void *b[CQ_LORA_MAX_MATS]; /* [n_adapters][out[j]][rank], w_dtype */
+    const float *y[CQ_LORA_MAX_MATS];/* [n_tokens][out[j]] */
+    float *y_out[CQ_LORA_MAX_MATS];  /* likewise; may be y[j] */
+    int64_t y_stride[CQ_LORA_MAX_MATS], y_out_stride[CQ_LORA_MAX_MATS];
+    int out[CQ_LORA_MAX_MATS];
+    int64_t x_stride;
+    int n_mats, n_tokens, n_seqs, n_adapters, in, rank;
+    int x_dtype;               /* CQ_T_F32, CQ_T_I8, or w_dtype */
+    int w_dtype;               /* CQ_T_F16 or CQ_T_BF16 */
+} cq_lora_desc;
+
+/* Low-rank adapters of many requests beside shared projections: for every
+ * token t of request s with adapter e = adapters[s] >= 0 and every matrix j
+ *   y_out[j][t] = y[j][t] + scales[e] * B_j[e] (A_j[e] x[t])
+ * where only the first ranks[e] rows of A_j[e] and columns of B_j[e] count;
+ * x is x_scale[t] * x[t] for int8. Tokens of a request without an adapter
+ * (-1) keep y: they are copied where y_out is not y, and cost nothing where
+ * it is. Rows that no request covers are neither read nor written. Products
+ * with 16-bit weights are exact; sums and the values between the two products
+ * are fp32 (the second product takes them as two terms of 11 bits, which leaves
+ * 2^-22). x must not overlap an output, nor one matrix's output another's.
+ * A request outside the tokens (cu_tokens not ascending in 0..n_tokens) is
+ * skipped, one whose adapter or rank is outside its size counts as having
+ * none; both mark the device status word (CQ_ERR_INDEX). Errors: CQ_ERR_ARG,
+ * CQ_ERR_SHAPE, CQ_ERR_CUDA. */
+int cq_lora_add(const cq_lora_desc *d, void *stream);
 
 /* Reads and clears the device-side status word (synchronises `stream`).
  * CQ_OK; CQ_ERR_TIMEOUT if a bounded wait gave up (results of that call are
