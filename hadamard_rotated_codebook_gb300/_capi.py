@@ -25,8 +25,11 @@ CQ_GEMV_MAX_BATCH = 16
 CQ_MAX_GROUPED = 256
 CQ_GEMM_NOALLOC_MAX_ELEMS = 2 * 1024 * 1024
 CQ_DTYPE_FP16, CQ_DTYPE_FP32, CQ_DTYPE_CQ, CQ_DTYPE_RAW = 1, 2, 3, 4
-CQ_T_F32, CQ_T_F16, CQ_T_BF16 = 0, 1, 2
+CQ_T_F32, CQ_T_F16, CQ_T_BF16, CQ_T_I8 = 0, 1, 2, 3
 CQ_TREE_MAX_NODES = 256
+CQ_GATE_PLAIN, CQ_GATE_SIGMOID, CQ_GATE_SILU = 0, 1, 2
+CQ_NORM_MAX_WIDTH = 16384
+CQ_LORA_MAX_RANK, CQ_LORA_MAX_MATS = 256, 8
 
 ERROR_NAMES = {
     CQ_ERR_ARG: "CQ_ERR_ARG", CQ_ERR_SHAPE: "CQ_ERR_SHAPE", CQ_ERR_FORMAT: "CQ_ERR_FORMAT",
@@ -102,6 +105,31 @@ class KvTree(ctypes.Structure):
     ]
 
 
+class NormDesc(ctypes.Structure):
+    _fields_ = [
+        ("x", c_void_p), ("residual", c_void_p), ("gate", c_void_p), ("branch_weight", c_void_p), ("weight", c_void_p),
+        ("residual_out", c_void_p), ("out", c_void_p), ("out_scale", c_void_p),
+        ("x_stride", c_int64), ("residual_stride", c_int64), ("gate_stride", c_int64),
+        ("residual_out_stride", c_int64), ("out_stride", c_int64),
+        ("x_dtype", c_int), ("residual_dtype", c_int), ("out_dtype", c_int), ("n_tokens", c_int), ("width", c_int),
+        ("gate_width", c_int), ("gate_act", c_int), ("post_norm", c_int),
+        ("branch_scale", c_float), ("residual_scale", c_float), ("eps", c_float), ("weight_offset", c_float),
+    ]
+
+
+class LoraDesc(ctypes.Structure):
+    _fields_ = [
+        ("x", c_void_p), ("x_scale", c_void_p), ("scales", c_void_p), ("ranks", c_void_p), ("adapters", c_void_p),
+        ("cu_tokens", c_void_p),
+        ("a", c_void_p * CQ_LORA_MAX_MATS), ("b", c_void_p * CQ_LORA_MAX_MATS),
+        ("y", c_void_p * CQ_LORA_MAX_MATS), ("y_out", c_void_p * CQ_LORA_MAX_MATS),
+        ("y_stride", c_int64 * CQ_LORA_MAX_MATS), ("y_out_stride", c_int64 * CQ_LORA_MAX_MATS),
+        ("out", c_int * CQ_LORA_MAX_MATS), ("x_stride", c_int64),
+        ("n_mats", c_int), ("n_tokens", c_int), ("n_seqs", c_int), ("n_adapters", c_int), ("in_", c_int), ("rank", c_int),
+        ("x_dtype", c_int), ("w_dtype", c_int),
+    ]
+
+
 class TensorDesc(ctypes.Structure):
     _fields_ = [
         ("dtype", ctypes.c_uint8), ("ndim", ctypes.c_uint8), ("shape", c_uint32 * 4),
@@ -140,6 +168,8 @@ SIGNATURES = {
                                   c_int, c_void_p, c_int, c_void_p]),
     "cq_kv_tree_workspace": (c_size_t, [P(KvGeom), c_int, c_int]),
     "cq_kv_tree_attend": (c_int, [P(KvGeom), P(KvTree), c_void_p]),
+    "cq_block_norm": (c_int, [P(NormDesc), c_void_p]),
+    "cq_lora_add": (c_int, [P(LoraDesc), c_void_p]),
     "cq_device_status": (c_int, [c_void_p]),
     "cq_selftest_wait_timeout": (c_int, [c_void_p]),
     "cq_selftest_tree_smem": (c_int, [c_int]),

@@ -8,6 +8,8 @@ using namespace cq;
 
 namespace {
 
+constexpr int kMaxSide = 1 << 28;  // inputs and outputs of an adapted projection
+
 bool is_float(int type) { return type >= CQ_T_F32 && type <= CQ_T_BF16; }
 bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
@@ -47,10 +49,10 @@ int cq_lora_add(const cq_lora_desc *d, void *stream) {
     if (d->n_mats < 0 || d->n_mats > CQ_LORA_MAX_MATS)
         return set_error(CQ_ERR_SHAPE, "at most %d matrices, got %d", CQ_LORA_MAX_MATS, d->n_mats);
     if (d->n_tokens < 0 || d->n_seqs < 0 || d->n_adapters < 0) return set_error(CQ_ERR_SHAPE, "negative size");
-    if (d->in < 1) return set_error(CQ_ERR_SHAPE, "in must be at least 1, got %d", d->in);
+    if (d->in < 1 || d->in > kMaxSide) return set_error(CQ_ERR_SHAPE, "in must be 1..%d, got %d", kMaxSide, d->in);
     if (d->rank < 1 || d->rank > CQ_LORA_MAX_RANK) return set_error(CQ_ERR_SHAPE, "rank must be 1..%d, got %d", CQ_LORA_MAX_RANK, d->rank);
     for (int j = 0; j < d->n_mats; ++j)
-        if (d->out[j] < 1) return set_error(CQ_ERR_SHAPE, "out must be at least 1, got %d", d->out[j]);
+        if (d->out[j] < 1 || d->out[j] > kMaxSide) return set_error(CQ_ERR_SHAPE, "out must be 1..%d, got %d", kMaxSide, d->out[j]);
     if (d->n_mats == 0 || d->n_tokens == 0 || d->n_seqs == 0) return CQ_OK;
     if (!d->x || !d->adapters || !d->cu_tokens) return set_error(CQ_ERR_ARG, "null x, adapters or cu_tokens");
     if (d->x_dtype == CQ_T_I8 && !d->x_scale) return set_error(CQ_ERR_ARG, "int8 activations need x_scale");
