@@ -60,9 +60,6 @@ __device__ __forceinline__ float load_one(const void *base, int64_t off, int typ
     if (type == CQ_T_F16) return __half2float(static_cast<const __half *>(base)[off]);
     return __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[off]);
 }
-__device__ __forceinline__ uint32_t pack_bits(float x, int type) {
-    return type == CQ_T_F16 ? (uint32_t)__half_as_ushort(__float2half_rn(x)) : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
 // A run read element by element: n of its 8 exist.
 __device__ __forceinline__ void load_each(Raw &r, const void *base, int64_t off, int type, int n) {
     uint32_t v[kRun];
@@ -78,72 +75,149 @@ __device__ __forceinline__ void load_each(Raw &r, const void *base, int64_t off,
         r.b = make_uint4(0, 0, 0, 0);
     }
 }
-__device__ __forceinline__ void unpack(const Raw &r, int type, float (&v)[kRun]) {
+// Two fp32 operations in one instruction; a run is four such pairs.
+struct F2 {
+    uint64_t v;
+};
+constexpr int kPairs = kRun / 2;
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 f2_get(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ void unpack(const Raw &r, int type, F2 (&v)[kPairs]) {
     const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
     if (type == CQ_T_F32) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+        for (int j = 0; j < kPairs; ++j) v[j] = f2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
     } else if (type == CQ_T_F16) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kPairs; ++j) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-            v[2 * j] = f.x, v[2 * j + 1] = f.y;
+            v[j] = f2(f.x, f.y);
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        for (int j = 0; j < kPairs; ++j) v[j] = f2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
     }
 }
 template <bool VEC>
-__device__ __forceinline__ void store_run(void *base, int64_t off, int type, const float (&v)[kRun], int n) {
-    if (!VEC) {
+__device__ __forceinline__ void store_run(void *base, int64_t off, int type, const F2 (&v)[kPairs], int n) {
+    uint32_t w[kRun];
+    if (type == CQ_T_F32) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            const float2 f = f2_get(v[j]);
+            w[2 * j] = __float_as_uint(f.x), w[2 * j + 1] = __float_as_uint(f.y);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            const float2 f = f2_get(v[j]);
+            if (type == CQ_T_F16) {
+                const __half2 h = __floats2half2_rn(f.x, f.y);
+                w[j] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+                w[j] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+    }
+    if (VEC) {
+        uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(base) + off * (type == CQ_T_F32 ? 4 : 2));
+        p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (type == CQ_T_F32) p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
 #pragma unroll
         for (int j = 0; j < kRun; ++j) {
             if (j >= n) continue;
-            if (type == CQ_T_F32) static_cast<float *>(base)[off + j] = v[j];
-            else static_cast<uint16_t *>(base)[off + j] = (uint16_t)pack_bits(v[j], type);
+            if (type == CQ_T_F32) static_cast<uint32_t *>(base)[off + j] = w[j];
+            else static_cast<uint16_t *>(base)[off + j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
         }
-        return;
     }
-    if (type == CQ_T_F32) {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + off);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
-        return;
-    }
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = pack_bits(v[2 * j], type) | pack_bits(v[2 * j + 1], type) << 16;
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + off) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// rint(v / step), v / step rounded to fp32 first, as bytes. Where the product with step's reciprocal is further than
+// kNear from a tie it decides: it and the rounded quotient are off by 2^-23 and 2^-24 of at most 127.5, 2.3e-5 together.
+// Adding 1.5 * 2^23 leaves the nearest integer in the low bits. `plain`: the row's quotients are at most 127.5 and
+// the reciprocal a normal number.
+constexpr float kNear = 4e-5f, kMagic = 12582912.0f;
 template <bool VEC>
-__device__ __forceinline__ void store_codes(int8_t *dst, const float (&v)[kRun], float step, int n) {
-    uint32_t q[2] = {0, 0};
+__device__ __forceinline__ void store_codes(int8_t *dst, const F2 (&v)[kPairs], float step, float back, bool plain, int n) {
+    uint32_t q[kRun];
+    float far = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        const float t = fminf(fmaxf(rintf(__fdiv_rn(v[j], step)), -128.0f), 127.0f);
-        q[j / 4] |= ((uint32_t)(int)t & 255u) << (8 * (j & 3));
+    for (int j = 0; j < kPairs; ++j) {
+        const F2 t = f2_mul(v[j], f2(back, back)), m = f2_add(t, f2(kMagic, kMagic));
+        const float2 d = f2_get(f2_fma(f2_add(m, f2(-kMagic, -kMagic)), f2(-1.0f, -1.0f), t)), i = f2_get(m);
+        far = max_nan(far, max_nan(fabsf(d.x), fabsf(d.y)));
+        q[2 * j] = __float_as_uint(i.x), q[2 * j + 1] = __float_as_uint(i.y);
     }
+    if (!plain || !(far <= 0.5f - kNear)) {  // no number counts as near
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            const float2 f = f2_get(v[j]);
+            q[2 * j] = (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(f.x, step)), -128.0f), 127.0f);
+            q[2 * j + 1] = (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(f.y, step)), -128.0f), 127.0f);
+        }
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        w[j] = __byte_perm(__byte_perm(q[4 * j], q[4 * j + 1], 0x0040), __byte_perm(q[4 * j + 2], q[4 * j + 3], 0x0040), 0x5410);
     if (VEC) {
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(q[0], q[1]);
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
         for (int j = 0; j < kRun; ++j)
-            if (j < n) dst[j] = (int8_t)(q[j / 4] >> (8 * (j & 3)));
+            if (j < n) dst[j] = (int8_t)(w[j / 4] >> (8 * (j & 3)));
     }
 }
+// offset + weight (zero past the row).
 template <bool VEC>
-__device__ __forceinline__ void load_weight(const float *w, int n, float (&t)[kRun]) {
+__device__ __forceinline__ void load_weight(const float *w, int n, float offset, F2 (&t)[kPairs]) {
     if (VEC) {
         const float4 a = __ldg(reinterpret_cast<const float4 *>(w)), b = __ldg(reinterpret_cast<const float4 *>(w) + 1);
-        t[0] = a.x, t[1] = a.y, t[2] = a.z, t[3] = a.w, t[4] = b.x, t[5] = b.y, t[6] = b.z, t[7] = b.w;
+        t[0] = f2(a.x, a.y), t[1] = f2(a.z, a.w), t[2] = f2(b.x, b.y), t[3] = f2(b.z, b.w);
     } else {
 #pragma unroll
-        for (int j = 0; j < kRun; ++j) t[j] = j < n ? __ldg(w + j) : 0.0f;
+        for (int j = 0; j < kPairs; ++j) t[j] = f2(2 * j < n ? __ldg(w + 2 * j) : 0.0f, 2 * j + 1 < n ? __ldg(w + 2 * j + 1) : 0.0f);
     }
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) t[j] = f2_add(t[j], f2(offset, offset));
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// 1 / (1 + 2^(-g log2 e)); beyond the range of the power it is 0 or 1.
+__device__ __forceinline__ float sigmoid(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
 __device__ __forceinline__ float open(float g, int act) {
     return act == CQ_GATE_PLAIN ? g : act == CQ_GATE_SIGMOID ? sigmoid(g) : g * sigmoid(g);
 }
@@ -232,7 +306,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : 32 * kMaxWarps) block
     for (int turn = 0; row < p.rows; row += teams, turn ^= 2) {
         const uint32_t from = mine + st * p.stage;
         if (VEC) wait(p, full + 8 * st, par, s_abort);
-        float v[CH][kRun], none = 0.0f, inv = 1.0f;
+        F2 v[CH][kPairs], sum = {0};
+        float none = 0.0f, ib = p.branch;  // what a branch's element is multiplied by, but for its weight
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int e = (c * lanes + lane) * kRun, n = p.d - e;
@@ -242,80 +317,95 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : 32 * kMaxWarps) block
             unpack(r, p.x_type, v[c]);
         }
         if (p.post) {
-            float s = 0.0f;
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int j = 0; j < kRun; ++j) s = fmaf(v[c][j], v[c][j], s);
+                for (int j = 0; j < kPairs; ++j) sum = f2_fma(v[c][j], v[c][j], sum);
+            const float2 two = f2_get(sum);
+            float s = two.x + two.y;
             reduce<WARP>(s, none, false, s_buf[turn]);
-            inv = rsqrtf(fmaf(s, p.inv_d, p.eps));
+            ib = rsqrtf(fmaf(s, p.inv_d, p.eps)) * p.branch;
+            if (!p.wb) ib *= p.offset + 1.0f;
         }
-        float s = 0.0f, top = 0.0f;
-        const float gate1 = GATE && p.one_gate ? open(load_one(p.gate, row * p.gate_st, p.x_type), p.act) : 1.0f;
+        if (GATE && p.one_gate) ib *= open(load_one(p.gate, row * p.gate_st, p.x_type), p.act);
+        float top = 0.0f;
+        sum = f2(0.0f, 0.0f);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int e = (c * lanes + lane) * kRun, n = p.d - e;
             if (n <= 0) continue;
             Raw r = {};
-            float t[kRun];
+            F2 t[kPairs];
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) v[c][j] = f2_mul(v[c][j], f2(ib, ib));
             if (p.wb) {
-                load_weight<VEC>(p.wb + e, n, t);
+                load_weight<VEC>(p.wb + e, n, p.offset, t);
 #pragma unroll
-                for (int j = 0; j < kRun; ++j) v[c][j] = v[c][j] * inv * (p.offset + t[j]);
-            } else {
-                const float one = p.post ? p.offset + 1.0f : 1.0f;
-#pragma unroll
-                for (int j = 0; j < kRun; ++j) v[c][j] = v[c][j] * inv * one;
+                for (int j = 0; j < kPairs; ++j) v[c][j] = f2_mul(v[c][j], t[j]);
             }
-            if (GATE && p.one_gate) {
-#pragma unroll
-                for (int j = 0; j < kRun; ++j) v[c][j] *= gate1;
-            } else if (GATE) {
+            if (GATE && !p.one_gate) {
                 if (VEC) take_run(r, from + p.at_gate + e * (p.x_type == CQ_T_F32 ? 4 : 2), p.x_type);
                 else load_each(r, p.gate, row * p.gate_st + e, p.x_type, n);
                 unpack(r, p.x_type, t);
 #pragma unroll
-                for (int j = 0; j < kRun; ++j) v[c][j] *= open(t[j], p.act);
+                for (int j = 0; j < kPairs; ++j) {
+                    const float2 g = f2_get(t[j]);
+                    v[c][j] = f2_mul(v[c][j], f2(open(g.x, p.act), open(g.y, p.act)));
+                }
             }
             if (p.res) {
                 if (VEC) take_run(r, from + p.at_res + e * (p.res_type == CQ_T_F32 ? 4 : 2), p.res_type);
                 else load_each(r, p.res, row * p.res_st + e, p.res_type, n);
                 unpack(r, p.res_type, t);
-            }
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) {
-                v[c][j] = p.res ? fmaf(p.keep, t[j], p.branch * v[c][j]) : p.branch * v[c][j];
-                if (!VEC && j >= n) v[c][j] = 0.0f;  // what is not there may have become no number (0 times an infinity)
-                s = fmaf(v[c][j], v[c][j], s);
+                for (int j = 0; j < kPairs; ++j) v[c][j] = f2_fma(f2(p.keep, p.keep), t[j], v[c][j]);
+            }
+            if (!VEC) {  // what is not there may have become no number (0 times an infinity)
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) {
+                    const float2 f = f2_get(v[c][j]);
+                    v[c][j] = f2(2 * j < n ? f.x : 0.0f, 2 * j + 1 < n ? f.y : 0.0f);
+                }
             }
             if (p.sum) store_run<VEC>(p.sum, row * p.sum_st + e, p.res_type, v[c], n);
             if (p.w) {
-                load_weight<VEC>(p.w + e, n, t);
-#pragma unroll
-                for (int j = 0; j < kRun; ++j) v[c][j] *= p.offset + t[j];
+                load_weight<VEC>(p.w + e, n, p.offset, t);
             } else {
 #pragma unroll
-                for (int j = 0; j < kRun; ++j) v[c][j] *= p.offset + 1.0f;
+                for (int j = 0; j < kPairs; ++j) t[j] = f2(p.offset + 1.0f, p.offset + 1.0f);
             }
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) top = fmaxf(top, fabsf(v[c][j]));
+            for (int j = 0; j < kPairs; ++j) {
+                sum = f2_fma(v[c][j], v[c][j], sum);
+                v[c][j] = f2_mul(v[c][j], t[j]);
+            }
+            if (p.scale) {
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) {
+                    const float2 f = f2_get(v[c][j]);
+                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            }
         }
+        const float2 two = f2_get(sum);
+        float s = two.x + two.y;
         reduce<WARP>(s, top, p.scale != nullptr, s_buf[turn + 1]);  // every lane has read its part of the stage
         if (VEC) {
             const int64_t ahead = row + p.depth * teams;
             if (lane == 0 && ahead < p.rows) fetch_row(p, ahead, from, full + 8 * st);
             if (++st == p.depth) st = 0, par ^= 1;
         }
-        inv = rsqrtf(fmaf(s, p.inv_d, p.eps));
-        const float most = top * inv, step = most > 0.0f ? __fdiv_rn(most, 127.0f) : 1.0f;
+        const float inv = rsqrtf(fmaf(s, p.inv_d, p.eps));
+        const float most = top * inv, step = most > 0.0f ? __fdiv_rn(most, 127.0f) : 1.0f, back = 1.0f / step;
+        const bool plain = step > 1e-36f && step < 1e36f;
         if (p.scale && lane == 0) p.scale[row] = step;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int e = (c * lanes + lane) * kRun, n = p.d - e;
             if (n <= 0) continue;
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) v[c][j] *= inv;
-            if (p.scale) store_codes<VEC>(static_cast<int8_t *>(p.y) + row * p.y_st + e, v[c], step, n);
+            for (int j = 0; j < kPairs; ++j) v[c][j] = f2_mul(v[c][j], f2(inv, inv));
+            if (p.scale) store_codes<VEC>(static_cast<int8_t *>(p.y) + row * p.y_st + e, v[c], step, back, plain, n);
             else store_run<VEC>(p.y, row * p.y_st + e, p.y_type, v[c], n);
         }
     }

@@ -11,8 +11,9 @@ def block_norm(x, res, w, *, post=False, wb=None, gate=None, act=None, branch=1.
 
     Roundings of 2^-24 (a unit): a sum of squares adds up to 32 elements one after the other and joins up to 9 + 5 partial
     sums, so it is off by 48 units at most, its root by half of that, rsqrtf by 4, the mean's product and sum by 1 each:
-    32 in all. A branch has 3 more products and the sum of its weight: 36; a gate's function 4 for its division, 2
-    for the sum and the product, and of __expf 2 + 1.2 |g| steps of two units; r is one fma of two products."""
+    32 in all. A branch has 3 more products and the sum of its weight: 36; a gate's function 2 for its reciprocal, 2
+    for the sum and the product, and of its power of two 4 and the 1.44 |g| by which its exponent is rounded; r is one
+    fma of two products."""
     f = np.float64
     x = x.astype(f)
     with np.errstate(over="ignore", invalid="ignore"):

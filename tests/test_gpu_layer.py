@@ -151,6 +151,27 @@ def test_norm_zeros_and_non_finite_rows_stay_apart(C):
         assert torch.equal(q, want[0]) and torch.equal(s, want[1]) and s[0] == 1 and (q[0] == 0).all()
 
 
+@pytest.mark.parametrize("d", [96, 333, 2048])
+def test_norm_codes_of_every_kind_of_row(C, d):
+    """Codes and scales are the quantiser's where quotients lie on ties, rows are tiny, huge or zero, or weights are no numbers."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x = torch.randint(-254, 255, (12, d), generator=g, device="cuda").float() / 2
+    x[:, 0] = 127.0  # the scale is 1 times the norm's factor: halves lie near ties
+    x[1] *= 1e-30
+    x[2] *= 1e30
+    x[3] *= 2.0 ** -140
+    x[4] = 0
+    x[5, 1] = 3e38
+    for eps in (1e-6, 0.0):
+        for weight in (None, torch.ones(d, device="cuda"), torch.randn(d, generator=g, device="cuda") * 1e-38,
+                       torch.randn(d, generator=g, device="cuda") * 1e37, torch.full((d,), 2.0, device="cuda").index_fill_(0, _i32([2]).long(), math.nan),
+                       torch.full((d,), 2.0, device="cuda").index_fill_(0, _i32([3]).long(), math.inf)):
+            y = C.cq_block_norm(x, None, weight, eps=eps)[1]
+            _, q, s = C.cq_block_norm(x, None, weight, eps=eps, out_dtype=I8)
+            want = C.cq_act_quant_int8(y)
+            assert torch.equal(q, want[0]) and torch.equal(s, want[1])
+
+
 def test_norm_gates_that_are_far_out(C):
     kw = _norm_inputs(1, 8, F32, None, 8, weights=False)
     kw["gate"][0] = torch.tensor([0.0, 100.0, -100.0, 1e4, -1e4, math.inf, -math.inf, 88.5])
