@@ -32,7 +32,7 @@ __all__ = [
     "cq_act_quant_int8", "cq_gemv", "cq_gemv_grouped", "cq_gemv_shared", "cq_gemm", "cq_gemm_grouped", "cq_gemm_noalloc",
     "cq_gather_rows", "cq_kv_write", "cq_kv_attend",
     "cq_rope_init", "cq_qk_norm_rope", "cq_kv_plan", "cq_kv_geometry", "cq_kv_write_slots", "cq_kv_tree_attend",
-    "cq_block_norm", "cq_lora_add",
+    "cq_kv_window_attend", "cq_block_norm", "cq_lora_add",
     "cq_device_status", "cq_cact_write", "cq_cact_open", "cq_cact_open_memory", "CactReader",
     "CQError", "library_path", "GROUP",
 ]
@@ -514,6 +514,6 @@ def cq_cact_open_memory(data: bytes) -> CactReader:
 
 
 # the paged cache's serving steps; imported last, they use the helpers above
-from .paged import (cq_kv_geometry, cq_kv_plan, cq_kv_tree_attend, cq_kv_write_slots,  # noqa: E402
+from .paged import (cq_kv_geometry, cq_kv_plan, cq_kv_tree_attend, cq_kv_window_attend, cq_kv_write_slots,  # noqa: E402
                     cq_qk_norm_rope, cq_rope_init)
 from .layer import cq_block_norm, cq_lora_add  # noqa: E402

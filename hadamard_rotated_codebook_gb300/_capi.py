@@ -105,6 +105,10 @@ class KvTree(ctypes.Structure):
     ]
 
 
+class KvWindow(ctypes.Structure):
+    _fields_ = [("positions", c_void_p), ("window", c_int), ("sinks", c_int)]
+
+
 class NormDesc(ctypes.Structure):
     _fields_ = [
         ("x", c_void_p), ("residual", c_void_p), ("gate", c_void_p), ("branch_weight", c_void_p), ("weight", c_void_p),
@@ -168,6 +172,7 @@ SIGNATURES = {
                                   c_int, c_void_p, c_int, c_void_p]),
     "cq_kv_tree_workspace": (c_size_t, [P(KvGeom), c_int, c_int]),
     "cq_kv_tree_attend": (c_int, [P(KvGeom), P(KvTree), c_void_p]),
+    "cq_kv_window_attend": (c_int, [P(KvGeom), P(KvTree), P(KvWindow), c_void_p]),
     "cq_block_norm": (c_int, [P(NormDesc), c_void_p]),
     "cq_lora_add": (c_int, [P(LoraDesc), c_void_p]),
     "cq_device_status": (c_int, [c_void_p]),

@@ -40,5 +40,6 @@ size_t tree_workspace(const cq_kv_geom &g, int n_seqs, int max_nodes);
 // lk, lv: level tables of the key and value codes (level_table).
 // give_up: nobody tells the products that the queries are there, and waits give up after a few polls (a self-test).
 int launch_kv_tree_attend(const cq_kv_geom &g, const cq_kv_tree &t, const float *lk, const float *lv, bool give_up, void *stream);
+int launch_kv_window_attend(const cq_kv_geom &g, const cq_kv_tree &t, const cq_kv_window &w, const float *lk, const float *lv, void *stream);
 
 }  // namespace cq

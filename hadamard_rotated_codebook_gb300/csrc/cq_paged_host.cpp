@@ -193,8 +193,8 @@ size_t cq_kv_tree_workspace(const cq_kv_geom *g, int n_seqs, int max_nodes) {
     return tree_workspace(*g, n_seqs, max_nodes);
 }
 
-static int tree_attend(const cq_kv_geom *g, const cq_kv_tree *t, bool give_up, void *stream) {
-    clear_error();
+// w: the window, or null.
+static int tree_attend(const cq_kv_geom *g, const cq_kv_tree *t, const cq_kv_window *w, bool give_up, void *stream) {
     TreeUnit u[kMaxUnits];
     int st = check_tree_geom(g, u);
     if (st) return st;
@@ -223,11 +223,25 @@ static int tree_attend(const cq_kv_geom *g, const cq_kv_tree *t, bool give_up, v
     float lk[16], lv[16];
     level_table(g->k_bits, g->k_codebook, lk);
     level_table(g->v_bits, g->v_codebook, lv);
-    return launch_kv_tree_attend(*g, *t, lk, lv, give_up, stream);
+    return w ? launch_kv_window_attend(*g, *t, *w, lk, lv, stream) : launch_kv_tree_attend(*g, *t, lk, lv, give_up, stream);
 }
 
-int cq_kv_tree_attend(const cq_kv_geom *g, const cq_kv_tree *t, void *stream) { return tree_attend(g, t, false, stream); }
+int cq_kv_tree_attend(const cq_kv_geom *g, const cq_kv_tree *t, void *stream) {
+    clear_error();
+    return tree_attend(g, t, nullptr, false, stream);
+}
 
-int cq_selftest_tree_timeout(const cq_kv_geom *g, const cq_kv_tree *t, void *stream) { return tree_attend(g, t, true, stream); }
+int cq_kv_window_attend(const cq_kv_geom *g, const cq_kv_tree *t, const cq_kv_window *w, void *stream) {
+    clear_error();
+    if (!w) return set_error(CQ_ERR_ARG, "null window");
+    if (w->window < 1 || w->sinks < 0)
+        return set_error(CQ_ERR_SHAPE, "a window has at least one token and sinks none below zero, got %d, %d", w->window, w->sinks);
+    return tree_attend(g, t, w, false, stream);
+}
+
+int cq_selftest_tree_timeout(const cq_kv_geom *g, const cq_kv_tree *t, void *stream) {
+    clear_error();
+    return tree_attend(g, t, nullptr, true, stream);
+}
 
 }  // extern "C"

@@ -20,7 +20,7 @@ import torch
 
 from . import _capi
 from . import _codebook_arg, cq_packed_bytes
-from ._capi import CQ_T_BF16, CQ_T_F16, CQ_T_F32, KvGeom, KvStep, KvTree, QkDesc, check
+from ._capi import CQ_T_BF16, CQ_T_F16, CQ_T_F32, KvGeom, KvStep, KvTree, KvWindow, QkDesc, check
 
 _TYPE = {torch.float32: CQ_T_F32, torch.float16: CQ_T_F16, torch.bfloat16: CQ_T_BF16}
 _load = _capi.load
@@ -290,6 +290,28 @@ def cq_kv_tree_attend(geom: KvGeometry, q: torch.Tensor, k_cache: torch.Tensor, 
     nothing gets zeros. Rows that no request covers (padding behind the last one,
     say) are not written: an o made by the call is uninitialised there, so give
     one where such rows are read."""
+    return _attend(geom, q, k_cache, v_cache, cap, block_table, block_size, context_lens, cu_nodes, mask, max_nodes, o, None)
+
+
+def cq_kv_window_attend(geom: KvGeometry, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, cap: int,
+                        block_table: torch.Tensor, block_size: int, context_lens: torch.Tensor, cu_nodes: torch.Tensor,
+                        mask: Optional[torch.Tensor], max_nodes: int, window: int, sinks: int = 0, *,
+                        positions: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """cq_kv_tree_attend over a sliding window with a few first tokens that stay
+    visible: a token at position p attends position t (of the context, or a
+    drafted token's whose bit is set) only if ``t < sinks`` or ``p - t <
+    window``. ``positions`` (int32 [nodes]) holds the drafted tokens' positions
+    (a tree's: context_lens + depth; None: context_lens + i, one after the
+    other). Rows and blocks between the sinks and the window of a request's first
+    drafted token are never read, and their table entries may be anything."""
+    if (window | sinks) >> 31:
+        _ints(window=window, sinks=sinks)
+    at = None if positions is None else _i32(positions, "positions", q.shape[0], q.device)
+    return _attend(geom, q, k_cache, v_cache, cap, block_table, block_size, context_lens, cu_nodes, mask, max_nodes, o,
+                   KvWindow(at, window, sinks))
+
+
+def _attend(geom, q, k_cache, v_cache, cap, block_table, block_size, context_lens, cu_nodes, mask, max_nodes, o, window) -> torch.Tensor:
     dev = q.device
     if (cap | block_size | max_nodes) >> 31:
         _ints(cap=cap, block_size=block_size, max_nodes=max_nodes)
@@ -320,5 +342,8 @@ def cq_kv_tree_attend(geom: KvGeometry, q: torch.Tensor, k_cache: torch.Tensor, 
                   block_table.stride(0) if n_seqs > 1 else block_table.shape[1],
                   qt, qh, ot, oh,
                   cap, block_table.shape[1], block_size, n_seqs, n, max_nodes, words, _TYPE[q.dtype])
-    _call(dev, _load().cq_kv_tree_attend, geom.c, tree)
+    if window is None:
+        _call(dev, _load().cq_kv_tree_attend, geom.c, tree)
+    else:
+        _call(dev, _load().cq_kv_window_attend, geom.c, tree, window)
     return o

@@ -550,6 +550,30 @@ size_t cq_kv_tree_workspace(const cq_kv_geom *geom, int n_seqs, int max_nodes);
 int cq_kv_tree_attend(const cq_kv_geom *geom, const cq_kv_tree *t,
                       void *stream);
 
+/* A window over what cq_kv_tree_attend reads. */
+typedef struct cq_kv_window {
+    const int32_t *positions; /* [n_nodes] position of each drafted token, device; NULL: context_lens + i */
+    int window;               /* a token attends itself and up to window - 1 positions before it; >= 1 */
+    int sinks;                /* positions 0 .. sinks - 1 stay visible to every token; >= 0 */
+} cq_kv_window;
+
+/* cq_kv_tree_attend over a sliding window: of the context, a token at
+ * position p attends position t only if t < sinks or p - t < window, and of
+ * the drafted tokens whose bit is set only those whose position is so. A
+ * tree's tokens stand at context_lens + depth, which `positions` holds (the
+ * positions that cq_qk_norm_rope turned them by); without, token i stands at
+ * context_lens + i. Rows between the sinks and the window of a request's
+ * first drafted token (position context_lens) are never read, nor are their
+ * entries of the block table, so that blocks that lie there as a whole may
+ * have gone back to the pool: the work of a call does not grow with the
+ * context beyond the window. Positions outside context_lens ..
+ * context_lens + CQ_TREE_MAX_NODES - 1 count as the nearer end and mark the
+ * device status word (CQ_ERR_INDEX). Everything else is as for
+ * cq_kv_tree_attend, the workspace (cq_kv_tree_workspace) too. Errors: as
+ * there, CQ_ERR_ARG for a null window, CQ_ERR_SHAPE for a bad one. */
+int cq_kv_window_attend(const cq_kv_geom *geom, const cq_kv_tree *t,
+                        const cq_kv_window *w, void *stream);
+
 /* --------------------------------------- a layer's other serving steps -- */
 /*
  * What stands between the quantised products of a layer beside the cache: the

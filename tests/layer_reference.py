@@ -84,3 +84,37 @@ def lora(ys, x, a, b, adapters, cu, scales=None, ranks=None, x_scale=None, terms
                 o[t] += u @ B.T
             out.append((o, e + TINY["float32"]))
     return out
+
+
+def attend_rows(q, k_blob, v_blob, cap, rows, sees, cu, geom, kb, vb, cbk, cbv, scale):
+    """Attention of tokens q [nodes, hq, dk] over cache rows rows[s], of which token i of request s attends those with
+    sees[s][i]: (o, bound) by the arithmetic and the reasoning of paged_reference.attend."""
+    from tests.paged_reference import dequant
+    hq, hkv, dk, dv = geom
+    per = hq // hkv
+    o, bound = np.zeros((len(q), hq, dv)), np.zeros((len(q), hq, dv))
+    for s, (at, see) in enumerate(zip(rows, sees)):
+        a, n = cu[s], cu[s + 1] - cu[s]
+        if n == 0 or not see.any():
+            continue
+        use = see.any(0)
+        at, see = at[use], see[:, use]
+        kd, kt = dequant(k_blob, cap, hkv * dk, kb, cbk, at)
+        vd, vt = dequant(v_blob, cap, hkv * dv, vb, cbv, at)
+        for h in range(hq):
+            g = h // per
+            k, v = kd[:, g * dk:(g + 1) * dk], vd[:, g * dv:(g + 1) * dv]
+            nk = np.linalg.norm(kt[:, g * dk // 128:((g + 1) * dk + 127) // 128].reshape(len(at), -1), axis=1)
+            nv = np.linalg.norm(vt[:, g * dv // 128:((g + 1) * dv + 127) // 128].reshape(len(at), -1), axis=1)
+            qh = q[a:a + n, h].astype(np.float64)
+            x = np.where(see, qh @ k.T * scale, -np.inf)
+            top = x.max(1, keepdims=True)
+            w = np.exp(x - np.where(np.isfinite(top), top, 0.0))
+            some = w.sum(1, keepdims=True)
+            w = w / np.where(some > 0, some, 1.0)
+            o[a:a + n, h] = w @ v
+            d = abs(scale) * (2 * 2.0 ** -11 + 2.0 ** -18) * np.linalg.norm(qh, axis=1) * np.where(see, nk, 0.0).max(1)
+            for i in range(n):
+                bound[a + i, h] = (np.expm1(2 * d[i]) * (w[i] @ np.abs(v - o[a + i, h])) + 2 * 2.0 ** -11 * (w[i] @ nv)
+                                   + 2.0 ** -24 * see[i].sum() * (w[i] * nv).max() + 2.0 ** -18 * (w[i] @ nv))
+    return o, bound

@@ -64,6 +64,20 @@ def test_lora_add_refuses(A, kw, code):
     assert A.load().cq_last_error()
 
 
+def test_window_attend_refuses(A):
+    cb = (ctypes.c_float * 4)(-0.13, -0.04, 0.04, 0.13)
+    g = A.KvGeom(n_q_heads=4, n_kv_heads=2, head_dim_k=48, head_dim_v=64, k_bits=2, v_bits=2, k_codebook=cb, v_codebook=cb, scale=0.1)
+    t = A.KvTree(k_cache=16, v_cache=16, block_table=16, context_lens=16, cu_nodes=16, q=16, o=16, table_stride=4, cap=64, max_blocks=4, block_size=16,
+                 n_seqs=2, n_nodes=0, max_nodes=2, dtype=1)
+    call = lambda w, tree=t: A.load().cq_kv_window_attend(ctypes.byref(g), ctypes.byref(tree), w, None)  # noqa: E731
+    assert call(None) == A.CQ_ERR_ARG
+    assert call(ctypes.byref(A.KvWindow(None, 1, 0))) == 0  # no nodes: nothing to do
+    for window, sinks in ((0, 0), (-1, 0), (1, -1)):
+        assert call(ctypes.byref(A.KvWindow(None, window, sinks))) == A.CQ_ERR_SHAPE and A.load().cq_last_error()
+    t.block_size = 0
+    assert call(ctypes.byref(A.KvWindow(None, 1, 0))) == A.CQ_ERR_SHAPE
+
+
 def test_empty_calls_do_nothing(A):
     lib = A.load()
     assert lib.cq_block_norm(ctypes.byref(_norm(A, n_tokens=0, x=None)), None) == 0
@@ -99,5 +113,5 @@ def _fields(A, struct):
 
 def test_binding_structures_match_the_header(A):
     """Field by field: the header's structs and the binding's have the same order and sizes."""
-    for name, cls in (("cq_norm_desc", A.NormDesc), ("cq_lora_desc", A.LoraDesc)):
+    for name, cls in (("cq_norm_desc", A.NormDesc), ("cq_lora_desc", A.LoraDesc), ("cq_kv_window", A.KvWindow)):
         assert [(f[0].rstrip("_"), ctypes.sizeof(f[1])) for f in cls._fields_] == _fields(A, name)
