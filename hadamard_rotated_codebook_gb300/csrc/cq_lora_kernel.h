@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cstdlib>
 #include <type_traits>
 
 #include "cq_layer.h"
@@ -33,6 +34,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxCluster = 8;
 constexpr int kSeqs = 4;  // requests that a lane looks at in one go
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -79,57 +81,84 @@ __device__ __forceinline__ uint32_t pair_of(float x, float y) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// XK: CQ_T_F32, CQ_T_I8, or 16 bits of the weights' own type (CQ_T_F16 stands for it). n of the run's 8 exist (VEC: all or none).
-template <typename T, int XK, bool VEC>
+// XK: CQ_T_F32, CQ_T_I8, or 16 bits of the weights' own type (CQ_T_F16 stands for it).
+template <int XK>
+__host__ __device__ constexpr int run_bytes() { return XK == CQ_T_F32 ? 32 : XK == CQ_T_I8 ? 8 : 16; }
+template <typename T>
+__device__ __forceinline__ void pairs_of_i8(const uint32_t (&w)[2], uint32_t (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t u = w[j / 2] >> (16 * (j & 1));
+        v[j] = pair_of<T>((float)(int8_t)(u & 255u), (float)(int8_t)(u >> 8 & 255u));
+    }
+}
+// n of the run's 8 elements, one by one.
+template <typename T, int XK>
 __device__ __forceinline__ XRun<XK> load_x(const void *x, int64_t at, int n) {
     XRun<XK> r = {};
-    if (n <= 0) return r;
-    if (XK == CQ_T_F32) {
-        const float *p = static_cast<const float *>(x) + at;
-        if (VEC) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
-            r.v[0] = a.x, r.v[1] = a.y, r.v[2] = a.z, r.v[3] = a.w;
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (j >= n) continue;
+        if (XK == CQ_T_F32) r.v[XK == CQ_T_F32 ? j : 0] = __float_as_uint(__ldg(static_cast<const float *>(x) + at + j));
+        else if (XK == CQ_T_I8) w[j / 4] |= (uint32_t)(uint8_t)__ldg(static_cast<const int8_t *>(x) + at + j) << (8 * (j & 3));
+        else r.v[j / 2] |= (uint32_t)__ldg(static_cast<const uint16_t *>(x) + at + j) << (16 * (j & 1));
+    }
+    if (XK == CQ_T_I8) pairs_of_i8<T>(w, reinterpret_cast<uint32_t (&)[4]>(r.v));
+    return r;
+}
+// Asynchronous copies of a lane's own runs into its own places of shared memory: nobody else reads them, so that the lane's own wait is
+// all they need. A run that is not there becomes zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+// Places of a run: 512 (or 256) bytes for a warp's 32 lanes, two such rows for fp32.
+template <int XK>
+__device__ __forceinline__ void send_x(uint32_t dst, int lane, const void *x, int64_t at, bool there) {
+    const uint8_t *from = static_cast<const uint8_t *>(x) + (there ? at * (run_bytes<XK>() / 8) : 0);
+    if (XK == CQ_T_I8) {
+        copy8(dst + lane * 8, from, there);
+    } else {
+        copy16(dst + lane * 16, from, there);
+        if (XK == CQ_T_F32) copy16(dst + 512 + lane * 16, from + 16, there);
+    }
+}
+template <typename T, int XK>
+__device__ __forceinline__ XRun<XK> take_x(uint32_t src, int lane) {
+    XRun<XK> r = {};
+    if (XK == CQ_T_I8) {
+        const uint2 w = lds8(src + lane * 8);
+        const uint32_t u[2] = {w.x, w.y};
+        pairs_of_i8<T>(u, reinterpret_cast<uint32_t (&)[4]>(r.v));
+    } else {
+        const uint4 a = lds16(src + lane * 16);
+        r.v[0] = a.x, r.v[1] = a.y, r.v[2] = a.z, r.v[3] = a.w;
+        if (XK == CQ_T_F32) {
+            const uint4 b = lds16(src + 512 + lane * 16);
             constexpr int o = XK == CQ_T_F32 ? 4 : 0;
             r.v[o] = b.x, r.v[o + 1] = b.y, r.v[o + 2] = b.z, r.v[o + 3] = b.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) r.v[XK == CQ_T_F32 ? j : 0] = __float_as_uint(__ldg(p + j));
-        }
-    } else if (XK == CQ_T_I8) {
-        const int8_t *p = static_cast<const int8_t *>(x) + at;
-        uint32_t w[2] = {0, 0};
-        if (VEC) {
-            const uint2 a = __ldg(reinterpret_cast<const uint2 *>(p));
-            w[0] = a.x, w[1] = a.y;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) w[j / 4] |= (uint32_t)(uint8_t)__ldg(p + j) << (8 * (j & 3));
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t u = w[j / 2] >> (16 * (j & 1));
-            r.v[j] = pair_of<T>((float)(int8_t)(u & 255u), (float)(int8_t)(u >> 8 & 255u));
-        }
-    } else {
-        const uint16_t *p = static_cast<const uint16_t *>(x) + at;
-        if (VEC) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-            r.v[0] = a.x, r.v[1] = a.y, r.v[2] = a.z, r.v[3] = a.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) r.v[j / 2] |= (uint32_t)__ldg(p + j) << (16 * (j & 1));
         }
     }
     return r;
 }
 // n of 8 consecutive weights of A.
-template <bool VEC>
 __device__ __forceinline__ uint4 load_a(const uint16_t *p, int n) {
-    if (n <= 0) return make_uint4(0, 0, 0, 0);
-    if (VEC) return __ldg(reinterpret_cast<const uint4 *>(p));
     uint32_t v[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -230,18 +259,28 @@ __device__ Piece find_piece(const LoraParams &p, int piece, bool skip, int lane,
 }
 
 // MT: tiles of 16 ranks; NT: tiles of 8 tokens of a warp; WT: warps side by side along the tokens (the others split k).
-template <int MT, int NT, int WT>
+template <int XK, int MT, int NT, int WT>
 struct Shape {
     static constexpr int kTok = 8 * NT * WT, kRank = 16 * MT, kParts = kWarps / WT;
     // row strides that keep the lanes of an access in different banks
     static constexpr int kPartRow = kRank + 4, kURow = MT == 1 ? 16 : kRank + 16;
-    static constexpr int kPartBytes = kParts * kTok * kPartRow * 4, kUBytes = kTok * kURow * 4;
-    static constexpr int kSmem = kPartBytes + 2 * kUBytes;
+    static constexpr int kSumBytes = kTok * kPartRow * 4, kUBytes = kTok * kURow * 4;
+    static constexpr int kBlocks = NT > 1 || MT == 4 ? 2 : MT == 2 ? 3 : 4;  // on an SM
+    static constexpr int kRoom = 228 * 1024 / kBlocks - 1024;
+    // a warp's ring for the first product: 32 inputs a stage. What it holds is read before the sums take its place.
+    static constexpr int kStage = 32 * (MT * 32 + NT * run_bytes<XK>());
+    static constexpr int kDepth = kRoom / (kWarps * kStage) < 4 ? kRoom / (kWarps * kStage) : 4;
+    static constexpr int kRing = kWarps * kDepth * kStage;
+    // and one for y, a kilobyte a tile of 8 tokens and 32 outputs, behind the block's own sums (which others may still read)
+    static constexpr int kDepthY = NT == 1 ? 0 : (kParts - 1) * kSumBytes > 48 * 1024 ? 6 : 4;
+    static constexpr int kPartBytes = kParts * kSumBytes > kSumBytes + kDepthY * kWarps * 1024 ? kParts * kSumBytes : kSumBytes + kDepthY * kWarps * 1024;
+    static constexpr int kSmem = kRing > kPartBytes + 2 * kUBytes ? kRing : kPartBytes + 2 * kUBytes;
+    static_assert(kDepth >= 2 && kSmem <= kRoom, "shared memory");
 };
 
 template <typename T, int XK, int MT, int NT, int WT, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant__ LoraParams p) {
-    using S = Shape<MT, NT, WT>;
+__global__ void __launch_bounds__(kThreads, (Shape<XK, MT, NT, WT>::kBlocks)) lora_kernel(const __grid_constant__ LoraParams p) {
+    using S = Shape<XK, MT, NT, WT>;
     extern __shared__ __align__(16) float smem[];
     float *part = smem, *u_hi = smem + S::kPartBytes / 4, *u_lo = u_hi + S::kUBytes / 4;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -260,6 +299,14 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
         const int64_t bytes = ((int64_t)min(out, g1 * 32) - g0 * 32) * p.d.rank * 2;
         for (int64_t i = tid * 128ll; i < bytes; i += kThreads * 128ll) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(from + i));
     }
+    if (NT > 1 && p.vec_y[mat]) {  // many tokens: y
+        const int w0 = g0 * 32, lines = (min(out, g1 * 32) - w0 + 31) / 32;
+        for (int i = tid; i < q.n * lines; i += kThreads) {
+            const int t = i / lines, l = i - t * lines;
+            asm volatile("prefetch.global.L2 [%0];\n" ::"l"(y + (int64_t)(q.first + t) * y_st + w0 + l * 32));
+        }
+    }
+    const float scale = q.rank && p.d.scales ? p.d.scales[q.adapter] : 1.0f;
     // Ranks in runs of kRank, each added to what the one before left (one run, nearly always).
 #pragma unroll 1
     for (int r0 = 0; r0 == 0 || r0 < q.rank; r0 += S::kRank) {
@@ -267,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
         if (rank > 0) {
             if (r0) {  // the other blocks have read this one's sums, and its warps u
                 if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+                __threadfence();  // copies will read what was stored
                 __syncthreads();
             }
             // ------------------------------------------------ u: this warp's part of k --
@@ -284,23 +332,55 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[m][t][j] = 0.0f;
-#pragma unroll(MT * NT >= 8 ? 1 : 2)
+            const uint32_t ring = smem_u32(smem) + warp * S::kDepth * S::kStage;
+            auto send = [&](int i, int st) {
+                const int k = i * 32 + c * 8;
+                const uint32_t to = ring + st * S::kStage;
+                if (i < c1) {
+#pragma unroll
+                    for (int h = 0; h < 2 * MT; ++h) {
+                        const int r = h * 8 + g;
+                        const bool there = r < rank && k < n_in;
+                        copy16(to + h * 512 + lane * 16, A + (there ? (int64_t)r * n_in + k : 0), there);
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        if (t < live) send_x<XK>(to + MT * 1024 + t * 32 * run_bytes<XK>(), lane, p.d.x, x_at[t] + k, k < n_in);
+                }
+                copies_sent();
+            };
+            if (VEC) {
+#pragma unroll
+                for (int j = 0; j < S::kDepth - 1; ++j) send(c0 + wk + j * S::kParts, j);
+            }
+            int st = 0;
+#pragma unroll 1
             for (int i = c0 + wk; i < c1; i += S::kParts) {
+                const uint32_t from = ring + st * S::kStage;
+                if (VEC) {
+                    const int behind = st == 0 ? S::kDepth - 1 : st - 1;  // the stage read in the round before
+                    send(i + (S::kDepth - 1) * S::kParts, behind);
+                    copies_landed<S::kDepth - 1>();
+                    if (++st == S::kDepth) st = 0;
+                }
                 const int k = i * 32 + c * 8, n = n_in - k;
-                uint4 a[MT][2];
                 XRun<XK> x[NT];
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int t = 0; t < NT; ++t) {
+                    if (t >= live) break;
+                    if (VEC) x[t] = take_x<T, XK>(from + MT * 1024 + t * 32 * run_bytes<XK>(), lane);
+                    else x[t] = load_x<T, XK>(p.d.x, x_at[t] + k, n);
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    uint4 a[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int r = m * 16 + h * 8 + g;
-                        a[m][h] = load_a<VEC>(A + (int64_t)r * n_in + k, r < rank ? n : 0);
+                        if (VEC) a[h] = lds16(from + (2 * m + h) * 512 + lane * 16);
+                        else a[h] = load_a(A + (int64_t)r * n_in + k, r < rank ? n : 0);
                     }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) x[t] = load_x<T, XK, VEC>(p.d.x, x_at[t] + k, t < live ? n : 0);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const uint32_t lo[4] = {a[m][0].x, a[m][0].y, a[m][0].z, a[m][0].w}, hi[4] = {a[m][1].x, a[m][1].y, a[m][1].z, a[m][1].w};
+                    const uint32_t lo[4] = {a[0].x, a[0].y, a[0].z, a[0].w}, hi[4] = {a[1].x, a[1].y, a[1].z, a[1].w};
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         if (t >= live) break;
@@ -320,6 +400,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
                         }
                     }
                 }
+            }
+            if (VEC) {
+                copies_landed<0>();
+                __syncthreads();  // the sums take the rings' place
             }
             float *to = part + (size_t)wk * S::kTok * S::kPartRow;
 #pragma unroll
@@ -342,20 +426,23 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
                 }
                 asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
             }
-            const float scale = p.d.scales ? p.d.scales[q.adapter] : 1.0f;
             for (int i = tid; i < cells; i += kThreads) {
                 const int t = i / S::kRank, r = i % S::kRank;
                 const float *at = part + t * S::kPartRow + r;
                 float s = 0.0f;
                 if (C > 1) {
                     const uint32_t here = smem_u32(at);
-                    for (int b = 0; b < C; ++b) {
+                    float v[kMaxCluster];  // all on their way before the first is added
+#pragma unroll
+                    for (int b = 0; b < kMaxCluster; ++b) {
+                        v[b] = 0.0f;
+                        if (b >= C) continue;
                         uint32_t there;
-                        float v;
                         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(there) : "r"(here), "r"(b));
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(there) : "memory");
-                        s += v;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v[b]) : "r"(there) : "memory");
                     }
+#pragma unroll
+                    for (int b = 0; b < kMaxCluster; ++b) s += v[b];
                 } else {
                     s = *at;
 #pragma unroll
@@ -373,26 +460,56 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
         // ---------------------------------------------------------- the outputs: 32 at a time --
         // Rows of a tile are dealt out so that a lane holds four consecutive outputs of two tokens.
         const bool vec_y = p.vec_y[mat];
-        const int tiles = (q.n + 7) / 8, kts = (rank + 15) / 16;
+        const int tiles = (q.n + 7) / 8, kts = (rank + 15) / 16, mine = g0 + warp < g1 ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;
+        const uint32_t ring = smem_u32(smem) + S::kSumBytes + warp * S::kDepthY * 1024 + lane * 16;
+        // A lane's elements of tile t of its j-th run of outputs are copied some tiles ahead of their turn.
+        int sj = 0, stile = 0, sst = 0;
+        auto send = [&]() {
+            if (sj < mine) {
+                const int o = (g0 + warp + sj * kWarps) * 32 + 4 * g;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int tok = stile * 8 + 2 * c + h;
+                    const bool there = tok < q.n && o < out;
+                    copy16(ring + sst * 1024 + h * 512, y + (there ? (int64_t)(q.first + tok) * y_st + o : 0), there);
+                }
+                if (++stile == tiles) stile = 0, ++sj;
+            }
+            copies_sent();
+            if (++sst == S::kDepthY) sst = 0;
+        };
+        const bool ahead = NT > 1 && vec_y;
+        if (ahead) {
 #pragma unroll 1
-        for (int og = g0 + warp; og < g1; og += kWarps) {
-            const int o = og * 32 + 4 * g, n_o = out - o;
+            for (int j = 0; j < S::kDepthY - 1; ++j) send();
+        }
+        int st = 0;
+#pragma unroll 1
+        for (int j = 0; j < mine; ++j) {
+            const int o = (g0 + warp + j * kWarps) * 32 + 4 * g, n_o = out - o;
             uint2 b[MT][4];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     b[m][i] = load_b(B + (int64_t)(o + i) * p.d.rank + r0 + m * 16 + 4 * c, i < n_o ? rank - m * 16 - 4 * c : 0, p.vec_b);
-#pragma unroll 2
+#pragma unroll 1
             for (int t = 0; t < tiles; ++t) {
                 float v[2][4];
+                if (ahead) {
+                    send();
+                    copies_landed<(S::kDepthY > 0 ? S::kDepthY - 1 : 0)>();
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int tok = t * 8 + 2 * c + h;
                     const float *from = y + (int64_t)(q.first + tok) * y_st + o;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[h][i] = 0.0f;
-                    if (tok < q.n && n_o > 0) {
+                    if (ahead) {
+                        const uint4 f = lds16(ring + st * 1024 + h * 512);
+                        v[h][0] = __uint_as_float(f.x), v[h][1] = __uint_as_float(f.y), v[h][2] = __uint_as_float(f.z), v[h][3] = __uint_as_float(f.w);
+                    } else if (tok < q.n && n_o > 0) {
                         if (vec_y) {
                             const float4 f = __ldcs(reinterpret_cast<const float4 *>(from));
                             v[h][0] = f.x, v[h][1] = f.y, v[h][2] = f.z, v[h][3] = f.w;
@@ -403,6 +520,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
                         }
                     }
                 }
+                if (++st == S::kDepthY) st = 0;
                 float d[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
@@ -437,6 +555,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
                 }
             }
         }
+        if (ahead) copies_landed<0>();
         y = yo, y_st = yo_st;
     }
     if (q.rank && C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");  // no block ends while another reads its sums
@@ -445,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
 // ---------------------------------------------------------------------- host --
 template <typename T, int XK, int MT, int NT, int WT, bool VEC>
 int launch_k(LoraParams &p, cudaStream_t st) {
-    using S = Shape<MT, NT, WT>;
+    using S = Shape<XK, MT, NT, WT>;
     auto k = lora_kernel<T, XK, MT, NT, WT, VEC>;
     if (S::kSmem > 48 * 1024) {
         const int rc = ensure_smem(reinterpret_cast<const void *>(k), S::kSmem);
@@ -456,7 +575,8 @@ int launch_k(LoraParams &p, cudaStream_t st) {
     int widest = p.d.in;
     for (int j = 0; j < p.d.n_mats; ++j) widest = std::max(widest, p.d.out[j]);
     int C = 1;
-    while (C < 8 && (widest > 512 * C || (widest > 128 * C && pieces * p.d.n_mats * C < 2 * sm_count()))) C *= 2;
+    while (C < kMaxCluster && (widest > 512 * C || (widest > 128 * C && pieces * p.d.n_mats * C < 2 * sm_count()))) C *= 2;
+    if (const char *e = getenv("LORA_C")) C = atoi(e);
     p.cluster = C;
     if (pieces * C > INT_MAX) return set_error(CQ_ERR_SHAPE, "%d tokens of %d requests are too many for one call", p.d.n_tokens, p.d.n_seqs);
     cudaLaunchConfig_t cfg = {};
@@ -482,7 +602,7 @@ int launch_k(LoraParams &p, cudaStream_t st) {
 template <typename T, int XK, bool VEC>
 int launch_x(LoraParams &p, cudaStream_t st) {
     const bool few = VEC && (long long)p.d.n_tokens <= 8ll * p.d.n_seqs;
-    if (p.d.rank <= 16) return few ? launch_k<T, XK, 1, 1, 1, true>(p, st) : launch_k<T, XK, 1, 8, 2, VEC>(p, st);
+    if (p.d.rank <= 16) return few ? launch_k<T, XK, 1, 1, 1, true>(p, st) : launch_k<T, XK, 1, XK == CQ_T_F32 ? 4 : 8, 2, VEC>(p, st);
     if (p.d.rank <= 32) return few ? launch_k<T, XK, 2, 1, 1, true>(p, st) : launch_k<T, XK, 2, 4, 2, VEC>(p, st);
     return few ? launch_k<T, XK, 4, 1, 1, true>(p, st) : launch_k<T, XK, 4, XK == CQ_T_F32 ? 2 : 4, 2, VEC>(p, st);
 }
