@@ -129,6 +129,7 @@ class LoraDesc(ctypes.Structure):
         ("y", c_void_p * CQ_LORA_MAX_MATS), ("y_out", c_void_p * CQ_LORA_MAX_MATS),
         ("y_stride", c_int64 * CQ_LORA_MAX_MATS), ("y_out_stride", c_int64 * CQ_LORA_MAX_MATS),
         ("out", c_int * CQ_LORA_MAX_MATS), ("x_stride", c_int64),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
         ("n_mats", c_int), ("n_tokens", c_int), ("n_seqs", c_int), ("n_adapters", c_int), ("in_", c_int), ("rank", c_int),
         ("x_dtype", c_int), ("w_dtype", c_int),
     ]
@@ -174,6 +175,7 @@ SIGNATURES = {
     "cq_kv_tree_attend": (c_int, [P(KvGeom), P(KvTree), c_void_p]),
     "cq_kv_window_attend": (c_int, [P(KvGeom), P(KvTree), P(KvWindow), c_void_p]),
     "cq_block_norm": (c_int, [P(NormDesc), c_void_p]),
+    "cq_lora_workspace": (c_size_t, [P(LoraDesc)]),
     "cq_lora_add": (c_int, [P(LoraDesc), c_void_p]),
     "cq_device_status": (c_int, [c_void_p]),
     "cq_selftest_wait_timeout": (c_int, [c_void_p]),

@@ -10,15 +10,29 @@ namespace cq {
 int launch_block_norm(const cq_norm_desc &d, void *stream);
 
 // A call of cq_lora_add as its kernels take it.
+constexpr int kMaxSplits = 8;
 struct LoraParams {
     cq_lora_desc d;
     unsigned int *status;
-    int cluster;  // blocks that share a piece of work
-    bool vec_b;   // rows of B in runs of 4
+    float *u;      // the workspace: what the blocks of the first product leave, [matrix][part][token][u_row]
+    int u_row;     // ranks, rounded up to what a block sums
+    int pieces;    // of up to so many tokens of a request as a block takes, at most
+    int splits;    // parts of k
+    int runs;      // of 32 outputs that a warp of the second product takes
+    bool few;      // requests have few tokens
+    bool vec;      // rows of x and A in runs of 8
+    bool vec_b;    // rows of B in runs of 4
     bool vec_y[CQ_LORA_MAX_MATS];  // rows of y likewise
 };
-// vec: rows of x and A in runs of 8.
-int launch_lora_f16(LoraParams &p, bool vec, void *stream);
-int launch_lora_bf16(LoraParams &p, bool vec, void *stream);
+// Tiles of 16 ranks that a block of the first product takes.
+constexpr int lora_rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
+// Tokens of a piece, by the activations' type and the tiles of ranks: 8 where requests have few, else as many as leave the
+// sums in registers and two stages of inputs in shared memory. And the warps that share them.
+constexpr int lora_tokens(int x_dtype, int tiles, bool few) {
+    return few ? 8 : tiles == 4 ? (x_dtype == CQ_T_F32 ? 32 : 64) : tiles == 2 || x_dtype == CQ_T_F32 ? 64 : 128;
+}
+constexpr int lora_warps_along(bool few) { return few ? 1 : 2; }
+int launch_lora_f16(LoraParams &p, void *stream);
+int launch_lora_bf16(LoraParams &p, void *stream);
 
 }  // namespace cq

@@ -1,4 +1,6 @@
 // cq_layer_host.cpp -- host side of the block norm's and the adapters' entry points: argument checks, alignment.
+#include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -12,6 +14,26 @@ constexpr int kMaxSide = 1 << 28;  // inputs and outputs of an adapted projectio
 
 bool is_float(int type) { return type >= CQ_T_F32 && type <= CQ_T_BF16; }
 bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// How a call is cut up, apart from its alignment; the workspace's bytes, or 0.
+size_t lora_plan(const cq_lora_desc &d, bool few, LoraParams &p) {
+    const int tiles = lora_rank_tiles(d.rank), ranks = 16 * tiles, tok = lora_tokens(d.x_dtype, tiles, few);
+    const long long pieces = std::min<long long>(d.n_tokens, (long long)d.n_seqs + d.n_tokens / tok);
+    p.few = few;
+    p.u_row = (d.rank + ranks - 1) / ranks * ranks;
+    // Parts of k: enough for three blocks on every SM, while a block keeps 512 inputs and more.
+    p.splits = 1;
+    while (p.splits < kMaxSplits && pieces * d.n_mats * p.splits < 3ll * sm_count() && d.in >= 1024 * p.splits) p.splits *= 2;
+    p.runs = 1;
+    if (pieces * p.splits > INT_MAX) {
+        set_error(CQ_ERR_SHAPE, "%d tokens of %d requests are too many for one call", d.n_tokens, d.n_seqs);
+        return 0;
+    }
+    p.pieces = (int)pieces;
+    return (size_t)d.n_mats * p.splits * d.n_tokens * p.u_row * sizeof(float);
+}
+// Requests have few tokens: more pieces of fewer.
+bool lora_few(const cq_lora_desc &d) { return d.n_tokens <= 8ll * d.n_seqs; }
 
 }  // namespace
 
@@ -40,8 +62,8 @@ int cq_block_norm(const cq_norm_desc *d, void *stream) {
     return launch_block_norm(*d, stream);
 }
 
-int cq_lora_add(const cq_lora_desc *d, void *stream) {
-    clear_error();
+// Sizes and types that a call needs right, whatever its pointers.
+static int check_lora(const cq_lora_desc *d) {
     if (!d) return set_error(CQ_ERR_ARG, "null descriptor");
     if (d->w_dtype != CQ_T_F16 && d->w_dtype != CQ_T_BF16) return set_error(CQ_ERR_ARG, "weights are fp16 or bf16, got element type %d", d->w_dtype);
     if (d->x_dtype != CQ_T_F32 && d->x_dtype != CQ_T_I8 && d->x_dtype != d->w_dtype)
@@ -53,6 +75,21 @@ int cq_lora_add(const cq_lora_desc *d, void *stream) {
     if (d->rank < 1 || d->rank > CQ_LORA_MAX_RANK) return set_error(CQ_ERR_SHAPE, "rank must be 1..%d, got %d", CQ_LORA_MAX_RANK, d->rank);
     for (int j = 0; j < d->n_mats; ++j)
         if (d->out[j] < 1 || d->out[j] > kMaxSide) return set_error(CQ_ERR_SHAPE, "out must be 1..%d, got %d", kMaxSide, d->out[j]);
+    return CQ_OK;
+}
+
+size_t cq_lora_workspace(const cq_lora_desc *d) {
+    clear_error();
+    LoraParams p;
+    if (check_lora(d) || !d->n_mats || !d->n_tokens || !d->n_seqs) return 0;
+    const size_t many = lora_plan(*d, false, p);
+    return many && lora_few(*d) ? std::max(many, lora_plan(*d, true, p)) : many;
+}
+
+int cq_lora_add(const cq_lora_desc *d, void *stream) {
+    clear_error();
+    const int st = check_lora(d);
+    if (st) return st;
     if (d->n_mats == 0 || d->n_tokens == 0 || d->n_seqs == 0) return CQ_OK;
     if (!d->x || !d->adapters || !d->cu_tokens) return set_error(CQ_ERR_ARG, "null x, adapters or cu_tokens");
     if (d->x_dtype == CQ_T_I8 && !d->x_scale) return set_error(CQ_ERR_ARG, "int8 activations need x_scale");
@@ -67,20 +104,24 @@ int cq_lora_add(const cq_lora_desc *d, void *stream) {
     }
     LoraParams p;
     p.d = *d;
-    p.cluster = 1;
-    p.status = device_status_ptr();
-    if (!p.status) return set_error(CQ_ERR_CUDA, "no device status word");
     // Where 16-byte loads (8 of int8) and 16-byte accesses to y may be used; single elements elsewhere.
     const int size = d->x_dtype == CQ_T_F32 ? 4 : d->x_dtype == CQ_T_I8 ? 1 : 2, run = d->x_dtype == CQ_T_I8 ? 8 : 16;
-    bool vec = d->in % 8 == 0 && aligned(d->x, run) && (d->n_tokens == 1 || d->x_stride * size % run == 0);
+    p.vec = d->in % 8 == 0 && aligned(d->x, run) && (d->n_tokens == 1 || d->x_stride * size % run == 0);
     p.vec_b = d->rank % 4 == 0;
     for (int j = 0; j < d->n_mats; ++j) {
-        vec = vec && aligned(d->a[j], 16);
+        p.vec = p.vec && aligned(d->a[j], 16);
         p.vec_b = p.vec_b && aligned(d->b[j], 8);
         p.vec_y[j] = d->out[j] % 4 == 0 && aligned(d->y[j], 16) && aligned(d->y_out[j], 16) &&
                      (d->n_tokens == 1 || (d->y_stride[j] % 4 == 0 && d->y_out_stride[j] % 4 == 0));
     }
-    return d->w_dtype == CQ_T_F16 ? launch_lora_f16(p, vec, stream) : launch_lora_bf16(p, vec, stream);
+    const size_t need = lora_plan(*d, p.vec && lora_few(*d), p);
+    if (!need) return CQ_ERR_SHAPE;
+    if (!d->workspace || d->workspace_bytes < need || !aligned(d->workspace, 16))
+        return set_error(CQ_ERR_ARG, "workspace of %zu bytes needed (16-byte aligned), got %zu", need, d->workspace ? d->workspace_bytes : 0);
+    p.u = static_cast<float *>(d->workspace);
+    p.status = device_status_ptr();
+    if (!p.status) return set_error(CQ_ERR_CUDA, "no device status word");
+    return d->w_dtype == CQ_T_F16 ? launch_lora_f16(p, stream) : launch_lora_bf16(p, stream);
 }
 
 }  // extern "C"

@@ -3,6 +3,6 @@
 
 namespace cq {
 
-int launch_lora_bf16(LoraParams &p, bool vec, void *stream) { return launch_t<__nv_bfloat16>(p, vec, reinterpret_cast<cudaStream_t>(stream)); }
+int launch_lora_bf16(LoraParams &p, void *stream) { return launch_t<__nv_bfloat16>(p, reinterpret_cast<cudaStream_t>(stream)); }
 
 }  // namespace cq

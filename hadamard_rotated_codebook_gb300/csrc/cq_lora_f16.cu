@@ -3,6 +3,6 @@
 
 namespace cq {
 
-int launch_lora_f16(LoraParams &p, bool vec, void *stream) { return launch_t<__half>(p, vec, reinterpret_cast<cudaStream_t>(stream)); }
+int launch_lora_f16(LoraParams &p, void *stream) { return launch_t<__half>(p, reinterpret_cast<cudaStream_t>(stream)); }
 
 }  // namespace cq

@@ -9,10 +9,11 @@
 // a lane loads 16 consecutive bytes of a row, and as both operands number their k the same way, any order of k will do. No
 // tile is staged, no descriptor built.
 //
-// Split. A piece is up to TOK tokens of one request. A cluster of C blocks takes a piece and a matrix: block c sums its c-th part of k for
-// all ranks, its warps a part of that part each; the blocks' sums meet over distributed shared memory, added in block
-// order by every block for itself; then block c does its c-th part of the outputs. One launch, no workspace, no
-// atomics, and nothing depends on timing. What a block will read of B is asked for (into L2) before it begins with A.
+// Split. A piece is up to TOK tokens of one request. The first kernel gives a piece and a matrix to `splits` blocks, each of
+// which sums its part of k for all ranks (its warps a part of that part each) and leaves the sum in a workspace; the second
+// gives runs of 32 outputs of a piece to warps, which add the parts in their order. No atomics, and nothing depends on
+// timing. The second kernel begins while the first still runs: its blocks have found their pieces and have y and B on
+// their way by the time the first one's sums are there.
 //
 // Precision. 16-bit and int8 activations meet the weights in one exact product each with fp32 sums. fp32 activations, and u in
 // the second product, are two terms of 11 bits (tf32, which holds fp16 and bf16 weights exactly): what is lost is 2^-22.
@@ -24,7 +25,6 @@
 
 #include <algorithm>
 #include <climits>
-#include <cstdlib>
 #include <type_traits>
 
 #include "cq_layer.h"
@@ -34,7 +34,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCluster = 8;
 constexpr int kSeqs = 4;  // requests that a lane looks at in one go
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -165,15 +164,15 @@ __device__ __forceinline__ uint4 load_a(const uint16_t *p, int n) {
         if (j < n) v[j / 2] |= (uint32_t)__ldg(p + j) << (16 * (j & 1));
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
-// n of 4 consecutive weights of B.
+// The first n of 4 consecutive weights of B: columns past an adapter's own rank may hold anything.
+__device__ __forceinline__ uint2 cut_b(uint2 v, int n) {
+    if (n < 4) v.y = n < 3 ? 0 : v.y & 0xFFFFu;
+    if (n < 2) v.x = n < 1 ? 0 : v.x & 0xFFFFu;
+    return v;
+}
 __device__ __forceinline__ uint2 load_b(const uint16_t *p, int n, bool vec) {
     if (n <= 0) return make_uint2(0, 0);
-    if (vec) {  // columns past an adapter's own rank may hold anything
-        uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-        if (n < 4) v.y = n < 3 ? 0 : v.y & 0xFFFFu;
-        if (n < 2) v.x &= 0xFFFFu;
-        return v;
-    }
+    if (vec) return cut_b(__ldg(reinterpret_cast<const uint2 *>(p)), n);
     uint32_t v[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -260,273 +259,282 @@ __device__ Piece find_piece(const LoraParams &p, int piece, bool skip, int lane,
 
 // MT: tiles of 16 ranks; NT: tiles of 8 tokens of a warp; WT: warps side by side along the tokens (the others split k).
 template <int XK, int MT, int NT, int WT>
-struct Shape {
+struct Down {
     static constexpr int kTok = 8 * NT * WT, kRank = 16 * MT, kParts = kWarps / WT;
-    // row strides that keep the lanes of an access in different banks
-    static constexpr int kPartRow = kRank + 4, kURow = MT == 1 ? 16 : kRank + 16;
-    static constexpr int kSumBytes = kTok * kPartRow * 4, kUBytes = kTok * kURow * 4;
-    static constexpr int kBlocks = NT > 1 || MT == 4 ? 2 : MT == 2 ? 3 : 4;  // on an SM
+    static constexpr int kRow = kRank + 4;  // keeps the lanes that write a sum in different banks
+    static constexpr int kBlocks = NT > 1 || MT == 4 ? 2 : 3;  // on an SM
     static constexpr int kRoom = 228 * 1024 / kBlocks - 1024;
-    // a warp's ring for the first product: 32 inputs a stage. What it holds is read before the sums take its place.
+    // a warp's ring: 32 inputs a stage. What it holds is read before the sums take its place.
     static constexpr int kStage = 32 * (MT * 32 + NT * run_bytes<XK>());
-    static constexpr int kDepth = kRoom / (kWarps * kStage) < 4 ? kRoom / (kWarps * kStage) : 4;
-    static constexpr int kRing = kWarps * kDepth * kStage;
-    // and one for y, a kilobyte a tile of 8 tokens and 32 outputs, behind the block's own sums (which others may still read)
-    static constexpr int kDepthY = NT == 1 ? 0 : (kParts - 1) * kSumBytes > 48 * 1024 ? 6 : 4;
-    static constexpr int kPartBytes = kParts * kSumBytes > kSumBytes + kDepthY * kWarps * 1024 ? kParts * kSumBytes : kSumBytes + kDepthY * kWarps * 1024;
-    static constexpr int kSmem = kRing > kPartBytes + 2 * kUBytes ? kRing : kPartBytes + 2 * kUBytes;
+    static constexpr int kDepth = kRoom / (kWarps * kStage) < 6 ? kRoom / (kWarps * kStage) : 6;
+    static constexpr int kRing = kWarps * kDepth * kStage, kSums = kParts * kTok * kRow * 4;
+    static constexpr int kSmem = kRing > kSums ? kRing : kSums;
     static_assert(kDepth >= 2 && kSmem <= kRoom, "shared memory");
 };
 
+// u[t][r] over a part of k: the blocks of a piece and matrix write parts of their own (p.u: [matrix][part][token][p.u_row]).
 template <typename T, int XK, int MT, int NT, int WT, bool VEC>
-__global__ void __launch_bounds__(kThreads, (Shape<XK, MT, NT, WT>::kBlocks)) lora_kernel(const __grid_constant__ LoraParams p) {
-    using S = Shape<XK, MT, NT, WT>;
+__global__ void __launch_bounds__(kThreads, (Down<XK, MT, NT, WT>::kBlocks)) lora_down_kernel(const __grid_constant__ LoraParams p) {
+    using S = Down<XK, MT, NT, WT>;
     extern __shared__ __align__(16) float smem[];
-    float *part = smem, *u_hi = smem + S::kPartBytes / 4, *u_lo = u_hi + S::kUBytes / 4;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const int C = p.cluster, cta = C > 1 ? blockIdx.x % C : 0, mat = blockIdx.y;
-    const float *y = p.d.y[mat];
-    float *yo = p.d.y_out[mat];
-    const Piece q = find_piece<S::kTok>(p, blockIdx.x / C, y == yo, lane, blockIdx.x + blockIdx.y + warp == 0);
-    if (!q.n) return;  // the whole cluster
-    const int out = p.d.out[mat], n_in = p.d.in;
-    const int64_t yo_st = p.d.y_out_stride[mat];
-    int64_t y_st = p.d.y_stride[mat];
-    const int groups = (out + 31) / 32, g0 = (int)((long long)groups * cta / C), g1 = (int)((long long)groups * (cta + 1) / C);
-    const uint16_t *B = static_cast<const uint16_t *>(p.d.b[mat]) + (int64_t)max(q.adapter, 0) * out * p.d.rank;
-    if (q.rank && NT == 1) {  // few tokens: the weights are what takes time
-        const uint8_t *from = reinterpret_cast<const uint8_t *>(B + (int64_t)g0 * 32 * p.d.rank);
-        const int64_t bytes = ((int64_t)min(out, g1 * 32) - g0 * 32) * p.d.rank * 2;
-        for (int64_t i = tid * 128ll; i < bytes; i += kThreads * 128ll) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(from + i));
+    const int cut = blockIdx.x % p.splits, mat = blockIdx.y, r0 = blockIdx.z * S::kRank;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const Piece q = find_piece<S::kTok>(p, blockIdx.x / p.splits, true, lane, blockIdx.x + blockIdx.y + blockIdx.z + warp == 0);
+    const int rank = min(S::kRank, q.rank - r0), n_in = p.d.in;
+    if (!q.n || rank <= 0) return;
+    const int wk = warp / WT, wt = warp % WT;
+    const int chunks = (n_in + 31) / 32, c0 = (int)((long long)chunks * cut / p.splits), c1 = (int)((long long)chunks * (cut + 1) / p.splits);
+    const int live = min(NT, (q.n - wt * 8 * NT + 7) / 8);  // tiles with a token
+    const uint16_t *A = static_cast<const uint16_t *>(p.d.a[mat]) + ((int64_t)q.adapter * p.d.rank + r0) * n_in;
+    int64_t x_at[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) x_at[t] = (int64_t)(q.first + min(q.n - 1, (wt * NT + t) * 8 + g)) * p.d.x_stride;
+    const uint32_t ring = smem_u32(smem) + warp * S::kDepth * S::kStage;
+    auto send = [&](int i, int st) {
+        const int k = i * 32 + c * 8;
+        const uint32_t to = ring + st * S::kStage;
+        if (i < c1) {
+#pragma unroll
+            for (int h = 0; h < 2 * MT; ++h) {
+                const int r = h * 8 + g;
+                const bool there = r < rank && k < n_in;
+                copy16(to + h * 512 + lane * 16, A + (there ? (int64_t)r * n_in + k : 0), there);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (t < live) send_x<XK>(to + MT * 1024 + t * 32 * run_bytes<XK>(), lane, p.d.x, x_at[t] + k, k < n_in);
+        }
+        copies_sent();
+    };
+    if (VEC) {
+#pragma unroll 1
+        for (int j = 0; j < S::kDepth - 1; ++j) send(c0 + wk + j * S::kParts, j);
     }
-    if (NT > 1 && p.vec_y[mat]) {  // many tokens: y
-        const int w0 = g0 * 32, lines = (min(out, g1 * 32) - w0 + 31) / 32;
-        for (int i = tid; i < q.n * lines; i += kThreads) {
-            const int t = i / lines, l = i - t * lines;
-            asm volatile("prefetch.global.L2 [%0];\n" ::"l"(y + (int64_t)(q.first + t) * y_st + w0 + l * 32));
+    const float scale = p.d.scales ? p.d.scales[q.adapter] : 1.0f;
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[m][t][j] = 0.0f;
+    int st = 0;
+#pragma unroll 1
+    for (int i = c0 + wk; i < c1; i += S::kParts) {
+        const uint32_t from = ring + st * S::kStage;
+        if (VEC) {
+            send(i + (S::kDepth - 1) * S::kParts, st == 0 ? S::kDepth - 1 : st - 1);  // where the round before was read
+            copies_landed<S::kDepth - 1>();
+            if (++st == S::kDepth) st = 0;
+        }
+        const int k = i * 32 + c * 8, n = n_in - k;
+        XRun<XK> x[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (t >= live) break;
+            if (VEC) x[t] = take_x<T, XK>(from + MT * 1024 + t * 32 * run_bytes<XK>(), lane);
+            else x[t] = load_x<T, XK>(p.d.x, x_at[t] + k, n);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            uint4 a[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = m * 16 + h * 8 + g;
+                if (VEC) a[h] = lds16(from + (2 * m + h) * 512 + lane * 16);
+                else a[h] = load_a(A + (int64_t)r * n_in + k, r < rank ? n : 0);
+            }
+            const uint32_t lo[4] = {a[0].x, a[0].y, a[0].z, a[0].w}, hi[4] = {a[1].x, a[1].y, a[1].z, a[1].w};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t >= live) break;
+                if (XK == CQ_T_F32) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t h0, l0, h1, l1;
+                        split(__uint_as_float(x[t].v[XK == CQ_T_F32 ? 2 * j : 0]), h0, l0);
+                        split(__uint_as_float(x[t].v[XK == CQ_T_F32 ? 2 * j + 1 : 0]), h1, l1);
+                        const uint32_t a0 = widen<T>(lo[j], 0), a1 = widen<T>(hi[j], 0), a2 = widen<T>(lo[j], 1), a3 = widen<T>(hi[j], 1);
+                        mma_tf32(acc[m][t], a0, a1, a2, a3, l0, l1);
+                        mma_tf32(acc[m][t], a0, a1, a2, a3, h0, h1);
+                    }
+                } else {
+                    mma16<T>(acc[m][t], lo[0], hi[0], lo[1], hi[1], x[t].v[0], x[t].v[1]);
+                    mma16<T>(acc[m][t], lo[2], hi[2], lo[3], hi[3], x[t].v[2], x[t].v[3]);
+                }
+            }
         }
     }
-    const float scale = q.rank && p.d.scales ? p.d.scales[q.adapter] : 1.0f;
+    if (VEC) {
+        copies_landed<0>();
+        __syncthreads();  // the sums take the rings' place
+    }
+    float *to = smem + (size_t)wk * S::kTok * S::kRow;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        if (t >= live) break;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) to[((wt * NT + t) * 8 + 2 * c + (j & 1)) * S::kRow + m * 16 + (j >> 1) * 8 + g] = acc[m][t][j];
+    }
+    __syncthreads();
+    float *u = p.u + (((int64_t)mat * p.splits + cut) * p.d.n_tokens + q.first) * p.u_row + r0;
+    for (int i = tid; i < q.n * S::kRank; i += kThreads) {
+        const int t = i / S::kRank, r = i % S::kRank;
+        const float *at = smem + t * S::kRow + r;
+        float s = *at;
+#pragma unroll
+        for (int k = 1; k < S::kParts; ++k) s += at[(size_t)k * S::kTok * S::kRow];
+        if (XK == CQ_T_I8) s *= p.d.x_scale[q.first + t];
+        u[(int64_t)t * p.u_row + r] = r < rank ? s * scale : 0.0f;  // ranks that are not there hold what x * 0 gave
+    }
+}
+
+// TOK: tokens of a piece, a multiple of 8. FEW: 8 tokens, and B comes through the ring too.
+template <int MT, int TOK, bool FEW>
+struct Up {
+    static constexpr int kRank = 16 * MT;
+    static constexpr int kRow = MT == 1 ? 16 : kRank + 16;  // rows of u that keep the lanes which read them in different banks
+    static constexpr int kU = TOK * kRow * 4;
+    static constexpr int kBlocks = MT == 4 ? 2 : 3;
+    // a warp's ring: a kilobyte of y (8 tokens, 32 outputs) a stage, and MT of B where there is a run of outputs to each
+    static constexpr int kStage = 1024 + (FEW ? MT * 1024 : 0), kDepth = FEW ? MT == 4 ? 2 : 3 : 5;
+    static constexpr int kSmem = 2 * kU + kWarps * kDepth * kStage;
+    static_assert(kSmem <= 228 * 1024 / kBlocks - 1024, "shared memory");
+};
+
+// y_out = y + B u over runs of 32 outputs: a block's warps take p.runs of them after another.
+template <typename T, int MT, int TOK, bool FEW>
+__global__ void __launch_bounds__(kThreads, (Up<MT, TOK, FEW>::kBlocks)) lora_up_kernel(const __grid_constant__ LoraParams p) {
+    using S = Up<MT, TOK, FEW>;
+    extern __shared__ __align__(16) float smem[];
+    float *u_hi = smem, *u_lo = smem + S::kU / 4;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3, mat = blockIdx.z;
+    const float *y = p.d.y[mat];
+    float *yo = p.d.y_out[mat];
+    const int out = p.d.out[mat], groups = (out + 31) / 32, g0 = blockIdx.y * p.runs * kWarps + warp, g1 = min(groups, ((int)blockIdx.y + 1) * p.runs * kWarps);
+    const Piece q = (int)blockIdx.y * p.runs * kWarps < groups ? find_piece<TOK>(p, blockIdx.x, y == yo, lane, false) : Piece{};
+    if (!q.n) {
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");  // every block: what follows this kernel also follows the one before it
+        return;
+    }
+    const int64_t yo_st = p.d.y_out_stride[mat];
+    int64_t y_st = p.d.y_stride[mat];
+    const uint16_t *B = static_cast<const uint16_t *>(p.d.b[mat]) + (int64_t)max(q.adapter, 0) * out * p.d.rank;
+    const bool vec_y = p.vec_y[mat], ring_b = FEW && p.vec_b;
+    const int tiles = (q.n + 7) / 8, mine = g0 < g1 ? (g1 - g0 + kWarps - 1) / kWarps : 0;
+    const uint32_t ring = smem_u32(smem) + 2 * S::kU + warp * S::kDepth * S::kStage;
     // Ranks in runs of kRank, each added to what the one before left (one run, nearly always).
 #pragma unroll 1
     for (int r0 = 0; r0 == 0 || r0 < q.rank; r0 += S::kRank) {
         const int rank = min(S::kRank, q.rank - r0);
-        if (rank > 0) {
-            if (r0) {  // the other blocks have read this one's sums, and its warps u
-                if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-                __threadfence();  // copies will read what was stored
-                __syncthreads();
-            }
-            // ------------------------------------------------ u: this warp's part of k --
-            const int wk = warp / WT, wt = warp % WT;
-            const int chunks = (n_in + 31) / 32, c0 = (int)((long long)chunks * cta / C), c1 = (int)((long long)chunks * (cta + 1) / C);
-            const int live = min(NT, (q.n - wt * 8 * NT + 7) / 8);  // tiles with a token
-            const uint16_t *A = static_cast<const uint16_t *>(p.d.a[mat]) + ((int64_t)q.adapter * p.d.rank + r0) * n_in;
-            int64_t x_at[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) x_at[t] = (int64_t)(q.first + min(q.n - 1, (wt * NT + t) * 8 + g)) * p.d.x_stride;
-            float acc[MT][NT][4];
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[m][t][j] = 0.0f;
-            const uint32_t ring = smem_u32(smem) + warp * S::kDepth * S::kStage;
-            auto send = [&](int i, int st) {
-                const int k = i * 32 + c * 8;
-                const uint32_t to = ring + st * S::kStage;
-                if (i < c1) {
-#pragma unroll
-                    for (int h = 0; h < 2 * MT; ++h) {
-                        const int r = h * 8 + g;
-                        const bool there = r < rank && k < n_in;
-                        copy16(to + h * 512 + lane * 16, A + (there ? (int64_t)r * n_in + k : 0), there);
-                    }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        if (t < live) send_x<XK>(to + MT * 1024 + t * 32 * run_bytes<XK>(), lane, p.d.x, x_at[t] + k, k < n_in);
-                }
-                copies_sent();
-            };
-            if (VEC) {
-#pragma unroll
-                for (int j = 0; j < S::kDepth - 1; ++j) send(c0 + wk + j * S::kParts, j);
-            }
-            int st = 0;
-#pragma unroll 1
-            for (int i = c0 + wk; i < c1; i += S::kParts) {
-                const uint32_t from = ring + st * S::kStage;
-                if (VEC) {
-                    const int behind = st == 0 ? S::kDepth - 1 : st - 1;  // the stage read in the round before
-                    send(i + (S::kDepth - 1) * S::kParts, behind);
-                    copies_landed<S::kDepth - 1>();
-                    if (++st == S::kDepth) st = 0;
-                }
-                const int k = i * 32 + c * 8, n = n_in - k;
-                XRun<XK> x[NT];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (t >= live) break;
-                    if (VEC) x[t] = take_x<T, XK>(from + MT * 1024 + t * 32 * run_bytes<XK>(), lane);
-                    else x[t] = load_x<T, XK>(p.d.x, x_at[t] + k, n);
-                }
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    uint4 a[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int r = m * 16 + h * 8 + g;
-                        if (VEC) a[h] = lds16(from + (2 * m + h) * 512 + lane * 16);
-                        else a[h] = load_a(A + (int64_t)r * n_in + k, r < rank ? n : 0);
-                    }
-                    const uint32_t lo[4] = {a[0].x, a[0].y, a[0].z, a[0].w}, hi[4] = {a[1].x, a[1].y, a[1].z, a[1].w};
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        if (t >= live) break;
-                        if (XK == CQ_T_F32) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t h0, l0, h1, l1;
-                                split(__uint_as_float(x[t].v[XK == CQ_T_F32 ? 2 * j : 0]), h0, l0);
-                                split(__uint_as_float(x[t].v[XK == CQ_T_F32 ? 2 * j + 1 : 0]), h1, l1);
-                                const uint32_t a0 = widen<T>(lo[j], 0), a1 = widen<T>(hi[j], 0), a2 = widen<T>(lo[j], 1), a3 = widen<T>(hi[j], 1);
-                                mma_tf32(acc[m][t], a0, a1, a2, a3, l0, l1);
-                                mma_tf32(acc[m][t], a0, a1, a2, a3, h0, h1);
-                            }
-                        } else {
-                            mma16<T>(acc[m][t], lo[0], hi[0], lo[1], hi[1], x[t].v[0], x[t].v[1]);
-                            mma16<T>(acc[m][t], lo[2], hi[2], lo[3], hi[3], x[t].v[2], x[t].v[3]);
-                        }
-                    }
-                }
-            }
-            if (VEC) {
-                copies_landed<0>();
-                __syncthreads();  // the sums take the rings' place
-            }
-            float *to = part + (size_t)wk * S::kTok * S::kPartRow;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (t >= live) break;
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) to[((wt * NT + t) * 8 + 2 * c + (j & 1)) * S::kPartRow + m * 16 + (j >> 1) * 8 + g] = acc[m][t][j];
-            }
-            __syncthreads();
-            // ------------------------------------------- u: the warps' parts, then the blocks' --
-            const int cells = (q.n + 7) / 8 * 8 * S::kRank;
-            if (C > 1) {
-                for (int i = tid; i < cells; i += kThreads) {
-                    float *at = part + i / S::kRank * S::kPartRow + i % S::kRank, s = *at;
-#pragma unroll
-                    for (int k = 1; k < S::kParts; ++k) s += at[(size_t)k * S::kTok * S::kPartRow];
-                    *at = s;
-                }
-                asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-            }
-            for (int i = tid; i < cells; i += kThreads) {
-                const int t = i / S::kRank, r = i % S::kRank;
-                const float *at = part + t * S::kPartRow + r;
-                float s = 0.0f;
-                if (C > 1) {
-                    const uint32_t here = smem_u32(at);
-                    float v[kMaxCluster];  // all on their way before the first is added
-#pragma unroll
-                    for (int b = 0; b < kMaxCluster; ++b) {
-                        v[b] = 0.0f;
-                        if (b >= C) continue;
-                        uint32_t there;
-                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(there) : "r"(here), "r"(b));
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v[b]) : "r"(there) : "memory");
-                    }
-#pragma unroll
-                    for (int b = 0; b < kMaxCluster; ++b) s += v[b];
-                } else {
-                    s = *at;
-#pragma unroll
-                    for (int k = 1; k < S::kParts; ++k) s += at[(size_t)k * S::kTok * S::kPartRow];
-                }
-                if (XK == CQ_T_I8) s *= p.d.x_scale[q.first + min(t, q.n - 1)];
-                uint32_t hi, lo;
-                split(r < rank ? s * scale : 0.0f, hi, lo);  // ranks that are not there hold what x * 0 gave
-                u_hi[t * S::kURow + r] = __uint_as_float(hi);
-                u_lo[t * S::kURow + r] = __uint_as_float(lo);
-            }
-            if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");  // this block has read the others
-            __syncthreads();
-        }
-        // ---------------------------------------------------------- the outputs: 32 at a time --
-        // Rows of a tile are dealt out so that a lane holds four consecutive outputs of two tokens.
-        const bool vec_y = p.vec_y[mat];
-        const int tiles = (q.n + 7) / 8, kts = (rank + 15) / 16, mine = g0 + warp < g1 ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;
-        const uint32_t ring = smem_u32(smem) + S::kSumBytes + warp * S::kDepthY * 1024 + lane * 16;
         // A lane's elements of tile t of its j-th run of outputs are copied some tiles ahead of their turn.
         int sj = 0, stile = 0, sst = 0;
         auto send = [&]() {
             if (sj < mine) {
-                const int o = (g0 + warp + sj * kWarps) * 32 + 4 * g;
+                const int o = (g0 + sj * kWarps) * 32 + 4 * g;
+                const uint32_t to = ring + sst * S::kStage;
+                if (vec_y) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int tok = stile * 8 + 2 * c + h;
-                    const bool there = tok < q.n && o < out;
-                    copy16(ring + sst * 1024 + h * 512, y + (there ? (int64_t)(q.first + tok) * y_st + o : 0), there);
+                    for (int h = 0; h < 2; ++h) {
+                        const int tok = stile * 8 + 2 * c + h;
+                        const bool there = tok < q.n && o < out;
+                        copy16(to + h * 512 + lane * 16, y + (there ? (int64_t)(q.first + tok) * y_st + o : 0), there);
+                    }
+                }
+                if (ring_b) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const bool there = o + i < out && m * 16 + 4 * c < rank;
+                            copy8(to + 1024 + (m * 4 + i) * 256 + lane * 8, B + (there ? (int64_t)(o + i) * p.d.rank + r0 + m * 16 + 4 * c : 0), there);
+                        }
                 }
                 if (++stile == tiles) stile = 0, ++sj;
             }
             copies_sent();
-            if (++sst == S::kDepthY) sst = 0;
+            if (++sst == S::kDepth) sst = 0;
         };
-        const bool ahead = NT > 1 && vec_y;
-        if (ahead) {
 #pragma unroll 1
-            for (int j = 0; j < S::kDepthY - 1; ++j) send();
+        for (int j = 0; j < S::kDepth - 1; ++j) send();
+        if (r0) __syncthreads();  // u is read
+        else asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        // ------------------------------------------------------------- u as two terms --
+        if (rank > 0) {
+            const float *from = p.u + ((int64_t)mat * p.splits * p.d.n_tokens + q.first) * p.u_row + r0;
+            const int64_t next = (int64_t)p.d.n_tokens * p.u_row;
+            for (int i = tid; i < tiles * 8 * (S::kRank / 4); i += kThreads) {
+                const int t = i / (S::kRank / 4), r = i % (S::kRank / 4) * 4;
+                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (t < q.n) {
+                    float4 v[kMaxSplits];  // all on their way before the first is added
+#pragma unroll
+                    for (int k = 0; k < kMaxSplits; ++k) {
+                        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (k < p.splits) v[k] = __ldcg(reinterpret_cast<const float4 *>(from + k * next + (int64_t)t * p.u_row + r));
+                    }
+#pragma unroll
+                    for (int k = 0; k < kMaxSplits; ++k) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
+                }
+                uint4 hi, lo;
+                split(s.x, hi.x, lo.x), split(s.y, hi.y, lo.y), split(s.z, hi.z, lo.z), split(s.w, hi.w, lo.w);
+                *reinterpret_cast<uint4 *>(u_hi + t * S::kRow + r) = hi;
+                *reinterpret_cast<uint4 *>(u_lo + t * S::kRow + r) = lo;
+            }
+            __syncthreads();
         }
+        // ---------------------------------------------------------- the outputs: 32 at a time --
+        // Rows of a tile are dealt out so that a lane holds four consecutive outputs of two tokens.
+        const int kts = (rank + 15) / 16;
         int st = 0;
 #pragma unroll 1
         for (int j = 0; j < mine; ++j) {
-            const int o = (g0 + warp + j * kWarps) * 32 + 4 * g, n_o = out - o;
+            const int o = (g0 + j * kWarps) * 32 + 4 * g, n_o = out - o;
             uint2 b[MT][4];
+            if (!ring_b) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    b[m][i] = load_b(B + (int64_t)(o + i) * p.d.rank + r0 + m * 16 + 4 * c, i < n_o ? rank - m * 16 - 4 * c : 0, p.vec_b);
+                    for (int i = 0; i < 4; ++i)
+                        b[m][i] = load_b(B + (int64_t)(o + i) * p.d.rank + r0 + m * 16 + 4 * c, i < n_o ? rank - m * 16 - 4 * c : 0, p.vec_b);
+            }
 #pragma unroll 1
             for (int t = 0; t < tiles; ++t) {
-                float v[2][4];
-                if (ahead) {
-                    send();
-                    copies_landed<(S::kDepthY > 0 ? S::kDepthY - 1 : 0)>();
+                send();
+                copies_landed<S::kDepth - 1>();
+                const uint32_t at = ring + st * S::kStage;
+                if (++st == S::kDepth) st = 0;
+                if (ring_b) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) b[m][i] = cut_b(lds8(at + 1024 + (m * 4 + i) * 256 + lane * 8), rank - m * 16 - 4 * c);
                 }
+                float v[2][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int tok = t * 8 + 2 * c + h;
-                    const float *from = y + (int64_t)(q.first + tok) * y_st + o;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[h][i] = 0.0f;
-                    if (ahead) {
-                        const uint4 f = lds16(ring + st * 1024 + h * 512);
+                    if (vec_y) {
+                        const uint4 f = lds16(at + h * 512 + lane * 16);
                         v[h][0] = __uint_as_float(f.x), v[h][1] = __uint_as_float(f.y), v[h][2] = __uint_as_float(f.z), v[h][3] = __uint_as_float(f.w);
-                    } else if (tok < q.n && n_o > 0) {
-                        if (vec_y) {
-                            const float4 f = __ldcs(reinterpret_cast<const float4 *>(from));
-                            v[h][0] = f.x, v[h][1] = f.y, v[h][2] = f.z, v[h][3] = f.w;
-                        } else {
+                    } else if (tok < q.n) {
+                        const float *from = y + (int64_t)(q.first + tok) * y_st + o;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (i < n_o) v[h][i] = from[i];
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            if (i < n_o) v[h][i] = from[i];
                     }
                 }
-                if (++st == S::kDepthY) st = 0;
                 float d[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     if (m >= kts) break;
-                    const int at = (t * 8 + g) * S::kURow + m * 16 + 4 * c;
-                    const uint4 hi = *reinterpret_cast<const uint4 *>(u_hi + at), lo = *reinterpret_cast<const uint4 *>(u_lo + at);
+                    const int row = (t * 8 + g) * S::kRow + m * 16 + 4 * c;
+                    const uint4 hi = *reinterpret_cast<const uint4 *>(u_hi + row), lo = *reinterpret_cast<const uint4 *>(u_lo + row);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const uint32_t h0 = k ? hi.z : hi.x, h1 = k ? hi.w : hi.y, l0 = k ? lo.z : lo.x, l1 = k ? lo.w : lo.y;
@@ -555,62 +563,79 @@ __global__ void __launch_bounds__(kThreads, (Shape<XK, MT, NT, WT>::kBlocks)) lo
                 }
             }
         }
-        if (ahead) copies_landed<0>();
+        copies_landed<0>();
+        if (r0 + S::kRank < q.rank) __threadfence();  // copies will read what was stored
         y = yo, y_st = yo_st;
     }
-    if (q.rank && C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");  // no block ends while another reads its sums
 }
 
 // ---------------------------------------------------------------------- host --
 template <typename T, int XK, int MT, int NT, int WT, bool VEC>
-int launch_k(LoraParams &p, cudaStream_t st) {
-    using S = Shape<XK, MT, NT, WT>;
-    auto k = lora_kernel<T, XK, MT, NT, WT, VEC>;
+int launch_down(const LoraParams &p, cudaStream_t st) {
+    using S = Down<XK, MT, NT, WT>;
+    auto k = lora_down_kernel<T, XK, MT, NT, WT, VEC>;
     if (S::kSmem > 48 * 1024) {
         const int rc = ensure_smem(reinterpret_cast<const void *>(k), S::kSmem);
         if (rc) return rc;
     }
-    const long long pieces = std::min<long long>(p.d.n_tokens, (long long)p.d.n_seqs + p.d.n_tokens / S::kTok);
-    // Blocks of a cluster: parts of about 512 inputs or outputs, smaller ones where there are fewer than two blocks an SM.
-    int widest = p.d.in;
-    for (int j = 0; j < p.d.n_mats; ++j) widest = std::max(widest, p.d.out[j]);
-    int C = 1;
-    while (C < kMaxCluster && (widest > 512 * C || (widest > 128 * C && pieces * p.d.n_mats * C < 2 * sm_count()))) C *= 2;
-    if (const char *e = getenv("LORA_C")) C = atoi(e);
-    p.cluster = C;
-    if (pieces * C > INT_MAX) return set_error(CQ_ERR_SHAPE, "%d tokens of %d requests are too many for one call", p.d.n_tokens, p.d.n_seqs);
+    k<<<dim3(p.pieces * p.splits, p.d.n_mats, p.u_row / S::kRank), kThreads, S::kSmem, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? CQ_OK : set_error(CQ_ERR_CUDA, "adapter launch: %s", cudaGetErrorString(e));
+}
+template <typename T, int MT, int TOK, bool FEW>
+int launch_up(LoraParams &p, cudaStream_t st) {
+    using S = Up<MT, TOK, FEW>;
+    auto k = lora_up_kernel<T, MT, TOK, FEW>;
+    if (S::kSmem > 48 * 1024) {
+        const int rc = ensure_smem(reinterpret_cast<const void *>(k), S::kSmem);
+        if (rc) return rc;
+    }
+    int groups = 1;
+    for (int j = 0; j < p.d.n_mats; ++j) groups = std::max(groups, (p.d.out[j] + 31) / 32);
+    // Runs of outputs of a warp: one, and more while that leaves every SM four blocks.
+    p.runs = 1;
+    while (p.runs < 8 && (long long)p.pieces * p.d.n_mats * ((groups + 2 * kWarps * p.runs - 1) / (2 * kWarps * p.runs)) >= 4ll * sm_count()) p.runs *= 2;
+    const int rows = (groups + kWarps * p.runs - 1) / (kWarps * p.runs);
+    if (rows > 65535) return set_error(CQ_ERR_SHAPE, "%d outputs are too many", groups * 32);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(pieces * C), (unsigned)p.d.n_mats);
+    cfg.gridDim = dim3((unsigned)p.pieces, (unsigned)rows, (unsigned)p.d.n_mats);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)C, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, k, p);
     if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return set_error(CQ_ERR_CUDA, "adapter launch: %s", cudaGetErrorString(e));
-    }
-    return CQ_OK;
+    if (e == cudaSuccess) return CQ_OK;
+    cudaGetLastError();
+    return set_error(CQ_ERR_CUDA, "adapter launch: %s", cudaGetErrorString(e));
 }
 
-// Tokens of a piece: 8 where requests have few, else as many as leave the sums of the first product in registers.
+template <typename T, int XK, int MT, bool VEC>
+int launch_r(LoraParams &p, cudaStream_t st) {
+    constexpr int WT = lora_warps_along(false), NT = lora_tokens(XK, MT, false) / (8 * WT);
+    int rc;
+    if (VEC && p.few) rc = launch_down<T, XK, MT, 1, 1, true>(p, st);
+    else rc = launch_down<T, XK, MT, NT, WT, VEC>(p, st);
+    if (rc) return rc;
+    return p.few ? launch_up<T, MT, 8, true>(p, st) : launch_up<T, MT, 8 * NT * WT, false>(p, st);
+}
 template <typename T, int XK, bool VEC>
 int launch_x(LoraParams &p, cudaStream_t st) {
-    const bool few = VEC && (long long)p.d.n_tokens <= 8ll * p.d.n_seqs;
-    if (p.d.rank <= 16) return few ? launch_k<T, XK, 1, 1, 1, true>(p, st) : launch_k<T, XK, 1, XK == CQ_T_F32 ? 4 : 8, 2, VEC>(p, st);
-    if (p.d.rank <= 32) return few ? launch_k<T, XK, 2, 1, 1, true>(p, st) : launch_k<T, XK, 2, 4, 2, VEC>(p, st);
-    return few ? launch_k<T, XK, 4, 1, 1, true>(p, st) : launch_k<T, XK, 4, XK == CQ_T_F32 ? 2 : 4, 2, VEC>(p, st);
+    switch (lora_rank_tiles(p.d.rank)) {
+    case 1: return launch_r<T, XK, 1, VEC>(p, st);
+    case 2: return launch_r<T, XK, 2, VEC>(p, st);
+    default: return launch_r<T, XK, 4, VEC>(p, st);
+    }
 }
 template <typename T>
-int launch_t(LoraParams &p, bool vec, cudaStream_t st) {
-    if (p.d.x_dtype == CQ_T_F32) return vec ? launch_x<T, CQ_T_F32, true>(p, st) : launch_x<T, CQ_T_F32, false>(p, st);
-    if (p.d.x_dtype == CQ_T_I8) return vec ? launch_x<T, CQ_T_I8, true>(p, st) : launch_x<T, CQ_T_I8, false>(p, st);
-    return vec ? launch_x<T, CQ_T_F16, true>(p, st) : launch_x<T, CQ_T_F16, false>(p, st);
+int launch_t(LoraParams &p, cudaStream_t st) {
+    if (p.d.x_dtype == CQ_T_F32) return p.vec ? launch_x<T, CQ_T_F32, true>(p, st) : launch_x<T, CQ_T_F32, false>(p, st);
+    if (p.d.x_dtype == CQ_T_I8) return p.vec ? launch_x<T, CQ_T_I8, true>(p, st) : launch_x<T, CQ_T_I8, false>(p, st);
+    return p.vec ? launch_x<T, CQ_T_F16, true>(p, st) : launch_x<T, CQ_T_F16, false>(p, st);
 }
 
 }  // namespace

@@ -12,10 +12,11 @@ import torch
 from . import _capi
 from ._capi import (CQ_GATE_PLAIN, CQ_GATE_SIGMOID, CQ_GATE_SILU, CQ_LORA_MAX_MATS, CQ_T_BF16, CQ_T_F16, CQ_T_F32, CQ_T_I8,
                     LoraDesc, NormDesc)
-from .paged import _call, _dev, _i32, _ints, _type, _weight
+from .paged import _call, _dev, _i32, _ints, _stay, _type, _weight
 
 _ACT = {None: CQ_GATE_PLAIN, "sigmoid": CQ_GATE_SIGMOID, "silu": CQ_GATE_SILU}
 _load = _capi.load
+_lora_bytes: dict = {}
 
 
 def _matrix(t: torch.Tensor, name: str, device, shape=None, out: bool = False) -> int:
@@ -159,5 +160,15 @@ def cq_lora_add(ys: Sequence[torch.Tensor], x: torch.Tensor, a: Sequence[torch.T
     d.n_mats, d.n_tokens, d.n_seqs, d.n_adapters, d.in_, d.rank = m, n, n_seqs, n_adapters, n_in, rank
     d.w_dtype = CQ_T_F16 if wd == torch.float16 else CQ_T_BF16
     d.x_dtype = CQ_T_F32 if x.dtype == torch.float32 else CQ_T_I8 if x.dtype == torch.int8 else d.w_dtype
+    key = (m, n, n_seqs, n_in, rank, d.x_dtype, dev.index)  # what the workspace goes by, besides the device
+    size = _lora_bytes.get(key)
+    if size is None:
+        with (_stay if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)):
+            size = _load().cq_lora_workspace(d)
+        if len(_lora_bytes) >= 4096:
+            _lora_bytes.clear()
+        _lora_bytes[key] = size
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    d.workspace, d.workspace_bytes = ws.data_ptr(), size
     _call(dev, _load().cq_lora_add, d)
     return list(outs)

@@ -645,10 +645,17 @@ typedef struct cq_lora_desc {
     int64_t y_stride[CQ_LORA_MAX_MATS], y_out_stride[CQ_LORA_MAX_MATS];
     int out[CQ_LORA_MAX_MATS];
     int64_t x_stride;
+    void *workspace;           /* cq_lora_workspace bytes, 16-byte aligned */
+    size_t workspace_bytes;
     int n_mats, n_tokens, n_seqs, n_adapters, in, rank;
     int x_dtype;               /* CQ_T_F32, CQ_T_I8, or w_dtype */
     int w_dtype;               /* CQ_T_F16 or CQ_T_BF16 */
 } cq_lora_desc;
+
+/* Bytes of workspace that cq_lora_add needs on the current device for these
+ * sizes and types (no pointer of d is looked at); 0 on invalid ones and where
+ * there is nothing to do. */
+size_t cq_lora_workspace(const cq_lora_desc *d);
 
 /* Low-rank adapters of many requests beside shared projections: for every
  * token t of request s with adapter e = adapters[s] >= 0 and every matrix j

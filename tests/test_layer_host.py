@@ -42,7 +42,8 @@ def test_block_norm_refuses(A, kw, code):
 
 
 def _lora(A, **kw):
-    d = dict(x=16, adapters=16, cu_tokens=16, x_stride=64, n_mats=1, n_tokens=4, n_seqs=2, n_adapters=3, in_=64, rank=8, x_dtype=0, w_dtype=1)
+    d = dict(x=16, adapters=16, cu_tokens=16, x_stride=64, n_mats=1, n_tokens=4, n_seqs=2, n_adapters=3, in_=64, rank=8, x_dtype=0, w_dtype=1,
+             workspace=32, workspace_bytes=1 << 20)
     first = dict(a=16, b=16, y=16, y_out=32, y_stride=32, y_out_stride=32, out=32)
     first.update({k: kw[k] for k in kw if k in first})
     d.update({k: kw[k] for k in kw if k not in first})
@@ -58,10 +59,21 @@ def _lora(A, **kw):
     (dict(in_=2 ** 30), "SHAPE"), (dict(rank=0), "SHAPE"), (dict(rank=257), "SHAPE"), (dict(out=0), "SHAPE"), (dict(out=2 ** 30), "SHAPE"),
     (dict(x=None), "ARG"), (dict(adapters=None), "ARG"), (dict(cu_tokens=None), "ARG"), (dict(x_dtype=3), "ARG"), (dict(a=None), "ARG"),
     (dict(b=None), "ARG"), (dict(y=None), "ARG"), (dict(y_out=None), "ARG"), (dict(y_out_stride=31), "SHAPE"), (dict(y=32, y_stride=40), "SHAPE"),
+    (dict(workspace=None), "ARG"), (dict(workspace_bytes=16), "ARG"), (dict(workspace=40), "ARG"),
 ])
 def test_lora_add_refuses(A, kw, code):
     assert A.load().cq_lora_add(ctypes.byref(_lora(A, **kw)), None) == getattr(A, "CQ_ERR_" + code)
     assert A.load().cq_last_error()
+
+
+def test_lora_workspace(A):
+    """A function of sizes and types; nothing where there is nothing to do or a size is bad."""
+    size = lambda **kw: A.load().cq_lora_workspace(ctypes.byref(_lora(A, **kw)))  # noqa: E731
+    assert size() >= 4 * 16 * 4 and size(x=None, adapters=None) == size()
+    assert size(n_tokens=400) > size() and size(rank=100) > size()
+    for kw in (dict(n_tokens=0), dict(n_seqs=0), dict(n_mats=0), dict(rank=0), dict(x_dtype=2), dict(out=0)):
+        assert size(**kw) == 0
+    assert A.load().cq_lora_workspace(None) == 0
 
 
 def test_window_attend_refuses(A):
@@ -104,9 +116,9 @@ def _fields(A, struct):
     body = re.search(r"typedef struct %s \{([^}]*)\} %s;" % (struct, struct), src).group(1)
     out = []
     for decl in filter(None, (s.strip() for s in body.split(";"))):
-        kind = re.match(r"(const )?(void|float|int32_t|int64_t|int)\b", decl)
+        kind = re.match(r"(const )?(void|float|int32_t|int64_t|size_t|int)\b", decl)
         for part in decl[kind.end():].split(","):
-            size = 8 if "*" in part else {"int64_t": 8, "int": 4, "float": 4}[kind.group(2)]
+            size = 8 if "*" in part else {"int64_t": 8, "size_t": 8, "int": 4, "float": 4}[kind.group(2)]
             out.append((re.search(r"\w+", part).group(0), size * (A.CQ_LORA_MAX_MATS if "[" in part else 1)))
     return out
 
