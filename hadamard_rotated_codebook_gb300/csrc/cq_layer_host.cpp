@@ -1,6 +1,7 @@
 // cq_layer_host.cpp -- host side of the block norm's and the adapters' entry points: argument checks, alignment.
 #include <algorithm>
 #include <climits>
+#include <cstdlib>
 #include <cmath>
 #include <cstdint>
 
@@ -24,6 +25,7 @@ size_t lora_plan(const cq_lora_desc &d, bool few, LoraParams &p) {
     // Parts of k: enough for three blocks on every SM, while a block keeps 512 inputs and more.
     p.splits = 1;
     while (p.splits < kMaxSplits && pieces * d.n_mats * p.splits < 3ll * sm_count() && d.in >= 1024 * p.splits) p.splits *= 2;
+    if (const char *e = getenv("LORA_S")) p.splits = atoi(e);
     p.runs = 1;
     if (pieces * p.splits > INT_MAX) {
         set_error(CQ_ERR_SHAPE, "%d tokens of %d requests are too many for one call", d.n_tokens, d.n_seqs);

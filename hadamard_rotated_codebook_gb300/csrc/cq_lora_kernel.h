@@ -15,8 +15,9 @@
 // timing. The second kernel begins while the first still runs: its blocks have found their pieces and have y and B on
 // their way by the time the first one's sums are there.
 //
-// Precision. 16-bit and int8 activations meet the weights in one exact product each with fp32 sums. fp32 activations, and u in
-// the second product, are two terms of 11 bits (tf32, which holds fp16 and bf16 weights exactly): what is lost is 2^-22.
+// Precision. 16-bit and int8 activations meet the weights in one exact product each with fp32 sums. fp32 activations are two
+// terms of 11 bits (tf32, which holds fp16 and bf16 weights exactly): what is lost is 2^-22. u, summed in fp32, is three
+// terms of bf16 or two of fp16 (Terms).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,6 +26,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cstdlib>
 #include <type_traits>
 
 #include "cq_layer.h"
@@ -34,6 +36,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr unsigned kSpin = 1u << 20;
 constexpr int kSeqs = 4;  // requests that a lane looks at in one go
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -197,9 +200,9 @@ __device__ __forceinline__ Piece seq_at(const LoraParams &p, int s, bool &bad) {
     return q;
 }
 // The piece-th piece of up to TOK tokens over all requests (those without an adapter have none where `skip`); n = 0 past the last.
-// Every warp finds it for itself.
+// (One warp.)
 template <int TOK>
-__device__ Piece find_piece(const LoraParams &p, int piece, bool skip, int lane, bool report) {
+__device__ Piece search_piece(const LoraParams &p, int piece, bool skip, int lane, bool report) {
     Piece q = {};
     bool bad = false;
     int before = 0;
@@ -257,6 +260,21 @@ __device__ Piece find_piece(const LoraParams &p, int piece, bool skip, int lane,
     return q;
 }
 
+// Likewise, for a whole block.
+template <int TOK>
+__device__ __forceinline__ Piece find_piece(const LoraParams &p, int piece, bool skip, int warp, int lane, bool report) {
+    __shared__ Piece found;
+    if (warp == 0) {
+        const Piece q = search_piece<TOK>(p, piece, skip, lane, report);
+        if (lane == 0) found = q;
+    }
+    __syncthreads();
+    Piece q;  // through a shuffle: the compiler would read shared memory again wherever they are used
+    q.first = __shfl_sync(0xFFFFFFFFu, found.first, 0), q.n = __shfl_sync(0xFFFFFFFFu, found.n, 0);
+    q.adapter = __shfl_sync(0xFFFFFFFFu, found.adapter, 0), q.rank = __shfl_sync(0xFFFFFFFFu, found.rank, 0);
+    return q;
+}
+
 // MT: tiles of 16 ranks; NT: tiles of 8 tokens of a warp; WT: warps side by side along the tokens (the others split k).
 template <int XK, int MT, int NT, int WT>
 struct Down {
@@ -280,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, (Down<XK, MT, NT, WT>::kBlocks)) lor
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int cut = blockIdx.x % p.splits, mat = blockIdx.y, r0 = blockIdx.z * S::kRank;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    const Piece q = find_piece<S::kTok>(p, blockIdx.x / p.splits, true, lane, blockIdx.x + blockIdx.y + blockIdx.z + warp == 0);
+    const Piece q = find_piece<S::kTok>(p, blockIdx.x / p.splits, true, warp, lane, blockIdx.x + blockIdx.y + blockIdx.z == 0);
     const int rank = min(S::kRank, q.rank - r0), n_in = p.d.in;
     if (!q.n || rank <= 0) return;
     const int wk = warp / WT, wt = warp % WT;
@@ -392,30 +410,107 @@ __global__ void __launch_bounds__(kThreads, (Down<XK, MT, NT, WT>::kBlocks)) lor
     }
 }
 
-// TOK: tokens of a piece, a multiple of 8. FEW: 8 tokens, and B comes through the ring too.
-template <int MT, int TOK, bool FEW>
+// u as the second product takes it, in terms of the weights' type: three of bf16 (24 bits together); two of fp16 (22), where a token's
+// values are first multiplied by the power of two that brings its largest to 2^13..2^14, so that no term leaves fp16.
+template <typename T> struct Terms { static constexpr int n = std::is_same<T, __half>::value ? 2 : 3; };
+template <typename T>
+__device__ __forceinline__ float term_of(float x) {
+    return std::is_same<T, __half>::value ? __half2float(__float2half_rn(x)) : __bfloat162float(__float2bfloat16_rn(x));
+}
+// The next term of four values, and what it leaves of them (of an infinity, and of what rounds to one, nothing; what is no number stays none).
+template <typename T>
+__device__ __forceinline__ uint2 next_term(float (&x)[4]) {
+    float t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        t[i] = term_of<T>(x[i]);
+        x[i] = fabsf(t[i]) == INFINITY ? 0.0f : x[i] - t[i];
+    }
+    return make_uint2(pair_of<T>(t[0], t[1]), pair_of<T>(t[2], t[3]));
+}
+
+// Magnitudes are ordered as integers; what is not finite scales nothing.
+__device__ __forceinline__ uint32_t magnitude(float x) {
+    const uint32_t m = __float_as_uint(x) & 0x7FFFFFFFu;
+    return m < 0x7F800000u ? m : 0u;
+}
+// What takes the power of two that brings the largest magnitude to 2^13..2^14 out again. (Its reciprocal has the exponent 254 - its own.)
+__device__ __forceinline__ float back_of(uint32_t top) { return __uint_as_float((uint32_t)(max(14, (int)(top >> 23)) - 13) << 23); }
+
+// The parts' sums of a piece's `tokens` (zero past its end), ranks r0 .. r0 + RANK - 1, as terms: put(term, token, rank, four values). A
+// token's power of two goes to back[token], or is there already (`scaled`). kThreads threads.
+template <typename T, int RANK, typename Put>
+__device__ __forceinline__ void gather_u(const LoraParams &p, const Piece &q, int mat, int r0, int tokens, float *back, bool scaled, Put put) {
+    constexpr int kFours = RANK / 4;  // of a token; they lie side by side in a warp
+    const float *from = p.u + ((int64_t)mat * p.splits * p.d.n_tokens + q.first) * p.u_row + r0;
+    const int64_t next = (int64_t)p.d.n_tokens * p.u_row;
+    const int cells = tokens * kFours;
+    for (int base = 0; base < cells; base += 2 * kThreads) {
+        float4 s[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+        for (int k0 = 0; k0 < p.splits; k0 += 4) {
+            float4 v[2][4];  // all on their way before the first is added
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = base + h * kThreads + (int)threadIdx.x, t = i / kFours, r = i % kFours * 4;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[h][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (t < q.n && k0 + k < p.splits) v[h][k] = __ldcg(reinterpret_cast<const float4 *>(from + (k0 + k) * next + (int64_t)t * p.u_row + r));
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[h].x += v[h][k].x, s[h].y += v[h][k].y, s[h].z += v[h][k].z, s[h].w += v[h][k].w;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = base + h * kThreads + (int)threadIdx.x, t = i / kFours, r = i % kFours * 4;
+            float x[4] = {s[h].x, s[h].y, s[h].z, s[h].w};
+            if (std::is_same<T, __half>::value) {
+                uint32_t top = max(max(magnitude(x[0]), magnitude(x[1])), max(magnitude(x[2]), magnitude(x[3])));
+#pragma unroll
+                for (int o = 1; o < kFours; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                float down = back_of(top);
+                if (scaled && i < cells) down = back[t];
+                else if (i < cells && r == 0) back[t] = down;
+                const float up = __uint_as_float((254u << 23) - __float_as_uint(down));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] *= up;
+            }
+            if (i >= cells) continue;
+#pragma unroll
+            for (int k = 0; k < Terms<T>::n; ++k) put(k, t, r, next_term<T>(x));
+        }
+    }
+}
+
+// The second product where requests have few tokens: pieces of 8.
+template <typename T, int MT>
 struct Up {
-    static constexpr int kRank = 16 * MT;
-    static constexpr int kRow = MT == 1 ? 16 : kRank + 16;  // rows of u that keep the lanes which read them in different banks
-    static constexpr int kU = TOK * kRow * 4;
+    static constexpr int kTok = 8, kRank = 16 * MT;
+    static constexpr int kRow = (kRank + (MT == 1 ? 0 : 16)) * 2;  // bytes of a row of a term: four rows' reads lie in different banks
+    static constexpr int kTerm = kTok * kRow, kU = (Terms<T>::n * kTerm + kTok * 4 + 1023) / 1024 * 1024;
     static constexpr int kBlocks = MT == 4 ? 2 : 3;
-    // a warp's ring: a kilobyte of y (8 tokens, 32 outputs) a stage, and MT of B where there is a run of outputs to each
-    static constexpr int kStage = 1024 + (FEW ? MT * 1024 : 0), kDepth = FEW ? MT == 4 ? 2 : 3 : 5;
-    static constexpr int kSmem = 2 * kU + kWarps * kDepth * kStage;
-    static_assert(kSmem <= 228 * 1024 / kBlocks - 1024, "shared memory");
+    // a warp's ring: a kilobyte of y (8 tokens, 32 outputs) and MT of B a stage
+    static constexpr int kStage = 1024 + MT * 1024, kDepth = MT == 1 ? 3 : 2;
+    static constexpr int kSmem = kU + kWarps * kDepth * kStage;
+    static_assert(kSmem <= 228 * 1024 / kBlocks - 2048, "shared memory");
 };
 
 // y_out = y + B u over runs of 32 outputs: a block's warps take p.runs of them after another.
-template <typename T, int MT, int TOK, bool FEW>
-__global__ void __launch_bounds__(kThreads, (Up<MT, TOK, FEW>::kBlocks)) lora_up_kernel(const __grid_constant__ LoraParams p) {
-    using S = Up<MT, TOK, FEW>;
-    extern __shared__ __align__(16) float smem[];
-    float *u_hi = smem, *u_lo = smem + S::kU / 4;
+template <typename T, int MT>
+__global__ void __launch_bounds__(kThreads, (Up<T, MT>::kBlocks)) lora_up_kernel(const __grid_constant__ LoraParams p) {
+    using S = Up<T, MT>;
+    constexpr int kTerms = Terms<T>::n;
+    extern __shared__ __align__(16) uint8_t smem_up[];
+    uint8_t *const u = smem_up;
+    float *const back = reinterpret_cast<float *>(u + kTerms * S::kTerm);  // what takes a token's power of two out again
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3, mat = blockIdx.z;
     const float *y = p.d.y[mat];
     float *yo = p.d.y_out[mat];
     const int out = p.d.out[mat], groups = (out + 31) / 32, g0 = blockIdx.y * p.runs * kWarps + warp, g1 = min(groups, ((int)blockIdx.y + 1) * p.runs * kWarps);
-    const Piece q = (int)blockIdx.y * p.runs * kWarps < groups ? find_piece<TOK>(p, blockIdx.x, y == yo, lane, false) : Piece{};
+    const Piece q = (int)blockIdx.y * p.runs * kWarps < groups ? find_piece<S::kTok>(p, blockIdx.x, y == yo, warp, lane, false) : Piece{};
     if (!q.n) {
         asm volatile("griddepcontrol.wait;\n" ::: "memory");  // every block: what follows this kernel also follows the one before it
         return;
@@ -423,9 +518,9 @@ __global__ void __launch_bounds__(kThreads, (Up<MT, TOK, FEW>::kBlocks)) lora_up
     const int64_t yo_st = p.d.y_out_stride[mat];
     int64_t y_st = p.d.y_stride[mat];
     const uint16_t *B = static_cast<const uint16_t *>(p.d.b[mat]) + (int64_t)max(q.adapter, 0) * out * p.d.rank;
-    const bool vec_y = p.vec_y[mat], ring_b = FEW && p.vec_b;
+    const bool vec_y = p.vec_y[mat], ring_b = p.vec_b;
     const int tiles = (q.n + 7) / 8, mine = g0 < g1 ? (g1 - g0 + kWarps - 1) / kWarps : 0;
-    const uint32_t ring = smem_u32(smem) + 2 * S::kU + warp * S::kDepth * S::kStage;
+    const uint32_t ring = smem_u32(smem_up) + S::kU + warp * S::kDepth * S::kStage;
     // Ranks in runs of kRank, each added to what the one before left (one run, nearly always).
 #pragma unroll 1
     for (int r0 = 0; r0 == 0 || r0 < q.rank; r0 += S::kRank) {
@@ -464,26 +559,9 @@ __global__ void __launch_bounds__(kThreads, (Up<MT, TOK, FEW>::kBlocks)) lora_up
         else asm volatile("griddepcontrol.wait;\n" ::: "memory");
         // ------------------------------------------------------------- u as two terms --
         if (rank > 0) {
-            const float *from = p.u + ((int64_t)mat * p.splits * p.d.n_tokens + q.first) * p.u_row + r0;
-            const int64_t next = (int64_t)p.d.n_tokens * p.u_row;
-            for (int i = tid; i < tiles * 8 * (S::kRank / 4); i += kThreads) {
-                const int t = i / (S::kRank / 4), r = i % (S::kRank / 4) * 4;
-                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (t < q.n) {
-                    float4 v[kMaxSplits];  // all on their way before the first is added
-#pragma unroll
-                    for (int k = 0; k < kMaxSplits; ++k) {
-                        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (k < p.splits) v[k] = __ldcg(reinterpret_cast<const float4 *>(from + k * next + (int64_t)t * p.u_row + r));
-                    }
-#pragma unroll
-                    for (int k = 0; k < kMaxSplits; ++k) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
-                }
-                uint4 hi, lo;
-                split(s.x, hi.x, lo.x), split(s.y, hi.y, lo.y), split(s.z, hi.z, lo.z), split(s.w, hi.w, lo.w);
-                *reinterpret_cast<uint4 *>(u_hi + t * S::kRow + r) = hi;
-                *reinterpret_cast<uint4 *>(u_lo + t * S::kRow + r) = lo;
-            }
+            gather_u<T, S::kRank>(p, q, mat, r0, tiles * 8, back, false, [&](int k, int t, int r, uint2 w) {
+                *reinterpret_cast<uint2 *>(u + k * S::kTerm + t * S::kRow + r * 2) = w;
+            });
             __syncthreads();
         }
         // ---------------------------------------------------------- the outputs: 32 at a time --
@@ -529,29 +607,29 @@ __global__ void __launch_bounds__(kThreads, (Up<MT, TOK, FEW>::kBlocks)) lora_up
                             if (i < n_o) v[h][i] = from[i];
                     }
                 }
-                float d[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+                float d[2][2][4] = {};  // the first term's products, and the others'
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     if (m >= kts) break;
-                    const int row = (t * 8 + g) * S::kRow + m * 16 + 4 * c;
-                    const uint4 hi = *reinterpret_cast<const uint4 *>(u_hi + row), lo = *reinterpret_cast<const uint4 *>(u_lo + row);
+                    const uint8_t *row = u + (t * 8 + g) * S::kRow + m * 32 + 8 * c;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t h0 = k ? hi.z : hi.x, h1 = k ? hi.w : hi.y, l0 = k ? lo.z : lo.x, l1 = k ? lo.w : lo.y;
+                    for (int k = kTerms - 1; k >= 0; --k) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(row + k * S::kTerm);
 #pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            const uint32_t w0 = k ? b[m][2 * f].y : b[m][2 * f].x, w1 = k ? b[m][2 * f + 1].y : b[m][2 * f + 1].x;
-                            const uint32_t a0 = widen<T>(w0, 0), a1 = widen<T>(w1, 0), a2 = widen<T>(w0, 1), a3 = widen<T>(w1, 1);
-                            mma_tf32(d[f], a0, a1, a2, a3, l0, l1);
-                            mma_tf32(d[f], a0, a1, a2, a3, h0, h1);
-                        }
+                        for (int f = 0; f < 2; ++f) mma16<T>(d[k > 0][f], b[m][2 * f].x, b[m][2 * f + 1].x, b[m][2 * f].y, b[m][2 * f + 1].y, w.x, w.y);
                     }
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int tok = t * 8 + 2 * c + h;
                     if (tok >= q.n || n_o <= 0) continue;
-                    if (rank > 0) v[h][0] += d[0][h], v[h][1] += d[0][2 + h], v[h][2] += d[1][h], v[h][3] += d[1][2 + h];
+                    if (rank > 0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float sum = d[0][i >> 1][2 * (i & 1) + h] + d[1][i >> 1][2 * (i & 1) + h];
+                            v[h][i] = std::is_same<T, __half>::value ? fmaf(sum, back[tok], v[h][i]) : v[h][i] + sum;
+                        }
+                    }
                     float *to = yo + (int64_t)(q.first + tok) * yo_st + o;
                     if (vec_y) {
                         *reinterpret_cast<float4 *>(to) = make_float4(v[h][0], v[h][1], v[h][2], v[h][3]);
@@ -569,6 +647,289 @@ __global__ void __launch_bounds__(kThreads, (Up<MT, TOK, FEW>::kBlocks)) lora_up
     }
 }
 
+// ------------------------------------------------------ many tokens: tcgen05 --
+// The outputs are the M side (128 to a tile) and 64 tokens the N side, so that what a thread reads back from tensor memory is one output of
+// 32 tokens: the lanes of a warp then meet y in whole lines, and an element costs a load, an addition and a store. The
+// terms of u lie behind each other along K, the weights are used again for each.
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+// The issuing warp runs as a whole and one elected lane issues.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xFFFFFFFF;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, e;\n elect.sync _|e, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// A K-major operand in 128-byte swizzled atoms of 8 rows of 128 bytes, atoms 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint32_t swizzled(int row, int byte) { return (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + (byte ^ ((row & 7) << 4))); }
+__device__ __forceinline__ void tmem_ld16(uint32_t a, float (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+                 "tcgen05.wait::ld.sync.aligned;\n"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+                   "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(a)
+                 : "memory");
+}
+// A product that is not done within kSpin polls marks the status word; the block then runs on without waiting.
+__device__ __forceinline__ void wait(const LoraParams &p, uint32_t bar, uint32_t parity, volatile int &abort) {
+    for (unsigned i = 0;; ++i) {
+        uint32_t ok;
+        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity), "r"(1000u)
+                     : "memory");
+        if (ok || abort) return;
+        if (i >= kSpin) {
+            atomicOr(p.status, 0x474B0001u);
+            abort = 1;
+            return;
+        }
+    }
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory"); }
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
+template <typename T, int MT>
+struct UpMany {
+    static constexpr int kTok = 64, kOut = 128, kRank = 16 * MT, kSteps = MT * Terms<T>::n;  // of 16 along K
+    static constexpr int kU = (kSteps + 3) / 4 * kTok * 128, kB = kOut * 128;  // 64 along K to a row of 128 bytes
+    static constexpr int kYRow = kOut * 4 + 16, kY = kTok * kYRow;  // of y, a token's 128 outputs
+    static constexpr int kStages = 2;
+    static constexpr int oB = kU, oY = oB + kB, oBack = oY + kStages * kY, kSmem = oBack + kTok * 4 + 1024;  // (the atoms start on 1024 bytes)
+    static constexpr int kBlocks = 2;
+    static constexpr uint32_t kDesc = (1u << 4) | (std::is_same<T, __nv_bfloat16>::value ? 1u << 7 | 1u << 10 : 0u) | (uint32_t)(kTok >> 3) << 17 |
+                                      (uint32_t)(kOut >> 4) << 24;
+    static_assert(kSmem <= 228 * 1024 / kBlocks - 2048, "shared memory");
+};
+constexpr int kManyThreads = kThreads + 32;
+
+// Eight warps compute: warp w has outputs 32 (w % 4) .. of a tile and tokens 32 (w / 4) .. of the piece. A ninth brings tiles of y by bulk
+// copies, a row to each, and takes the results back from the same place. (BULK: rows start on 16 bytes. Else the eight read
+// and write y themselves.) Ranks beyond kRank are summed in tensor memory, with u made anew for every tile.
+template <typename T, int MT, bool BULK>
+__global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_up_many_kernel(const __grid_constant__ LoraParams p) {
+    using S = UpMany<T, MT>;
+    extern __shared__ uint8_t smem_many[];
+    __shared__ uint64_t s_bars[1 + 2 * S::kStages];  // products done, y there, results there
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31, mat = blockIdx.z;
+    const float *y = p.d.y[mat];
+    float *yo = p.d.y_out[mat];
+    const int out = p.d.out[mat], t0 = blockIdx.y * p.runs, tiles = min((out + S::kOut - 1) / S::kOut - t0, p.runs);  // of outputs
+    const Piece q = tiles > 0 ? find_piece<S::kTok>(p, blockIdx.x, y == yo, warp, lane, false) : Piece{};
+    if (!q.n) {
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");  // every block: what follows this kernel also follows the one before it
+        return;
+    }
+    uint8_t *const smem = smem_many + (1024 - (smem_u32(smem_many) & 1023)) % 1024;
+    float *const back = reinterpret_cast<float *>(smem + S::oBack);
+    const uint32_t done = smem_u32(s_bars), full = done + 8, ready = full + 8 * S::kStages, base = smem_u32(smem);
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&s_tmem)), "r"(S::kTok));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
+    }
+    if (tid == 0) {
+        s_abort = 0;
+        for (int i = 0; i < 1 + 2 * S::kStages; ++i)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(done + 8 * i), "r"(i < 1 + S::kStages ? 1 : kWarps));
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const int64_t yo_st = p.d.y_out_stride[mat], y_st = p.d.y_stride[mat];
+    if (warp == kWarps) {
+        if (BULK) {
+            auto bytes = [&](int i) { return 4u * (uint32_t)min(S::kOut, out - (t0 + i) * S::kOut); };
+            auto at = [&](int i, int t) { return base + S::oY + i % S::kStages * S::kY + t * S::kYRow; };
+            auto load = [&](int i) {
+                const uint32_t n = bytes(i), bar = full + i % S::kStages * 8;
+                if (lane == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(n * q.n) : "memory");
+                __syncwarp();
+                for (int t = lane; t < q.n; t += 32)
+                    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(at(i, t)),
+                                 "l"(y + (int64_t)(q.first + t) * y_st + (int64_t)(t0 + i) * S::kOut), "r"(n), "r"(bar)
+                                 : "memory");
+            };
+            for (int i = 0; i < S::kStages && i < tiles; ++i) load(i);
+#pragma unroll 1
+            for (int i = 0; i < tiles; ++i) {
+                wait(p, ready + i % S::kStages * 8, (uint32_t)(i / S::kStages) & 1, s_abort);
+                for (int t = lane; t < q.n; t += 32)
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(
+                                     yo + (int64_t)(q.first + t) * yo_st + (int64_t)(t0 + i) * S::kOut),
+                                 "r"(at(i, t)), "r"(bytes(i))
+                                 : "memory");
+                asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+                if (i + S::kStages < tiles) {
+                    asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+                    __syncwarp();
+                    load(i + S::kStages);
+                }
+            }
+            asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+        }
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    } else {
+        const uint16_t *B = static_cast<const uint16_t *>(p.d.b[mat]) + (int64_t)max(q.adapter, 0) * out * p.d.rank;
+        const bool vec_b = p.d.rank % 8 == 0 && (reinterpret_cast<uintptr_t>(p.d.b[mat]) & 15) == 0;
+        const int chunks = (q.rank + S::kRank - 1) / S::kRank;
+        uint32_t par = 0;
+        // 128 rows of B, 8 ranks at a time, zeros where there is nothing
+        auto fill = [&](int tile, int chunk) {
+            const int r0 = chunk * S::kRank, rank = min(S::kRank, q.rank - r0);
+#pragma unroll 1
+            for (int i = tid; i < S::kOut * 2 * MT; i += kThreads) {
+                const int row = i / (2 * MT), r = i % (2 * MT) * 8, o = (t0 + tile) * S::kOut + row, n = o < out ? rank - r : 0;
+                const uint32_t to = base + S::oB + swizzled(row, r * 2);
+                const uint16_t *from = B + (n > 0 ? (int64_t)o * p.d.rank + r0 + r : 0);
+                if (n >= 8 && vec_b) {
+                    copy16(to, from, true);
+                } else {
+                    const uint4 v = load_a(from, n);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+                }
+            }
+            copies_sent();
+        };
+        auto make_u = [&](int chunk) {
+            gather_u<T, S::kRank>(p, q, mat, chunk * S::kRank, S::kTok, back, chunks > 1, [&](int k, int t, int r, uint2 w) {
+                const int at = k * S::kRank + r;  // along K
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};\n" ::"r"(base + (at >> 6) * (S::kTok * 128) + swizzled(t, (at & 63) * 2)), "r"(w.x), "r"(w.y)
+                             : "memory");
+            });
+        };
+        // What was filled is there, and all eight warps have read the products before.
+        auto issue = [&](bool more) {
+            copies_landed<0>();
+            fence_async();
+            fence_before();
+            bar_sync(1, kThreads);
+            if (warp) return;
+            fence_after();
+            const uint64_t a = desc_sw128(base + S::oB), b = desc_sw128(base);
+            const uint32_t d = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
+#pragma unroll
+            for (int k = 0; k < S::kSteps; ++k) {  // the smallest terms first
+                const int at = S::kSteps - MT + k % MT - k / MT * MT;
+                mma_ss(d, a + (uint64_t)((k % MT) * 32 >> 4), b + (uint64_t)(((at >> 2) * (S::kTok * 128) + (at & 3) * 32) >> 4), S::kDesc, more || k);
+            }
+            mma_commit(done);
+        };
+        auto products = [&]() {
+            wait(p, done, par, s_abort);
+            par ^= 1;
+            fence_after();
+        };
+        // One power of two for all of a token's ranks, where they come in chunks.
+        auto scale_all = [&]() {
+            uint32_t *top = reinterpret_cast<uint32_t *>(back);
+            for (int i = tid; i < S::kTok; i += kThreads) top[i] = 0;
+            bar_sync(1, kThreads);
+            const float *from = p.u + ((int64_t)mat * p.splits * p.d.n_tokens + q.first) * p.u_row;
+            const int64_t next = (int64_t)p.d.n_tokens * p.u_row;
+            for (int i = tid; i < q.n * chunks * S::kRank; i += kThreads) {
+                const int t = i / (chunks * S::kRank), r = i - t * chunks * S::kRank;
+                float x = 0.0f;
+                for (int k = 0; k < p.splits; ++k) x += __ldcg(from + k * next + (int64_t)t * p.u_row + r);
+                atomicMax(&top[t], magnitude(x));
+            }
+            bar_sync(1, kThreads);
+            for (int i = tid; i < S::kTok; i += kThreads) back[i] = back_of(top[i]);
+            bar_sync(1, kThreads);
+        };
+        // Every chunk of a tile whose ranks are many, but for the last one's wait.
+        auto all_chunks = [&](int tile) {
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                if (c) products();
+                fill(tile, c);
+                make_u(c);
+                issue(c > 0);
+            }
+        };
+        if (chunks == 1) fill(0, 0);
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        if (std::is_same<T, __half>::value && chunks > 1) scale_all();
+        if (chunks == 1) make_u(0), issue(false);
+        else all_chunks(0);
+        const int tok0 = 32 * (warp >> 2), toks = min(32, q.n - tok0);
+        const uint32_t from = base + S::oY + tok0 * S::kYRow + (32 * (warp & 3) + lane) * 4;
+#pragma unroll 1
+        for (int i = 0; i < tiles; ++i) {
+            if (chunks) products();
+            if (chunks == 1 && i + 1 < tiles) fill(i + 1, 0);
+            const int o = (t0 + i) * S::kOut + 32 * (warp & 3) + lane;
+            const uint32_t mine = from + i % S::kStages * S::kY;
+            if (BULK) wait(p, full + i % S::kStages * 8, (uint32_t)(i / S::kStages) & 1, s_abort);
+            const float *src = y + (int64_t)(q.first + min(tok0, q.n - 1)) * y_st + min(o, out - 1);  // (what is not there: the last one again)
+            float *dst = yo + (int64_t)(q.first + tok0) * yo_st + o;
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+                if (BULK && !chunks) continue;  // y goes back as it came
+                float d[16] = {}, v[16];
+                if (chunks) tmem_ld16(s_tmem + ((uint32_t)(32 * (warp & 3)) << 16) + tok0 + h, d);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    if (BULK) {
+                        asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v[k]) : "r"(mine + (h + k) * S::kYRow));
+                    } else {
+                        asm volatile("ld.global.cs.f32 %0, [%1];\n" : "=f"(v[k]) : "l"(src));
+                        if (h + k + 1 < toks) src += y_st;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                    if (!chunks) continue;
+                    if (std::is_same<T, __half>::value) {
+                        const float4 f = *reinterpret_cast<const float4 *>(back + tok0 + h + k);
+                        v[k] = fmaf(d[k], f.x, v[k]), v[k + 1] = fmaf(d[k + 1], f.y, v[k + 1]);
+                        v[k + 2] = fmaf(d[k + 2], f.z, v[k + 2]), v[k + 3] = fmaf(d[k + 3], f.w, v[k + 3]);
+                    } else {
+                        v[k] += d[k], v[k + 1] += d[k + 1], v[k + 2] += d[k + 2], v[k + 3] += d[k + 3];
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    if (BULK) {
+                        asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(mine + (h + k) * S::kYRow), "f"(v[k]) : "memory");
+                    } else {
+                        if (h + k < toks && o < out) *dst = v[k];
+                        dst += yo_st;
+                    }
+                }
+            }
+            if (BULK) {
+                fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ready + i % S::kStages * 8);
+            }
+            if (i + 1 < tiles) {
+                if (chunks == 1) issue(false);
+                else if (chunks) all_chunks(i + 1);
+            }
+        }
+        fence_before();
+    }
+    __syncthreads();
+    if (warp == 0) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(s_tmem), "r"(S::kTok));
+    }
+}
+
 // ---------------------------------------------------------------------- host --
 template <typename T, int XK, int MT, int NT, int WT, bool VEC>
 int launch_down(const LoraParams &p, cudaStream_t st) {
@@ -582,25 +943,18 @@ int launch_down(const LoraParams &p, cudaStream_t st) {
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? CQ_OK : set_error(CQ_ERR_CUDA, "adapter launch: %s", cudaGetErrorString(e));
 }
-template <typename T, int MT, int TOK, bool FEW>
-int launch_up(LoraParams &p, cudaStream_t st) {
-    using S = Up<MT, TOK, FEW>;
-    auto k = lora_up_kernel<T, MT, TOK, FEW>;
-    if (S::kSmem > 48 * 1024) {
-        const int rc = ensure_smem(reinterpret_cast<const void *>(k), S::kSmem);
+// The kernel of the second product behind the first's: begun before that one has ended.
+template <typename K>
+int launch_after(K k, const LoraParams &p, dim3 grid, int threads, int smem, cudaStream_t st) {
+    if (smem > 48 * 1024) {
+        const int rc = ensure_smem(reinterpret_cast<const void *>(k), smem);
         if (rc) return rc;
     }
-    int groups = 1;
-    for (int j = 0; j < p.d.n_mats; ++j) groups = std::max(groups, (p.d.out[j] + 31) / 32);
-    // Runs of outputs of a warp: one, and more while that leaves every SM four blocks.
-    p.runs = 1;
-    while (p.runs < 8 && (long long)p.pieces * p.d.n_mats * ((groups + 2 * kWarps * p.runs - 1) / (2 * kWarps * p.runs)) >= 4ll * sm_count()) p.runs *= 2;
-    const int rows = (groups + kWarps * p.runs - 1) / (kWarps * p.runs);
-    if (rows > 65535) return set_error(CQ_ERR_SHAPE, "%d outputs are too many", groups * 32);
+    if (grid.y > 65535) return set_error(CQ_ERR_SHAPE, "too many outputs for one call");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.pieces, (unsigned)rows, (unsigned)p.d.n_mats);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -613,6 +967,28 @@ int launch_up(LoraParams &p, cudaStream_t st) {
     cudaGetLastError();
     return set_error(CQ_ERR_CUDA, "adapter launch: %s", cudaGetErrorString(e));
 }
+template <typename T, int MT>
+int launch_up(LoraParams &p, cudaStream_t st) {
+    int widest = 1;
+    for (int j = 0; j < p.d.n_mats; ++j) widest = std::max(widest, p.d.out[j]);
+    const int tile = p.few ? 32 * kWarps : UpMany<T, MT>::kOut, tiles = (widest + tile - 1) / tile;
+    const long long pieces = p.few ? p.pieces : std::min<long long>(p.d.n_tokens, (long long)p.d.n_seqs + p.d.n_tokens / UpMany<T, MT>::kTok);
+    const long long room = (long long)sm_count() * (p.few ? Up<T, MT>::kBlocks : UpMany<T, MT>::kBlocks);
+    // Tiles that a block takes after another: a block's beginning costs about as much as two, and blocks that do not fit wait for others.
+    long long best = LLONG_MAX;
+    p.runs = 1;
+    for (int r = 1; r <= tiles; r *= 2) {
+        const long long waves = (pieces * p.d.n_mats * ((tiles + r - 1) / r) + room - 1) / room, cost = waves * (r + 2);
+        if (cost < best) best = cost, p.runs = r;
+    }
+    if (const char *e = getenv("LORA_R")) p.runs = atoi(e);
+    const dim3 grid((unsigned)pieces, (unsigned)((tiles + p.runs - 1) / p.runs), (unsigned)p.d.n_mats);
+    if (p.few) return launch_after(lora_up_kernel<T, MT>, p, grid, kThreads, Up<T, MT>::kSmem, st);
+    bool bulk = true;
+    for (int j = 0; j < p.d.n_mats; ++j) bulk = bulk && p.vec_y[j];
+    return bulk ? launch_after(lora_up_many_kernel<T, MT, true>, p, grid, kManyThreads, UpMany<T, MT>::kSmem, st)
+                : launch_after(lora_up_many_kernel<T, MT, false>, p, grid, kManyThreads, UpMany<T, MT>::kSmem, st);
+}
 
 template <typename T, int XK, int MT, bool VEC>
 int launch_r(LoraParams &p, cudaStream_t st) {
@@ -621,7 +997,7 @@ int launch_r(LoraParams &p, cudaStream_t st) {
     if (VEC && p.few) rc = launch_down<T, XK, MT, 1, 1, true>(p, st);
     else rc = launch_down<T, XK, MT, NT, WT, VEC>(p, st);
     if (rc) return rc;
-    return p.few ? launch_up<T, MT, 8, true>(p, st) : launch_up<T, MT, 8 * NT * WT, false>(p, st);
+    return launch_up<T, MT>(p, st);
 }
 template <typename T, int XK, bool VEC>
 int launch_x(LoraParams &p, cudaStream_t st) {

@@ -281,13 +281,14 @@ def test_lora_types(C, w, x, new):
 def test_lora_ranks(C, rank):
     for new in ([1, 1, 1], [70, 2]):
         who = [i % 2 for i in range(len(new))]
-        for w, x in ((BF16, F32), (F16, I8), (BF16, BF16)):
-            kw = _lora_inputs(new, who, 160, (96, 33), rank, w, x, seed=rank)
+        for w, x, outs in ((BF16, F32, (96, 33)), (F16, I8, (96, 33)), (BF16, BF16, (300,)), (F16, F16, (300,))):
+            kw = _lora_inputs(new, who, 160, outs, rank, w, x, seed=rank)
             a, b = _check_lora(C, kw), _check_lora(C, kw, True)
             assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
-@pytest.mark.parametrize("n_in,out", [(1, 1), (7, 5), (8, 4), (31, 33), (32, 32), (40, 64), (1000, 777), (1001, 100), (2048, 36), (520, 2052), (6000, 4100)])
+@pytest.mark.parametrize("n_in,out", [(1, 1), (7, 5), (8, 4), (31, 33), (32, 32), (40, 64), (1000, 777), (1001, 100), (2048, 36), (520, 2052), (6000, 4100), (136, 128),
+                                        (264, 129), (72, 1000)])
 @pytest.mark.parametrize("x", [F32, I8, F16])
 def test_lora_sizes(C, n_in, out, x):
     _check_lora(C, _lora_inputs([1, 2, 1], [0, 1, 0], n_in, (out,), 8, F16, x, seed=n_in))
@@ -329,6 +330,17 @@ def test_lora_rows_behind_the_last_request_stay(C):
     y = kw["ys"][0].clone()
     C.cq_lora_add(**kw)
     assert torch.equal(kw["ys"][0][:4], y[:4]) and torch.equal(kw["ys"][0][9:], y[9:]) and not torch.equal(kw["ys"][0][4:9], y[4:9])
+
+
+def test_lora_values_of_every_size(C):
+    """The terms of the second product hold large and small values side by side: tokens of any scale, ranks of any scale."""
+    for w in (F16, BF16):
+        for new in ([2, 3], [70, 40]):
+            for rank in (16, 40, 130):
+                kw = _lora_inputs(new, [0, 1], 128, (140,), rank, w, F32, seed=rank)
+                kw["x"] *= torch.exp2(torch.linspace(-60, 60, sum(new), device="cuda"))[:, None]
+                kw["a"][0] *= torch.exp2(-(torch.arange(rank, device="cuda") % 9).float())[None, :, None].to(w)
+                _check_lora(C, kw)
 
 
 def test_lora_without_anything(C):
