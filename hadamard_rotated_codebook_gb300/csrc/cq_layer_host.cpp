@@ -17,8 +17,8 @@ bool is_float(int type) { return type >= CQ_T_F32 && type <= CQ_T_BF16; }
 bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 // How a call is cut up, apart from its alignment; the workspace's bytes, or 0.
-size_t lora_plan(const cq_lora_desc &d, bool few, LoraParams &p) {
-    const int tiles = lora_rank_tiles(d.rank), ranks = 16 * tiles, tok = lora_tokens(d.x_dtype, tiles, few);
+size_t lora_plan(const cq_lora_desc &d, bool few, bool vec, LoraParams &p) {
+    const int tiles = lora_rank_tiles(d.rank), ranks = 16 * tiles, tok = lora_tokens(d.x_dtype, tiles, few, vec);
     const long long pieces = std::min<long long>(d.n_tokens, (long long)d.n_seqs + d.n_tokens / tok);
     p.few = few;
     p.u_row = (d.rank + ranks - 1) / ranks * ranks;
@@ -73,6 +73,7 @@ static int check_lora(const cq_lora_desc *d) {
     if (d->n_mats < 0 || d->n_mats > CQ_LORA_MAX_MATS)
         return set_error(CQ_ERR_SHAPE, "at most %d matrices, got %d", CQ_LORA_MAX_MATS, d->n_mats);
     if (d->n_tokens < 0 || d->n_seqs < 0 || d->n_adapters < 0) return set_error(CQ_ERR_SHAPE, "negative size");
+    if (d->rank > 0 && d->n_adapters > INT_MAX / d->rank) return set_error(CQ_ERR_SHAPE, "%d adapters of rank %d are too many", d->n_adapters, d->rank);
     if (d->in < 1 || d->in > kMaxSide) return set_error(CQ_ERR_SHAPE, "in must be 1..%d, got %d", kMaxSide, d->in);
     if (d->rank < 1 || d->rank > CQ_LORA_MAX_RANK) return set_error(CQ_ERR_SHAPE, "rank must be 1..%d, got %d", CQ_LORA_MAX_RANK, d->rank);
     for (int j = 0; j < d->n_mats; ++j)
@@ -84,8 +85,8 @@ size_t cq_lora_workspace(const cq_lora_desc *d) {
     clear_error();
     LoraParams p;
     if (check_lora(d) || !d->n_mats || !d->n_tokens || !d->n_seqs) return 0;
-    const size_t many = lora_plan(*d, false, p);
-    return many && lora_few(*d) ? std::max(many, lora_plan(*d, true, p)) : many;
+    const size_t plain = lora_plan(*d, false, false, p), many = lora_plan(*d, false, true, p), few = lora_few(*d) ? lora_plan(*d, true, true, p) : 0;
+    return plain && many ? std::max(plain, std::max(many, few)) : 0;
 }
 
 int cq_lora_add(const cq_lora_desc *d, void *stream) {
@@ -107,16 +108,16 @@ int cq_lora_add(const cq_lora_desc *d, void *stream) {
     LoraParams p;
     p.d = *d;
     // Where 16-byte loads (8 of int8) and 16-byte accesses to y may be used; single elements elsewhere.
-    const int size = d->x_dtype == CQ_T_F32 ? 4 : d->x_dtype == CQ_T_I8 ? 1 : 2, run = d->x_dtype == CQ_T_I8 ? 8 : 16;
-    p.vec = d->in % 8 == 0 && aligned(d->x, run) && (d->n_tokens == 1 || d->x_stride * size % run == 0);
+    const int size = d->x_dtype == CQ_T_F32 ? 4 : d->x_dtype == CQ_T_I8 ? 1 : 2, run = d->x_dtype == CQ_T_I8 && lora_few(*d) ? 8 : 16;
+    p.vec = d->in % 8 == 0 && d->n_adapters && aligned(d->x, run) && (d->n_tokens == 1 || (d->x_stride * size % run == 0 && d->x_stride >= d->in));
     p.vec_b = d->rank % 4 == 0;
     for (int j = 0; j < d->n_mats; ++j) {
         p.vec = p.vec && aligned(d->a[j], 16);
         p.vec_b = p.vec_b && aligned(d->b[j], 8);
         p.vec_y[j] = d->out[j] % 4 == 0 && aligned(d->y[j], 16) && aligned(d->y_out[j], 16) &&
-                     (d->n_tokens == 1 || (d->y_stride[j] % 4 == 0 && d->y_out_stride[j] % 4 == 0));
+                     (d->n_tokens == 1 || (d->y_stride[j] % 4 == 0 && d->y_stride[j] >= d->out[j] && d->y_out_stride[j] % 4 == 0));
     }
-    const size_t need = lora_plan(*d, p.vec && lora_few(*d), p);
+    const size_t need = lora_plan(*d, p.vec && lora_few(*d), p.vec, p);
     if (!need) return CQ_ERR_SHAPE;
     if (!d->workspace || d->workspace_bytes < need || !aligned(d->workspace, 16))
         return set_error(CQ_ERR_ARG, "workspace of %zu bytes needed (16-byte aligned), got %zu", need, d->workspace ? d->workspace_bytes : 0);

@@ -20,6 +20,7 @@
 // terms of bf16 or two of fp16 (Terms).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, (Down<XK, MT, NT, WT>::kBlocks)) lor
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int cut = blockIdx.x % p.splits, mat = blockIdx.y, r0 = blockIdx.z * S::kRank;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    const Piece q = find_piece<S::kTok>(p, blockIdx.x / p.splits, true, warp, lane, blockIdx.x + blockIdx.y + blockIdx.z == 0);
+    const Piece q = search_piece<S::kTok>(p, blockIdx.x / p.splits, true, lane, blockIdx.x + blockIdx.y + blockIdx.z + warp == 0);
     const int rank = min(S::kRank, q.rank - r0), n_in = p.d.in;
     if (!q.n || rank <= 0) return;
     const int wk = warp / WT, wt = warp % WT;
@@ -696,6 +697,11 @@ __device__ __forceinline__ void wait(const LoraParams &p, uint32_t bar, uint32_t
     }
 }
 
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst), "l"(map),
+                 "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
@@ -704,7 +710,7 @@ template <typename T, int MT>
 struct UpMany {
     static constexpr int kTok = 64, kOut = 128, kRank = 16 * MT, kSteps = MT * Terms<T>::n;  // of 16 along K
     static constexpr int kU = (kSteps + 3) / 4 * kTok * 128, kB = kOut * 128;  // 64 along K to a row of 128 bytes
-    static constexpr int kYRow = kOut * 4 + 16, kY = kTok * kYRow;  // of y, a token's 128 outputs
+    static constexpr int kYRow = kOut * 4, kY = kTok * kYRow;  // of y, a token's 128 outputs
     static constexpr int kStages = 2;
     static constexpr int oB = kU, oY = oB + kB, oBack = oY + kStages * kY, kSmem = oBack + kTok * 4 + 1024;  // (the atoms start on 1024 bytes)
     static constexpr int kBlocks = 2;
@@ -713,12 +719,16 @@ struct UpMany {
     static_assert(kSmem <= 228 * 1024 / kBlocks - 2048, "shared memory");
 };
 constexpr int kManyThreads = kThreads + 32;
+// y and y_out as tensor maps: boxes of 128 outputs x 64 tokens.
+struct UpMaps {
+    CUtensorMap in[CQ_LORA_MAX_MATS], out[CQ_LORA_MAX_MATS];
+};
 
-// Eight warps compute: warp w has outputs 32 (w % 4) .. of a tile and tokens 32 (w / 4) .. of the piece. A ninth brings tiles of y by bulk
-// copies, a row to each, and takes the results back from the same place. (BULK: rows start on 16 bytes. Else the eight read
-// and write y themselves.) Ranks beyond kRank are summed in tensor memory, with u made anew for every tile.
+// Eight warps compute: warp w has outputs 32 (w % 4) .. of a tile and tokens 32 (w / 4) .. of the piece. A ninth brings tiles of y by tensor
+// copies and takes the results back from the same place. (BULK: rows start on 16 bytes. Else the eight read and write y themselves.) Ranks beyond kRank are summed in tensor memory, with u made anew for every tile.
 template <typename T, int MT, bool BULK>
-__global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_up_many_kernel(const __grid_constant__ LoraParams p) {
+__global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_up_many_kernel(const __grid_constant__ LoraParams p,
+                                                                                               const __grid_constant__ UpMaps maps) {
     using S = UpMany<T, MT>;
     extern __shared__ uint8_t smem_many[];
     __shared__ uint64_t s_bars[1 + 2 * S::kStages];  // products done, y there, results there
@@ -752,26 +762,32 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
     const int64_t yo_st = p.d.y_out_stride[mat], y_st = p.d.y_stride[mat];
     if (warp == kWarps) {
         if (BULK) {
-            auto bytes = [&](int i) { return 4u * (uint32_t)min(S::kOut, out - (t0 + i) * S::kOut); };
-            auto at = [&](int i, int t) { return base + S::oY + i % S::kStages * S::kY + t * S::kYRow; };
+            // A copy reads whole tiles (rows of the next piece among them) and writes only what is the piece's: a piece of fewer tokens row by row.
+            const bool whole = q.n == S::kTok;
             auto load = [&](int i) {
-                const uint32_t n = bytes(i), bar = full + i % S::kStages * 8;
-                if (lane == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(n * q.n) : "memory");
-                __syncwarp();
-                for (int t = lane; t < q.n; t += 32)
-                    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(at(i, t)),
-                                 "l"(y + (int64_t)(q.first + t) * y_st + (int64_t)(t0 + i) * S::kOut), "r"(n), "r"(bar)
-                                 : "memory");
+                if (lane == 0) {
+                    const uint32_t bar = full + i % S::kStages * 8;
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(S::kY) : "memory");
+                    tma_load(base + S::oY + i % S::kStages * S::kY, &maps.in[mat], (t0 + i) * S::kOut, q.first, bar);
+                }
             };
             for (int i = 0; i < S::kStages && i < tiles; ++i) load(i);
 #pragma unroll 1
             for (int i = 0; i < tiles; ++i) {
                 wait(p, ready + i % S::kStages * 8, (uint32_t)(i / S::kStages) & 1, s_abort);
-                for (int t = lane; t < q.n; t += 32)
-                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(
-                                     yo + (int64_t)(q.first + t) * yo_st + (int64_t)(t0 + i) * S::kOut),
-                                 "r"(at(i, t)), "r"(bytes(i))
-                                 : "memory");
+                const uint32_t from = base + S::oY + i % S::kStages * S::kY;
+                const int o = (t0 + i) * S::kOut;
+                if (whole) {
+                    if (lane == 0)
+                        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(&maps.out[mat]), "r"(o), "r"(q.first),
+                                     "r"(from)
+                                     : "memory");
+                } else {
+                    for (int t = lane; t < q.n; t += 32)
+                        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(yo + (int64_t)(q.first + t) * yo_st + o),
+                                     "r"(from + t * S::kYRow), "r"(4 * min(S::kOut, out - o))
+                                     : "memory");
+                }
                 asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
                 if (i + S::kStages < tiles) {
                     asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
@@ -930,6 +946,136 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
     }
 }
 
+// The first product on tcgen05: 128 tokens are the M side, the ranks the N side, 64 inputs a stage. One warp brings stages by tensor copies, one
+// issues; four read the sums back, and turn int8 stages into the weights' type before that.
+struct DownMaps {
+    CUtensorMap x, a[CQ_LORA_MAX_MATS];
+};
+template <typename T, int XK, int MT>
+struct DownMany {
+    static constexpr int kTok = 128, kRank = 16 * MT, kIn = 64;
+    static constexpr int kX = kTok * 128, kA = kRank * 128, kRaw = XK == CQ_T_I8 ? kTok * 64 : 0, kStage = kX + kA + kRaw;
+    static constexpr int kBlocks = 2, kRoom = 228 * 1024 / kBlocks - 2048 - 1024;  // (stages start on 1024 bytes)
+    static constexpr int kDepth = kRoom / kStage < 6 ? kRoom / kStage : 6, kSmem = kDepth * kStage + 1024;
+    static constexpr int kCols = kRank < 32 ? 32 : kRank;
+    static constexpr uint32_t kDesc = (1u << 4) | (std::is_same<T, __nv_bfloat16>::value ? 1u << 7 | 1u << 10 : 0u) | (uint32_t)(kRank >> 3) << 17 |
+                                      (uint32_t)(kTok >> 4) << 24;
+    static_assert(kDepth >= 2, "shared memory");
+};
+constexpr int kDownThreads = 192;
+
+template <typename T, int XK, int MT>
+__global__ void __launch_bounds__(kDownThreads, (DownMany<T, XK, MT>::kBlocks)) lora_down_many_kernel(const __grid_constant__ LoraParams p,
+                                                                                                     const __grid_constant__ DownMaps maps) {
+    using S = DownMany<T, XK, MT>;
+    extern __shared__ uint8_t smem_down[];
+    __shared__ uint64_t s_bars[3 * S::kDepth + 1];  // stages there, turned, free; the sums done
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
+    const int cut = blockIdx.x % p.splits, mat = blockIdx.y, r0 = blockIdx.z * S::kRank;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const Piece q = find_piece<S::kTok>(p, blockIdx.x / p.splits, true, warp, lane, blockIdx.x + blockIdx.y + blockIdx.z == 0);
+    const int rank = min(S::kRank, q.rank - r0);
+    if (!q.n || rank <= 0) return;
+    const int chunks = (p.d.in + S::kIn - 1) / S::kIn, c0 = (int)((long long)chunks * cut / p.splits), n = (int)((long long)chunks * (cut + 1) / p.splits) - c0;
+    const uint32_t base = (smem_u32(smem_down) + 1023) & ~1023u, full = smem_u32(s_bars), turned = full + 8 * S::kDepth, empty = turned + 8 * S::kDepth,
+                   done = empty + 8 * S::kDepth;
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&s_tmem)), "r"(S::kCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
+    }
+    if (tid == 0) {
+        s_abort = 0;
+        for (int i = 0; i < 3 * S::kDepth + 1; ++i)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(full + 8 * i), "r"(i >= S::kDepth && i < 2 * S::kDepth ? 4 : 1));
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 0) {
+        if (lane == 0) {
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                const int st = i % S::kDepth;
+                const uint32_t at = base + st * S::kStage, bar = full + 8 * st;
+                if (i >= S::kDepth) wait(p, empty + 8 * st, (uint32_t)(i / S::kDepth - 1) & 1, s_abort);
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"((XK == CQ_T_I8 ? S::kRaw : S::kX) + S::kA) : "memory");
+                tma_load(XK == CQ_T_I8 ? at + S::kX + S::kA : at, &maps.x, (c0 + i) * S::kIn, q.first, bar);
+                tma_load(at + S::kX, &maps.a[mat], (c0 + i) * S::kIn, q.adapter * p.d.rank + r0, bar);
+            }
+        }
+    } else if (warp == 1) {
+        const uint32_t d = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const int st = i % S::kDepth;
+            const uint32_t par = (uint32_t)(i / S::kDepth) & 1;
+            wait(p, full + 8 * st, par, s_abort);
+            if (XK == CQ_T_I8) wait(p, turned + 8 * st, par, s_abort);
+            __syncwarp();
+            fence_after();
+            const uint64_t a = desc_sw128(base + st * S::kStage), b = desc_sw128(base + st * S::kStage + S::kX);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_ss(d, a + (uint64_t)(k * 32 >> 4), b + (uint64_t)(k * 32 >> 4), S::kDesc, (i | k) != 0);
+            mma_commit(empty + 8 * st);
+        }
+        mma_commit(done);
+    } else {
+        const int row = 32 * (warp & 3) + lane;
+        if (XK == CQ_T_I8) {
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {  // a token to a thread
+                const int st = i % S::kDepth;
+                const uint32_t to = base + st * S::kStage, from = to + S::kX + S::kA + row * 64;
+                wait(p, full + 8 * st, (uint32_t)(i / S::kDepth) & 1, s_abort);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 v = lds16(from + ((j ^ (row >> 1 & 3)) << 4));  // 16 inputs, 64-byte swizzled
+                    uint32_t w[4];
+                    const uint32_t lo[2] = {v.x, v.y}, hi[2] = {v.z, v.w};
+                    pairs_of_i8<T>(lo, w);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to + swizzled(row, 32 * j)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                 : "memory");
+                    pairs_of_i8<T>(hi, w);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to + swizzled(row, 32 * j + 16)), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                                 "r"(w[3])
+                                 : "memory");
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(turned + 8 * st);
+            }
+        }
+        float scale = p.d.scales ? p.d.scales[q.adapter] : 1.0f, own = 1.0f;
+        if (XK == CQ_T_I8) own = p.d.x_scale[q.first + min(row, q.n - 1)];
+        wait(p, done, 0, s_abort);
+        fence_after();
+        float *u = p.u + (((int64_t)mat * p.splits + cut) * p.d.n_tokens + q.first + row) * p.u_row + r0;
+#pragma unroll
+        for (int h = 0; h < S::kRank; h += 16) {
+            float v[16];
+            tmem_ld16(s_tmem + ((uint32_t)(32 * (warp & 3)) << 16) + h, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                if (XK == CQ_T_I8) v[j] *= own;
+                v[j] = h + j < rank ? v[j] * scale : 0.0f;  // ranks that are not there hold what other rows gave
+            }
+            if (row < q.n) {
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4 *>(u + h + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            }
+        }
+        fence_before();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(s_tmem), "r"(S::kCols));
+    }
+}
+
 // ---------------------------------------------------------------------- host --
 template <typename T, int XK, int MT, int NT, int WT, bool VEC>
 int launch_down(const LoraParams &p, cudaStream_t st) {
@@ -943,9 +1089,48 @@ int launch_down(const LoraParams &p, cudaStream_t st) {
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? CQ_OK : set_error(CQ_ERR_CUDA, "adapter launch: %s", cudaGetErrorString(e));
 }
+// A tensor map over rows of `width` elements: boxes of box_x x box_y.
+inline int make_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *at, int width, long long rows, int64_t stride, int box_x, int box_y,
+                    CUtensorMapSwizzle swizzle) {
+    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                               const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static Encode fn = nullptr;  // every writer stores the same value
+    if (!fn) {
+        cudaDriverEntryPointQueryResult found;
+        void *f = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess || !f) {
+            cudaGetLastError();
+            return set_error(CQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+        }
+        fn = reinterpret_cast<Encode>(f);
+    }
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * size};
+    const cuuint32_t box[2] = {(cuuint32_t)box_x, (cuuint32_t)box_y}, one[2] = {1, 1};
+    const CUresult r = fn(map, type, 2, const_cast<void *>(at), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? CQ_OK : set_error(CQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+template <typename T, int XK, int MT>
+int launch_down_many(const LoraParams &p, cudaStream_t st) {
+    using S = DownMany<T, XK, MT>;
+    auto k = lora_down_many_kernel<T, XK, MT>;
+    const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    DownMaps maps;
+    int rc = XK == CQ_T_I8 ? make_map(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.d.x, p.d.in, p.d.n_tokens, p.d.x_stride, S::kIn, S::kTok, CU_TENSOR_MAP_SWIZZLE_64B)
+                           : make_map(&maps.x, type, 2, p.d.x, p.d.in, p.d.n_tokens, p.d.x_stride, S::kIn, S::kTok, CU_TENSOR_MAP_SWIZZLE_128B);
+    for (int j = 0; !rc && j < p.d.n_mats; ++j)
+        rc = make_map(&maps.a[j], type, 2, p.d.a[j], p.d.in, (long long)p.d.n_adapters * p.d.rank, p.d.in, S::kIn, S::kRank, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!rc) rc = ensure_smem(reinterpret_cast<const void *>(k), S::kSmem);
+    if (rc) return rc;
+    k<<<dim3(p.pieces * p.splits, p.d.n_mats, p.u_row / S::kRank), kDownThreads, S::kSmem, st>>>(p, maps);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? CQ_OK : set_error(CQ_ERR_CUDA, "adapter launch: %s", cudaGetErrorString(e));
+}
+
 // The kernel of the second product behind the first's: begun before that one has ended.
-template <typename K>
-int launch_after(K k, const LoraParams &p, dim3 grid, int threads, int smem, cudaStream_t st) {
+template <typename K, typename... A>
+int launch_after(K k, dim3 grid, int threads, int smem, cudaStream_t st, const A &...args) {
     if (smem > 48 * 1024) {
         const int rc = ensure_smem(reinterpret_cast<const void *>(k), smem);
         if (rc) return rc;
@@ -961,7 +1146,7 @@ int launch_after(K k, const LoraParams &p, dim3 grid, int threads, int smem, cud
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e == cudaSuccess) return CQ_OK;
     cudaGetLastError();
@@ -983,18 +1168,28 @@ int launch_up(LoraParams &p, cudaStream_t st) {
     }
     if (const char *e = getenv("LORA_R")) p.runs = atoi(e);
     const dim3 grid((unsigned)pieces, (unsigned)((tiles + p.runs - 1) / p.runs), (unsigned)p.d.n_mats);
-    if (p.few) return launch_after(lora_up_kernel<T, MT>, p, grid, kThreads, Up<T, MT>::kSmem, st);
+    if (p.few) return launch_after(lora_up_kernel<T, MT>, grid, kThreads, Up<T, MT>::kSmem, st, p);
+    using S = UpMany<T, MT>;
+    UpMaps maps;
     bool bulk = true;
     for (int j = 0; j < p.d.n_mats; ++j) bulk = bulk && p.vec_y[j];
-    return bulk ? launch_after(lora_up_many_kernel<T, MT, true>, p, grid, kManyThreads, UpMany<T, MT>::kSmem, st)
-                : launch_after(lora_up_many_kernel<T, MT, false>, p, grid, kManyThreads, UpMany<T, MT>::kSmem, st);
+    if (!bulk) return launch_after(lora_up_many_kernel<T, MT, false>, grid, kManyThreads, S::kSmem, st, p, maps);
+    for (int j = 0; j < p.d.n_mats; ++j) {
+        int rc = make_map(&maps.in[j], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.d.y[j], p.d.out[j], p.d.n_tokens, p.d.y_stride[j], S::kOut, S::kTok,
+                          CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (!rc) rc = make_map(&maps.out[j], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.d.y_out[j], p.d.out[j], p.d.n_tokens, p.d.y_out_stride[j], S::kOut, S::kTok,
+                               CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (rc) return rc;
+    }
+    return launch_after(lora_up_many_kernel<T, MT, true>, grid, kManyThreads, S::kSmem, st, p, maps);
 }
 
 template <typename T, int XK, int MT, bool VEC>
 int launch_r(LoraParams &p, cudaStream_t st) {
-    constexpr int WT = lora_warps_along(false), NT = lora_tokens(XK, MT, false) / (8 * WT);
+    constexpr int WT = lora_warps_along(false), NT = lora_tokens(XK, MT, false, false) / (8 * WT);
     int rc;
     if (VEC && p.few) rc = launch_down<T, XK, MT, 1, 1, true>(p, st);
+    else if (VEC && XK != CQ_T_F32) rc = launch_down_many<T, XK == CQ_T_F32 ? CQ_T_F16 : XK, MT>(p, st);
     else rc = launch_down<T, XK, MT, NT, WT, VEC>(p, st);
     if (rc) return rc;
     return launch_up<T, MT>(p, st);

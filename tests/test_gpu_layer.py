@@ -355,6 +355,24 @@ def test_lora_without_anything(C):
     C.cq_device_status()
 
 
+def test_lora_of_many_tokens_without_anything(C):
+    """Prompts of a server that has loaded no adapter, and of requests that have none."""
+    kw = _lora_inputs([200, 90], [-1, -1], 64, (160,), 8, n_adapters=1)
+    none = dict(kw, a=[kw["a"][0][:0]], b=[kw["b"][0][:0]], scales=None)
+    for k in (kw, none):
+        outs = [torch.full_like(kw["ys"][0], 7.0)]
+        assert torch.equal(C.cq_lora_add(**dict(k, outs=outs))[0], kw["ys"][0])
+    C.cq_device_status()
+
+
+def test_lora_shared_rows(C):
+    """One row of x and y for every token (strides of zero)."""
+    kw = _lora_inputs([1, 90], [0, 1], 64, (160,), 8)
+    kw["x"] = kw["x"][:1].expand(91, 64)
+    kw["ys"] = [kw["ys"][0][:1].expand(91, 160)]
+    _check_lora(C, kw)
+
+
 def test_lora_strides(C):
     """Rows of wider tensors, on and off vector boundaries."""
     kw = _lora_inputs([3, 40], [0, 1], 256, (128, 64), 16)
