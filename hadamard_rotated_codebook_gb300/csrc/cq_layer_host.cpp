@@ -1,7 +1,6 @@
 // cq_layer_host.cpp -- host side of the block norm's and the adapters' entry points: argument checks, alignment.
 #include <algorithm>
 #include <climits>
-#include <cstdlib>
 #include <cmath>
 #include <cstdint>
 
@@ -25,7 +24,6 @@ size_t lora_plan(const cq_lora_desc &d, bool few, bool vec, LoraParams &p) {
     // Parts of k: enough for three blocks on every SM, while a block keeps 512 inputs and more.
     p.splits = 1;
     while (p.splits < kMaxSplits && pieces * d.n_mats * p.splits < 3ll * sm_count() && d.in >= 1024 * p.splits) p.splits *= 2;
-    if (const char *e = getenv("LORA_S")) p.splits = atoi(e);
     p.runs = 1;
     if (pieces * p.splits > INT_MAX) {
         set_error(CQ_ERR_SHAPE, "%d tokens of %d requests are too many for one call", d.n_tokens, d.n_seqs);
@@ -34,8 +32,9 @@ size_t lora_plan(const cq_lora_desc &d, bool few, bool vec, LoraParams &p) {
     p.pieces = (int)pieces;
     return (size_t)d.n_mats * p.splits * d.n_tokens * p.u_row * sizeof(float);
 }
-// Requests have few tokens: more pieces of fewer.
-bool lora_few(const cq_lora_desc &d) { return d.n_tokens <= 8ll * d.n_seqs; }
+// Requests have few tokens on average: pieces of 8 then, on mma.sync. (32 requests of 20 tokens, 4096 to 4096, rank 16: 18.7 us against 26; 19 of 0 to
+// 32, 1000 to 777: 7.3 against 11.3. 8 of 40 tokens, two of 2048 to 2048, rank 64: 21 against 16.6.)
+bool lora_few(const cq_lora_desc &d) { return d.n_tokens <= 32ll * d.n_seqs; }
 
 }  // namespace
 

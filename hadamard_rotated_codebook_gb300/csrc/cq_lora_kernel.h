@@ -27,7 +27,6 @@
 
 #include <algorithm>
 #include <climits>
-#include <cstdlib>
 #include <type_traits>
 
 #include "cq_layer.h"
@@ -1154,19 +1153,20 @@ int launch_after(K k, dim3 grid, int threads, int smem, cudaStream_t st, const A
 }
 template <typename T, int MT>
 int launch_up(LoraParams &p, cudaStream_t st) {
-    int widest = 1;
-    for (int j = 0; j < p.d.n_mats; ++j) widest = std::max(widest, p.d.out[j]);
-    const int tile = p.few ? 32 * kWarps : UpMany<T, MT>::kOut, tiles = (widest + tile - 1) / tile;
+    const int tile = p.few ? 32 * kWarps : UpMany<T, MT>::kOut;
     const long long pieces = p.few ? p.pieces : std::min<long long>(p.d.n_tokens, (long long)p.d.n_seqs + p.d.n_tokens / UpMany<T, MT>::kTok);
     const long long room = (long long)sm_count() * (p.few ? Up<T, MT>::kBlocks : UpMany<T, MT>::kBlocks);
+    int tiles = 1;  // of the widest matrix
+    for (int j = 0; j < p.d.n_mats; ++j) tiles = std::max(tiles, (p.d.out[j] + tile - 1) / tile);
     // Tiles that a block takes after another: a block's beginning costs about as much as two, and blocks that do not fit wait for others.
     long long best = LLONG_MAX;
     p.runs = 1;
     for (int r = 1; r <= tiles; r *= 2) {
-        const long long waves = (pieces * p.d.n_mats * ((tiles + r - 1) / r) + room - 1) / room, cost = waves * (r + 2);
+        long long blocks = 0;
+        for (int j = 0; j < p.d.n_mats; ++j) blocks += pieces * (((p.d.out[j] + tile - 1) / tile + r - 1) / r);
+        const long long cost = (blocks + room - 1) / room * (r + 2);
         if (cost < best) best = cost, p.runs = r;
     }
-    if (const char *e = getenv("LORA_R")) p.runs = atoi(e);
     const dim3 grid((unsigned)pieces, (unsigned)((tiles + p.runs - 1) / p.runs), (unsigned)p.d.n_mats);
     if (p.few) return launch_after(lora_up_kernel<T, MT>, grid, kThreads, Up<T, MT>::kSmem, st, p);
     using S = UpMany<T, MT>;
