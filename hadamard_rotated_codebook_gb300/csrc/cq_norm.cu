@@ -13,7 +13,14 @@
 //
 // Codes: y_k = inv * t_k, t_k = r_k (offset + w_k). A product with one positive factor keeps the order of its values, so the
 // largest |y| is inv * max|t|, rounded, and the maximum is reduced together with the sum of squares. Scale and codes then
-// are those of cq_act_quant_int8 over the fp32 y, bit for bit.
+// are those of cq_act_quant_int8 over the fp32 y, bit for bit. A code is the rounded product with the scale's reciprocal, and the rounded
+// quotient only where that lies next to a tie (store_codes): a division per element took 88 us where this takes 61.
+//
+// The bound is memory, and issue slots next to it (two elements to an instruction where there is one for that). 8190 rows of
+// 4096 in fp32 onto bf16 with a norm of the branch, to int8 (302 MB): 61 us, 4.9 TB/s or 73% of the copy rate; 16383 of 2048 in bf16 with
+// a silu gate for every element (336 MB): 70 us, 70%, issue slots at 60%; 8190 of 4096 in bf16 without either: 47 us, 84%. Steps of a
+// few rows take 3 to 5 us, which is two latencies of memory and the launch. Rows of 16384 in fp32 leave the ring one stage (51%).
+// Tried and slower: four runs a lane instead of two (94 against 69 us: half as many warps wait).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -207,8 +214,10 @@ __device__ __forceinline__ void load_weight(const float *w, int n, float offset,
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) t[j] = f2(2 * j < n ? __ldg(w + 2 * j) : 0.0f, 2 * j + 1 < n ? __ldg(w + 2 * j + 1) : 0.0f);
     }
+    if (offset != 0.0f) {
 #pragma unroll
-    for (int j = 0; j < kPairs; ++j) t[j] = f2_add(t[j], f2(offset, offset));
+        for (int j = 0; j < kPairs; ++j) t[j] = f2_add(t[j], f2(offset, offset));
+    }
 }
 
 // 1 / (1 + 2^(-g log2 e)); beyond the range of the power it is 0 or 1.
@@ -222,25 +231,24 @@ __device__ __forceinline__ float open(float g, int act) {
     return act == CQ_GATE_PLAIN ? g : act == CQ_GATE_SIGMOID ? sigmoid(g) : g * sigmoid(g);
 }
 
-// Sum of s and maximum of m over the team. Block teams: one barrier, the warps' parts in a buffer that alternates.
+__device__ __forceinline__ float warp_max(float x) {  // of values that are not below zero: ordered as integers; NaNs are not among them
+    return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x)));
+}
+// Sum of s and maximum of m (not below zero) over the team. Block teams: one barrier, the warps' parts in a buffer that alternates.
 template <bool WARP>
 __device__ __forceinline__ void reduce(float &s, float &m, bool with_max, float2 *buf) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        if (with_max) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    }
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (with_max) m = warp_max(m);
     if (WARP) return;
-    const int warps = blockDim.x >> 5, part = threadIdx.x & (kMaxWarps - 1);
+    const int warps = blockDim.x >> 5, all = 1 << (32 - __clz(warps - 1)), part = threadIdx.x & (all - 1);  // (a block has two warps and more)
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(s, m);
     __syncthreads();
-    const float2 v = part < warps ? buf[part] : make_float2(0.0f, 0.0f);  // both halves of a warp hold them all
-    s = v.x, m = v.y;
-#pragma unroll
-    for (int o = kMaxWarps / 2; o; o >>= 1) {
-        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        if (with_max) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    }
+    const float2 v = part < warps ? buf[part] : make_float2(0.0f, 0.0f);  // every `all` lanes hold them all
+    s = v.x;
+#pragma unroll 1
+    for (int o = all >> 1; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (with_max) m = warp_max(v.y);
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -465,7 +473,7 @@ int launch_block_norm(const cq_norm_desc &d, void *stream) {
     p.stage = p.at_gate + (p.gate && !p.one_gate ? p.d * size_of(p.x_type) : 0);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (d.width <= kWarpRow) {
-        const int per_sm = 6;
+        const int per_sm = chunks <= 64 ? 12 : 6;  // 65536 rows of 512 in bf16: 61 us with 6, 54 with 12; a lane with four runs has registers for 6
         p.depth = std::max(1, std::min(kMaxDepth, ring_bytes(per_sm) / kWarpTeams / p.stage));
         const int grid = (int)std::min<long long>(((long long)p.rows + kWarpTeams - 1) / kWarpTeams, (long long)sms * per_sm);
         if (chunks <= 32) return launch_c<1, true>(p, vec, grid, 32 * kWarpTeams, st);
@@ -473,8 +481,10 @@ int launch_block_norm(const cq_norm_desc &d, void *stream) {
         return launch_c<4, true>(p, vec, grid, 32 * kWarpTeams, st);
     }
     const int ch = chunks <= 2 * 32 * kMaxWarps ? 2 : 4, threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
+    // Blocks of an SM before stages of a block: the prompt of 8190 rows of 4096 takes 61 us with four blocks of two stages, 69 with three of
+    // three, 81 with two of four (the reductions of more rows overlap).
     int per_sm = std::max(1, 1024 / threads);
-    while (per_sm > 1 && ring_bytes(per_sm) / p.stage < 3) --per_sm;
+    while (per_sm > 1 && ring_bytes(per_sm) / p.stage < 2) --per_sm;
     p.depth = std::max(1, std::min(kMaxDepth, ring_bytes(per_sm) / p.stage));
     const int grid = std::min(p.rows, per_sm * sms);
     return ch == 2 ? launch_c<2, false>(p, vec, grid, threads, st) : launch_c<4, false>(p, vec, grid, threads, st);
