@@ -4,7 +4,7 @@
 //   r = residual_scale * res + branch_scale * act(gate) z
 //   y = r / sqrt(mean(r^2) + eps) * (offset + w),   or int8 codes of y with a scale per row
 //
-// A row's second mean needs all of r, so a row stays in registers: a team of lanes (a warp for rows of up to 1024
+// A row's second mean needs all of r, so a row stays in registers: a team of lanes (a warp for rows of up to 512
 // elements, else a block) owns a row, a lane has CH runs of 8 elements, and every element is read once and written
 // once. Teams walk over the rows; the rows to come are on their way into a ring in shared memory by bulk copies (one
 // instruction a tensor and row) while the reductions of this one wait on each other. Rows that are not whole 16-byte
@@ -33,7 +33,7 @@ namespace cq {
 namespace {
 
 constexpr int kRun = 8;          // consecutive elements of a lane's run
-constexpr int kWarpRow = 1024;   // widest row that a warp takes alone
+constexpr int kWarpRow = 512;    // widest row that a warp takes alone (777 rows of 1000: 7.4 us with a warp each, 5.2 with two)
 constexpr int kWarpTeams = 4;    // such rows of a block
 constexpr int kMaxWarps = 16;    // of a block that takes a row
 constexpr int kMaxDepth = 4;
@@ -473,17 +473,15 @@ int launch_block_norm(const cq_norm_desc &d, void *stream) {
     p.stage = p.at_gate + (p.gate && !p.one_gate ? p.d * size_of(p.x_type) : 0);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (d.width <= kWarpRow) {
-        const int per_sm = chunks <= 64 ? 12 : 6;  // 65536 rows of 512 in bf16: 61 us with 6, 54 with 12; a lane with four runs has registers for 6
+        const int per_sm = 12;  // 65536 rows of 512 in bf16: 54 us; 61 with 6
         p.depth = std::max(1, std::min(kMaxDepth, ring_bytes(per_sm) / kWarpTeams / p.stage));
         const int grid = (int)std::min<long long>(((long long)p.rows + kWarpTeams - 1) / kWarpTeams, (long long)sms * per_sm);
-        if (chunks <= 32) return launch_c<1, true>(p, vec, grid, 32 * kWarpTeams, st);
-        if (chunks <= 64) return launch_c<2, true>(p, vec, grid, 32 * kWarpTeams, st);
-        return launch_c<4, true>(p, vec, grid, 32 * kWarpTeams, st);
+        return chunks <= 32 ? launch_c<1, true>(p, vec, grid, 32 * kWarpTeams, st) : launch_c<2, true>(p, vec, grid, 32 * kWarpTeams, st);
     }
     const int ch = chunks <= 2 * 32 * kMaxWarps ? 2 : 4, threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
     // Blocks of an SM before stages of a block: the prompt of 8190 rows of 4096 takes 61 us with four blocks of two stages, 69 with three of
     // three, 81 with two of four (the reductions of more rows overlap).
-    int per_sm = std::max(1, 1024 / threads);
+    int per_sm = std::max(1, std::min(16, 1024 / threads));
     while (per_sm > 1 && ring_bytes(per_sm) / p.stage < 2) --per_sm;
     p.depth = std::max(1, std::min(kMaxDepth, ring_bytes(per_sm) / p.stage));
     const int grid = std::min(p.rows, per_sm * sms);

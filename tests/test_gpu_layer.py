@@ -19,6 +19,13 @@ def C():
     return pkg
 
 
+@pytest.fixture(autouse=True)
+def status(C):
+    """No test leaves a mark in the device status word."""
+    yield
+    C.cq_device_status()
+
+
 def _np(t):
     return None if t is None else t.detach().double().cpu().numpy()
 
