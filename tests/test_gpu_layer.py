@@ -442,7 +442,7 @@ def test_lora_refuses_bad_tensors(C):
 
 def test_lora_is_the_same_every_time(C):
     for new, rank in (([1] * 20, 16), ([300, 5, 1], 64)):
-        kw = _lora_inputs(new, [i % 4 for i in range(len(new))], 4096, (1024,), rank, BF16, I8)
+        kw = _lora_inputs(new, [i % 4 for i in range(len(new))], 4096, (1024,), rank, BF16, I8, n_adapters=4)
         outs = [torch.empty_like(kw["ys"][0])]
         want = C.cq_lora_add(**dict(kw, outs=outs))[0].clone()
         g = torch.cuda.CUDAGraph()
