@@ -21,15 +21,16 @@ struct LoraParams {
     int runs;      // of 32 outputs that a warp of the second product takes
     bool few;      // requests have few tokens
     bool vec;      // rows of x and A in runs of 8
+    bool tensor;   // x and A by tensor copies: rows on 16 bytes, and no fp32
     bool vec_b;    // rows of B in runs of 4
     bool vec_y[CQ_LORA_MAX_MATS];  // rows of y likewise
 };
 // Tiles of 16 ranks that a block of the first product takes.
 constexpr int lora_rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
 // Tokens of a piece, by the activations' type and the tiles of ranks: 8 where requests have few, else as many as leave the
-// sums in registers and two stages of inputs in shared memory; 128 on tcgen05 (`vec`, and no fp32). And the warps that share them.
-constexpr int lora_tokens(int x_dtype, int tiles, bool few, bool vec) {
-    return few ? 8 : vec && x_dtype != CQ_T_F32 ? 128 : tiles == 4 ? (x_dtype == CQ_T_F32 ? 32 : 64) : tiles == 2 || x_dtype == CQ_T_F32 ? 64 : 128;
+// sums in registers and two stages of inputs in shared memory; 128 by tensor copies. And the warps that share them.
+constexpr int lora_tokens(int x_dtype, int tiles, bool few, bool tensor) {
+    return few ? 8 : tensor ? 128 : tiles == 4 ? (x_dtype == CQ_T_F32 ? 32 : 64) : tiles == 2 || x_dtype == CQ_T_F32 ? 64 : 128;
 }
 constexpr int lora_warps_along(bool few) { return few ? 1 : 2; }
 int launch_lora_f16(LoraParams &p, void *stream);

@@ -16,10 +16,11 @@ bool is_float(int type) { return type >= CQ_T_F32 && type <= CQ_T_BF16; }
 bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 // How a call is cut up, apart from its alignment; the workspace's bytes, or 0.
-size_t lora_plan(const cq_lora_desc &d, bool few, bool vec, LoraParams &p) {
-    const int tiles = lora_rank_tiles(d.rank), ranks = 16 * tiles, tok = lora_tokens(d.x_dtype, tiles, few, vec);
+size_t lora_plan(const cq_lora_desc &d, bool few, bool tensor, LoraParams &p) {
+    const int tiles = lora_rank_tiles(d.rank), ranks = 16 * tiles, tok = lora_tokens(d.x_dtype, tiles, few, tensor);
     const long long pieces = std::min<long long>(d.n_tokens, (long long)d.n_seqs + d.n_tokens / tok);
     p.few = few;
+    p.tensor = tensor;
     p.u_row = (d.rank + ranks - 1) / ranks * ranks;
     // Parts of k: enough for three blocks on every SM, while a block keeps 512 inputs and more.
     p.splits = 1;
@@ -84,7 +85,7 @@ size_t cq_lora_workspace(const cq_lora_desc *d) {
     clear_error();
     LoraParams p;
     if (check_lora(d) || !d->n_mats || !d->n_tokens || !d->n_seqs) return 0;
-    const size_t plain = lora_plan(*d, false, false, p), many = lora_plan(*d, false, true, p), few = lora_few(*d) ? lora_plan(*d, true, true, p) : 0;
+    const size_t plain = lora_plan(*d, false, false, p), many = lora_plan(*d, false, true, p), few = lora_few(*d) ? lora_plan(*d, true, false, p) : 0;
     return plain && many ? std::max(plain, std::max(many, few)) : 0;
 }
 
@@ -107,8 +108,8 @@ int cq_lora_add(const cq_lora_desc *d, void *stream) {
     LoraParams p;
     p.d = *d;
     // Where 16-byte loads (8 of int8) and 16-byte accesses to y may be used; single elements elsewhere.
-    const int size = d->x_dtype == CQ_T_F32 ? 4 : d->x_dtype == CQ_T_I8 ? 1 : 2, run = d->x_dtype == CQ_T_I8 && lora_few(*d) ? 8 : 16;
-    p.vec = d->in % 8 == 0 && d->n_adapters && aligned(d->x, run) && (d->n_tokens == 1 || (d->x_stride * size % run == 0 && d->x_stride >= d->in));
+    const int size = d->x_dtype == CQ_T_F32 ? 4 : d->x_dtype == CQ_T_I8 ? 1 : 2, run = d->x_dtype == CQ_T_I8 ? 8 : 16;
+    p.vec = d->in % 8 == 0 && d->n_adapters && aligned(d->x, run) && (d->n_tokens == 1 || d->x_stride * size % run == 0);
     p.vec_b = d->rank % 4 == 0;
     for (int j = 0; j < d->n_mats; ++j) {
         p.vec = p.vec && aligned(d->a[j], 16);
@@ -116,7 +117,9 @@ int cq_lora_add(const cq_lora_desc *d, void *stream) {
         p.vec_y[j] = d->out[j] % 4 == 0 && aligned(d->y[j], 16) && aligned(d->y_out[j], 16) &&
                      (d->n_tokens == 1 || (d->y_stride[j] % 4 == 0 && d->y_stride[j] >= d->out[j] && d->y_out_stride[j] % 4 == 0));
     }
-    const size_t need = lora_plan(*d, p.vec && lora_few(*d), p.vec, p);
+    const bool few = p.vec && lora_few(*d);
+    const bool tensor = !few && p.vec && d->x_dtype != CQ_T_F32 && aligned(d->x, 16) && (d->n_tokens == 1 || (d->x_stride * size % 16 == 0 && d->x_stride >= d->in));
+    const size_t need = lora_plan(*d, few, tensor, p);
     if (!need) return CQ_ERR_SHAPE;
     if (!d->workspace || d->workspace_bytes < need || !aligned(d->workspace, 16))
         return set_error(CQ_ERR_ARG, "workspace of %zu bytes needed (16-byte aligned), got %zu", need, d->workspace ? d->workspace_bytes : 0);

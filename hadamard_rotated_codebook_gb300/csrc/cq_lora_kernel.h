@@ -3,21 +3,32 @@
 //   u[t][r] = sum_k A[e][r][k] x[t][k],   y_out[t][o] = y[t][o] + scale[e] sum_r B[e][o][r] u[t][r],   e the adapter of t's request
 //
 // What bounds it is memory: a decode step reads each request's adapter once (2 rank (in + out) bytes), a prompt reads x and reads and
-// writes y, while either product is a handful of operations a byte. Neither product fills a tensor core's tile: rank is the
-// M side of the first (16 rows of A to a tile) and outputs are the M side of the second, tokens the N side in steps of 8, so that
-// one token costs one narrow tile. mma.sync takes both operands from registers, which fit them as they come from memory:
-// a lane loads 16 consecutive bytes of a row, and as both operands number their k the same way, any order of k will do. No
-// tile is staged, no descriptor built.
+// writes y, while either product is a handful of operations a byte.
 //
-// Split. A piece is up to TOK tokens of one request. The first kernel gives a piece and a matrix to `splits` blocks, each of
-// which sums its part of k for all ranks (its warps a part of that part each) and leaves the sum in a workspace; the second
-// gives runs of 32 outputs of a piece to warps, which add the parts in their order. No atomics, and nothing depends on
-// timing. The second kernel begins while the first still runs: its blocks have found their pieces and have y and B on
-// their way by the time the first one's sums are there.
+// Split. A piece is up to so many tokens of one request. The first kernel gives a piece and a matrix to `splits` blocks, each of
+// which sums its part of k for all ranks and leaves the sum in a workspace; the second gives tiles of outputs to blocks, which
+// add the parts in their order. No atomics on values, and nothing depends on timing. The second kernel begins while the first still
+// runs: its blocks have found their pieces and have y and B on their way by the time the first one's sums are there. (One kernel
+// of clusters that met over distributed shared memory took 32 us for 64 decodes where the two take 18, and 211 us for the
+// prompt below: a cluster's barriers stand between its loads.)
+//
+// Few tokens a request (lora_down_kernel, lora_up_kernel): pieces of 8 on mma.sync. Rank is the M side of the first product (16 rows of A to a
+// tile), outputs are the M side of the second, tokens the N side, so that one token costs one narrow tile; tcgen05's least tile is
+// 128 rows. A lane copies 16 consecutive bytes of a row, and as both operands number their k the same way, any order of k will
+// do: what it copied is what it needs, and its own wait is all the synchronisation there is.
+// Many tokens (lora_down_many_kernel, lora_up_many_kernel): tcgen05, fed by tensor copies. Tokens are the M side of the first product and
+// outputs of the second, see there. Rows that tensor copies cannot reach and fp32 activations take lora_down_kernel in larger pieces.
 //
 // Precision. 16-bit and int8 activations meet the weights in one exact product each with fp32 sums. fp32 activations are two
 // terms of 11 bits (tf32, which holds fp16 and bf16 weights exactly): what is lost is 2^-22. u, summed in fp32, is three
 // terms of bf16 or two of fp16 (Terms).
+//
+// Measured: 64 decodes with 60 adapters, 4096 to 4096, 1024 and 1024, rank 16, int8 (38.8 MB): 18 us, 2.1 TB/s or 31% of the copy rate, 5.7 us being
+// the floor: the two kernels take 12 us each from cold caches (they overlap), with issue slots at 47 to 59%, memory's latency twice in
+// a row and the launch; 256 decodes 50 us, 47%. A prompt of 8190 tokens of three requests, 4096 to 4096, rank 64, bf16 (339 MB): 78 us, 64% (22 us
+// and 59 us; floor 50); rank 16, int8: 72 us, 62%. One token, 512 to 512, 256 and 256, rank 8: 5.1 us, two kernels' latency.
+// Tried and slower for prompts: mma.sync in both (97 to 146 us: 1.4 instructions an element), y in rows of 512 bytes by plain bulk copies (125 us: a
+// copy of any size costs the copy engine as much), y loaded by the threads that add (124 us).
 #pragma once
 
 #include <cuda.h>
@@ -589,7 +600,13 @@ __global__ void __launch_bounds__(kThreads, (Up<T, MT>::kBlocks)) lora_up_kernel
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) b[m][i] = cut_b(lds8(at + 1024 + (m * 4 + i) * 256 + lane * 8), rank - m * 16 - 4 * c);
+                        for (int i = 0; i < 4; ++i) b[m][i] = lds8(at + 1024 + (m * 4 + i) * 256 + lane * 8);
+                    if (rank & 3) {  // (uniform) a run that ends inside four
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) b[m][i] = cut_b(b[m][i], rank - m * 16 - 4 * c);
+                    }
                 }
                 float v[2][4];
 #pragma unroll
@@ -1104,6 +1121,7 @@ inline int make_map(CUtensorMap *map, CUtensorMapDataType type, int size, const 
         }
         fn = reinterpret_cast<Encode>(f);
     }
+    if (rows == 1) stride = (int64_t)(width + 15) / 16 * 16;  // of no meaning, but checked
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * size};
     const cuuint32_t box[2] = {(cuuint32_t)box_x, (cuuint32_t)box_y}, one[2] = {1, 1};
     const CUresult r = fn(map, type, 2, const_cast<void *>(at), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
@@ -1189,7 +1207,7 @@ int launch_r(LoraParams &p, cudaStream_t st) {
     constexpr int WT = lora_warps_along(false), NT = lora_tokens(XK, MT, false, false) / (8 * WT);
     int rc;
     if (VEC && p.few) rc = launch_down<T, XK, MT, 1, 1, true>(p, st);
-    else if (VEC && XK != CQ_T_F32) rc = launch_down_many<T, XK == CQ_T_F32 ? CQ_T_F16 : XK, MT>(p, st);
+    else if (VEC && XK != CQ_T_F32 && p.tensor) rc = launch_down_many<T, XK == CQ_T_F32 ? CQ_T_F16 : XK, MT>(p, st);
     else rc = launch_down<T, XK, MT, NT, WT, VEC>(p, st);
     if (rc) return rc;
     return launch_up<T, MT>(p, st);

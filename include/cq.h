@@ -663,10 +663,12 @@ size_t cq_lora_workspace(const cq_lora_desc *d);
  * where only the first ranks[e] rows of A_j[e] and columns of B_j[e] count;
  * x is x_scale[t] * x[t] for int8. Tokens of a request without an adapter
  * (-1) keep y: they are copied where y_out is not y, and cost nothing where
- * it is. Rows that no request covers are neither read nor written. Products
- * with 16-bit weights are exact; sums and the values between the two products
- * are fp32 (the second product takes them as two terms of 11 bits, which leaves
- * 2^-22). x must not overlap an output, nor one matrix's output another's.
+ * it is. Rows that no request covers are not written. Products with 16-bit
+ * weights are exact; sums and the values between the two products are fp32
+ * (the products take fp32 activations as two terms of 11 bits and those values
+ * as three terms of bf16 or two of fp16, by the weights' type: 2^-22 and
+ * less is lost). A token's result depends on the other requests by the order
+ * of its sums alone. x must not overlap an output, nor one matrix's output another's.
  * A request outside the tokens (cu_tokens not ascending in 0..n_tokens) is
  * skipped, one whose adapter or rank is outside its size counts as having
  * none; both mark the device status word (CQ_ERR_INDEX). Errors: CQ_ERR_ARG,

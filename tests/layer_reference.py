@@ -56,7 +56,7 @@ def lora(ys, x, a, b, adapters, cu, scales=None, ranks=None, x_scale=None, terms
     A tensor core's sum of 8 or 16 products loses a step of 2^-23 of what it adds up at most, as does each addition after
     it: one sum runs over 2 or 8 (fp32: two terms, 8 inputs at a time) products for each 32 inputs that a warp has (a
     quarter of them at least), then over 4 to 8 warps and up to 8 blocks, all within sum |a x|. Two terms of 11 bits leave
-    2^-21 of a value of fp32 (x, and u in the second product)."""
+    2^-21 of a value of fp32 at most (x in two of tf32; u, in the second product, in two of fp16 or three of bf16)."""
     f = np.float64
     x = x.astype(f)
     if x_scale is not None:

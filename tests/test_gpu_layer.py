@@ -372,6 +372,17 @@ def test_lora_of_many_tokens_without_anything(C):
     C.cq_device_status()
 
 
+def test_lora_rows_on_eight_bytes(C):
+    """int8 rows that tensor copies do not reach, and a single token with rows of any stride."""
+    for n_in in (1000, 1016, 1032):
+        _check_lora(C, _lora_inputs([300, 40], [0, 1], n_in, (160,), 16, BF16, I8, seed=n_in))
+    kw = _lora_inputs([1], [0], 33, (160,), 8, extra=6)
+    wide = torch.randn(7, 163, device="cuda")
+    kw["ys"] = [wide[:, :160][:1]]
+    kw["x"] = kw["x"][:1]
+    _check_lora(C, kw)
+
+
 def test_lora_shared_rows(C):
     """One row of x and y for every token (strides of zero)."""
     kw = _lora_inputs([1, 90], [0, 1], 64, (160,), 8)
