@@ -5,6 +5,7 @@ and marshalled, all arithmetic runs in libcq's kernels.
 """
 from __future__ import annotations
 
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -17,6 +18,9 @@ from .paged import _call, _dev, _i32, _ints, _stay, _type, _weight
 _ACT = {None: CQ_GATE_PLAIN, "sigmoid": CQ_GATE_SIGMOID, "silu": CQ_GATE_SILU}
 _load = _capi.load
 _lora_bytes: dict = {}
+_LORA_W = {torch.float16: CQ_T_F16, torch.bfloat16: CQ_T_BF16}
+_LORA_X = {torch.float32: CQ_T_F32, torch.int8: CQ_T_I8}
+_LORA_PACK = struct.Struct("@6P32P16q8iqPN8i").pack  # LoraDesc, field by field: its arrays cost a Python object an access
 
 
 def _matrix(t: torch.Tensor, name: str, device, shape=None, out: bool = False) -> int:
@@ -111,64 +115,89 @@ def cq_lora_add(ys: Sequence[torch.Tensor], x: torch.Tensor, a: Sequence[torch.T
     tokens, and an adapter or rank outside its size, make a following
     cq_device_status raise."""
     dev = x.device
-    xs = _matrix(x, "x", dev)
     m = len(ys)
     outs = ys if outs is None else outs
     if not m or not (len(a) == len(b) == len(outs) == m) or m > CQ_LORA_MAX_MATS:
         raise ValueError(f"ys, a, b (and outs) must be 1 to {CQ_LORA_MAX_MATS} tensors each, got {m}, {len(a)}, {len(b)}, {len(outs)}")
+    xs = _matrix(x, "x", dev)
     n, n_in = x.shape
-    wd = a[0].dtype
-    if wd not in (torch.float16, torch.bfloat16):
+    wd, xd, at, index = a[0].dtype, x.dtype, a[0].shape, dev.index
+    wt = _LORA_W.get(wd)
+    if wt is None:
         raise TypeError(f"a must be float16 or bfloat16, got {wd}")
-    if a[0].dim() != 3:
-        raise ValueError(f"a must be [adapters, rank, in], got {tuple(a[0].shape)}")
-    n_adapters, rank = a[0].shape[:2]
-    if x.dtype not in (torch.float32, torch.int8, wd):
-        raise TypeError(f"x must be float32, int8 or the weights' {wd}, got {x.dtype}")
+    xt = wt if xd == wd else _LORA_X.get(xd)
+    if xt is None:
+        raise TypeError(f"x must be float32, int8 or the weights' {wd}, got {xd}")
+    if len(at) != 3:
+        raise ValueError(f"a must be [adapters, rank, in], got {tuple(at)}")
+    n_adapters, rank, _ = at
     n_seqs = adapters.numel()
     if (n | n_in | n_seqs | n_adapters) >> 31:
         _ints(tokens=n, n_in=n_in, requests=n_seqs, adapters=n_adapters)
-    d = LoraDesc()
+    a_ptr, b_ptr, y_ptr, o_ptr, y_stride, o_stride, widths = [0] * 8, [0] * 8, [0] * 8, [0] * 8, [0] * 8, [0] * 8, [0] * 8
     for j in range(m):
         y, o, aj, bj = ys[j], outs[j], a[j], b[j]
-        if y.dtype != torch.float32 or o.dtype != torch.float32:
-            raise TypeError(f"ys and outs must be float32, got {y.dtype}, {o.dtype}")
-        d.y_stride[j] = _matrix(y, "y", dev, None, o is y)
-        if y.shape[0] != n:
-            raise ValueError(f"y has {y.shape[0]} rows, x has {n}")
-        width = y.shape[1]
+        try:  # what a good call passes in a few looks
+            rows, width = y.shape
+            st = y.stride()
+            good = (y.dtype is torch.float32 and rows == n and (st[1] == 1 or width <= 1) and y.get_device() == index
+                    and aj.dtype is wd and bj.dtype is wd and aj.shape == (n_adapters, rank, n_in) and bj.shape == (n_adapters, width, rank)
+                    and aj.is_contiguous() and bj.is_contiguous() and aj.get_device() == index and bj.get_device() == index)
+            so = st[0]
+            if o is y:
+                good = good and (n <= 1 or so >= width)
+            else:
+                su = o.stride()
+                so = su[0]
+                good = (good and o.dtype is torch.float32 and o.shape == y.shape and (su[1] == 1 or width <= 1) and (n <= 1 or so >= width)
+                        and o.get_device() == index)
+        except (AttributeError, ValueError, IndexError):
+            good = False
+        if not good:
+            _lora_complain(y, o, aj, bj, dev, wd, n, (n_adapters, rank, n_in))
         if width >> 31:
             _ints(out=width)
-        d.y_out_stride[j] = d.y_stride[j] if o is y else _matrix(o, "out", dev, y.shape, True)
-        for t, name, shape in ((aj, "a", (n_adapters, rank, n_in)), (bj, "b", (n_adapters, width, rank))):
-            _dev(t, name, dev)
-            if t.dtype != wd or t.shape != shape or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous {wd} {list(shape)}, got {t.dtype} {list(t.shape)}")
-        d.a[j], d.b[j], d.y[j], d.y_out[j], d.out[j] = aj.data_ptr(), bj.data_ptr(), y.data_ptr(), o.data_ptr(), width
+        a_ptr[j], b_ptr[j], y_ptr[j], widths[j], y_stride[j], o_stride[j] = aj.data_ptr(), bj.data_ptr(), y.data_ptr(), width, st[0], so
+        o_ptr[j] = y_ptr[j] if o is y else o.data_ptr()
     for t, name, size in ((scales, "scales", n_adapters), (x_scale, "x_scale", n)):
         if t is None:
             continue
         _dev(t, name, dev)
         if t.dtype != torch.float32 or t.numel() < size or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous float32 with at least {size} entries, got {t.dtype} {tuple(t.shape)}")
-        setattr(d, name, t.data_ptr())
-    if x.dtype == torch.int8 and x_scale is None:
+    if xt == CQ_T_I8 and x_scale is None:
         raise ValueError("int8 activations need x_scale")
-    d.x, d.x_stride = x.data_ptr(), xs
-    d.ranks = None if ranks is None else _i32(ranks, "ranks", n_adapters, dev)
-    d.adapters, d.cu_tokens = _i32(adapters, "adapters", n_seqs, dev), _i32(cu_tokens, "cu_tokens", n_seqs + 1, dev)
-    d.n_mats, d.n_tokens, d.n_seqs, d.n_adapters, d.in_, d.rank = m, n, n_seqs, n_adapters, n_in, rank
-    d.w_dtype = CQ_T_F16 if wd == torch.float16 else CQ_T_BF16
-    d.x_dtype = CQ_T_F32 if x.dtype == torch.float32 else CQ_T_I8 if x.dtype == torch.int8 else d.w_dtype
-    key = (m, n, n_seqs, n_in, rank, d.x_dtype, dev.index)  # what the workspace goes by, besides the device
+    key = (m, n, n_seqs, n_in, rank, xt, index)  # what the workspace goes by, besides the device
     size = _lora_bytes.get(key)
+
+    def desc(ws, size):
+        return LoraDesc.from_buffer_copy(_LORA_PACK(
+            x.data_ptr(), 0 if x_scale is None else x_scale.data_ptr(), 0 if scales is None else scales.data_ptr(),
+            0 if ranks is None else _i32(ranks, "ranks", n_adapters, dev), _i32(adapters, "adapters", n_seqs, dev),
+            _i32(cu_tokens, "cu_tokens", n_seqs + 1, dev), *a_ptr, *b_ptr, *y_ptr, *o_ptr, *y_stride, *o_stride, *widths, xs, ws, size,
+            m, n, n_seqs, n_adapters, n_in, rank, xt, wt))
+
     if size is None:
-        with (_stay if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)):
-            size = _load().cq_lora_workspace(d)
+        with (_stay if index == torch.cuda.current_device() else torch.cuda.device(dev)):
+            size = _load().cq_lora_workspace(desc(0, 0))
         if len(_lora_bytes) >= 4096:
             _lora_bytes.clear()
         _lora_bytes[key] = size
     ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    d.workspace, d.workspace_bytes = ws.data_ptr(), size
-    _call(dev, _load().cq_lora_add, d)
+    _call(dev, _load().cq_lora_add, desc(ws.data_ptr(), size))
     return list(outs)
+
+
+def _lora_complain(y, o, aj, bj, dev, wd, n, a_shape) -> None:
+    """Says what is wrong with a matrix's tensors."""
+    _matrix(y, "y", dev, None, o is y)
+    _matrix(o, "out", dev, y.shape, True)
+    if y.dtype != torch.float32 or o.dtype != torch.float32:
+        raise TypeError(f"ys and outs must be float32, got {y.dtype}, {o.dtype}")
+    if y.shape[0] != n:
+        raise ValueError(f"y has {y.shape[0]} rows, x has {n}")
+    for t, name, shape in ((aj, "a", a_shape), (bj, "b", (a_shape[0], y.shape[1], a_shape[1]))):
+        _dev(t, name, dev)
+        if t.dtype != wd or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {wd} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    raise ValueError("ys, outs, a and b do not belong together")

@@ -123,6 +123,19 @@ def _fields(A, struct):
     return out
 
 
+def test_packed_adapters_match_the_structure(C, A):
+    """The binding packs LoraDesc in one go: every value arrives in its field."""
+    from hadamard_rotated_codebook_gb300 import layer
+    values = list(range(1, 74))
+    data = layer._LORA_PACK(*values)
+    assert len(data) == ctypes.sizeof(A.LoraDesc)
+    d, got = A.LoraDesc.from_buffer_copy(data), []
+    for name, _ in A.LoraDesc._fields_:
+        v = getattr(d, name)
+        got += list(v) if isinstance(v, ctypes.Array) else [v]
+    assert got == values
+
+
 def test_binding_structures_match_the_header(A):
     """Field by field: the header's structs and the binding's have the same order and sizes."""
     for name, cls in (("cq_norm_desc", A.NormDesc), ("cq_lora_desc", A.LoraDesc), ("cq_kv_window", A.KvWindow)):
