@@ -29,9 +29,9 @@
 // of 65536 rows 1 to 4% (32 requests; 6% for single tokens of heads over two groups) and shorter parts nothing. (References
 // below the largest logit keep such weights too, but rise often: 8 powers of two lower 314 -> 455 us for the server.)
 //
-// Windows. What a request's tokens attend lies in its first rows and from the first token's window on: those rows, side by side, are
-// the item's rows (`gap` rows are left out between them), so that tiles hold nothing else and rows in between are never
-// read. A token further on in a chunk has left some of them behind; in the tiles that hold such rows a thread compares how far its
+// Windows. What an item's tokens attend lies in the request's first rows and from their first one's window on: those rows, side by side,
+// are the item's rows (`gap` rows are left out between them), so that tiles hold nothing else and rows in between are never
+// read. Column tiles of a long chunk so read windows of their own, not the whole chunk's. A token further on in a chunk has left some of them behind; in the tiles that hold such rows a thread compares how far its
 // row lies behind the window's beginning with the depths of the columns' tokens, four at a time.
 //
 // Queries in fp16. Each column is rounded at the power of two of its own largest element (rotate_queries), so that a query of any
@@ -101,19 +101,20 @@ constexpr int kGuard = 10;                   // a tile's columns share one scale
 
 // What only windows need, without a byte of it elsewhere.
 template <bool WIN> struct WinParams {
-    static constexpr int window = INT_MAX, sinks = 0;
+    static constexpr int window = INT_MAX, sinks = 0, span = 0;
     static constexpr const int32_t *positions = nullptr;
 };
 template <> struct WinParams<true> {
     const int32_t *positions;
     int window, sinks;
+    int span;  // most tokens whose windows an item's rows cover: a column tile's, or a request's
 };
 template <bool WIN> struct WinSeq {
-    static constexpr int gap = 0, edge = 0;
+    static constexpr int gap = 0;
 };
 template <> struct WinSeq<true> {
-    int gap;   // rows left out behind the sinks
-    int edge;  // the item's row where the first token's window begins (below zero: before the request does)
+    int all;  // rows that the request has
+    int gap;  // of an item: rows left out behind the sinks
 };
 template <bool WIN> struct WinShared {};
 template <> struct WinShared<true> {
@@ -305,17 +306,18 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { r
 // One request as the kernel takes it: lengths outside the given sizes are cut to
 // them (`bad`), so that no index leaves its buffer whatever the device holds.
 struct Seq : WinSeq<kWindow> {
-    int first, n, ctx, len;  // ctx, len: of the item's rows, the rows left out not among them
+    int first, n, ctx, len;  // len: the most rows that one of its items has
     bool bad;
 };
-__device__ __forceinline__ void leave_out(const TreeParams &, Seq &, WinSeq<false> &) {}
-__device__ __forceinline__ void leave_out(const TreeParams &p, Seq &q, WinSeq<true> &w) {
-    const long long edge = (long long)q.ctx - p.window + 1;
-    w.gap = q.len ? (int)max(0ll, edge - p.sinks) : 0;
-    if (w.gap >= q.len) w.gap = q.len = 0;  // a context past its table: reported, nothing is read
-    q.ctx -= w.gap;
-    q.len -= w.gap;
-    w.edge = (int)max(edge - w.gap, -(long long)CQ_TREE_MAX_NODES);
+// Tokens that follow each other leave the window one by one, and a column tile holds a run of them: its items then
+// begin at their own first token's window and end with their own last token. (16 chunks of 256 tokens, 32 heads over 8,
+// windows of 4096 rows 589 -> 535 us, of 512 248 -> 214 us. Tiles of 16 and 32 columns go without: their requests are short,
+// and it slowed 256 single tokens from 49 to 51 us.)
+__host__ __device__ __forceinline__ bool in_line(int N, const int32_t *positions, const uint32_t *mask) { return kWindow && N >= 64 && !positions && !mask; }
+__device__ __forceinline__ void bound_rows(const TreeParams &, Seq &, WinSeq<false> &) {}
+__device__ __forceinline__ void bound_rows(const TreeParams &p, Seq &q, WinSeq<true> &w) {
+    w.all = q.len;
+    q.len = (int)min((long long)q.len, (long long)p.sinks + p.window - 1 + min(q.n, p.span));
 }
 __device__ __forceinline__ Seq seq_at(const TreeParams &p, int s) {
     Seq q;
@@ -330,7 +332,7 @@ __device__ __forceinline__ Seq seq_at(const TreeParams &p, int s) {
     q.bad |= q.n && ctx + q.n > room;
     q.ctx = (int)ctx;
     q.len = q.n ? (int)min(ctx + q.n, room) : 0;
-    leave_out(p, q, q);
+    bound_rows(p, q, q);
     return q;
 }
 __device__ __forceinline__ int tiles_of(int len) { return max(1, (int)(((long long)len + kTile - 1) / kTile)); }
@@ -348,17 +350,35 @@ struct Cursor : WinSeq<kWindow> {
         ntiles = tiles_of(len);
         ncol = cols_of(p, n, N);
     }
+    // The first and the last of an item's tokens.
+    __device__ __forceinline__ int2 tokens(const TreeParams &p, int N) const {
+        if (ncol == 1 || !in_line(N, p.positions, p.t.mask)) return make_int2(0, n - 1);
+        const int rows = p.unit[u].nh * p.per;
+        return make_int2(min(n - 1, c * N / rows), min(n - 1, (c * N + N - 1) / rows));
+    }
+    // The item's rows, once its request, unit and column tile are known.
+    __device__ __forceinline__ void bound(const TreeParams &, int, WinSeq<false> &) {}
+    __device__ __forceinline__ void bound(const TreeParams &p, int N, WinSeq<true> &w) {
+        const int2 t = tokens(p, N);
+        const unsigned end = min((unsigned)w.all, (unsigned)ctx + (unsigned)t.y + 1);
+        const long long out = max(0ll, (long long)ctx + t.x + 1 - p.window - p.sinks);
+        w.gap = out < end ? (int)out : 0;
+        len = out < end ? (int)(end - (unsigned)out) : 0;  // (a context past its table: reported, nothing is read)
+    }
     __device__ void next_item(const TreeParams &p, int N) {
         tile = 0;
         ++item;
-        if (++c < ncol) return;
-        c = 0;
-        if (++u < p.n_units) return;
-        u = 0;
-        do {
-            if (++s >= p.t.n_seqs) return;
-            take(p, N);
-        } while (!n);
+        if (++c >= ncol) {
+            c = 0;
+            if (++u >= p.n_units) {
+                u = 0;
+                do {
+                    if (++s >= p.t.n_seqs) return;
+                    take(p, N);
+                } while (!n);
+            }
+        }
+        bound(p, N, *this);
     }
     __device__ __forceinline__ bool advance(const TreeParams &p, int N) {  // to the next tile; false after the last
         if (--left <= 0) return false;
@@ -487,6 +507,7 @@ __device__ bool find_run(const TreeParams &p, Shared &sh) {
             c.u = it / c.ncol;
             c.c = it - c.u * c.ncol;
             c.item = (int)item;
+            c.bound(p, N, c);
             sh.first = w0 + (c.tile - in);
             sh.start = c;
         }
@@ -1227,7 +1248,7 @@ __device__ float rotate_queries(const TreeParams &p, Shared &sh, uint8_t *smem, 
 // How far behind the context a drafted token stands.
 __device__ __forceinline__ int depth_of(const TreeParams &p, const Cursor &c, int node) {
     if (!p.positions || node >= c.n) return min(node, CQ_TREE_MAX_NODES - 1);
-    const long long d = (long long)p.positions[c.first + node] - c.ctx - c.gap;
+    const long long d = (long long)p.positions[c.first + node] - c.ctx;
     if (d < 0 || d >= CQ_TREE_MAX_NODES) atomicOr(p.status, kStatusIndex);
     return (int)max(0ll, min(d, (long long)CQ_TREE_MAX_NODES - 1));
 }
@@ -1248,7 +1269,7 @@ __device__ void gather_mask(const TreeParams &p, Shared &sh, const Cursor &c, in
 #pragma unroll 4
             for (int j = 0; j < 32; ++j) {
                 const int d = __shfl_sync(0xFFFFFFFFu, other, j);
-                if (mine - d >= p.window && (long long)c.ctx + c.gap + d >= p.sinks) w &= ~(1u << j);
+                if (mine - d >= p.window && (long long)c.ctx + d >= p.sinks) w &= ~(1u << j);
             }
         }
         uint32_t mine = 0;
@@ -1261,24 +1282,51 @@ __device__ void gather_mask(const TreeParams &p, Shared &sh, const Cursor &c, in
     }
 }
 
-// Rows behind the window's beginning that not all tokens of an item attend: a token at depth d has left d of them behind.
-__device__ __forceinline__ int left_behind(const TreeParams &p, const Cursor &c) {
-    return !kWindow ? 0 : p.positions ? CQ_TREE_MAX_NODES - 1 : c.n - 1;
-}
-// The depths of an item's columns.
+// An item as softmax sees it: which of its rows not every token attends.
+template <bool WIN> struct Visible {
+    __device__ __forceinline__ void take(const TreeParams &, const Cursor &, int) {}
+    __device__ __forceinline__ bool all(const Cursor &c, int tok) const { return tok + kTile <= c.ctx; }
+};
+template <> struct Visible<true> {
+    int drafts_from;  // rows from here on are drafted tokens
+    int gap;
+    int edge;       // where the window of the first token begins (far below zero: before the request does)
+    int near_from, near_to;  // rows whose bits differ between the columns: a token at depth d has left d of those behind the edge
+    int first_tok, near;
+    __device__ __forceinline__ void take(const TreeParams &p, const Cursor &c, int N) {
+        const int2 t = c.tokens(p, N);
+        const long long e = (long long)c.ctx + t.x - p.window + 1;
+        edge = (int)max(e, -1ll << 20);
+        gap = c.gap;
+        first_tok = p.positions ? 0 : t.x;
+        near = p.positions ? CQ_TREE_MAX_NODES - 1 : t.y - t.x;
+        drafts_from = c.ctx < p.sinks ? c.ctx : max(p.sinks, c.ctx - gap);
+        near_from = p.sinks;
+        near_to = near ? (int)min((long long)drafts_from, (long long)edge + near - gap) : 0;  // (one token has left none)
+    }
+    __device__ __forceinline__ bool all(const Cursor &, int tok) const { return tok + kTile <= drafts_from && (tok + kTile <= near_from || tok >= near_to); }
+};
+// The depths of an item's columns, counted from its first token.
 template <int N>
-__device__ __forceinline__ void gather_depths(const TreeParams &, WinShared<false> &, const Cursor &, int, int) {}
+__device__ __forceinline__ void gather_depths(const TreeParams &, WinShared<false> &, const Cursor &, const Visible<false> &, int, int) {}
 template <int N>
-__device__ __forceinline__ void gather_depths(const TreeParams &p, WinShared<true> &sh, const Cursor &c, int thread, int threads) {
+__device__ __forceinline__ void gather_depths(const TreeParams &p, WinShared<true> &sh, const Cursor &c, const Visible<true> &v, int thread, int threads) {
+    if (!v.near) return;
     const int rows = p.unit[c.u].nh * p.per;
-    for (int k = thread; k < N; k += threads) sh.depth[k] = (uint8_t)depth_of(p, c, (c.c * N + k) / rows);
+    for (int k = thread; k < N; k += threads) sh.depth[k] = (uint8_t)max(0, depth_of(p, c, (c.c * N + k) / rows) - v.first_tok);
 }
-// Which of columns cx .. cx + 31 attend row v of the item, part of the context (bits).
-__device__ __forceinline__ uint32_t near_bits(const TreeParams &, const WinShared<false> &, const Cursor &, int, int) { return 0xFFFFFFFFu; }
-__device__ __forceinline__ uint32_t near_bits(const TreeParams &p, const WinShared<true> &sh, const Cursor &c, int v, int cx) {
-    const int e = v - c.edge;  // not below zero for a row past the sinks
-    if (v < p.sinks || e >= left_behind(p, c)) return 0xFFFFFFFFu;
-    const uint32_t limit = 0x01010101u * (uint32_t)max(e, 0);
+// Which of columns cx .. cx + 31 attend row r of the item (bits), in a tile that not all of them attend as a whole. (A window's,
+// needed for few tiles, is a call: inline it cost the tiles that all attend 3%, 553 -> 537 us.)
+__device__ __forceinline__ uint32_t column_bits(const TreeParams &, const WinShared<false> &, const uint32_t (*mask)[4], const Cursor &c, const Visible<false> &, int r, int cx) {
+    const int j = r - c.ctx;
+    return j >= 0 && j < c.n ? mask[j][cx >> 5] >> (cx & 31) : 0xFFFFFFFFu;
+}
+__noinline__ __device__ uint32_t column_bits(const TreeParams &p, const WinShared<true> &sh, const uint32_t (*mask)[4], const Cursor &c, const Visible<true> &v, int r, int cx) {
+    const bool sink = r < p.sinks;
+    const int t = sink ? r : (int)((unsigned)r + (unsigned)v.gap), j = (int)((unsigned)t - (unsigned)c.ctx);  // (rows past the last may leave 31 bits: j is right)
+    if (j >= 0 && j < c.n) return mask[j][cx >> 5] >> (cx & 31);
+    if (sink || r >= v.near_to) return 0xFFFFFFFFu;
+    const uint32_t limit = 0x01010101u * (uint32_t)(t - v.edge);  // (a row past the sinks is not before the edge)
     uint32_t bits = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {  // four columns at a time: bytes of ones where the depth is at most e, one bit of each kept
@@ -1439,17 +1487,19 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
     bool more = true, again = false;  // again: a chunk of the same item's part
     float mult = 0.0f;
     bool wide = false;
+    Visible<kWindow> seen;
     stash_queries<N, NG, ZT>(p, smem, c, warp, lane);
     while (more) {
         // ------------------------------------------ a chunk of an item's part --
         const TreeUnit u = p.unit[c.u];
         const int cols = min(N, c.n * u.nh * p.per - c.c * N), slot = blockIdx.x + c.item;
         if (!again) {
+            seen.take(p, c, N);
             bar_sync(1, kSoftThreads);  // the item before is finished: the exponents, m, mask may be written
             if (warp == 0 && lane == 0) sh.ztop = kNoEx, sh.zlow = -kNoEx;
             if (row < NC) sh.minus_m[c0 + row] = -kNoMax;
             gather_mask<N>(p, sh, c, warp, L::kSoft, lane);
-            gather_depths<N>(p, sh, c, 32 * warp + lane, kSoftThreads);
+            gather_depths<N>(p, sh, c, seen, 32 * warp + lane, kSoftThreads);
             bar_sync(1, kSoftThreads);
             mult = rotate_queries<N, NG, ZT>(p, sh, smem, c, warp, lane, wide);
             fence_async();
@@ -1470,16 +1520,10 @@ __device__ void softmax_role(const TreeParams &p, Shared &sh, uint8_t *smem, int
             const int b = i & 1;
             const uint32_t par = (uint32_t)(i >> 1) & 1;
             const int tok = (c.tile + it) * kTile;
-            // the tile holds drafted tokens, or rows that some tokens have left behind
-            const bool masked = tok + kTile > c.ctx || (kWindow && tok + kTile > p.sinks && tok < c.edge + left_behind(p, c));
+            const bool masked = !seen.all(c, tok);  // the tile holds drafted tokens, or rows that some tokens have left behind
             uint32_t see[(NC + 31) / 32];
 #pragma unroll
-            for (int k = 0; k < (NC + 31) / 32; ++k) {
-                const int j = tok + row - c.ctx;
-                see[k] = j >= 0 && j < c.n ? sh.mask[j][(c0 + 32 * k) >> 5] >> (c0 & 31)
-                         : kWindow && masked && j < 0 ? near_bits(p, sh, c, tok + row, c0 + 32 * k)
-                                                      : 0xFFFFFFFFu;
-            }
+            for (int k = 0; k < (NC + 31) / 32; ++k) see[k] = !kWindow || masked ? column_bits(p, sh, sh.mask, c, seen, tok + row, c0 + 32 * k) : 0xFFFFFFFFu;
             wait(p, sh, &sh.sc_full[b], par, 0x47490009u);
             const float nk = sh.scal[b][0][row] * mult, ln = sh.scal[b][1][row], inv = sh.scal[b][2][row];
             float r0 = 1.0f, r1 = 0.0f;

@@ -247,3 +247,10 @@ def test_window_refuses(C):
             C.cq_kv_window_attend(*c.args(), **{**dict(window=8, sinks=0), **kw})
     with pytest.raises(TypeError):
         C.cq_kv_window_attend(*c.args(), 8, 0, positions=torch.zeros(2, device="cuda"))
+
+
+@pytest.mark.parametrize("geom", [(8, 2, 64, 64), (32, 8, 128, 128), (16, 1, 128, 128), (6, 6, 48, 64), (8, 1, 256, 256), (14, 7, 40, 40)])
+@pytest.mark.parametrize("window,sinks,ctx", [(20, 0, 0), (33, 100, 10), (64, 3, 500), (300, 500, 200), (40, 30, 25), (257, 1, 1000)])
+def test_window_column_tiles_have_windows_of_their_own(C, geom, window, sinks, ctx):
+    """Chunks over many column tiles: windows that begin before, within and behind the chunk, sinks that reach into it."""
+    Case(C, [ctx, 7, 0], [150, 256, 31], window, sinks, geom, (2, 2), 32, dtype=BF16, seed=window).check()
