@@ -22,9 +22,11 @@ size_t lora_plan(const cq_lora_desc &d, bool few, bool tensor, LoraParams &p) {
     p.few = few;
     p.tensor = tensor;
     p.u_row = (d.rank + ranks - 1) / ranks * ranks;
-    // Parts of k: enough for three blocks on every SM, while a block keeps 512 inputs and more.
+    // Parts of k: enough for three blocks on every SM, while a block keeps 512 inputs and more. On tcgen05 no more blocks than the two of
+    // an SM that run at once, and fewer sums to add (8190 tokens, 4096 to 4096, rank 64: 73 us with four parts, 77 with eight).
+    const long long room = tensor ? sm_count() : 3ll * sm_count() - 1;
     p.splits = 1;
-    while (p.splits < kMaxSplits && pieces * d.n_mats * p.splits < 3ll * sm_count() && d.in >= 1024 * p.splits) p.splits *= 2;
+    while (p.splits < kMaxSplits && pieces * d.n_mats * p.splits <= room && d.in >= 1024 * p.splits) p.splits *= 2;
     p.runs = 1;
     if (pieces * p.splits > INT_MAX) {
         set_error(CQ_ERR_SHAPE, "%d tokens of %d requests are too many for one call", d.n_tokens, d.n_seqs);

@@ -25,8 +25,8 @@
 //
 // Measured: 64 decodes with 60 adapters, 4096 to 4096, 1024 and 1024, rank 16, int8 (38.8 MB): 18 us, 2.1 TB/s or 31% of the copy rate, 5.7 us being
 // the floor: the two kernels take 12 us each from cold caches (they overlap), with issue slots at 47 to 59%, memory's latency twice in
-// a row and the launch; 256 decodes 50 us, 47%. A prompt of 8190 tokens of three requests, 4096 to 4096, rank 64, bf16 (339 MB): 78 us, 64% (22 us
-// and 59 us; floor 50); rank 16, int8: 72 us, 62%. One token, 512 to 512, 256 and 256, rank 8: 5.1 us, two kernels' latency.
+// a row and the launch; 256 decodes 50 us, 47%. A prompt of 8190 tokens of three requests, 4096 to 4096, rank 64, bf16 (339 MB): 73 us, 68% (18 us
+// and 59 us; floor 50); rank 16, int8: 68 us, 66%. One token, 512 to 512, 256 and 256, rank 8: 5.1 us, two kernels' latency.
 // Tried and slower for prompts: mma.sync in both (97 to 146 us: 1.4 instructions an element), y in rows of 512 bytes by plain bulk copies (125 us: a
 // copy of any size costs the copy engine as much), y loaded by the threads that add (124 us).
 #pragma once
