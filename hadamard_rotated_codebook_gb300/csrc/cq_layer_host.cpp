@@ -63,6 +63,7 @@ int cq_block_norm(const cq_norm_desc *d, void *stream) {
     if (d->n_tokens > 1 && ((d->residual_out && d->residual_out_stride < d->width) || d->out_stride < d->width))
         return set_error(CQ_ERR_SHAPE, "output rows of %d elements are %lld and %lld apart", d->width, (long long)d->residual_out_stride,
                          (long long)d->out_stride);
+    if (d->residual_out == d->out) return set_error(CQ_ERR_ARG, "the two outputs share memory");
     return launch_block_norm(*d, stream);
 }
 
@@ -106,6 +107,11 @@ int cq_lora_add(const cq_lora_desc *d, void *stream) {
         if (d->y[j] == d->y_out[j] && d->n_tokens > 1 && d->y_stride[j] != d->y_out_stride[j])
             return set_error(CQ_ERR_SHAPE, "y is added to in place with rows %lld and %lld apart", (long long)d->y_stride[j],
                              (long long)d->y_out_stride[j]);
+    }
+    for (int j = 0; j < d->n_mats; ++j) {
+        if (d->y_out[j] == d->x) return set_error(CQ_ERR_ARG, "an output is x");
+        for (int k = 0; k < d->n_mats; ++k)
+            if (k != j && (d->y_out[j] == d->y_out[k] || d->y_out[j] == d->y[k])) return set_error(CQ_ERR_ARG, "outputs %d and %d share memory", j, k);
     }
     LoraParams p;
     p.d = *d;

@@ -668,7 +668,7 @@ size_t cq_lora_workspace(const cq_lora_desc *d);
  * (the products take fp32 activations as two terms of 11 bits and those values
  * as three terms of bf16 or two of fp16, by the weights' type: 2^-22 and
  * less is lost). A token's result depends on the other requests by the order
- * of its sums alone. x must not overlap an output, nor one matrix's output another's.
+ * of its sums alone. x must not overlap an output, nor one matrix's output another's or its y.
  * A request outside the tokens (cu_tokens not ascending in 0..n_tokens) is
  * skipped, one whose adapter or rank is outside its size counts as having
  * none; both mark the device status word (CQ_ERR_INDEX). Errors: CQ_ERR_ARG,

@@ -66,6 +66,22 @@ def test_lora_add_refuses(A, kw, code):
     assert A.load().cq_last_error()
 
 
+def test_outputs_that_share_memory_are_refused(A):
+    lib = A.load()
+    assert lib.cq_block_norm(ctypes.byref(_norm(A)), None) == A.CQ_ERR_ARG and b"share" in lib.cq_last_error()
+
+    def two(**kw):
+        t = _lora(A, n_mats=2)
+        for f, v in dict(a=16, b=16, y=48, y_out=64, y_stride=32, y_out_stride=32, out=32).items():
+            getattr(t, f)[1] = kw.get(f, v)
+        return lib.cq_lora_add(ctypes.byref(t), None)
+
+    for kw in (dict(y_out=32), dict(y=32), dict(y_out=16)):  # the other's output twice, the other's output as y, x
+        assert two(**kw) == A.CQ_ERR_ARG and b"output" in lib.cq_last_error()
+    t = _lora(A, x=32)
+    assert lib.cq_lora_add(ctypes.byref(t), None) == A.CQ_ERR_ARG and b"output" in lib.cq_last_error()
+
+
 def test_lora_workspace(A):
     """A function of sizes and types; nothing where there is nothing to do or a size is bad."""
     size = lambda **kw: A.load().cq_lora_workspace(ctypes.byref(_lora(A, **kw)))  # noqa: E731
