@@ -1747,6 +1747,18 @@ __global__ void __launch_bounds__(Plan<N, NG, ZT>::kThreads, 1) tree_kernel(cons
 constexpr int kJoinWarps = 8;
 constexpr int kFewParts = 16;
 
+// x / d of whole numbers, x below 2^22, d up to 2^10 and x / d up to 2^10, with inv = 1 / d: (x + 1/2) / d lies 2^-11 or more from any whole
+// number, and two roundings move it by 2^-13 at most.
+__device__ __forceinline__ int quotient(int x, float inv) { return (int)(((float)x + 0.5f) * inv); }
+__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 template <int NG>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ TreeParams p, int N, int CG) {
     __shared__ float s_acc[kJoinWarps][NG][kGroup];
@@ -1762,6 +1774,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     int2 rec = p.rec[item];
     if (rec.x < 0 || rec.y < 0 || rec.x > p.slots - rec.y) rec.y = 0;  // an item that no block wrote
     const bool many = rec.y > kFewParts;
+    const float per_row = 1.0f / (float)rows, per_head = 1.0f / (float)p.per;
     for (int k = many ? 0 : warp; k < CG && first + k < cols; k += many ? 1 : kJoinWarps) {
         const int col = first + k;
         float M = kNoMax, sum = 0.0f, acc[NG][4];
@@ -1812,7 +1825,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
                     for (int j = 0; j < 4; ++j) acc[g][j] = fmaf(s_acc[w][g][4 * lane + j], f, acc[g][j]);
             }
         }
-        const int at = ct * N + col, node = at / rows, r = at - node * rows, h = u.h0 + r / p.per;
+        const int at = ct * N + col, node = quotient(at, per_row), r = at - node * rows, h = u.h0 + quotient(r, per_head);
         const float f = sum == 0.0f ? 0.0f : p.v_mult / sum;  // zero: a token that attends nothing
         const int64_t dst = (int64_t)(q.first + node) * p.t.o_stride_t + (int64_t)(u.h0 * p.per + r) * p.t.o_stride_h;
 #pragma unroll
@@ -1820,6 +1833,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
             if (g >= u.ngv) break;
             fwht(acc[g], lane);
             const int d0 = (u.gv + g) * kGroup + 4 * lane - h * p.dv;
+            if (d0 < 0 || d0 >= p.dv) {
+                if (d0 <= -4 || d0 >= p.dv) continue;
+            } else if (d0 + 4 <= p.dv && !((uintptr_t)(static_cast<__half *>(p.t.o) + dst + d0) & 7)) {
+                uint2 w;
+                if (p.t.dtype == CQ_T_F16) w = make_uint2(pack_f16(acc[g][0] * f, acc[g][1] * f), pack_f16(acc[g][2] * f, acc[g][3] * f));
+                else w = make_uint2(pack_bf16(acc[g][0] * f, acc[g][1] * f), pack_bf16(acc[g][2] * f, acc[g][3] * f));
+                *reinterpret_cast<uint2 *>(static_cast<__half *>(p.t.o) + dst + d0) = w;
+                continue;
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (d0 + j < 0 || d0 + j >= p.dv) continue;
