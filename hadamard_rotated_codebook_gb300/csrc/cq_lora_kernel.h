@@ -776,10 +776,12 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
     __syncthreads();
     fence_after();
     const int64_t yo_st = p.d.y_out_stride[mat], y_st = p.d.y_stride[mat];
+    // A tensor copy writes whole tiles: of a piece of fewer tokens each thread writes its own results. (A copy for each row instead held
+    // the launch up: 8190 tokens of three requests 73 us against 64.)
+    const bool whole = q.n == S::kTok;
     if (warp == kWarps) {
         if (BULK) {
-            // A copy reads whole tiles (rows of the next piece among them) and writes only what is the piece's: a piece of fewer tokens row by row.
-            const bool whole = q.n == S::kTok;
+            // A copy reads whole tiles, rows of the next piece among them.
             auto load = [&](int i) {
                 if (lane == 0) {
                     const uint32_t bar = full + i % S::kStages * 8;
@@ -793,17 +795,10 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
                 wait(p, ready + i % S::kStages * 8, (uint32_t)(i / S::kStages) & 1, s_abort);
                 const uint32_t from = base + S::oY + i % S::kStages * S::kY;
                 const int o = (t0 + i) * S::kOut;
-                if (whole) {
-                    if (lane == 0)
-                        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(&maps.out[mat]), "r"(o), "r"(q.first),
-                                     "r"(from)
-                                     : "memory");
-                } else {
-                    for (int t = lane; t < q.n; t += 32)
-                        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(yo + (int64_t)(q.first + t) * yo_st + o),
-                                     "r"(from + t * S::kYRow), "r"(4 * min(S::kOut, out - o))
-                                     : "memory");
-                }
+                if (whole && lane == 0)
+                    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(&maps.out[mat]), "r"(o), "r"(q.first),
+                                 "r"(from)
+                                 : "memory");
                 asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
                 if (i + S::kStages < tiles) {
                     asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
@@ -910,7 +905,7 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
             float *dst = yo + (int64_t)(q.first + tok0) * yo_st + o;
 #pragma unroll
             for (int h = 0; h < 32; h += 16) {
-                if (BULK && !chunks) continue;  // y goes back as it came
+                if (BULK && whole && !chunks) continue;  // y goes back as it came
                 float d[16] = {}, v[16];
                 if (chunks) tmem_ld16(s_tmem + ((uint32_t)(32 * (warp & 3)) << 16) + tok0 + h, d);
 #pragma unroll
@@ -935,7 +930,7 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
                 }
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    if (BULK) {
+                    if (BULK && whole) {
                         asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(mine + (h + k) * S::kYRow), "f"(v[k]) : "memory");
                     } else {
                         if (h + k < toks && o < out) *dst = v[k];
