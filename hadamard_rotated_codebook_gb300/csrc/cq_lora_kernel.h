@@ -1174,7 +1174,8 @@ int launch_up(LoraParams &p, cudaStream_t st) {
     // Tiles that a block takes after another: a block's beginning costs about as much as two, and blocks that do not fit wait for others.
     long long best = LLONG_MAX;
     p.runs = 1;
-    for (int r = 1; r <= tiles; r *= 2) {
+    for (int parts = 1; parts <= tiles; parts += parts < 16 ? 1 : parts) {
+        const int r = (tiles + parts - 1) / parts;
         long long blocks = 0;
         for (int j = 0; j < p.d.n_mats; ++j) blocks += pieces * (((p.d.out[j] + tile - 1) / tile + r - 1) / r);
         const long long cost = (blocks + room - 1) / room * (r + 2);
