@@ -22,9 +22,10 @@ size_t lora_plan(const cq_lora_desc &d, bool few, bool tensor, LoraParams &p) {
     p.few = few;
     p.tensor = tensor;
     p.u_row = (d.rank + ranks - 1) / ranks * ranks;
-    // Parts of k: enough for three blocks on every SM, while a block keeps 512 inputs and more. On tcgen05 no more blocks than the two of
-    // an SM that run at once, and fewer sums to add (8190 tokens, 4096 to 4096, rank 64: 73 us with four parts, 77 with eight).
-    const long long room = tensor ? sm_count() : 3ll * sm_count() - 1;
+    // Parts of k, while a block keeps 512 inputs and more: no more blocks than run at once (three an SM for few tokens: 32 requests of 8
+    // tokens 11.0 us, 13.3 with twice the parts; two on tcgen05: 8190 tokens, rank 64 73 us, 77 with twice), as the sums of all are
+    // read again. fp32 prompts, which cost more instructions, want the last round full (50.2 us, 51.7 with half the parts).
+    const long long room = tensor ? sm_count() : few ? 3ll * sm_count() / 2 : 3ll * sm_count() - 1;
     p.splits = 1;
     while (p.splits < kMaxSplits && pieces * d.n_mats * p.splits <= room && d.in >= 1024 * p.splits) p.splits *= 2;
     p.runs = 1;
@@ -35,9 +36,17 @@ size_t lora_plan(const cq_lora_desc &d, bool few, bool tensor, LoraParams &p) {
     p.pieces = (int)pieces;
     return (size_t)d.n_mats * p.splits * d.n_tokens * p.u_row * sizeof(float);
 }
-// Requests have few tokens on average: pieces of 8 then, on mma.sync. (32 requests of 20 tokens, 4096 to 4096, rank 16: 18.7 us against 26; 19 of 0 to
-// 32, 1000 to 777: 7.3 against 11.3. 8 of 40 tokens, two of 2048 to 2048, rank 64: 21 against 16.6.)
-bool lora_few(const cq_lora_desc &d) { return d.n_tokens <= 32ll * d.n_seqs; }
+// Pieces of 8 tokens on mma.sync: where requests have few tokens each, whose adapters are then what there is to read, and where there
+// are few tokens in all, as tcgen05's kernels take 6 us longer to begin and end. Their cost a token goes by the ranks and, as y is
+// read and written, more by the outputs than by the inputs. (4096 to 4096, few against many: rank 16, a prompt of 40 tokens 5.7 us
+// against 12.6, of 512 12.3 against 15.5, four of 512 31 against 24; 32 requests of 20 16 against 26; rank 64, one of 256 15.1 against
+// 18.5, one of 512 23.0 against 19.6, 16 requests of 32 29 against 23, 64 of 16 50 against 49.)
+bool lora_few(const cq_lora_desc &d) {
+    const long long tiles = (d.rank + 15) / 16;
+    long long side = d.in;
+    for (int j = 0; j < d.n_mats; ++j) side += 3ll * d.out[j];
+    return d.n_tokens <= std::max(16ll, 32 / tiles) * d.n_seqs || (double)d.n_tokens * (double)(tiles * side) <= 12e6;
+}
 
 }  // namespace
 
@@ -88,8 +97,8 @@ size_t cq_lora_workspace(const cq_lora_desc *d) {
     clear_error();
     LoraParams p;
     if (check_lora(d) || !d->n_mats || !d->n_tokens || !d->n_seqs) return 0;
-    const size_t plain = lora_plan(*d, false, false, p), many = lora_plan(*d, false, true, p), few = lora_few(*d) ? lora_plan(*d, true, false, p) : 0;
-    return plain && many ? std::max(plain, std::max(many, few)) : 0;
+    const size_t plain = lora_plan(*d, false, false, p), many = lora_plan(*d, false, true, p), few = lora_plan(*d, true, false, p);
+    return plain && many && few ? std::max(plain, std::max(many, few)) : 0;
 }
 
 int cq_lora_add(const cq_lora_desc *d, void *stream) {

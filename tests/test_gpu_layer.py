@@ -1,6 +1,7 @@
 """GPU parity of a layer's other serving steps (cq_block_norm, cq_lora_add)
 with their 64-bit definitions."""
 import math
+import sys
 
 import numpy as np
 import pytest
@@ -468,3 +469,147 @@ def test_lora_is_the_same_every_time(C):
         g.replay()
         ref = C.cq_lora_add(**dict(kw, outs=[torch.empty_like(want)]))[0]
         assert torch.equal(outs[0], ref) and not torch.equal(ref, want)
+
+
+# Which kernels a call takes goes by its tokens, ranks and widths. What stands above is taken once more with so many rows that no
+# request covers that the kernels of many tokens run.
+
+def _rows_for_many(new, n_in, outs, rank):
+    return 13_000_000 // (-(-rank // 16) * (n_in + 3 * sum(outs))) + 33 * len(new)
+
+
+@pytest.fixture
+def many(monkeypatch):
+    make = _lora_inputs
+
+    def wide(new, adapters, n_in, outs, rank, *args, extra=0, **kw):
+        return make(new, adapters, n_in, outs, rank, *args, extra=extra + _rows_for_many(new, n_in, outs, rank), **kw)
+
+    monkeypatch.setattr(sys.modules[__name__], "_lora_inputs", wide)
+
+
+def _both_ways(C, kw, n):
+    """Into outputs of their own and in place: the same bits (of the requests' rows)."""
+    a, b = _check_lora(C, kw), _check_lora(C, kw, True)
+    assert all(torch.equal(p[:n], q[:n]) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("w,x", W_X)
+@pytest.mark.parametrize("new", [[1], [5, 0, 33, 1], [200, 3], [64, 0, 128, 65, 63]])
+def test_lora_of_many_types(C, many, w, x, new):
+    kw = _lora_inputs(new, [i % 3 for i in range(len(new))], 512, (256, 128), 16, w, x, seed=len(new))
+    _both_ways(C, kw, sum(new))
+
+
+@pytest.mark.parametrize("rank", [1, 8, 15, 16, 17, 20, 32, 33, 48, 64, 65, 100, 128, 255, 256])
+def test_lora_of_many_ranks(C, many, rank):
+    for new in ([1, 1, 1], [70, 2]):
+        for w, x, outs in ((BF16, F32, (96, 33)), (F16, I8, (96, 33)), (BF16, BF16, (300,)), (F16, F16, (300,))):
+            _both_ways(C, _lora_inputs(new, [i % 2 for i in range(len(new))], 160, outs, rank, w, x, seed=rank), sum(new))
+
+
+@pytest.mark.parametrize("n_in,out", [(1, 1), (7, 5), (8, 4), (31, 33), (32, 32), (40, 64), (1000, 777), (1001, 100), (2048, 36), (520, 2052), (6000, 4100), (136, 128),
+                                        (264, 129), (72, 1000)])
+@pytest.mark.parametrize("x", [F32, I8, F16])
+def test_lora_of_many_sizes(C, many, n_in, out, x):
+    test_lora_sizes(C, n_in, out, x)
+
+
+def test_lora_of_many_long_prompts(C, many):
+    test_lora_long_prompts(C)
+    test_lora_many_requests(C)
+    test_lora_rows_on_eight_bytes(C)
+
+
+@pytest.mark.parametrize("new", [[3, 1, 1, 2], [100, 30, 1, 2]])
+def test_lora_of_many_ranks_in_use(C, many, new):
+    test_lora_ranks_in_use(C, new)
+
+
+def test_lora_of_many_values_of_every_size(C, many):
+    for w in (F16, BF16):
+        for rank in (16, 40, 130):
+            kw = _lora_inputs([70, 40], [0, 1], 128, (140,), rank, w, F32, seed=rank)
+            kw["x"][:110] *= torch.exp2(torch.linspace(-60, 60, 110, device="cuda"))[:, None]
+            kw["a"][0] *= torch.exp2(-(torch.arange(rank, device="cuda") % 9).float())[None, :, None].to(w)
+            _check_lora(C, kw)
+
+
+def test_lora_of_many_without_adapters(C, many):
+    kw = _lora_inputs([200, 90], [-1, -1], 64, (160,), 8, n_adapters=1)
+    none = dict(kw, a=[kw["a"][0][:0]], b=[kw["b"][0][:0]], scales=None)
+    for k in (kw, none):
+        outs = [torch.full_like(kw["ys"][0], 7.0)]
+        C.cq_lora_add(**dict(k, outs=outs))
+        assert torch.equal(outs[0][:290], kw["ys"][0][:290]) and (outs[0][290:] == 7.0).all()
+    C.cq_device_status()
+
+
+def test_lora_of_many_strides(C, many):
+    """Rows of wider tensors, on and off vector boundaries; one row of x and y for every token."""
+    for x in (F32, BF16):
+        kw = _lora_inputs([3, 70], [0, 1], 256, (128, 64), 16, BF16, x)
+        n = kw["x"].shape[0]
+        cu = [0, 3, 73]
+        args = [_np(a) for a in kw["a"]], [_np(b) for b in kw["b"]], [0, 1], cu, _np(kw["scales"])
+        want = L.lora([_np(y) for y in kw["ys"]], _np(kw["x"]), *args, terms=x == F32)
+        for off in (8, 4, 1):
+            wide = torch.zeros(n, 256 + 8, device="cuda", dtype=x)
+            wide[:, off:off + 256] = kw["x"]
+            packed = torch.full((n, 128 + 64 + 8), 3.0, device="cuda")
+            parts = [packed[:, off:off + 128], packed[:, off + 128:off + 192]]
+            for p, y in zip(parts, kw["ys"]):
+                p.copy_(y)
+            got = C.cq_lora_add(**dict(kw, x=wide[:, off:off + 256], ys=parts))
+            for p, (o, e) in zip(got, want):
+                assert (np.abs(_np(p) - o) <= e).all()
+            assert (packed[:, :off] == 3.0).all() and (packed[:, off + 192:] == 3.0).all()
+        kw["x"] = kw["x"][:1].expand(n, 256)
+        kw["ys"] = [y[:1].expand(n, y.shape[1]) for y in kw["ys"]]
+        _check_lora(C, kw)
+
+
+def test_lora_of_many_non_finite_tokens_stay_apart(C, many):
+    for x in (F32, BF16):
+        kw = _lora_inputs([60, 50], [0, 1], 96, (48,), 20, BF16, x)
+        want = C.cq_lora_add(**dict(kw, outs=[torch.zeros_like(kw["ys"][0])]))[0]
+        kw["x"][1, 5], kw["x"][2, 9] = math.nan, math.inf
+        kw["x"][110:] = math.nan  # rows that no request covers
+        got = C.cq_lora_add(**dict(kw, outs=[torch.zeros_like(kw["ys"][0])]))[0]
+        keep = torch.ones(len(got), dtype=torch.bool, device="cuda")
+        keep[1:3] = False
+        assert got[1].isnan().all() and not got[2].isfinite().any() and torch.equal(got[keep], want[keep])
+
+
+def test_lora_of_many_is_the_same_every_time(C):
+    new = [600, 5, 1]
+    kw = _lora_inputs(new, [0, 1, 2], 4096, (1024,), 64, BF16, I8, n_adapters=4)
+    outs = [torch.empty_like(kw["ys"][0])]
+    want = C.cq_lora_add(**dict(kw, outs=outs))[0].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        C.cq_lora_add(**dict(kw, outs=outs))
+    for _ in range(5):
+        outs[0].zero_()
+        g.replay()
+        assert torch.equal(outs[0], want)
+    kw["adapters"].copy_(_i32([3, 0, 1]))
+    kw["cu_tokens"].copy_(_i32([0, 70, 71, 606]))
+    g.replay()
+    ref = C.cq_lora_add(**dict(kw, outs=[torch.empty_like(want)]))[0]
+    assert torch.equal(outs[0], ref) and not torch.equal(ref, want)
+
+
+def test_lora_kernels_agree_over_the_whole_range(C):
+    """The same requests in calls of either kind."""
+    for x, rank in ((I8, 16), (F32, 40), (BF16, 200)):
+        kw = _lora_inputs([90, 0, 33, 1], [0, 1, 2, -1], 512, (260, 64), rank, BF16, x, seed=rank)
+        got = _check_lora(C, kw)
+        more = _rows_for_many([90, 0, 33, 1], 512, (260, 64), rank)
+
+        def pad(t):
+            return torch.cat([t, torch.ones(more, *t.shape[1:], device="cuda").to(t.dtype)])
+
+        wide = dict(kw, x=pad(kw["x"]), ys=[pad(y) for y in kw["ys"]], x_scale=None if kw["x_scale"] is None else pad(kw["x_scale"]))
+        both = _check_lora(C, wide)
+        assert not torch.equal(both[0][:124], got[0]) or x == I8  # other orders of the sums
