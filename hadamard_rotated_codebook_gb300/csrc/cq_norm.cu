@@ -17,10 +17,11 @@
 // quotient only where that lies next to a tie (store_codes): a division per element took 88 us where this takes 61.
 //
 // The bound is memory, and issue slots next to it (two elements to an instruction where there is one for that). 8190 rows of
-// 4096 in fp32 onto bf16 with a norm of the branch, to int8 (302 MB): 61 us, 4.9 TB/s or 73% of the copy rate; 16383 of 2048 in bf16 with
-// a silu gate for every element (336 MB): 70 us, 70%, issue slots at 60%; 8190 of 4096 in bf16 without either: 47 us, 84%. Steps of a
+// 4096 in fp32 onto bf16 with a norm of the branch, to int8 (302 MB): 61 us, 5.0 TB/s or 73% of the copy rate; 16383 of 2048 in bf16 with
+// a silu gate for every element (336 MB): 68 us, 73%, issue slots at 70%; 8190 of 4096 in bf16 without either: 47 us, 84%. Steps of a
 // few rows take 3 to 5 us, which is two latencies of memory and the launch. Rows of 16384 in fp32 leave the ring one stage (51%).
-// Tried and slower: four runs a lane instead of two (94 against 69 us: half as many warps wait).
+// Tried and slower: four runs a lane instead of two (94 against 69 us: half as many warps wait), one run a lane (78
+// against 61 us to int8: an element costs more instructions, though single rows are 0.5 us faster), weights loaded before the reductions (76 us: registers).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -288,9 +289,11 @@ __device__ __forceinline__ void take_run(Raw &r, uint32_t from, int type) {
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(r.b.x), "=r"(r.b.y), "=r"(r.b.z), "=r"(r.b.w) : "r"(from + 16) : "memory");
 }
 
-// VEC: rows are whole runs on 16-byte boundaries and come through the ring.
+// VEC: rows are whole runs on 16-byte boundaries and come through the ring. Without a least number of blocks given the compiler takes 2 to 18
+// registers fewer, at a price in instructions: 16383 rows of 2048, gated, 71 us against 68, 65536 of 512 54 against 51. Rows read element by
+// element want the warps instead (40000 of 333: 95 us with one block, 86 with six).
 template <int CH, bool WARP, bool VEC, bool GATE>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : 32 * kMaxWarps) block_norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : 32 * kMaxWarps, WARP && !VEC ? 6 : 1) block_norm_kernel(const __grid_constant__ NormParams p) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 s_buf[4][kMaxWarps];
     __shared__ uint64_t s_full[WARP ? kWarpTeams : 1][kMaxDepth];
@@ -473,7 +476,7 @@ int launch_block_norm(const cq_norm_desc &d, void *stream) {
     p.stage = p.at_gate + (p.gate && !p.one_gate ? p.d * size_of(p.x_type) : 0);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (d.width <= kWarpRow) {
-        const int per_sm = 12;  // 65536 rows of 512 in bf16: 54 us; 61 with 6
+        const int per_sm = 12;  // 65536 rows of 512 in bf16: 51 us; 54 with 10, 55 with 24
         p.depth = std::max(1, std::min(kMaxDepth, ring_bytes(per_sm) / kWarpTeams / p.stage));
         const int grid = (int)std::min<long long>(((long long)p.rows + kWarpTeams - 1) / kWarpTeams, (long long)sms * per_sm);
         return chunks <= 32 ? launch_c<1, true>(p, vec, grid, 32 * kWarpTeams, st) : launch_c<2, true>(p, vec, grid, 32 * kWarpTeams, st);
