@@ -613,3 +613,22 @@ def test_lora_kernels_agree_over_the_whole_range(C):
         wide = dict(kw, x=pad(kw["x"]), ys=[pad(y) for y in kw["ys"]], x_scale=None if kw["x_scale"] is None else pad(kw["x_scale"]))
         both = _check_lora(C, wide)
         assert not torch.equal(both[0][:124], got[0]) or x == I8  # other orders of the sums
+
+
+@pytest.mark.parametrize("new,rank", [([1] * 20, 16), ([1200, 0, 5], 64)])
+def test_lora_on_two_streams_at_once(C, new, rank):
+    """Calls of different inputs side by side, each with a workspace of its own."""
+    kws = [_lora_inputs(new, [i % 3 for i in range(len(new))], 1024, (1024, 256), rank, BF16, BF16, seed=s, n_adapters=3) for s in range(2)]
+    want = [C.cq_lora_add(**dict(kw, outs=[torch.empty_like(y) for y in kw["ys"]])) for kw in kws]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in kws]
+    outs = [[[torch.zeros_like(y) for y in kw["ys"]] for _ in range(8)] for kw in kws]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for kw, s, o in zip(kws, streams, outs):
+            with torch.cuda.stream(s):
+                C.cq_lora_add(**dict(kw, outs=o[i]))
+    torch.cuda.synchronize()
+    C.cq_device_status()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(a, b) for got in o for a, b in zip(got, w))

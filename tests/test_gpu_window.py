@@ -254,3 +254,18 @@ def test_window_refuses(C):
 def test_window_column_tiles_have_windows_of_their_own(C, geom, window, sinks, ctx):
     """Chunks over many column tiles: windows that begin before, within and behind the chunk, sinks that reach into it."""
     Case(C, [ctx, 7, 0], [150, 256, 31], window, sinks, geom, (2, 2), 32, dtype=BF16, seed=window).check()
+
+
+def test_window_on_two_streams_at_once(C):
+    cases = [Case(C, [700, 90, 3], [1, 30, 200], 64, 4, seed=1), Case(C, [300, 2000], [4, 1], 500, 0, bits=(4, 3), seed=2)]
+    want = [c.run() for c in cases]
+    args = [(c.args(), torch.cuda.Stream(), [torch.zeros_like(w) for _ in range(8)]) for c, w in zip(cases, want)]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for c, (a, s, o) in zip(cases, args):
+            with torch.cuda.stream(s):
+                C.cq_kv_window_attend(*a, c.window, c.sinks, o=o[i])
+    torch.cuda.synchronize()
+    C.cq_device_status()
+    for w, (_, _, o) in zip(want, args):
+        assert all(torch.equal(x, w) for x in o)
