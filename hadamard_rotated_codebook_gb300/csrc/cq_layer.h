@@ -24,6 +24,8 @@ struct LoraParams {
     bool tensor;   // x and A by tensor copies: rows on 16 bytes, and no fp32
     bool vec_b;    // rows of B in runs of 4
     bool vec_y[CQ_LORA_MAX_MATS];  // rows of y likewise
+    unsigned spin;  // polls after which a wait gives up
+    bool give_up;   // the kernels on tcgen05 wait for what never ends, and a few polls at most (a self-test)
 };
 // Tiles of 16 ranks that a block of the first product takes.
 constexpr int lora_rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }

@@ -101,7 +101,7 @@ size_t cq_lora_workspace(const cq_lora_desc *d) {
     return plain && many && few ? std::max(plain, std::max(many, few)) : 0;
 }
 
-int cq_lora_add(const cq_lora_desc *d, void *stream) {
+static int lora_add(const cq_lora_desc *d, bool give_up, void *stream) {
     clear_error();
     const int st = check_lora(d);
     if (st) return st;
@@ -142,8 +142,12 @@ int cq_lora_add(const cq_lora_desc *d, void *stream) {
         return set_error(CQ_ERR_ARG, "workspace of %zu bytes needed (16-byte aligned), got %zu", need, d->workspace ? d->workspace_bytes : 0);
     p.u = static_cast<float *>(d->workspace);
     p.status = device_status_ptr();
+    p.give_up = give_up;
     if (!p.status) return set_error(CQ_ERR_CUDA, "no device status word");
     return d->w_dtype == CQ_T_F16 ? launch_lora_f16(p, stream) : launch_lora_bf16(p, stream);
 }
+
+int cq_lora_add(const cq_lora_desc *d, void *stream) { return lora_add(d, false, stream); }
+int cq_selftest_lora_timeout(const cq_lora_desc *d, void *stream) { return lora_add(d, true, stream); }
 
 }  // extern "C"

@@ -696,21 +696,31 @@ __device__ __forceinline__ void tmem_ld16(uint32_t a, float (&v)[16]) {
                  : "r"(a)
                  : "memory");
 }
-// A product that is not done within kSpin polls marks the status word; the block then runs on without waiting.
-__device__ __forceinline__ void wait(const LoraParams &p, uint32_t bar, uint32_t parity, volatile int &abort) {
-    for (unsigned i = 0;; ++i) {
-        uint32_t ok;
-        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-                     : "=r"(ok)
-                     : "r"(bar), "r"(parity), "r"(1000u)
-                     : "memory");
-        if (ok || abort) return;
-        if (i >= kSpin) {
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity), "r"(1000u)
+                 : "memory");
+    return ok;
+}
+// A wait that is not over within p.spin polls marks the status word and sets `abort`, at which every wait of the block that is not over gives up (false).
+// Who gave up sends no copy, product or arrival after it; what was sent is waited for at the block's end (drain).
+__device__ __forceinline__ bool wait(const LoraParams &p, uint32_t bar, uint32_t parity, volatile int &abort) {
+    for (unsigned i = 0; !poll(bar, parity); ++i) {
+        if (abort) return false;
+        if (i >= p.spin) {
             atomicOr(p.status, 0x474B0001u);
             abort = 1;
-            return;
+            return false;
         }
     }
+    return true;
+}
+__device__ __forceinline__ bool all(bool ok) { return __all_sync(0xFFFFFFFFu, ok); }
+// The end of a copy or product that was sent, for a block that gave up.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+    for (unsigned i = 0; i < kSpin && !poll(bar, parity); ++i) {}
 }
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
@@ -747,7 +757,7 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
                                                                                                const __grid_constant__ UpMaps maps) {
     using S = UpMany<T, MT>;
     extern __shared__ uint8_t smem_many[];
-    __shared__ uint64_t s_bars[1 + 2 * S::kStages];  // products done, y there, results there
+    __shared__ uint64_t s_bars[2 + 2 * S::kStages];  // products done, y there, results there; one that nothing completes
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31, mat = blockIdx.z;
@@ -768,7 +778,7 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
     }
     if (tid == 0) {
         s_abort = 0;
-        for (int i = 0; i < 1 + 2 * S::kStages; ++i)
+        for (int i = 0; i < 2 + 2 * S::kStages; ++i)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(done + 8 * i), "r"(i < 1 + S::kStages ? 1 : kWarps));
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -779,10 +789,12 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
     // A tensor copy writes whole tiles: of a piece of fewer tokens each thread writes its own results. (A copy for each row instead held
     // the launch up: 8190 tokens of three requests 73 us against 64.)
     const bool whole = q.n == S::kTok;
+    int sent = 0;  // tiles of y (the ninth warp's); products (the others')
     if (warp == kWarps) {
         if (BULK) {
             // A copy reads whole tiles, rows of the next piece among them.
             auto load = [&](int i) {
+                sent = i + 1;
                 if (lane == 0) {
                     const uint32_t bar = full + i % S::kStages * 8;
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(S::kY) : "memory");
@@ -792,7 +804,7 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
             for (int i = 0; i < S::kStages && i < tiles; ++i) load(i);
 #pragma unroll 1
             for (int i = 0; i < tiles; ++i) {
-                wait(p, ready + i % S::kStages * 8, (uint32_t)(i / S::kStages) & 1, s_abort);
+                if (!all(wait(p, ready + i % S::kStages * 8, (uint32_t)(i / S::kStages) & 1, s_abort))) break;
                 const uint32_t from = base + S::oY + i % S::kStages * S::kY;
                 const int o = (t0 + i) * S::kOut;
                 if (whole && lane == 0)
@@ -814,6 +826,7 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
         const bool vec_b = p.d.rank % 8 == 0 && (reinterpret_cast<uintptr_t>(p.d.b[mat]) & 15) == 0;
         const int chunks = (q.rank + S::kRank - 1) / S::kRank;
         uint32_t par = 0;
+        bool live = true;  // (of the issuing warp) products have come to their end so far
         // 128 rows of B, 8 ranks at a time, zeros where there is nothing
         auto fill = [&](int tile, int chunk) {
             const int r0 = chunk * S::kRank, rank = min(S::kRank, q.rank - r0);
@@ -844,7 +857,8 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
             fence_async();
             fence_before();
             bar_sync(1, kThreads);
-            if (warp) return;
+            if (warp || !live) return;
+            ++sent;
             fence_after();
             const uint64_t a = desc_sw128(base + S::oB), b = desc_sw128(base);
             const uint32_t d = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
@@ -856,7 +870,8 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
             mma_commit(done);
         };
         auto products = [&]() {
-            wait(p, done, par, s_abort);
+            const bool ended = wait(p, p.give_up ? done + 8 * (1 + 2 * S::kStages) : done, par, s_abort);
+            if (warp == 0) live = all(live && ended);
             par ^= 1;
             fence_after();
         };
@@ -900,7 +915,8 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
             if (chunks == 1 && i + 1 < tiles) fill(i + 1, 0);
             const int o = (t0 + i) * S::kOut + 32 * (warp & 3) + lane;
             const uint32_t mine = from + i % S::kStages * S::kY;
-            if (BULK) wait(p, full + i % S::kStages * 8, (uint32_t)(i / S::kStages) & 1, s_abort);
+            bool there = true;
+            if (BULK) there = wait(p, full + i % S::kStages * 8, (uint32_t)(i / S::kStages) & 1, s_abort);
             const float *src = y + (int64_t)(q.first + min(tok0, q.n - 1)) * y_st + min(o, out - 1);  // (what is not there: the last one again)
             float *dst = yo + (int64_t)(q.first + tok0) * yo_st + o;
 #pragma unroll
@@ -941,7 +957,7 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
             if (BULK) {
                 fence_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(ready + i % S::kStages * 8);
+                if (lane == 0 && there) mbar_arrive(ready + i % S::kStages * 8);
             }
             if (i + 1 < tiles) {
                 if (chunks == 1) issue(false);
@@ -951,6 +967,12 @@ __global__ void __launch_bounds__(kManyThreads, (UpMany<T, MT>::kBlocks)) lora_u
         fence_before();
     }
     __syncthreads();
+    if (s_abort) {  // no wait of a block that gave up says that these have ended
+        if (warp == kWarps)
+            for (int i = max(0, sent - S::kStages); i < sent; ++i) drain(full + i % S::kStages * 8, (uint32_t)(i / S::kStages) & 1);
+        else if (warp == 0 && sent) drain(done, (uint32_t)(sent - 1) & 1);
+        __syncwarp();
+    }
     if (warp == 0) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(s_tmem), "r"(S::kTok));
@@ -980,7 +1002,7 @@ __global__ void __launch_bounds__(kDownThreads, (DownMany<T, XK, MT>::kBlocks)) 
                                                                                                      const __grid_constant__ DownMaps maps) {
     using S = DownMany<T, XK, MT>;
     extern __shared__ uint8_t smem_down[];
-    __shared__ uint64_t s_bars[3 * S::kDepth + 1];  // stages there, turned, free; the sums done
+    __shared__ uint64_t s_bars[3 * S::kDepth + 2];  // stages there, turned, free; the sums done; one that nothing completes
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
@@ -998,20 +1020,22 @@ __global__ void __launch_bounds__(kDownThreads, (DownMany<T, XK, MT>::kBlocks)) 
     }
     if (tid == 0) {
         s_abort = 0;
-        for (int i = 0; i < 3 * S::kDepth + 1; ++i)
+        for (int i = 0; i < 3 * S::kDepth + 2; ++i)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(full + 8 * i), "r"(i >= S::kDepth && i < 2 * S::kDepth ? 4 : 1));
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     fence_before();
     __syncthreads();
     fence_after();
+    int sent = 0;  // stages (lane 0 of warp 0)
     if (warp == 0) {
         if (lane == 0) {
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 const int st = i % S::kDepth;
                 const uint32_t at = base + st * S::kStage, bar = full + 8 * st;
-                if (i >= S::kDepth) wait(p, empty + 8 * st, (uint32_t)(i / S::kDepth - 1) & 1, s_abort);
+                if (i >= S::kDepth && !wait(p, empty + 8 * st, (uint32_t)(i / S::kDepth - 1) & 1, s_abort)) break;
+                sent = i + 1;
                 asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"((XK == CQ_T_I8 ? S::kRaw : S::kX) + S::kA) : "memory");
                 tma_load(XK == CQ_T_I8 ? at + S::kX + S::kA : at, &maps.x, (c0 + i) * S::kIn, q.first, bar);
                 tma_load(at + S::kX, &maps.a[mat], (c0 + i) * S::kIn, q.adapter * p.d.rank + r0, bar);
@@ -1023,9 +1047,9 @@ __global__ void __launch_bounds__(kDownThreads, (DownMany<T, XK, MT>::kBlocks)) 
         for (int i = 0; i < n; ++i) {
             const int st = i % S::kDepth;
             const uint32_t par = (uint32_t)(i / S::kDepth) & 1;
-            wait(p, full + 8 * st, par, s_abort);
-            if (XK == CQ_T_I8) wait(p, turned + 8 * st, par, s_abort);
-            __syncwarp();
+            bool there = wait(p, p.give_up ? done + 8 : full + 8 * st, par, s_abort);
+            if (XK == CQ_T_I8) there = wait(p, turned + 8 * st, par, s_abort) && there;
+            if (!all(there)) break;
             fence_after();
             const uint64_t a = desc_sw128(base + st * S::kStage), b = desc_sw128(base + st * S::kStage + S::kX);
 #pragma unroll
@@ -1040,7 +1064,7 @@ __global__ void __launch_bounds__(kDownThreads, (DownMany<T, XK, MT>::kBlocks)) 
             for (int i = 0; i < n; ++i) {  // a token to a thread
                 const int st = i % S::kDepth;
                 const uint32_t to = base + st * S::kStage, from = to + S::kX + S::kA + row * 64;
-                wait(p, full + 8 * st, (uint32_t)(i / S::kDepth) & 1, s_abort);
+                if (!all(wait(p, full + 8 * st, (uint32_t)(i / S::kDepth) & 1, s_abort))) break;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint4 v = lds16(from + ((j ^ (row >> 1 & 3)) << 4));  // 16 inputs, 64-byte swizzled
@@ -1081,6 +1105,11 @@ __global__ void __launch_bounds__(kDownThreads, (DownMany<T, XK, MT>::kBlocks)) 
         fence_before();
     }
     __syncthreads();
+    if (s_abort) {  // no wait of a block that gave up says that these have ended
+        for (int i = max(0, sent - S::kDepth); i < sent; ++i) drain(full + 8 * (i % S::kDepth), (uint32_t)(i / S::kDepth) & 1);
+        if (warp == 1) drain(done, 0);
+        __syncwarp();
+    }
     if (warp == 1) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(s_tmem), "r"(S::kCols));
@@ -1218,6 +1247,7 @@ int launch_x(LoraParams &p, cudaStream_t st) {
 }
 template <typename T>
 int launch_t(LoraParams &p, cudaStream_t st) {
+    p.spin = p.give_up ? 4 : kSpin;
     if (p.d.x_dtype == CQ_T_F32) return p.vec ? launch_x<T, CQ_T_F32, true>(p, st) : launch_x<T, CQ_T_F32, false>(p, st);
     if (p.d.x_dtype == CQ_T_I8) return p.vec ? launch_x<T, CQ_T_I8, true>(p, st) : launch_x<T, CQ_T_I8, false>(p, st);
     return p.vec ? launch_x<T, CQ_T_F16, true>(p, st) : launch_x<T, CQ_T_F16, false>(p, st);

@@ -715,6 +715,15 @@ int cq_selftest_tree_smem(int reserved);
 int cq_selftest_tree_timeout(const cq_kv_geom *geom, const cq_kv_tree *t,
                              void *stream);
 
+/* Diagnostic without a counterpart on the pages: cq_lora_add whose kernels of
+ * many tokens wait for what nothing ends, and give up after a few polls: no
+ * further copy or product is sent, those in flight are waited for (bounded),
+ * tensor memory is freed. Outputs hold nothing of use; a following
+ * cq_device_status reports CQ_ERR_TIMEOUT (code 0x474B0001), and the next call
+ * works as ever. (The kernels of few tokens wait for nothing that could fail
+ * to come.) Errors: as for cq_lora_add. */
+int cq_selftest_lora_timeout(const cq_lora_desc *d, void *stream);
+
 /* -------------------------------------------------------- container -- */
 /*
  * Own .cact-shaped container (the pages disagree on the header: 196 bytes
