@@ -181,6 +181,7 @@ SIGNATURES = {
     "cq_selftest_wait_timeout": (c_int, [c_void_p]),
     "cq_selftest_tree_smem": (c_int, [c_int]),
     "cq_selftest_tree_timeout": (c_int, [P(KvGeom), P(KvTree), c_void_p]),
+    "cq_selftest_norm_timeout": (c_int, [P(NormDesc), c_void_p]),
     "cq_selftest_lora_timeout": (c_int, [P(LoraDesc), c_void_p]),
     "cq_selftest_dirty_counters": (c_int, [c_void_p]),
     "cq_cact_write": (c_int, [c_char_p, P(TensorDesc), c_int, P(c_float), c_uint32]),

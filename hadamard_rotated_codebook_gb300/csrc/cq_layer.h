@@ -7,7 +7,8 @@
 
 namespace cq {
 
-int launch_block_norm(const cq_norm_desc &d, void *stream);
+// give_up: the kernel waits for what never lands, and a few polls at most (a self-test).
+int launch_block_norm(const cq_norm_desc &d, bool give_up, void *stream);
 
 // A call of cq_lora_add as its kernels take it.
 constexpr int kMaxSplits = 8;

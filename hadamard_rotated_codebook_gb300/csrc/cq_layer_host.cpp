@@ -52,7 +52,7 @@ bool lora_few(const cq_lora_desc &d) {
 
 extern "C" {
 
-int cq_block_norm(const cq_norm_desc *d, void *stream) {
+static int block_norm(const cq_norm_desc *d, bool give_up, void *stream) {
     clear_error();
     if (!d) return set_error(CQ_ERR_ARG, "null descriptor");
     if (!is_float(d->x_dtype) || !is_float(d->residual_dtype) || (!is_float(d->out_dtype) && d->out_dtype != CQ_T_I8))
@@ -73,8 +73,11 @@ int cq_block_norm(const cq_norm_desc *d, void *stream) {
         return set_error(CQ_ERR_SHAPE, "output rows of %d elements are %lld and %lld apart", d->width, (long long)d->residual_out_stride,
                          (long long)d->out_stride);
     if (d->residual_out == d->out) return set_error(CQ_ERR_ARG, "the two outputs share memory");
-    return launch_block_norm(*d, stream);
+    return launch_block_norm(*d, give_up, stream);
 }
+
+int cq_block_norm(const cq_norm_desc *d, void *stream) { return block_norm(d, false, stream); }
+int cq_selftest_norm_timeout(const cq_norm_desc *d, void *stream) { return block_norm(d, true, stream); }
 
 // Sizes and types that a call needs right, whatever its pointers.
 static int check_lora(const cq_lora_desc *d) {

@@ -55,6 +55,8 @@ struct NormParams {
     bool post, one_gate;  // one_gate: a gate per row
     float eps, offset, branch, keep, inv_d;
     unsigned int *status;
+    unsigned spin;        // polls after which a wait gives up
+    bool give_up;         // waits are for what never lands (a self-test)
     int depth;            // stages of a team's ring
     int stage, at_res, at_gate;  // bytes of a stage; where its tensors begin
 };
@@ -267,26 +269,39 @@ __device__ __forceinline__ void fetch_row(const NormParams &p, int64_t row, uint
     if (nr) bulk(to + p.at_res, static_cast<const uint8_t *>(p.res) + row * p.res_st * rsize, nr, bar);
     if (ng) bulk(to + p.at_gate, static_cast<const uint8_t *>(p.gate) + row * p.gate_st * size, ng, bar);
 }
-// A copy that does not land within kSpin polls marks the status word; the block then runs on without waiting.
-__device__ __forceinline__ void wait(const NormParams &p, uint32_t bar, uint32_t parity, volatile int &abort) {
-    for (unsigned i = 0;; ++i) {
-        uint32_t ok;
-        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-                     : "=r"(ok)
-                     : "r"(bar), "r"(parity), "r"(1000u)
-                     : "memory");
-        if (ok || abort) return;
-        if (i >= kSpin) {
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity), "r"(1000u)
+                 : "memory");
+    return ok;
+}
+// A copy that does not land within p.spin polls marks the status word; no wait of the block waits any longer then (false: it has not landed).
+__device__ __forceinline__ bool wait(const NormParams &p, uint32_t bar, uint32_t parity, volatile int &abort) {
+    for (unsigned i = 0; !poll(bar, parity); ++i) {
+        if (abort) return false;
+        if (i >= p.spin) {
             atomicOr(p.status, 0x474A0001u);
             abort = 1;
-            return;
+            return false;
         }
     }
+    return true;
 }
 __device__ __forceinline__ void take_run(Raw &r, uint32_t from, int type) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w) : "r"(from) : "memory");
     if (type == CQ_T_F32)
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(r.b.x), "=r"(r.b.y), "=r"(r.b.z), "=r"(r.b.w) : "r"(from + 16) : "memory");
+}
+
+// Waits (bounded) for copies of a team that gave up, whose ends no wait has seen: those of `row` (none past the last), in stage st with parity par, and of
+// the rows after it.
+__noinline__ __device__ void land(const NormParams &p, int64_t row, int st, uint32_t par, int64_t teams, uint32_t full) {
+    for (int i = 0; i < p.depth && row + i * teams < p.rows; ++i) {
+        const int at = st + i;
+        for (unsigned k = 0; k < kSpin && !poll(full + 8 * (at % p.depth), par ^ (at >= p.depth)); ++k) {}
+    }
 }
 
 // VEC: rows are whole runs on 16-byte boundaries and come through the ring. Without a least number of blocks given the compiler takes 2 to 18
@@ -297,13 +312,19 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : 32 * kMaxWarps, WARP 
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 s_buf[4][kMaxWarps];
     __shared__ uint64_t s_full[WARP ? kWarpTeams : 1][kMaxDepth];
+    __shared__ uint64_t s_never;
+    __shared__ volatile int s_left, s_stage;  // of a block that gave up: see land
+    __shared__ volatile uint32_t s_par;
     __shared__ volatile int s_abort;
     const int lanes = WARP ? 32 : blockDim.x, lane = WARP ? threadIdx.x & 31 : threadIdx.x, team = WARP ? threadIdx.x >> 5 : 0;
     const int64_t teams = WARP ? gridDim.x * kWarpTeams : gridDim.x;
     int64_t row = WARP ? blockIdx.x * kWarpTeams + team : blockIdx.x;
     const uint32_t mine = smem_u32(ring) + team * p.depth * p.stage, full = smem_u32(s_full[team]);
     if (VEC) {
-        if (threadIdx.x == 0) s_abort = 0;
+        if (threadIdx.x == 0) {
+            s_abort = 0, s_left = -1;
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(smem_u32(&s_never)));
+        }
         if (lane == 0) {
             for (int i = 0; i < p.depth; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(full + 8 * i));
             asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -316,7 +337,10 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : 32 * kMaxWarps, WARP 
 #pragma unroll 1
     for (int turn = 0; row < p.rows; row += teams, turn ^= 2) {
         const uint32_t from = mine + st * p.stage;
-        if (VEC) wait(p, full + 8 * st, par, s_abort);
+        if (VEC) {
+            const bool there = wait(p, p.give_up ? smem_u32(&s_never) : full + 8 * st, par, s_abort);
+            if (WARP && !__all_sync(0xFFFFFFFFu, there)) break;  // (a block's teams go on, for their barriers)
+        }
         F2 v[CH][kPairs], sum = {0};
         float none = 0.0f, ib = p.branch;  // what a branch's element is multiplied by, but for its weight
 #pragma unroll
@@ -403,7 +427,13 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : 32 * kMaxWarps, WARP 
         reduce<WARP>(s, top, p.scale != nullptr, s_buf[turn + 1]);  // every lane has read its part of the stage
         if (VEC) {
             const int64_t ahead = row + p.depth * teams;
-            if (lane == 0 && ahead < p.rows) fetch_row(p, ahead, from, full + 8 * st);
+            if (lane == 0) {
+                if (WARP || !s_abort) {
+                    if (ahead < p.rows) fetch_row(p, ahead, from, full + 8 * st);
+                } else if (s_left < 0) {
+                    s_left = (int)row, s_stage = st, s_par = par;
+                }
+            }
             if (++st == p.depth) st = 0, par ^= 1;
         }
         const float inv = rsqrtf(fmaf(s, p.inv_d, p.eps));
@@ -420,6 +450,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : 32 * kMaxWarps, WARP 
             else store_run<VEC>(p.y, row * p.y_st + e, p.y_type, v[c], n);
         }
     }
+    if (VEC && WARP && lane == 0) land(p, row, st, par, teams, full);
+    if (VEC && !WARP && lane == 0 && s_abort && s_left >= 0) land(p, s_left, s_stage, s_par, teams, full);
 }
 
 template <int CH, bool WARP, bool VEC, bool GATE>
@@ -445,7 +477,7 @@ int size_of(int type) { return type == CQ_T_F32 ? 4 : type == CQ_T_I8 ? 1 : 2; }
 
 }  // namespace
 
-int launch_block_norm(const cq_norm_desc &d, void *stream) {
+int launch_block_norm(const cq_norm_desc &d, bool give_up, void *stream) {
     NormParams p;
     p.x = d.x, p.res = d.residual, p.gate = d.gate, p.w = d.weight, p.wb = d.branch_weight;
     p.sum = d.residual_out, p.y = d.out, p.scale = d.out_dtype == CQ_T_I8 ? d.out_scale : nullptr;
@@ -456,6 +488,7 @@ int launch_block_norm(const cq_norm_desc &d, void *stream) {
     p.eps = d.eps, p.offset = d.weight_offset, p.branch = d.branch_scale, p.keep = d.residual_scale;
     p.inv_d = 1.0f / (float)d.width;
     p.status = device_status_ptr();
+    p.spin = give_up ? 4 : kSpin, p.give_up = give_up;
     if (!p.status) return set_error(CQ_ERR_CUDA, "no device status word");
     // Rows in bulk copies and 16-byte accesses (8 of int8) need every row to start on such a boundary.
     bool vec = d.width % kRun == 0;

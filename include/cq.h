@@ -715,6 +715,15 @@ int cq_selftest_tree_smem(int reserved);
 int cq_selftest_tree_timeout(const cq_kv_geom *geom, const cq_kv_tree *t,
                              void *stream);
 
+/* Diagnostic without a counterpart on the pages: cq_block_norm whose waits for
+ * rows are for what never lands, and give up after a few polls: no further row
+ * is fetched, and those on their way are waited for (bounded). Outputs hold
+ * nothing of use; a following cq_device_status reports
+ * CQ_ERR_TIMEOUT (code 0x474A0001), and the next call works as ever. (Rows
+ * that are read element by element are not waited for.) Errors: as for
+ * cq_block_norm. */
+int cq_selftest_norm_timeout(const cq_norm_desc *d, void *stream);
+
 /* Diagnostic without a counterpart on the pages: cq_lora_add whose kernels of
  * many tokens wait for what nothing ends, and give up after a few polls: no
  * further copy or product is sent, those in flight are waited for (bounded),

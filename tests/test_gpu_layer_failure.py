@@ -59,3 +59,26 @@ def test_adapters_whose_waits_run_out(C, lib, monkeypatch, w, x, rank, out):
         C.cq_device_status()
         assert torch.equal(o[:, :4], sides[0]) and torch.equal(o[:, out + 4:], sides[1])
         assert torch.equal(call(), want)
+
+
+@pytest.mark.parametrize("n,d", [(3, 64), (5000, 128), (20000, 512), (2, 4096), (3001, 1024), (5000, 2048), (2000, 8192), (700, 16384)])
+@pytest.mark.parametrize("dtype,out", [(F32, I8), (BF16, BF16)])
+def test_norms_whose_waits_run_out(C, lib, monkeypatch, n, d, dtype, out):
+    """Rows of a warp and of a block, rings of one stage and of several, one row of a team and many."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x = torch.randn(n, d, generator=g, device="cuda").to(dtype)
+    res, gate = torch.randn(n, d, generator=g, device="cuda").to(dtype), torch.randn(n, d, generator=g, device="cuda").to(dtype)
+    w = torch.randn(d, generator=g, device="cuda")
+
+    def call():
+        return C.cq_block_norm(x, res, w, post_norm=True, gate=gate, gate_act="silu", out_dtype=out)
+
+    want = call()
+    C.cq_device_status()
+    with monkeypatch.context() as m:
+        m.setattr(lib, "cq_block_norm", lib.cq_selftest_norm_timeout)
+        call()
+    with pytest.raises(C.CQError, match="0x474a0001"):
+        C.cq_device_status()
+    C.cq_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(call(), want))
