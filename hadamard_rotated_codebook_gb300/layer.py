@@ -180,9 +180,10 @@ def cq_lora_add(ys: Sequence[torch.Tensor], x: torch.Tensor, a: Sequence[torch.T
     if size is None:
         with (_stay if index == torch.cuda.current_device() else torch.cuda.device(dev)):
             size = _load().cq_lora_workspace(desc(0, 0))
-        if len(_lora_bytes) >= 4096:
-            _lora_bytes.clear()
-        _lora_bytes[key] = size
+        if size:  # (none: nothing to do, or the library refuses something that the key may not hold)
+            if len(_lora_bytes) >= 4096:
+                _lora_bytes.clear()
+            _lora_bytes[key] = size
     ws = torch.empty(size, dtype=torch.uint8, device=dev)
     _call(dev, _load().cq_lora_add, desc(ws.data_ptr(), size))
     return list(outs)
