@@ -56,8 +56,8 @@ def cq_block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weig
     dev = x.device
     xs = _matrix(x, "x", dev)
     n, d = x.shape
-    if n >> 31:
-        _ints(tokens=n)
+    if (n | d) >> 31:
+        _ints(tokens=n, width=d)
     xt = _type(x, "x")
     rd, rs, rt, gs, gw = x.dtype, 0, xt, 0, 0
     if residual is not None:
@@ -132,8 +132,8 @@ def cq_lora_add(ys: Sequence[torch.Tensor], x: torch.Tensor, a: Sequence[torch.T
         raise ValueError(f"a must be [adapters, rank, in], got {tuple(at)}")
     n_adapters, rank, _ = at
     n_seqs = adapters.numel()
-    if (n | n_in | n_seqs | n_adapters) >> 31:
-        _ints(tokens=n, n_in=n_in, requests=n_seqs, adapters=n_adapters)
+    if (n | n_in | n_seqs | n_adapters | rank) >> 31:
+        _ints(tokens=n, n_in=n_in, requests=n_seqs, adapters=n_adapters, rank=rank)
     a_ptr, b_ptr, y_ptr, o_ptr, y_stride, o_stride, widths = [0] * 8, [0] * 8, [0] * 8, [0] * 8, [0] * 8, [0] * 8, [0] * 8
     for j in range(m):
         y, o, aj, bj = ys[j], outs[j], a[j], b[j]

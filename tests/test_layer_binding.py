@@ -42,3 +42,20 @@ def test_a_refused_call_leaves_no_size_behind(layer):
         layer._lora_bytes.clear()
         assert call(*refused) == 0  # what is wrong with it is the library's to say
         assert call(32) == need
+
+
+def test_norm_widths_that_leave_32_bits_are_refused(layer):
+    """The library's sizes are 32 bits wide: a row of 2^32 + 64 elements is not one of 64."""
+    for width in (2 ** 32 + 64, 2 ** 31, 2 ** 33):
+        with pytest.raises(ValueError, match="32 bits"):
+            layer.cq_block_norm(_new(1, width, dtype=F16))
+    assert not layer.calls
+    layer.cq_block_norm(_new(1, 64, dtype=F16))
+    assert layer.calls[-1].width == 64
+
+
+def test_ranks_that_leave_32_bits_are_refused(layer):
+    rank = 2 ** 32 + 8
+    with pytest.raises(ValueError, match="32 bits"):
+        layer.cq_lora_add([_new(1, 4)], _new(1, 8), [_new(1, rank, 8, dtype=F16)], [_new(1, 4, rank, dtype=F16)], _new(1, dtype=torch.int32),
+                          _new(2, dtype=torch.int32))
