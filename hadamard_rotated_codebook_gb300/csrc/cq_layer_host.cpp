@@ -15,6 +15,40 @@ constexpr int kMaxSide = 1 << 28;  // inputs and outputs of an adapted projectio
 bool is_float(int type) { return type >= CQ_T_F32 && type <= CQ_T_BF16; }
 bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
+// Rows of a tensor: n of them, `bytes` long and `stride` bytes apart.
+struct Rows {
+    const void *at;
+    int64_t stride, bytes;
+    int type;  // of the elements
+};
+Rows rows_of(const void *at, int64_t stride, int64_t width, int type) {
+    const int size = type == CQ_T_F32 ? 4 : type == CQ_T_I8 ? 1 : 2;
+    return {at, stride * size, width * size, type};
+}
+// a / b of whole numbers, rounded down; b above zero.
+__int128 floor_div(__int128 a, __int128 b) { return a / b - (a % b < 0); }
+// Whether two tensors of n rows share a byte. (Column slices of one tensor do not, though one's rows lie between the other's.)
+bool overlap(Rows a, Rows b, int64_t n) {
+    if (!a.at || !b.at || n < 1 || a.bytes < 1 || b.bytes < 1) return false;
+    if (n == 1) a.stride = b.stride = 0;
+    __int128 p = reinterpret_cast<uintptr_t>(a.at), q = reinterpret_cast<uintptr_t>(b.at), s = a.stride, t = b.stride;
+    if (s < 0) p += s * (n - 1), s = -s;  // the last row first
+    if (t < 0) q += t * (n - 1), t = -t;
+    if (p >= q + t * (n - 1) + b.bytes || q >= p + s * (n - 1) + a.bytes) return false;
+    // Rows of b, `step` apart and numbered lo .. hi, of which one meets `bytes` from `at` on.
+    auto meets = [&](__int128 at, int64_t bytes, __int128 step, int64_t lo, int64_t hi) {
+        if (step == 0) return at < q + b.bytes && q < at + bytes;
+        const __int128 first = floor_div(at - b.bytes - q, step) + 1, last = floor_div(at + bytes - 1 - q, step);
+        return std::max<__int128>(first, lo) <= std::min<__int128>(last, hi);
+    };
+    if (s == t) return meets(p, a.bytes, s, 1 - n, n - 1);  // only the distance of the rows' numbers counts
+    for (int64_t i = 0; i < n; ++i)
+        if (meets(p + s * i, a.bytes, t, 0, n - 1)) return true;
+    return false;
+}
+// The same tensor, element by element.
+bool same(const Rows &a, const Rows &b, int64_t n) { return a.at == b.at && a.type == b.type && (n == 1 || a.stride == b.stride); }
+
 // How a call is cut up, apart from its alignment; the workspace's bytes, or 0.
 size_t lora_plan(const cq_lora_desc &d, bool few, bool tensor, LoraParams &p) {
     const int tiles = lora_rank_tiles(d.rank), ranks = 16 * tiles, tok = lora_tokens(d.x_dtype, tiles, few, tensor);
@@ -72,7 +106,21 @@ static int block_norm(const cq_norm_desc *d, bool give_up, void *stream) {
     if (d->n_tokens > 1 && ((d->residual_out && d->residual_out_stride < d->width) || d->out_stride < d->width))
         return set_error(CQ_ERR_SHAPE, "output rows of %d elements are %lld and %lld apart", d->width, (long long)d->residual_out_stride,
                          (long long)d->out_stride);
-    if (d->residual_out == d->out) return set_error(CQ_ERR_ARG, "the two outputs share memory");
+    // An element of an output may take the place of the same element of an input: the lane that writes it has read it. Anything else would be
+    // written while others read.
+    const int64_t n = d->n_tokens, w = d->width;
+    const Rows out[3] = {rows_of(d->out, d->out_stride, w, d->out_dtype), rows_of(d->residual_out, d->residual_out_stride, w, d->residual_dtype),
+                         rows_of(d->out_dtype == CQ_T_I8 ? d->out_scale : nullptr, 1, 1, CQ_T_F32)};
+    const Rows in[5] = {rows_of(d->x, d->x_stride, w, d->x_dtype), rows_of(d->residual, d->residual_stride, w, d->residual_dtype),
+                        rows_of(d->gate, d->gate_stride, d->gate_width, d->x_dtype), rows_of(d->weight, 0, w, CQ_T_F32),
+                        rows_of(d->branch_weight, 0, w, CQ_T_F32)};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j], n)) return set_error(CQ_ERR_ARG, "two outputs share memory");
+        for (int j = 0; j < 5; ++j)
+            if (overlap(out[i], in[j], n) && !(i < 2 && j < 3 && out[i].bytes == in[j].bytes && same(out[i], in[j], n)))
+                return set_error(CQ_ERR_ARG, "an output and an input share memory in another way than element by element");
+    }
     return launch_block_norm(*d, give_up, stream);
 }
 
@@ -120,10 +168,16 @@ static int lora_add(const cq_lora_desc *d, bool give_up, void *stream) {
             return set_error(CQ_ERR_SHAPE, "y is added to in place with rows %lld and %lld apart", (long long)d->y_stride[j],
                              (long long)d->y_out_stride[j]);
     }
+    const Rows x = rows_of(d->x, d->x_stride, d->in, d->x_dtype);
     for (int j = 0; j < d->n_mats; ++j) {
-        if (d->y_out[j] == d->x) return set_error(CQ_ERR_ARG, "an output is x");
-        for (int k = 0; k < d->n_mats; ++k)
-            if (k != j && (d->y_out[j] == d->y_out[k] || d->y_out[j] == d->y[k])) return set_error(CQ_ERR_ARG, "outputs %d and %d share memory", j, k);
+        const Rows o = rows_of(d->y_out[j], d->y_out_stride[j], d->out[j], CQ_T_F32);
+        if (overlap(o, x, d->n_tokens)) return set_error(CQ_ERR_ARG, "an output shares memory with x");
+        for (int k = 0; k < d->n_mats; ++k) {
+            const Rows y = rows_of(d->y[k], d->y_stride[k], d->out[k], CQ_T_F32);
+            if ((k != j && overlap(o, rows_of(d->y_out[k], d->y_out_stride[k], d->out[k], CQ_T_F32), d->n_tokens)) ||
+                (!(k == j && same(o, y, d->n_tokens)) && overlap(o, y, d->n_tokens)))
+                return set_error(CQ_ERR_ARG, "output %d shares memory with output %d or its y", j, k);
+        }
     }
     LoraParams p;
     p.d = *d;

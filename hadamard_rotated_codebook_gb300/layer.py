@@ -52,7 +52,9 @@ def cq_block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weig
     itself); weights are fp32 [width]; the residual may have another type than x
     (None: zeros). Returns (r in the residual's type, y), or with out_dtype
     torch.int8 (r, codes, scales) with the bits of cq_act_quant_int8 over the
-    fp32 y. Outputs may be given; residual_out may be residual, out may be x."""
+    fp32 y. Outputs may be given; residual_out and out
+    may each be x, residual or a gate of full width itself. Outputs that share
+    memory with each other, or in another way with an input, are refused."""
     dev = x.device
     xs = _matrix(x, "x", dev)
     n, d = x.shape
@@ -111,7 +113,8 @@ def cq_lora_add(ys: Sequence[torch.Tensor], x: torch.Tensor, a: Sequence[torch.T
     b[j] [adapters, out_j, rank], both fp16 or bf16; ys[j] is fp32 [tokens,
     out_j], up to 8 of them. ``ranks`` (int32 [adapters]): how many ranks of each
     adapter are in use. Without ``outs`` the ys are added to in place. Returns the
-    outs. Rows that no request covers are not written. A request outside the
+    outs. An output that shares memory with x, another output or a y (but its own,
+    in place) is refused. Rows that no request covers are not written. A request outside the
     tokens, and an adapter or rank outside its size, make a following
     cq_device_status raise."""
     dev = x.device

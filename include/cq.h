@@ -619,9 +619,10 @@ typedef struct cq_norm_desc {
  * in fp32, each output rounded once: y is the norm of the unrounded r. A
  * missing weight of a norm counts as 1 (weight_offset is added to it too).
  * With out_dtype CQ_T_I8 out holds the int8 codes of y and out_scale their
- * scales, the bits of cq_act_quant_int8 over the fp32 y. residual_out may be
- * residual itself and out may be x itself (same pointer, stride and type); an
- * output must not overlap an input in another way, nor the other output.
+ * scales, the bits of cq_act_quant_int8 over the fp32 y. residual_out and
+ * out may each be x, residual or a gate of full width itself (same pointer,
+ * stride and type); an output that overlaps an input in another way, or
+ * another output, is refused (CQ_ERR_ARG).
  * Errors: CQ_ERR_ARG, CQ_ERR_SHAPE, CQ_ERR_CUDA. */
 int cq_block_norm(const cq_norm_desc *d, void *stream);
 
@@ -668,7 +669,9 @@ size_t cq_lora_workspace(const cq_lora_desc *d);
  * (the products take fp32 activations as two terms of 11 bits and those values
  * as three terms of bf16 or two of fp16, by the weights' type: 2^-22 and
  * less is lost). A token's result depends on the other requests by the order
- * of its sums alone. x must not overlap an output, nor one matrix's output another's or its y.
+ * of its sums alone. An output that
+ * overlaps x, another output or a y (but y_out[j] that is y[j] itself) is
+ * refused (CQ_ERR_ARG).
  * A request outside the tokens (cu_tokens not ascending in 0..n_tokens) is
  * skipped, one whose adapter or rank is outside its size counts as having
  * none; both mark the device status word (CQ_ERR_INDEX). Errors: CQ_ERR_ARG,
