@@ -20,7 +20,7 @@ struct LoraParams {
     int pieces;    // of up to so many tokens of a request as a block takes, at most
     int splits;    // parts of k
     int runs;      // of 32 outputs that a warp of the second product takes
-    bool few;      // requests have few tokens
+    bool few;      // pieces of 8: few tokens a request, or few in all
     bool vec;      // rows of x and A in runs of 8
     bool tensor;   // x and A by tensor copies: rows on 16 bytes, and no fp32
     bool vec_b;    // rows of B in runs of 4

@@ -530,14 +530,14 @@ __global__ void __launch_bounds__(kThreads, (Up<T, MT>::kBlocks)) lora_up_kernel
     int64_t y_st = p.d.y_stride[mat];
     const uint16_t *B = static_cast<const uint16_t *>(p.d.b[mat]) + (int64_t)max(q.adapter, 0) * out * p.d.rank;
     const bool vec_y = p.vec_y[mat], ring_b = p.vec_b;
-    const int tiles = (q.n + 7) / 8, mine = g0 < g1 ? (g1 - g0 + kWarps - 1) / kWarps : 0;
+    const int mine = g0 < g1 ? (g1 - g0 + kWarps - 1) / kWarps : 0;
     const uint32_t ring = smem_u32(smem_up) + S::kU + warp * S::kDepth * S::kStage;
     // Ranks in runs of kRank, each added to what the one before left (one run, nearly always).
 #pragma unroll 1
     for (int r0 = 0; r0 == 0 || r0 < q.rank; r0 += S::kRank) {
         const int rank = min(S::kRank, q.rank - r0);
-        // A lane's elements of tile t of its j-th run of outputs are copied some tiles ahead of their turn.
-        int sj = 0, stile = 0, sst = 0;
+        // A lane's elements of its j-th run of outputs are copied some runs ahead of their turn.
+        int sj = 0, sst = 0;
         auto send = [&]() {
             if (sj < mine) {
                 const int o = (g0 + sj * kWarps) * 32 + 4 * g;
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, (Up<T, MT>::kBlocks)) lora_up_kernel
                 if (vec_y) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int tok = stile * 8 + 2 * c + h;
+                        const int tok = 2 * c + h;
                         const bool there = tok < q.n && o < out;
                         copy16(to + h * 512 + lane * 16, y + (there ? (int64_t)(q.first + tok) * y_st + o : 0), there);
                     }
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, (Up<T, MT>::kBlocks)) lora_up_kernel
                             copy8(to + 1024 + (m * 4 + i) * 256 + lane * 8, B + (there ? (int64_t)(o + i) * p.d.rank + r0 + m * 16 + 4 * c : 0), there);
                         }
                 }
-                if (++stile == tiles) stile = 0, ++sj;
+                ++sj;
             }
             copies_sent();
             if (++sst == S::kDepth) sst = 0;
@@ -568,9 +568,9 @@ __global__ void __launch_bounds__(kThreads, (Up<T, MT>::kBlocks)) lora_up_kernel
         for (int j = 0; j < S::kDepth - 1; ++j) send();
         if (r0) __syncthreads();  // u is read
         else asm volatile("griddepcontrol.wait;\n" ::: "memory");
-        // ------------------------------------------------------------- u as two terms --
+        // ---------------------------------------------------------------- u in terms --
         if (rank > 0) {
-            gather_u<T, S::kRank>(p, q, mat, r0, tiles * 8, back, false, [&](int k, int t, int r, uint2 w) {
+            gather_u<T, S::kRank>(p, q, mat, r0, S::kTok, back, false, [&](int k, int t, int r, uint2 w) {
                 *reinterpret_cast<uint2 *>(u + k * S::kTerm + t * S::kRow + r * 2) = w;
             });
             __syncthreads();
@@ -590,71 +590,68 @@ __global__ void __launch_bounds__(kThreads, (Up<T, MT>::kBlocks)) lora_up_kernel
                     for (int i = 0; i < 4; ++i)
                         b[m][i] = load_b(B + (int64_t)(o + i) * p.d.rank + r0 + m * 16 + 4 * c, i < n_o ? rank - m * 16 - 4 * c : 0, p.vec_b);
             }
-#pragma unroll 1
-            for (int t = 0; t < tiles; ++t) {
-                send();
-                copies_landed<S::kDepth - 1>();
-                const uint32_t at = ring + st * S::kStage;
-                if (++st == S::kDepth) st = 0;
-                if (ring_b) {
+            send();
+            copies_landed<S::kDepth - 1>();
+            const uint32_t at = ring + st * S::kStage;
+            if (++st == S::kDepth) st = 0;
+            if (ring_b) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) b[m][i] = lds8(at + 1024 + (m * 4 + i) * 256 + lane * 8);
+                if (rank & 3) {  // (uniform) a run that ends inside four
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) b[m][i] = lds8(at + 1024 + (m * 4 + i) * 256 + lane * 8);
-                    if (rank & 3) {  // (uniform) a run that ends inside four
+                        for (int i = 0; i < 4; ++i) b[m][i] = cut_b(b[m][i], rank - m * 16 - 4 * c);
+                }
+            }
+            float v[2][4];
 #pragma unroll
-                        for (int m = 0; m < MT; ++m)
+            for (int h = 0; h < 2; ++h) {
+                const int tok = 2 * c + h;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) b[m][i] = cut_b(b[m][i], rank - m * 16 - 4 * c);
+                for (int i = 0; i < 4; ++i) v[h][i] = 0.0f;
+                if (vec_y) {
+                    const uint4 f = lds16(at + h * 512 + lane * 16);
+                    v[h][0] = __uint_as_float(f.x), v[h][1] = __uint_as_float(f.y), v[h][2] = __uint_as_float(f.z), v[h][3] = __uint_as_float(f.w);
+                } else if (tok < q.n) {
+                    const float *from = y + (int64_t)(q.first + tok) * y_st + o;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < n_o) v[h][i] = from[i];
+                }
+            }
+            float d[2][2][4] = {};  // the first term's products, and the others'
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                if (m >= kts) break;
+                const uint8_t *row = u + g * S::kRow + m * 32 + 8 * c;
+#pragma unroll
+                for (int k = kTerms - 1; k >= 0; --k) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(row + k * S::kTerm);
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) mma16<T>(d[k > 0][f], b[m][2 * f].x, b[m][2 * f + 1].x, b[m][2 * f].y, b[m][2 * f + 1].y, w.x, w.y);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int tok = 2 * c + h;
+                if (tok >= q.n || n_o <= 0) continue;
+                if (rank > 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float sum = d[0][i >> 1][2 * (i & 1) + h] + d[1][i >> 1][2 * (i & 1) + h];
+                        v[h][i] = std::is_same<T, __half>::value ? fmaf(sum, back[tok], v[h][i]) : v[h][i] + sum;
                     }
                 }
-                float v[2][4];
+                float *to = yo + (int64_t)(q.first + tok) * yo_st + o;
+                if (vec_y) {
+                    *reinterpret_cast<float4 *>(to) = make_float4(v[h][0], v[h][1], v[h][2], v[h][3]);
+                } else {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int tok = t * 8 + 2 * c + h;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[h][i] = 0.0f;
-                    if (vec_y) {
-                        const uint4 f = lds16(at + h * 512 + lane * 16);
-                        v[h][0] = __uint_as_float(f.x), v[h][1] = __uint_as_float(f.y), v[h][2] = __uint_as_float(f.z), v[h][3] = __uint_as_float(f.w);
-                    } else if (tok < q.n) {
-                        const float *from = y + (int64_t)(q.first + tok) * y_st + o;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (i < n_o) v[h][i] = from[i];
-                    }
-                }
-                float d[2][2][4] = {};  // the first term's products, and the others'
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if (m >= kts) break;
-                    const uint8_t *row = u + (t * 8 + g) * S::kRow + m * 32 + 8 * c;
-#pragma unroll
-                    for (int k = kTerms - 1; k >= 0; --k) {
-                        const uint2 w = *reinterpret_cast<const uint2 *>(row + k * S::kTerm);
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) mma16<T>(d[k > 0][f], b[m][2 * f].x, b[m][2 * f + 1].x, b[m][2 * f].y, b[m][2 * f + 1].y, w.x, w.y);
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int tok = t * 8 + 2 * c + h;
-                    if (tok >= q.n || n_o <= 0) continue;
-                    if (rank > 0) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float sum = d[0][i >> 1][2 * (i & 1) + h] + d[1][i >> 1][2 * (i & 1) + h];
-                            v[h][i] = std::is_same<T, __half>::value ? fmaf(sum, back[tok], v[h][i]) : v[h][i] + sum;
-                        }
-                    }
-                    float *to = yo + (int64_t)(q.first + tok) * yo_st + o;
-                    if (vec_y) {
-                        *reinterpret_cast<float4 *>(to) = make_float4(v[h][0], v[h][1], v[h][2], v[h][3]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (i < n_o) to[i] = v[h][i];
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        if (i < n_o) to[i] = v[h][i];
                 }
             }
         }
