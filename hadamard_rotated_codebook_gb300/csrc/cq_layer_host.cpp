@@ -72,9 +72,13 @@ size_t lora_plan(const cq_lora_desc &d, bool few, bool tensor, LoraParams &p) {
 }
 // Pieces of 8 tokens on mma.sync: where requests have few tokens each, whose adapters are then what there is to read, and where there
 // are few tokens in all, as tcgen05's kernels take 6 us longer to begin and end. Their cost a token goes by the ranks and, as y is
-// read and written, more by the outputs than by the inputs. (4096 to 4096, few against many: rank 16, a prompt of 40 tokens 5.7 us
-// against 12.6, of 512 12.3 against 15.5, four of 512 31 against 24; 32 requests of 20 16 against 26; rank 64, one of 256 15.1 against
-// 18.5, one of 512 23.0 against 19.6, 16 requests of 32 29 against 23, 64 of 16 50 against 49.)
+// read and written, more by the outputs than by the inputs. (4096 to 4096, int8, few against many: rank 16, a prompt of 40 tokens 5.5 us
+// against 12.5, of 512 11.8 against 15.4, of 1024 18.0 against 18.4, four of 512 30 against 24; 32 requests of 20 15 against 25; rank 64,
+// one of 512 23.4 against 19.7, 16 requests of 32 29 against 24, 64 of 16 50 against 49.)
+// The rule knows a call's sums alone, and takes the slower kernels in between: 16 requests of 48 tokens at rank 16 (21 us, 15 with few), 32
+// of 50 (32, 28), at rank 64 one of 256 (18, 14) and 8 of 28 (20, 16). It counts rows that no request covers, so that 64 decodes in
+// buffers of 4096 rows take the kernels of many tokens (92 us, 26 with few), and it does not see one prompt of 2000 tokens beside 255
+// single tokens (rank 64: 145 us, 82 and 29 in calls of their own; rank 16: 51, 25 and 24).
 bool lora_few(const cq_lora_desc &d) {
     const long long tiles = (d.rank + 15) / 16;
     long long side = d.in;

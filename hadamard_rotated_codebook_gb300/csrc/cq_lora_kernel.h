@@ -9,7 +9,7 @@
 // which sums its part of k for all ranks and leaves the sum in a workspace; the second gives tiles of outputs to blocks, which
 // add the parts in their order. No atomics on values, and nothing depends on timing. The second kernel begins while the first still
 // runs: its blocks have found their pieces and have y and B on their way by the time the first one's sums are there. (One kernel
-// of clusters that met over distributed shared memory took 32 us for 64 decodes where the two take 17, and 211 us for the
+// of clusters that met over distributed shared memory took 32 us for 64 decodes where the two take 16, and 211 us for the
 // prompt below: a cluster's barriers stand between its loads.)
 //
 // Few tokens a request (lora_down_kernel, lora_up_kernel): pieces of 8 on mma.sync. Rank is the M side of the first product (16 rows of A to a
@@ -23,10 +23,10 @@
 // terms of 11 bits (tf32, which holds fp16 and bf16 weights exactly): what is lost is 2^-22. u, summed in fp32, is three
 // terms of bf16 or two of fp16 (Terms).
 //
-// Measured: 64 decodes with 60 adapters, 4096 to 4096, 1024 and 1024, rank 16, int8 (38.8 MB): 17 us, 2.3 TB/s or 34% of the copy rate, 5.7 us
-// being the floor: memory's latency twice in a row and the launch, with issue slots at half; 256 decodes 47 us, 51%. A prompt of 8190
-// tokens of three requests, 4096 to 4096, rank 64, bf16 (339 MB): 66 us, 76%, floor 50; rank 16, int8: 61 us, 73%. One token, 512 to
-// 512, 256 and 256, rank 8: 4.9 us, two kernels' latency.
+// Measured: 64 decodes with 60 adapters, 4096 to 4096, 1024 and 1024, rank 16, int8 (38.8 MB): 16 us, 2.4 TB/s or 36% of the copy rate, 5.7 us
+// being the floor: memory's latency twice in a row and the launch, with issue slots at half; 256 decodes 45 us, 53%. A prompt of 8190
+// tokens of three requests, 4096 to 4096, rank 64, bf16 (339 MB): 67 us, 75%, floor 50; rank 16, int8: 61 us, 73%. One token, 512 to
+// 512, 256 and 256, rank 8: 5 us, two kernels' latency.
 // Tried and slower for prompts: mma.sync in both (97 to 146 us: 1.4 instructions an element), y in rows of 512 bytes by plain bulk copies (125 us: a
 // copy of any size costs the copy engine as much), y loaded by the threads that add (124 us).
 #pragma once

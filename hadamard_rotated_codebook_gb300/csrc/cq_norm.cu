@@ -18,8 +18,9 @@
 //
 // The bound is memory, and issue slots next to it (two elements to an instruction where there is one for that). 8190 rows of
 // 4096 in fp32 onto bf16 with a norm of the branch, to int8 (302 MB): 61 us, 5.0 TB/s or 73% of the copy rate; 16383 of 2048 in bf16 with
-// a silu gate for every element (336 MB): 68 us, 73%, issue slots at 70%; 8190 of 4096 in bf16 without either: 47 us, 84%. Steps of a
-// few rows take 3 to 5 us, which is two latencies of memory and the launch. Rows of 16384 in fp32 leave the ring one stage (51%).
+// a silu gate for every element (336 MB): 69 us, 72%, issue slots at 68%; 8190 of 4096 in bf16 without either: 47 us, 84%. Steps of a
+// few rows take 3 to 5 us, which is two latencies of memory and the launch. Rows of 16384 in fp32 leave the ring one stage
+// (129 us for 2048 of them with a norm of the branch, 61%), and 40000 of 333 in fp32, read element by element, take 86 us (36%).
 // Tried and slower: four runs a lane instead of two (94 against 69 us: half as many warps wait), one run a lane (78
 // against 61 us to int8: an element costs more instructions, though single rows are 0.5 us faster), weights loaded before the reductions (76 us: registers).
 #include <cuda_bf16.h>

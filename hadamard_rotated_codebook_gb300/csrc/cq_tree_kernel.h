@@ -35,7 +35,7 @@
 // of its rows behind; in the tiles that hold such rows a thread compares how far its row lies behind the window's beginning
 // with the depths of the columns' tokens, four at a time. Window of 2048 and 4 sinks, 256 single tokens as in the decode batch
 // below: 49 us, 11% of the copy rate (the tree attention of their whole contexts 115); chunks of 200 to 256 tokens for 16
-// requests, 32 heads over 8 of 128, window of 4096: 534 us, 23% of the dense rate. What bounds them is what bounds every tile here.
+// requests, 32 heads over 8 of 128, window of 4096: 533 us, 23% of the dense rate. What bounds them is what bounds every tile here.
 //
 // Queries in fp16. Each column is rounded at the power of two of its own largest element (rotate_queries), so that a query of any
 // size leaves its tile mates' bits alone. The product then takes the columns at the tile's largest scale where that is exact for
@@ -63,8 +63,8 @@
 // the latencies of five roles that hand each other buffers, with 46 to 51% of the issue slots used and
 // shared memory busy for 45 to 66% of the time. An item (a request, unit and column tile) costs another
 // 15000 to 20000 cycles to begin and end. Measured: 256 requests of 8000 tokens, 12 heads on 2 of 48/64, 2 bits,
-// one token each, 117 us; 32 requests of 2000 to 8000 tokens with trees of 40 to 64, 32 heads on 8 of 128, 4 bits,
-// 316 us; one of 131071 tokens with a tree of 64, the same heads, 2 bits, 205 us.
+// one token each, 115 us; 32 requests of 2000 to 8000 tokens with trees of 40 to 64, 32 heads on 8 of 128, 4 bits,
+// 312 us; one of 131071 tokens with a tree of 64, the same heads, 2 bits, 203 us.
 // Tried and slower: both sides or the keys alone looked up by byte permutes instead of tables (server 355 -> 495 us: the
 // integer pipe runs at half rate), two expander warpgroups a side, two softmax streams or eight fetchers for 16
 // columns (117 -> 120 to 145 us), leaving out the runs of 32 columns that a tree does not fill (203 -> 215 us and

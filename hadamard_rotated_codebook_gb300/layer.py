@@ -105,7 +105,7 @@ def cq_lora_add(ys: Sequence[torch.Tensor], x: torch.Tensor, a: Sequence[torch.T
                 ranks: Optional[torch.Tensor] = None, x_scale: Optional[torch.Tensor] = None,
                 outs: Optional[Sequence[torch.Tensor]] = None) -> list:
     """Low-rank adapters of many requests beside shared projections, in one
-    launch: ``outs[j][t] = ys[j][t] + scales[e] * b[j][e] @ (a[j][e] @ x[t])`` with
+    call (two kernels): ``outs[j][t] = ys[j][t] + scales[e] * b[j][e] @ (a[j][e] @ x[t])`` with
     e = adapters[s] the adapter of token t's request (-1: none; tokens of
     request s are cu_tokens[s] .. cu_tokens[s + 1] - 1, as cq_kv_plan gives them).
     x is [tokens, in] in fp32, the weights' type, or int8 with per-token scales
@@ -114,9 +114,10 @@ def cq_lora_add(ys: Sequence[torch.Tensor], x: torch.Tensor, a: Sequence[torch.T
     out_j], up to 8 of them. ``ranks`` (int32 [adapters]): how many ranks of each
     adapter are in use. Without ``outs`` the ys are added to in place. Returns the
     outs. An output that shares memory with x, another output or a y (but its own,
-    in place) is refused. Rows that no request covers are not written. A request outside the
-    tokens, and an adapter or rank outside its size, make a following
-    cq_device_status raise."""
+    in place) is refused. Rows that no request covers are not written, but count
+    where kernels are chosen: give a decode step's tensors no more rows than its
+    graph needs. A request outside the tokens, and an adapter or rank outside its
+    size, make a following cq_device_status raise."""
     dev = x.device
     m = len(ys)
     outs = ys if outs is None else outs

@@ -669,7 +669,11 @@ size_t cq_lora_workspace(const cq_lora_desc *d);
  * (the products take fp32 activations as two terms of 11 bits and those values
  * as three terms of bf16 or two of fp16, by the weights' type: 2^-22 and
  * less is lost). A token's result depends on the other requests by the order
- * of its sums alone. An output that
+ * of its sums alone. The kernels are chosen for a call as a whole, by n_tokens
+ * (rows that no request covers among them), n_seqs, rank and the widths: a
+ * long prompt beside many single tokens is faster in a call of its own from
+ * rank 64 on, and a decode step in buffers of thousands of rows than it has
+ * tokens takes the kernels of long prompts. An output that
  * overlaps x, another output or a y (but y_out[j] that is y[j] itself) is
  * refused (CQ_ERR_ARG).
  * A request outside the tokens (cu_tokens not ascending in 0..n_tokens) is
